@@ -410,6 +410,150 @@ dpf_status dpfused_projected_adam_step(const float* grad, float* m, float* v, fl
                                        const void* P, int32_t p_dtype, uint64_t p_seed,
                                        uint64_t p_offset, float p_scale, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The two ends of a language model, next to its linear layers: the token
+ * embedding, and the log probabilities of the next tokens.  Token ids are
+ * read on the device only, so an id cannot be refused: one outside [0, V)
+ * marks its position inactive, like a mask byte of 0.
+ * ------------------------------------------------------------------------ */
+typedef enum { DPF_I32 = 0, DPF_I64 = 1 } dpf_id_type;
+
+/* [B, T] token ids in device memory; the ids of one sample are contiguous,
+ * samples start stride_b >= T ELEMENTS apart (so ids[:, 1:] of a longer
+ * array can be given as it is).  `data` needs its element's alignment. */
+typedef struct {
+  const void* data;
+  int32_t type;      /* dpf_id_type */
+  int32_t reserved;  /* must be 0 */
+  int64_t B, T;
+  int64_t stride_b;
+} dpf_ids;
+
+/* out[b][t] = scale * table[ids[b][t]], rounded once to out_dtype (nearest
+ * even for bf16); 0 where the position is inactive (mask byte 0, or an id
+ * outside [0, V)).
+ *
+ *   table      [V, D], table_dtype, rows contiguous, stride_v >= D elements
+ *              apart, 16-byte aligned
+ *   mask       [B, T] uint8 or NULL
+ *   scale      finite
+ *   out        [B, T, D] contiguous, out_dtype, 16-byte aligned, overwritten
+ *
+ * The table is read through 16-byte loads where D and stride_v are multiples
+ * of 8 (4: half as wide; else element by element).
+ * Errors: DPF_ERR_INVALID_ARGUMENT for NULL ids, table or out, B, T, V or
+ * D < 1, stride_b < T, stride_v < D, scale not finite; DPF_ERR_UNSUPPORTED
+ * for an unknown type or dtype, a non-zero reserved field, a misaligned
+ * pointer, B * T > 2^25, V > 2^24, D > 2^22 or V * D > 2^33. */
+dpf_status dpfused_embedding_lookup(const dpf_ids* ids, const void* table, int32_t table_dtype,
+                                    int64_t V, int64_t D, int64_t stride_v, const uint8_t* mask,
+                                    float scale, int32_t out_dtype, void* out, void* stream);
+
+/* The fused DP step for an embedding table, the gradient of
+ * dpfused_embedding_lookup clipped per sample (the per-layer clipping of the
+ * FlashDP abstract, for the layer whose per-sample gradients are the largest
+ * and the sparsest):
+ *
+ *   g_i[v]       = scale * sum over the active t with ids[i][t] = v of G_i[t]   [V, D]
+ *   n_i          = ||g_i||_F,  c_i = 1 if n_i <= C, else C / n_i
+ *   grad_out     = beta * grad_out + (sum_i c_i g_i + sigma * C * xi) / denom
+ *   norms_out[i] = n_i
+ *
+ * xi over the row-major [V, D] result as for dpfused_linear_clip_accumulate
+ * (every row gets noise, also those whose token does not occur: which tokens
+ * occurred is itself private).  A call consumes dpfused_noise_blocks(V * D)
+ * blocks.
+ *
+ * The positions are sorted by token (a stable sort on the device); equal
+ * tokens of a sample are summed before they are squared, equal tokens of the
+ * batch are one row of the result.  No per-sample gradient is stored.
+ * Sums in float32, norms in float64, in a fixed order.
+ *
+ *   ids, G       [B, T] and [B, T, D] (bf16 or f32)
+ *   V            rows of the table
+ *   scale        the lookup's
+ *   C, sigma, seed, offset, denom, accumulate (beta)   as for
+ *                dpfused_linear_clip_accumulate_ex
+ *   grad_out     [V, D] float32 row-major, 16-byte aligned
+ *   norms_out    [B] float32 or NULL
+ *
+ * Errors as for dpfused_embedding_lookup and
+ * dpfused_linear_clip_accumulate_ex; DPF_ERR_INVALID_ARGUMENT where ids and G
+ * disagree on B or T. */
+dpf_status dpfused_embedding_clip_accumulate(const dpf_ids* ids, const dpf_act* G,
+                                             const uint8_t* mask, int64_t V, float scale, float C,
+                                             float sigma, uint64_t seed, uint64_t offset,
+                                             float denom, int32_t accumulate, float* grad_out,
+                                             float* norms_out, void* stream);
+
+/* The building blocks of the above, for one clip factor per sample over the
+ * embedding and other layers (dpfused_per_sample_sqnorms of the linears,
+ * dpfused_clip_factors): ||g_i||^2 in float64, added to sqnorms_out with
+ * accumulate != 0; and (sum_i c[i] g_i + noise_std * xi) / B for given
+ * factors c[B] (device float32, each finite and > 0; noise_std finite and
+ * >= 0). */
+dpf_status dpfused_embedding_sqnorms(const dpf_ids* ids, const dpf_act* G, const uint8_t* mask,
+                                     int64_t V, float scale, double* sqnorms_out,
+                                     int32_t accumulate, void* stream);
+dpf_status dpfused_embedding_scaled_accumulate(const dpf_ids* ids, const dpf_act* G,
+                                               const uint8_t* mask, int64_t V, float scale,
+                                               const float* c, float noise_std, uint64_t seed,
+                                               uint64_t offset, float* grad_out, void* stream);
+
+/* Log probabilities of given tokens under rows of logits z [V], with the
+ * rows' entropy and best alternatives, in one pass over the logits:
+ *
+ *   lse     = log sum_j exp(z_j)
+ *   logp    = z_y - lse, y the target; 0 where y is outside [0, V)
+ *   entropy = -sum_j p_j log p_j,  p_j = exp(z_j - lse)
+ *   top_ids, top_logp   the top_k largest z_j and their z_j - lse, the
+ *             largest first, equal values by the lower index first
+ *
+ * all in float32.  A logit of -inf is a token of probability 0.  A row that
+ * holds NaN or +inf, or only -inf, has NaN logp, entropy and top_logp (and
+ * lse, but for the -inf row's -inf); top_ids then still orders the entries
+ * that are not NaN, and is -1 past them.  A masked row is not read: its
+ * values are 0, its top_ids -1.
+ *
+ *   logits   [B, T, V] bf16 or f32, strided as any dpf_act, 16-byte aligned
+ *   targets  [B, T] ids, or NULL (logp must then be NULL)
+ *   mask     [B, T] uint8 or NULL
+ *   top_k    0 .. min(32, V); top_logp and top_ids are [B, T, top_k], not
+ *            NULL where top_k > 0
+ *   logp, entropy, lse   [B, T] float32, each may be NULL
+ *
+ * Errors: DPF_ERR_INVALID_ARGUMENT for bad logits (as for
+ * dpfused_linear_clip_accumulate) or targets, B or T that disagree, top_k out
+ * of range, logp without targets, no output at all; DPF_ERR_UNSUPPORTED for
+ * B * T >= 2^24 or V > 2^23. */
+dpf_status dpfused_token_logprobs(const dpf_act* logits, const dpf_ids* targets,
+                                  const uint8_t* mask, int32_t top_k, float* logp, float* entropy,
+                                  float* lse, float* top_logp, int32_t* top_ids, void* stream);
+
+/* The gradient of the above to the logits, from the upstream gradients of
+ * logp and entropy (of a loss -sum w logp, dlogp = -w):
+ *
+ *   dz_j = dlogp (1[j = y] - p_j) - dentropy p_j (log p_j + entropy)
+ *
+ * A target outside [0, V) drops the first term; a masked row is 0.  The
+ * result is the G of the output layer's clip-and-accumulate call, so a
+ * per-sample loss keeps its rows apart (dlogp = -1 / T_i, not -1 / (B T)).
+ *
+ *   lse, entropy     what the forward call gave for the same logits;
+ *                    entropy may be NULL where dentropy is
+ *   dlogp, dentropy  [B, T] float32; either may be NULL (taken as 0), not both
+ *   dlogits          [B, T, V] bf16 or f32, strided; may be the logits
+ *                    themselves (same dtype and strides), else must not
+ *                    overlap them
+ *   targets          may be NULL where dlogp is
+ *
+ * Errors as above. */
+dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids* targets,
+                                           const uint8_t* mask, const float* lse,
+                                           const float* entropy, const float* dlogp,
+                                           const float* dentropy, const dpf_act* dlogits,
+                                           void* stream);
+
 /* Raw Philox4x32-10 words of the noise generator (the noise added after
  * clipping in the FlashDP abstract and in the DP-GRAPE explainer,
  * Methodology, is drawn from this counter-based generator; Salmon, Moraes,

@@ -15,16 +15,18 @@ from __future__ import annotations
 
 import ctypes
 import math
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 from . import _lib
-from ._lib import DpfAct, DpfError, DPF_BF16, DPF_F32  # noqa: F401
+from ._lib import DpfAct, DpfError, DpfIds, DPF_BF16, DPF_F32, DPF_I32, DPF_I64  # noqa: F401
 
 __all__ = [
     "linear_clip_accumulate", "linear_clip_accumulate_noalloc", "linear_clip_accumulate_projected",
     "linear_clip_accumulate_projected_seeded", "linear_clip_accumulate_bias", "project",
     "group_clip_accumulate", "consecutive_offsets", "projected_adam_step",
     "linear_clip_accumulate_projected_many",
+    "embedding_lookup", "embedding_clip_accumulate", "embedding_sqnorms",
+    "embedding_scaled_accumulate", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
     "per_sample_sqnorms",
     "clip_factors", "scaled_accumulate", "philox4x32_10", "gaussian_fill", "noise_blocks",
     "set_option", "get_option", "timing_reset", "timing_collect", "DpfError", "load",
@@ -479,6 +481,187 @@ def scaled_accumulate(X, G, c, mask=None, noise_std: float = 0.0, seed: int = 0,
                                               grad_out.data_ptr(), _stream(X, stream))
     _lib.check(st)
     return grad_out
+
+
+def _ids(t, name: str) -> DpfIds:
+    torch = _torch()
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [B, T]")
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    B, T = t.shape
+    if T > 1 and t.stride(1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # a single sample's stride is arbitrary: nothing is read past its row
+    return DpfIds(t.data_ptr(), DPF_I64 if t.dtype == torch.int64 else DPF_I32, 0, B, T,
+                  t.stride(0) if B > 1 else T)
+
+
+def embedding_lookup(ids, table, mask=None, scale: float = 1.0, out_dtype=None, out=None,
+                     stream=None):
+    """out[b, t] = scale * table[ids[b, t]] as [B, T, D] in out_dtype (default: the table's),
+    rounded once; 0 where the mask is 0 or the id is outside [0, V).
+
+    ids [B, T] int32 or int64; table [V, D] bf16 or fp32, rows contiguous (a float32 master
+    table can give bf16 activations directly)."""
+    torch = _torch()
+    ia = _ids(ids, "ids")
+    if table.dim() != 2 or table.stride(1) != 1:
+        raise ValueError("table must be [V, D] with contiguous rows")
+    _same_device(table, ids.device, "table")
+    V, D = table.shape
+    if out_dtype is None:
+        out_dtype = table.dtype if out is None else out.dtype
+    if out is None:
+        out = torch.empty((*ids.shape, D), dtype=out_dtype, device=ids.device)
+    _check_out(out, (*ids.shape, D), "out", ids.device, dtype=out_dtype)
+    st = _lib.lib().dpfused_embedding_lookup(
+        ctypes.byref(ia), table.data_ptr(), _dtype_code(table), int(V), int(D),
+        int(table.stride(0)) if V > 1 else int(D), _mask_ptr(mask, *ids.shape, ids.device),
+        float(scale), _dtype_code(out), out.data_ptr(), _stream(ids, stream))
+    _lib.check(st)
+    return out
+
+
+def embedding_clip_accumulate(ids, G, V: int, mask=None, scale: float = 1.0, C: float = 1.0,
+                              sigma: float = 0.0, seed: int = 0, offset: int = 0, grad_out=None,
+                              norms_out=None, stream=None, want_norms: bool = True,
+                              denom: Optional[float] = None, accumulate: bool = False):
+    """Fused DP step of an embedding table of V rows: the gradient of embedding_lookup, clipped
+    per sample, summed, noised (every row) and divided; returns (grad_out [V, D] fp32, norms).
+
+    G [B, T, D] is the gradient of the lookup's output; denom and accumulate as for
+    linear_clip_accumulate."""
+    torch = _torch()
+    ia, ga = _ids(ids, "ids"), _act(G)
+    _same_device(G, ids.device, "G")
+    B, T, D = G.shape
+    if accumulate and grad_out is None:
+        raise ValueError("accumulate=True needs grad_out")
+    if grad_out is None:
+        grad_out = torch.empty((int(V), D), dtype=torch.float32, device=G.device)
+    _check_out(grad_out, (int(V), D), "grad_out", G.device)
+    if norms_out is None and want_norms:
+        norms_out = torch.empty((B,), dtype=torch.float32, device=G.device)
+    if norms_out is not None:
+        _check_out(norms_out, (B,), "norms_out", G.device)
+    st = _lib.lib().dpfused_embedding_clip_accumulate(
+        ctypes.byref(ia), ctypes.byref(ga), _mask_ptr(mask, B, T, G.device), int(V), float(scale),
+        float(C), float(sigma), int(seed), int(offset), float(B if denom is None else denom),
+        int(bool(accumulate)), grad_out.data_ptr(), _ptr(norms_out), _stream(G, stream))
+    _lib.check(st)
+    return grad_out, norms_out
+
+
+def embedding_sqnorms(ids, G, V: int, mask=None, scale: float = 1.0, out=None,
+                      accumulate: bool = False, stream=None):
+    """||g_i||^2 of the embedding's per-sample gradients (fp64 [B]); with accumulate=True added
+    into ``out``, for clipping the embedding together with other layers."""
+    torch = _torch()
+    ia, ga = _ids(ids, "ids"), _act(G)
+    _same_device(G, ids.device, "G")
+    B, T, _ = G.shape
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs an out tensor")
+        out = torch.empty((B,), dtype=torch.float64, device=G.device)
+    _check_out(out, (B,), "out", G.device, torch.float64)
+    st = _lib.lib().dpfused_embedding_sqnorms(
+        ctypes.byref(ia), ctypes.byref(ga), _mask_ptr(mask, B, T, G.device), int(V), float(scale),
+        out.data_ptr(), 1 if accumulate else 0, _stream(G, stream))
+    _lib.check(st)
+    return out
+
+
+def embedding_scaled_accumulate(ids, G, c, V: int, mask=None, scale: float = 1.0,
+                                noise_std: float = 0.0, seed: int = 0, offset: int = 0,
+                                grad_out=None, stream=None):
+    """(sum_i c_i g_i + noise_std xi) / B of the embedding's gradients, for given fp32 c [B]."""
+    torch = _torch()
+    ia, ga = _ids(ids, "ids"), _act(G)
+    _same_device(G, ids.device, "G")
+    B, T, D = G.shape
+    _check_out(c, (B,), "c", G.device)
+    if grad_out is None:
+        grad_out = torch.empty((int(V), D), dtype=torch.float32, device=G.device)
+    _check_out(grad_out, (int(V), D), "grad_out", G.device)
+    st = _lib.lib().dpfused_embedding_scaled_accumulate(
+        ctypes.byref(ia), ctypes.byref(ga), _mask_ptr(mask, B, T, G.device), int(V), float(scale),
+        c.data_ptr(), float(noise_std), int(seed), int(offset), grad_out.data_ptr(),
+        _stream(G, stream))
+    _lib.check(st)
+    return grad_out
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns: float32 [B, T] each (logp None without targets), and
+    top_logp float32 / top_ids int32 [B, T, top_k] (None without alternatives)."""
+    logp: object
+    entropy: object
+    lse: object
+    top_logp: object
+    top_ids: object
+
+
+def token_logprobs(logits, targets=None, mask=None, top_k: int = 0, stream=None) -> TokenLogprobs:
+    """Log probabilities of the targets, entropy, log-sum-exp and the top_k best alternatives
+    (largest first, equal logits by the lower id) of logits [B, T, V] (bf16 or fp32).
+
+    targets [B, T] int32 or int64, one outside [0, V) gives logp 0; masked rows give 0 and id -1."""
+    torch = _torch()
+    za = _act(logits)
+    B, T, V = logits.shape
+    dev = logits.device
+    ta = None
+    if targets is not None:
+        ta = _ids(targets, "targets")
+        _same_device(targets, dev, "targets")
+    top_k = int(top_k)
+    f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+    logp = f32(B, T) if targets is not None else None
+    entropy, lse = f32(B, T), f32(B, T)
+    top_logp = f32(B, T, top_k) if top_k > 0 else None
+    top_ids = torch.empty((B, T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
+    st = _lib.lib().dpfused_token_logprobs(
+        ctypes.byref(za), None if ta is None else ctypes.byref(ta), _mask_ptr(mask, B, T, dev),
+        top_k, _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(top_logp), _ptr(top_ids),
+        _stream(logits, stream))
+    _lib.check(st)
+    return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
+
+
+def token_logprobs_backward(logits, targets, lse, dlogp, entropy=None, dentropy=None, mask=None,
+                            out=None, out_dtype=None, stream=None):
+    """Gradient to the logits from dlogp and dentropy ([B, T] fp32, either may be None), given
+    the forward call's lse (and entropy): [B, T, V] in out_dtype (default: the logits').
+
+    ``out`` may be the logits themselves.  The result is the G of the output layer's
+    linear_clip_accumulate; there is no gradient through top_logp."""
+    torch = _torch()
+    za = _act(logits)
+    B, T, V = logits.shape
+    dev = logits.device
+    ta = None
+    if targets is not None:
+        ta = _ids(targets, "targets")
+        _same_device(targets, dev, "targets")
+    for t, name in ((lse, "lse"), (dlogp, "dlogp"), (entropy, "entropy"), (dentropy, "dentropy")):
+        if t is not None:
+            _check_out(t, (B, T), name, dev)
+    if out is None:
+        out = torch.empty((B, T, V), dtype=out_dtype or logits.dtype, device=dev)
+    elif tuple(out.shape) != (B, T, V) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {(B, T, V)} of out_dtype")
+    _same_device(out, dev, "out")
+    oa = _act(out)
+    st = _lib.lib().dpfused_token_logprobs_backward(
+        ctypes.byref(za), None if ta is None else ctypes.byref(ta), _mask_ptr(mask, B, T, dev),
+        _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dentropy), ctypes.byref(oa),
+        _stream(logits, stream))
+    _lib.check(st)
+    return out
 
 
 def philox4x32_10(seed: int, offset: int, nblocks: int, out=None, device="cuda", stream=None):

@@ -19,6 +19,9 @@ DPF_ERR_HIP = 4
 DPF_F32 = 0
 DPF_BF16 = 1
 
+DPF_I32 = 0
+DPF_I64 = 1
+
 
 class DpfAct(ctypes.Structure):
     """Mirror of dpf_act: one [B, T, D] tensor, last dim contiguous, strides in elements."""
@@ -31,6 +34,18 @@ class DpfAct(ctypes.Structure):
         ("D", ctypes.c_int64),
         ("stride_b", ctypes.c_int64),
         ("stride_t", ctypes.c_int64),
+    ]
+
+
+class DpfIds(ctypes.Structure):
+    """Mirror of dpf_ids: [B, T] token ids, a sample's contiguous, stride in elements."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("B", ctypes.c_int64),
+        ("T", ctypes.c_int64),
+        ("stride_b", ctypes.c_int64),
     ]
 
 
@@ -91,6 +106,29 @@ _SIGNATURES = {
     "dpfused_scaled_accumulate": (ctypes.c_int, [
         ctypes.POINTER(DpfAct), ctypes.POINTER(DpfAct), ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
+    "dpfused_embedding_lookup": (ctypes.c_int, [
+        ctypes.POINTER(DpfIds), ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+        ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p,
+        ctypes.c_void_p]),
+    "dpfused_embedding_clip_accumulate": (ctypes.c_int, [
+        ctypes.POINTER(DpfIds), ctypes.POINTER(DpfAct), ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64,
+        ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "dpfused_embedding_sqnorms": (ctypes.c_int, [
+        ctypes.POINTER(DpfIds), ctypes.POINTER(DpfAct), ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_float, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "dpfused_embedding_scaled_accumulate": (ctypes.c_int, [
+        ctypes.POINTER(DpfIds), ctypes.POINTER(DpfAct), ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_float, ctypes.c_void_p, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64,
+        ctypes.c_void_p, ctypes.c_void_p]),
+    "dpfused_token_logprobs": (ctypes.c_int, [
+        ctypes.POINTER(DpfAct), ctypes.POINTER(DpfIds), ctypes.c_void_p, ctypes.c_int32,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p]),
+    "dpfused_token_logprobs_backward": (ctypes.c_int, [
+        ctypes.POINTER(DpfAct), ctypes.POINTER(DpfIds), ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(DpfAct),
+        ctypes.c_void_p]),
     "dpfused_philox4x32_10": (ctypes.c_int, [
         ctypes.c_uint64, ctypes.c_uint64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
     "dpfused_gaussian_fill": (ctypes.c_int, [

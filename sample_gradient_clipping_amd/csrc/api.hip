@@ -24,6 +24,7 @@
 
 #include "dpfused.h"
 #include "kernels.hpp"
+#include "lm.hpp"
 
 // Static scratch of dpfused_linear_clip_accumulate_noalloc, for callers that
 // cannot allocate (graph capture, tight serving loops): 80 MiB, which holds
@@ -1499,6 +1500,315 @@ dpf_status dpfused_projected_adam_step(const float* grad, float* m, float* v, fl
   a.pbuf = pbuf ? ws.at<void>(off_p) : nullptr;
   hipError_t e = dpf::launch_projected_adam(a, s);
   if (e != hipSuccess) return hip_fail(e, "projected Adam launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+// Embedding and token log probabilities
+// ---------------------------------------------------------------------------
+namespace {
+
+dpf_status check_ids(const dpf_ids* ids, const char* name) {
+  const std::string n(name);
+  if (ids == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, n + " is NULL");
+  if (ids->data == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, n + ".data is NULL");
+  if (ids->type != DPF_I32 && ids->type != DPF_I64)
+    return fail(DPF_ERR_UNSUPPORTED, n + ".type is not DPF_I32 or DPF_I64");
+  if (ids->reserved != 0) return fail(DPF_ERR_UNSUPPORTED, n + ".reserved must be 0");
+  if (ids->B < 1 || ids->T < 1) return fail(DPF_ERR_INVALID_ARGUMENT, n + ": B and T must be >= 1");
+  if (ids->stride_b < ids->T)
+    return fail(DPF_ERR_INVALID_ARGUMENT, n + ".stride_b < T (samples overlap)");
+  if ((reinterpret_cast<uintptr_t>(ids->data) & (ids->type == DPF_I64 ? 7u : 3u)) != 0)
+    return fail(DPF_ERR_UNSUPPORTED, n + ".data is not aligned to its elements");
+  return DPF_OK;
+}
+
+dpf::Ids to_ids(const dpf_ids* ids) {
+  return dpf::Ids{ids->data, ids->type == DPF_I64 ? 1 : 0, ids->stride_b};
+}
+
+dpf_status check_table(int64_t B, int64_t T, int64_t V, int64_t D, float scale) {
+  if (V < 1 || D < 1) return fail(DPF_ERR_INVALID_ARGUMENT, "V and D must be >= 1");
+  if (!std::isfinite(scale)) return fail(DPF_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (B > dpf::kEmbedMaxN || T > dpf::kEmbedMaxN || B * T > dpf::kEmbedMaxN)
+    return fail(DPF_ERR_UNSUPPORTED, "B * T is above 2^25");
+  if (V > dpf::kEmbedMaxV || D > dpf::kEmbedMaxD || V * D > dpf::kEmbedMaxTable)
+    return fail(DPF_ERR_UNSUPPORTED, "the table is too large (V <= 2^24, D <= 2^22, V * D <= 2^33)");
+  return DPF_OK;
+}
+
+dpf_status check_embed(const dpf_ids* ids, const dpf_act* G, int64_t V, float scale) {
+  dpf_status st = check_ids(ids, "ids");
+  if (st != DPF_OK) return st;
+  if ((st = check_act(G, "G")) != DPF_OK) return st;
+  if (ids->B != G->B || ids->T != G->T)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "ids and G disagree on B or T");
+  return check_table(G->B, G->T, V, G->D, scale);
+}
+
+// Workspace of the embedding's gradient: the sort's buffers and what the
+// kernels after it read.
+struct EmbedWs {
+  size_t key[2], pos[2], hist, seg, off, smp, part, sq, c;
+};
+
+dpf::EmbedArgs embed_args(const dpf_ids* ids, const dpf_act* G, const uint8_t* mask, int64_t V,
+                          float scale) {
+  dpf::EmbedArgs a{};
+  a.ids = to_ids(ids);
+  a.mask = mask;
+  a.G = to_act(G);
+  a.dtype = G->dtype;
+  a.B = G->B;
+  a.T = G->T;
+  a.V = V;
+  a.D = G->D;
+  a.scale = scale;
+  a.denom = (float)G->B;
+  return a;
+}
+
+EmbedWs reserve_embed(const dpf::EmbedArgs& a, Workspace& ws, bool norms) {
+  const size_t N = (size_t)(a.B * a.T);
+  EmbedWs o{};
+  for (int k = 0; k < 2; ++k) {
+    o.key[k] = ws.reserve(N * sizeof(uint32_t));
+    o.pos[k] = ws.reserve(N * sizeof(uint32_t));
+  }
+  o.hist = ws.reserve((size_t)dpf::embed_hist_words((int64_t)N, a.V) * sizeof(uint32_t));
+  o.seg = ws.reserve((size_t)a.V * sizeof(uint2));
+  o.off = ws.reserve(N * sizeof(int64_t));
+  o.smp = ws.reserve(N * sizeof(uint32_t));
+  if (norms) {
+    o.part = ws.reserve(N * (size_t)dpf::embed_norm_parts(a) * sizeof(double));
+    o.c = ws.reserve((size_t)a.B * sizeof(float));
+  }
+  return o;
+}
+
+void point_embed(dpf::EmbedArgs& a, const Workspace& ws, const EmbedWs& o, bool norms) {
+  for (int k = 0; k < 2; ++k) {
+    a.key[k] = ws.at<uint32_t>(o.key[k]);
+    a.pos[k] = ws.at<uint32_t>(o.pos[k]);
+  }
+  a.hist = ws.at<uint32_t>(o.hist);
+  a.seg = ws.at<uint2>(o.seg);
+  a.off = ws.at<int64_t>(o.off);
+  a.smp = ws.at<uint32_t>(o.smp);
+  if (norms) a.partials = ws.at<double>(o.part);
+}
+
+// A sample's norm partials are summed as one int-indexed row.
+bool embed_parts_fit(const dpf::EmbedArgs& a) {
+  return a.T * dpf::embed_norm_parts(a) <= (int64_t)INT32_MAX;
+}
+
+int64_t act_bytes(const dpf_act* a) {
+  return ((a->B - 1) * a->stride_b + (a->T - 1) * a->stride_t + a->D) * (int64_t)elem_size(a->dtype);
+}
+
+dpf_status check_logits(const dpf_act* logits, const dpf_ids* targets) {
+  dpf_status st = check_act(logits, "logits");
+  if (st != DPF_OK) return st;
+  if (targets != nullptr) {
+    if ((st = check_ids(targets, "targets")) != DPF_OK) return st;
+    if (targets->B != logits->B || targets->T != logits->T)
+      return fail(DPF_ERR_INVALID_ARGUMENT, "logits and targets disagree on B or T");
+  }
+  if (logits->B * logits->T >= dpf::kLogprobsMaxN || logits->D > dpf::kLogprobsMaxV)
+    return fail(DPF_ERR_UNSUPPORTED, "too many rows or logits (B * T < 2^24, V <= 2^23)");
+  return DPF_OK;
+}
+
+}  // namespace
+
+dpf_status dpfused_embedding_lookup(const dpf_ids* ids, const void* table, int32_t table_dtype,
+                                    int64_t V, int64_t D, int64_t stride_v, const uint8_t* mask,
+                                    float scale, int32_t out_dtype, void* out, void* stream) {
+  CallScope call_("dpfused_embedding_lookup");
+  dpf_status st = check_ids(ids, "ids");
+  if (st != DPF_OK) return st;
+  if (table == nullptr || out == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "table and out must not be NULL");
+  if ((table_dtype != DPF_F32 && table_dtype != DPF_BF16) ||
+      (out_dtype != DPF_F32 && out_dtype != DPF_BF16))
+    return fail(DPF_ERR_UNSUPPORTED, "unknown dtype");
+  if ((st = check_table(ids->B, ids->T, V, D, scale)) != DPF_OK) return st;
+  if (stride_v < D) return fail(DPF_ERR_INVALID_ARGUMENT, "stride_v < D (rows overlap)");
+  if (!aligned16(table) || !aligned16(out))
+    return fail(DPF_ERR_UNSUPPORTED, "table and out must be 16-byte aligned");
+  dpf::LookupArgs a{to_ids(ids), mask, ids->B * ids->T, ids->T, table, table_dtype, V, D, stride_v,
+                    scale, out, out_dtype};
+  const hipError_t e = dpf::launch_embedding_lookup(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "embedding lookup launch");
+  return ok();
+}
+
+dpf_status dpfused_embedding_clip_accumulate(const dpf_ids* ids, const dpf_act* G,
+                                             const uint8_t* mask, int64_t V, float scale, float C,
+                                             float sigma, uint64_t seed, uint64_t offset,
+                                             float denom, int32_t accumulate, float* grad_out,
+                                             float* norms_out, void* stream) {
+  CallScope call_("dpfused_embedding_clip_accumulate");
+  dpf_status st = check_embed(ids, G, V, scale);
+  if (st != DPF_OK) return st;
+  if ((st = check_clip(C, sigma)) != DPF_OK) return st;
+  if (!std::isfinite(denom) || !(denom > 0.0f))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "denom must be finite and > 0");
+  if (accumulate != 0 && accumulate != 1)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "accumulate must be 0 or 1");
+  if (grad_out == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "grad_out is NULL");
+  if (!aligned16(grad_out)) return fail(DPF_ERR_UNSUPPORTED, "grad_out is not 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  dpf::EmbedArgs a = embed_args(ids, G, mask, V, scale);
+  if (!embed_parts_fit(a)) return fail(DPF_ERR_UNSUPPORTED, "T * D is too large");
+  Workspace ws(s);
+  const EmbedWs o = reserve_embed(a, ws, true);
+  if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+  point_embed(a, ws, o, true);
+  float* c = ws.at<float>(o.c);
+  hipError_t e = dpf::launch_embed_sort(a, s);
+  if (e == hipSuccess) e = dpf::launch_embed_norm(a, s);
+  if (e != hipSuccess) return hip_fail(e, "embedding norm launch");
+  e = dpf::launch_finalize(a.partials, (int)a.B, (int)(a.T * dpf::embed_norm_parts(a)), nullptr, 0,
+                           C, c, norms_out, s);
+  if (e != hipSuccess) return hip_fail(e, "clip factor launch");
+  a.c = c;
+  a.noise_std = sigma * C;
+  a.seed = seed;
+  a.offset = offset;
+  a.denom = denom;
+  a.beta = accumulate;
+  a.out = grad_out;
+  if ((e = dpf::launch_embed_accumulate(a, s)) != hipSuccess)
+    return hip_fail(e, "embedding accumulate launch");
+  return ok();
+}
+
+dpf_status dpfused_embedding_sqnorms(const dpf_ids* ids, const dpf_act* G, const uint8_t* mask,
+                                     int64_t V, float scale, double* sqnorms_out,
+                                     int32_t accumulate, void* stream) {
+  CallScope call_("dpfused_embedding_sqnorms");
+  dpf_status st = check_embed(ids, G, V, scale);
+  if (st != DPF_OK) return st;
+  if (sqnorms_out == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "sqnorms_out is NULL");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  dpf::EmbedArgs a = embed_args(ids, G, mask, V, scale);
+  if (!embed_parts_fit(a)) return fail(DPF_ERR_UNSUPPORTED, "T * D is too large");
+  Workspace ws(s);
+  const EmbedWs o = reserve_embed(a, ws, true);
+  if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+  point_embed(a, ws, o, true);
+  hipError_t e = dpf::launch_embed_sort(a, s);
+  if (e == hipSuccess) e = dpf::launch_embed_norm(a, s);
+  if (e != hipSuccess) return hip_fail(e, "embedding norm launch");
+  e = dpf::launch_finalize(a.partials, (int)a.B, (int)(a.T * dpf::embed_norm_parts(a)), sqnorms_out,
+                           accumulate != 0 ? 1 : 0, 1.0f, nullptr, nullptr, s);
+  if (e != hipSuccess) return hip_fail(e, "norm sum launch");
+  return ok();
+}
+
+dpf_status dpfused_embedding_scaled_accumulate(const dpf_ids* ids, const dpf_act* G,
+                                               const uint8_t* mask, int64_t V, float scale,
+                                               const float* c, float noise_std, uint64_t seed,
+                                               uint64_t offset, float* grad_out, void* stream) {
+  CallScope call_("dpfused_embedding_scaled_accumulate");
+  dpf_status st = check_embed(ids, G, V, scale);
+  if (st != DPF_OK) return st;
+  if (c == nullptr || grad_out == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "c and grad_out must not be NULL");
+  if (!std::isfinite(noise_std) || noise_std < 0.0f)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "noise_std must be finite and >= 0");
+  if (!aligned16(grad_out)) return fail(DPF_ERR_UNSUPPORTED, "grad_out is not 16-byte aligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  dpf::EmbedArgs a = embed_args(ids, G, mask, V, scale);
+  Workspace ws(s);
+  const EmbedWs o = reserve_embed(a, ws, false);
+  if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+  point_embed(a, ws, o, false);
+  a.c = c;
+  a.noise_std = noise_std;
+  a.seed = seed;
+  a.offset = offset;
+  a.out = grad_out;
+  hipError_t e = dpf::launch_embed_sort(a, s);
+  if (e == hipSuccess) e = dpf::launch_embed_accumulate(a, s);
+  if (e != hipSuccess) return hip_fail(e, "embedding accumulate launch");
+  return ok();
+}
+
+dpf_status dpfused_token_logprobs(const dpf_act* logits, const dpf_ids* targets,
+                                  const uint8_t* mask, int32_t top_k, float* logp, float* entropy,
+                                  float* lse, float* top_logp, int32_t* top_ids, void* stream) {
+  CallScope call_("dpfused_token_logprobs");
+  dpf_status st = check_logits(logits, targets);
+  if (st != DPF_OK) return st;
+  if (top_k < 0 || top_k > dpf::kMaxTopK || top_k > logits->D)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "top_k must be in 0 .. min(32, V)");
+  if (top_k > 0 && (top_logp == nullptr || top_ids == nullptr))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "top_logp and top_ids must not be NULL with top_k > 0");
+  if (logp != nullptr && targets == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "logp needs targets");
+  if (top_k == 0 && logp == nullptr && entropy == nullptr && lse == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "no output was asked for");
+  dpf::LogprobArgs a{};
+  a.Z = to_act(logits);
+  a.dtype = logits->dtype;
+  a.N = logits->B * logits->T;
+  a.T = logits->T;
+  a.V = logits->D;
+  if (targets != nullptr) a.targets = to_ids(targets);
+  a.mask = mask;
+  a.top_k = top_k;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_logp = top_logp;
+  a.top_ids = top_ids;
+  const hipError_t e = dpf::launch_token_logprobs(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "token log probabilities launch");
+  return ok();
+}
+
+dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids* targets,
+                                           const uint8_t* mask, const float* lse,
+                                           const float* entropy, const float* dlogp,
+                                           const float* dentropy, const dpf_act* dlogits,
+                                           void* stream) {
+  CallScope call_("dpfused_token_logprobs_backward");
+  dpf_status st = check_logits(logits, targets);
+  if (st != DPF_OK) return st;
+  if ((st = check_act(dlogits, "dlogits")) != DPF_OK) return st;
+  if (dlogits->B != logits->B || dlogits->T != logits->T || dlogits->D != logits->D)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "logits and dlogits have different shapes");
+  if (lse == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "lse is NULL");
+  if (dlogp == nullptr && dentropy == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "dlogp and dentropy are both NULL");
+  if (dlogp != nullptr && targets == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "dlogp needs targets");
+  if (dentropy != nullptr && entropy == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "dentropy needs entropy");
+  const bool same = dlogits->data == logits->data && dlogits->dtype == logits->dtype &&
+                    dlogits->stride_b == logits->stride_b && dlogits->stride_t == logits->stride_t;
+  const uintptr_t z0 = (uintptr_t)logits->data, d0 = (uintptr_t)dlogits->data;
+  if (!same && z0 < d0 + (uintptr_t)act_bytes(dlogits) && d0 < z0 + (uintptr_t)act_bytes(logits))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "dlogits overlaps logits without being the same tensor");
+  dpf::LogprobGradArgs a{};
+  a.Z = to_act(logits);
+  a.dZ = to_act(dlogits);
+  a.dtype = logits->dtype;
+  a.out_dtype = dlogits->dtype;
+  a.N = logits->B * logits->T;
+  a.T = logits->T;
+  a.V = logits->D;
+  if (targets != nullptr) a.targets = to_ids(targets);
+  a.mask = mask;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.dlogp = dlogp;
+  a.dentropy = dentropy;
+  const hipError_t e = dpf::launch_token_logprobs_backward(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "token log probabilities gradient launch");
   return ok();
 }
 

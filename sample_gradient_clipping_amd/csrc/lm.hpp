@@ -1,0 +1,152 @@
+// Internal interface of the operators at a language model's two ends and of
+// its optimizer: embedding rows, token log probabilities, the orthogonalised
+// update.
+#pragma once
+
+#include "kernels.hpp"
+
+namespace dpf {
+
+// [B, T] token ids in device memory (int32, or int64 when wide), rows
+// stride_b elements apart.
+struct Ids {
+  const void* data;
+  int wide;
+  int64_t stride_b;
+  __device__ __forceinline__ int64_t at(int64_t b, int64_t t) const {
+    const int64_t e = b * stride_b + t;
+    return wide ? ((const int64_t*)data)[e] : (int64_t)((const int32_t*)data)[e];
+  }
+};
+
+// V consecutive elements (V = 1, 4 or 8; V > 1: naturally aligned) as float32,
+// and back (bf16 rounded to nearest even).
+template <class E, int V>
+__device__ __forceinline__ void load_f32(const typename E::storage* p, float (&x)[V]) {
+  if constexpr (V == 1) {
+    x[0] = E::to_float(p[0]);
+  } else if constexpr (sizeof(typename E::storage) == 4) {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const f32x4 w = *(const f32x4*)(p + k);
+      x[k] = w.x; x[k + 1] = w.y; x[k + 2] = w.z; x[k + 3] = w.w;
+    }
+  } else if constexpr (V == 4) {
+    const u16x4 w = *(const u16x4*)p;
+    x[0] = E::to_float(w.s0); x[1] = E::to_float(w.s1);
+    x[2] = E::to_float(w.s2); x[3] = E::to_float(w.s3);
+  } else {
+    const u16x8 w = *(const u16x8*)p;
+    x[0] = E::to_float(w.s0); x[1] = E::to_float(w.s1);
+    x[2] = E::to_float(w.s2); x[3] = E::to_float(w.s3);
+    x[4] = E::to_float(w.s4); x[5] = E::to_float(w.s5);
+    x[6] = E::to_float(w.s6); x[7] = E::to_float(w.s7);
+  }
+}
+
+template <class E, int V>
+__device__ __forceinline__ void store_f32(typename E::storage* p, const float (&x)[V]) {
+  if constexpr (sizeof(typename E::storage) == 4) {
+    if constexpr (V == 1) {
+      p[0] = x[0];
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        f32x4 w; w.x = x[k]; w.y = x[k + 1]; w.z = x[k + 2]; w.w = x[k + 3];
+        *(f32x4*)(p + k) = w;
+      }
+    }
+  } else if constexpr (V == 1) {
+    p[0] = f32_to_bf16_rne(x[0]);
+  } else if constexpr (V == 4) {
+    u16x4 w;
+    w.s0 = f32_to_bf16_rne(x[0]); w.s1 = f32_to_bf16_rne(x[1]);
+    w.s2 = f32_to_bf16_rne(x[2]); w.s3 = f32_to_bf16_rne(x[3]);
+    *(u16x4*)p = w;
+  } else {
+    u16x8 w;
+    w.s0 = f32_to_bf16_rne(x[0]); w.s1 = f32_to_bf16_rne(x[1]);
+    w.s2 = f32_to_bf16_rne(x[2]); w.s3 = f32_to_bf16_rne(x[3]);
+    w.s4 = f32_to_bf16_rne(x[4]); w.s5 = f32_to_bf16_rne(x[5]);
+    w.s6 = f32_to_bf16_rne(x[6]); w.s7 = f32_to_bf16_rne(x[7]);
+    *(u16x8*)p = w;
+  }
+}
+
+// Embedding (embedding.hip).
+struct LookupArgs {
+  Ids ids;
+  const uint8_t* mask;      // [B, T] or null
+  int64_t N, T;             // N = B * T positions
+  const void* table;        // [V, D], rows stride_v elements apart
+  int table_dtype;
+  int64_t V, D, stride_v;
+  float scale;
+  void* out;                // [B, T, D] contiguous
+  int out_dtype;
+};
+hipError_t launch_embedding_lookup(const LookupArgs& a, hipStream_t s);
+
+struct EmbedArgs {
+  Ids ids;
+  const uint8_t* mask;      // [B, T] or null
+  Act G;                    // [B, T, D]
+  int dtype;
+  int64_t B, T, V, D;
+  float scale;
+  // workspace
+  uint32_t *key[2], *pos[2];   // [N] each: sort buffers, ping and pong
+  uint32_t* hist;              // [sort workgroups, bins]
+  uint2* seg;                  // [V] sorted range of each row
+  int64_t* off;                // [N] element offset of each sorted position's row in G
+  uint32_t* smp;               // [N] its sample
+  double* partials;            // [N, embed_norm_parts] squared run norms
+  // clipped sum
+  const float* c;              // [B]
+  float noise_std;
+  uint64_t seed, offset;
+  float denom;
+  int beta;
+  float* out;                  // [V, D]
+};
+// Launch limits (threads of one grid dimension stay below 2^32).
+constexpr int64_t kEmbedMaxN = (int64_t)1 << 25, kEmbedMaxV = (int64_t)1 << 24;
+constexpr int64_t kEmbedMaxD = (int64_t)1 << 22, kEmbedMaxTable = (int64_t)1 << 33;
+// Elements of a.hist, and partials per sorted position.
+int64_t embed_hist_words(int64_t N, int64_t V);
+int embed_norm_parts(const EmbedArgs& a);
+// Sorts the positions by (token, sample, position); fills key/pos (the sorted
+// copies are key[embed_sorted], pos[embed_sorted]), seg, off and smp.
+int embed_sorted(int64_t V);
+hipError_t launch_embed_sort(const EmbedArgs& a, hipStream_t s);
+hipError_t launch_embed_norm(const EmbedArgs& a, hipStream_t s);
+hipError_t launch_embed_accumulate(const EmbedArgs& a, hipStream_t s);
+
+// Token log probabilities (logprobs.hip).
+constexpr int kMaxTopK = 32;
+constexpr int64_t kLogprobsMaxN = (int64_t)1 << 24, kLogprobsMaxV = (int64_t)1 << 23;
+struct LogprobArgs {
+  Act Z;                    // logits [B, T, V]
+  int dtype;
+  int64_t N, T, V;          // N = B * T rows
+  Ids targets;              // data null: none
+  const uint8_t* mask;      // [B, T] or null
+  int top_k;
+  float *logp, *entropy, *lse;   // [B, T] each, or null
+  float* top_logp;          // [B, T, top_k]
+  int32_t* top_ids;         // [B, T, top_k]
+};
+hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s);
+
+struct LogprobGradArgs {
+  Act Z, dZ;                // logits and their gradient, [B, T, V]
+  int dtype, out_dtype;
+  int64_t N, T, V;
+  Ids targets;              // data null: none
+  const uint8_t* mask;
+  const float *lse, *entropy;      // [B, T] from the forward call
+  const float *dlogp, *dentropy;   // [B, T], either may be null
+};
+hipError_t launch_token_logprobs_backward(const LogprobGradArgs& a, hipStream_t s);
+
+}  // namespace dpf
