@@ -554,6 +554,60 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
                                            const float* dentropy, const dpf_act* dlogits,
                                            void* stream);
 
+/* The orthogonal factor of each of n matrices, approximately, by Newton-Schulz
+ * products (the orthogonalised update of the Muon optimizer):
+ *
+ *   X_0 = M / max(||M||_F, eps)
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X      `steps` times
+ *   out = X
+ *
+ * so that every singular value s of M / ||M||_F goes through the polynomial
+ * a s + b s^3 + c s^5 while the singular vectors stay.  With the usual
+ * (3.4445, -4.7750, 2.0315) and 5 steps they end up between about 0.7 and
+ * 1.2.  A zero matrix gives 0; one whose norm is not finite gives NaN.
+ *
+ * The products run on half-precision matrix cores with operands split in two
+ * (22 bits) and float32 sums: the accuracy is that of float32 products.
+ *
+ *   M      [n, rows, cols] contiguous, dtype, read
+ *   out    the same shape and dtype; may be M itself, else must not overlap it
+ *   steps  1 .. 32
+ *   a, b, c  finite; no singular value in [0, 1] may grow past 4 within the
+ *          steps (checked on the host)
+ *   eps    finite and > 0
+ *
+ * Errors: DPF_ERR_INVALID_ARGUMENT for NULL or overlapping pointers, n, rows
+ * or cols < 1, steps, coefficients or eps out of range; DPF_ERR_UNSUPPORTED
+ * for an unknown dtype, pointers not 16-byte aligned, n > 65535, rows or cols
+ * > 2^17 or n * rows * cols > 2^33; DPF_ERR_OUT_OF_MEMORY when the workspace
+ * (8 bytes per element, and 8 per element of the [n, m, m] products, m =
+ * min(rows, cols)) cannot be allocated. */
+dpf_status dpfused_orthogonalize(const void* M, int32_t dtype, int64_t n, int64_t rows,
+                                 int64_t cols, int32_t steps, float a, float b, float c, float eps,
+                                 void* out, void* stream);
+
+/* One optimizer step of n linears of one shape with an orthogonalised update,
+ * from their privatised gradients (the grad_out of the clip-and-accumulate
+ * calls; what is done with them afterwards costs no privacy):
+ *
+ *   momentum <- beta momentum + grad
+ *   U = grad + beta momentum  (nesterov != 0), or momentum
+ *   W <- (1 - lr weight_decay) W - lr scale NS(U)
+ *
+ * NS as in dpfused_orthogonalize, each matrix on its own.
+ *
+ *   grad           [n, dout, din] float32, read
+ *   momentum, W    [n, dout, din] float32, updated in place
+ *   lr, weight_decay   finite; beta in [0, 1)
+ *   scale          finite; NaN or <= 0: sqrt(max(1, dout / din))
+ *
+ * All pointers 16-byte aligned, none overlapping another.  Other arguments
+ * and errors as above; nothing is written on error. */
+dpf_status dpfused_muon_step(const float* grad, float* momentum, float* W, int64_t n, int64_t dout,
+                             int64_t din, float lr, float beta, int32_t nesterov,
+                             float weight_decay, float scale, int32_t steps, float a, float b,
+                             float c, float eps, void* stream);
+
 /* Raw Philox4x32-10 words of the noise generator (the noise added after
  * clipping in the FlashDP abstract and in the DP-GRAPE explainer,
  * Methodology, is drawn from this counter-based generator; Salmon, Moraes,

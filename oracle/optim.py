@@ -40,3 +40,30 @@ def projected_adam_step(grad, m, v, W, step: int, lr: float, beta1: float, beta2
     U = adam_direction(m, v, step, beta1, beta2, eps)
     W = np.asarray(W, dtype=np.float64) - lr * (U @ np.asarray(P, dtype=np.float64).T)
     return m, v, W
+
+
+def newton_schulz(M, steps: int, coeffs, eps: float, dtype=np.float64):
+    """X = M / max(||M||_F, eps), then steps times X <- a X + b (X X^T) X + c (X X^T)^2 X, in
+    ``dtype`` throughout (float64: the reference; float32: what plain float32 products give)."""
+    a, b, c = (dtype(x) for x in coeffs)
+    X = np.asarray(M, dtype=dtype)
+    norm = np.sqrt((np.asarray(M, np.float64) ** 2).sum())
+    X = X / dtype(max(norm, eps))
+    flip = X.shape[0] > X.shape[1]
+    if flip:
+        X = X.T
+    for _ in range(steps):
+        A = X @ X.T
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return X.T if flip else X
+
+
+def muon_step(grad, momentum, W, lr: float, beta: float, nesterov: bool, weight_decay: float,
+              scale, steps: int, coeffs, eps: float):
+    """(momentum, W, update) after one step with the orthogonalised update, in float64."""
+    g, m, w = (np.asarray(x, np.float64) for x in (grad, momentum, W))
+    m = beta * m + g
+    U = newton_schulz(g + beta * m if nesterov else m, steps, coeffs, eps)
+    if scale is None:
+        scale = np.sqrt(max(1.0, w.shape[0] / w.shape[1]))
+    return m, (1.0 - lr * weight_decay) * w - lr * scale * U, U

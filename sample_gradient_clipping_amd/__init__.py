@@ -27,6 +27,7 @@ __all__ = [
     "linear_clip_accumulate_projected_many",
     "embedding_lookup", "embedding_clip_accumulate", "embedding_sqnorms",
     "embedding_scaled_accumulate", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
+    "orthogonalize", "muon_step", "NEWTON_SCHULZ",
     "per_sample_sqnorms",
     "clip_factors", "scaled_accumulate", "philox4x32_10", "gaussian_fill", "noise_blocks",
     "set_option", "get_option", "timing_reset", "timing_collect", "DpfError", "load",
@@ -662,6 +663,60 @@ def token_logprobs_backward(logits, targets, lse, dlogp, entropy=None, dentropy=
         _stream(logits, stream))
     _lib.check(st)
     return out
+
+
+# Coefficients (a, b, c) that take a singular value s to a s + b s^3 + c s^5 in each step.
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(M, steps: int = 5, coeffs=NEWTON_SCHULZ, eps: float = 1e-7, out=None,
+                  stream=None):
+    """Newton-Schulz orthogonalisation of M [rows, cols], or of each matrix of a stack
+    [n, rows, cols] (bf16 or fp32, contiguous): X = M / max(||M||_F, eps), then ``steps`` times
+    X <- a X + b (X X^T) X + c (X X^T)^2 X.  ``out`` may be M."""
+    torch = _torch()
+    if M.dim() not in (2, 3) or not M.is_contiguous() or not M.is_cuda:
+        raise ValueError("M must be a contiguous [rows, cols] or [n, rows, cols] GPU tensor")
+    code = _dtype_code(M)
+    if out is None:
+        out = torch.empty_like(M)
+    _check_out(out, M.shape, "out", M.device, dtype=M.dtype)
+    a, b, c = (float(x) for x in coeffs)
+    n = M.shape[0] if M.dim() == 3 else 1
+    st = _lib.lib().dpfused_orthogonalize(M.data_ptr(), code, int(n), int(M.shape[-2]),
+                                          int(M.shape[-1]), int(steps), a, b, c, float(eps),
+                                          out.data_ptr(), _stream(M, stream))
+    _lib.check(st)
+    return out
+
+
+def muon_step(grad, momentum, W, lr: float, beta: float = 0.95, nesterov: bool = True,
+              weight_decay: float = 0.0, scale: Optional[float] = None, steps: int = 5,
+              coeffs=NEWTON_SCHULZ, eps: float = 1e-7, stream=None):
+    """One optimizer step with an orthogonalised update, in place on momentum and W, from the
+    privatised gradient ``grad`` (all [dout, din], or [n, dout, din] for n linears of one shape,
+    contiguous fp32):
+
+        momentum <- beta momentum + grad;  U = grad + beta momentum (nesterov) or momentum
+        W <- (1 - lr weight_decay) W - lr scale orthogonalize(U)
+
+    scale=None takes sqrt(max(1, dout / din)).  Returns (momentum, W)."""
+    torch = _torch()
+    for t, name in ((grad, "grad"), (momentum, "momentum"), (W, "W")):
+        if t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous float32 GPU tensor")
+        if t.dim() not in (2, 3) or t.shape != grad.shape:
+            raise ValueError("grad, momentum and W must all be [dout, din] or [n, dout, din]")
+        _same_device(t, grad.device, name)
+    a, b, c = (float(x) for x in coeffs)
+    n = grad.shape[0] if grad.dim() == 3 else 1
+    st = _lib.lib().dpfused_muon_step(
+        grad.data_ptr(), momentum.data_ptr(), W.data_ptr(), int(n), int(grad.shape[-2]),
+        int(grad.shape[-1]), float(lr), float(beta), int(bool(nesterov)), float(weight_decay),
+        math.nan if scale is None else float(scale), int(steps), a, b, c, float(eps),
+        _stream(grad, stream))
+    _lib.check(st)
+    return momentum, W
 
 
 def philox4x32_10(seed: int, offset: int, nblocks: int, out=None, device="cuda", stream=None):

@@ -1812,6 +1812,113 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
   return ok();
 }
 
+// ---------------------------------------------------------------------------
+// Orthogonalised update
+// ---------------------------------------------------------------------------
+namespace {
+
+bool ranges_overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + nq && b < a + np;
+}
+
+dpf_status check_ortho(const dpf::OrthoArgs& a) {
+  if (a.n < 1 || a.R < 1 || a.C < 1)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "n and the matrix's dimensions must be >= 1");
+  if (a.n > 65535 || a.R > (1 << 17) || a.C > (1 << 17) ||
+      a.n * a.R * a.C > ((int64_t)1 << 33))
+    return fail(DPF_ERR_UNSUPPORTED, "the matrices are too many or too large");
+  if (a.steps < 1 || a.steps > dpf::kOrthoMaxSteps)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "steps must be in 1 .. 32");
+  if (!std::isfinite(a.eps) || !(a.eps > 0.0))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "eps must be finite and > 0");
+  if (!std::isfinite(a.a) || !std::isfinite(a.b) || !std::isfinite(a.c) || !dpf::ortho_coeffs_ok(a))
+    return fail(DPF_ERR_INVALID_ARGUMENT,
+                "the coefficients let a singular value grow past 4 within the steps");
+  return DPF_OK;
+}
+
+dpf_status queue_ortho(dpf::OrthoArgs& a, hipStream_t s, const char* where) {
+  Workspace ws(s);
+  const size_t at = ws.reserve(dpf::ortho_workspace_bytes(a));
+  if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+  a.ws = ws.at<void>(at);
+  const hipError_t e = dpf::launch_ortho(a, s);
+  if (e != hipSuccess) return hip_fail(e, where);
+  return ok();
+}
+
+}  // namespace
+
+dpf_status dpfused_orthogonalize(const void* M, int32_t dtype, int64_t n, int64_t rows,
+                                 int64_t cols, int32_t steps, float a, float b, float c, float eps,
+                                 void* out, void* stream) {
+  CallScope call_("dpfused_orthogonalize");
+  if (M == nullptr || out == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "M and out must not be NULL");
+  if (dtype != DPF_F32 && dtype != DPF_BF16) return fail(DPF_ERR_UNSUPPORTED, "unknown dtype");
+  dpf::OrthoArgs o{};
+  o.n = n;
+  o.R = rows;
+  o.C = cols;
+  o.steps = steps;
+  o.a = a;
+  o.b = b;
+  o.c = c;
+  o.eps = eps;
+  o.in = M;
+  o.out = out;
+  o.dtype = dtype;
+  const dpf_status st = check_ortho(o);
+  if (st != DPF_OK) return st;
+  if (!aligned16(M) || !aligned16(out))
+    return fail(DPF_ERR_UNSUPPORTED, "M and out must be 16-byte aligned");
+  const size_t bytes = (size_t)(n * rows * cols) * elem_size(dtype);
+  if (M != out && ranges_overlap(M, bytes, out, bytes))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "out overlaps M without being M");
+  return queue_ortho(o, static_cast<hipStream_t>(stream), "orthogonalisation launch");
+}
+
+dpf_status dpfused_muon_step(const float* grad, float* momentum, float* W, int64_t n, int64_t dout,
+                             int64_t din, float lr, float beta, int32_t nesterov,
+                             float weight_decay, float scale, int32_t steps, float a, float b,
+                             float c, float eps, void* stream) {
+  CallScope call_("dpfused_muon_step");
+  if (grad == nullptr || momentum == nullptr || W == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "grad, momentum and W must not be NULL");
+  dpf::OrthoArgs o{};
+  o.n = n;
+  o.R = dout;
+  o.C = din;
+  o.steps = steps;
+  o.a = a;
+  o.b = b;
+  o.c = c;
+  o.eps = eps;
+  o.grad = grad;
+  o.momentum = momentum;
+  o.W = W;
+  const dpf_status st = check_ortho(o);
+  if (st != DPF_OK) return st;
+  if (!std::isfinite(lr) || !std::isfinite(weight_decay))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "lr and weight_decay must be finite");
+  if (!(beta >= 0.0f && beta < 1.0f)) return fail(DPF_ERR_INVALID_ARGUMENT, "beta must be in [0, 1)");
+  if (std::isinf(scale)) return fail(DPF_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (!aligned16(grad) || !aligned16(momentum) || !aligned16(W))
+    return fail(DPF_ERR_UNSUPPORTED, "grad, momentum and W must be 16-byte aligned");
+  const size_t bytes = (size_t)(n * dout * din) * sizeof(float);
+  if (ranges_overlap(grad, bytes, momentum, bytes) || ranges_overlap(grad, bytes, W, bytes) ||
+      ranges_overlap(momentum, bytes, W, bytes))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "grad, momentum and W must not overlap");
+  const double by = std::isnan(scale) || scale <= 0.0f
+                        ? std::sqrt(std::max(1.0, (double)dout / (double)din))
+                        : (double)scale;
+  o.beta = beta;
+  o.nesterov = nesterov != 0 ? 1 : 0;
+  o.decay = (float)(1.0 - (double)lr * (double)weight_decay);
+  o.size = (float)((double)lr * by);
+  return queue_ortho(o, static_cast<hipStream_t>(stream), "optimizer step launch");
+}
+
 dpf_status dpfused_philox4x32_10(uint64_t seed, uint64_t offset, int64_t nblocks, uint32_t* out,
                                  void* stream) {
   CallScope call_("dpfused_philox4x32_10");

@@ -149,4 +149,28 @@ struct LogprobGradArgs {
 };
 hipError_t launch_token_logprobs_backward(const LogprobGradArgs& a, hipStream_t s);
 
+// Orthogonalised update (ortho.hip): n matrices [R, C] stacked contiguously.
+constexpr int kOrthoMaxSteps = 32;
+struct OrthoArgs {
+  int64_t n, R, C;
+  int steps;
+  double a, b, c, eps;      // X <- a X + b (X X^T) X + c (X X^T)^2 X
+  // orthogonalize: out = NS(in); both of dtype
+  const void* in;
+  void* out;
+  int dtype;
+  // optimizer step (W not null): momentum <- beta momentum + grad, then
+  // W <- decay W - size NS(update)
+  const float* grad;
+  float *momentum, *W;
+  float beta, decay, size;
+  int nesterov;
+  void* ws;                 // ortho_workspace_bytes(a)
+};
+// False where the coefficients let a singular value grow past 4 within the
+// steps (the half-precision factors are scaled for that range).
+bool ortho_coeffs_ok(const OrthoArgs& a);
+size_t ortho_workspace_bytes(const OrthoArgs& a);
+hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s);
+
 }  // namespace dpf

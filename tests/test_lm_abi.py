@@ -167,3 +167,48 @@ def test_oracle_logprobs_by_torch():
     (torch.from_numpy(dl) * tl + torch.from_numpy(dh) * th).sum().backward()
     g = lm.oracle_logprobs_grad(z, y, None, lse, ent, dl, dh)
     assert np.abs(g - t.grad.numpy()).max() < 1e-12
+
+
+NS = (3.4445, -4.7750, 2.0315)
+
+
+@pytest.mark.parametrize("case,status", [
+    (dict(M=None), BAD), (dict(out=None), BAD), (dict(dt=4), UNS), (dict(n=0), BAD), (dict(r=0), BAD),
+    (dict(c=0), BAD), (dict(n=65536), UNS), (dict(r=(1 << 17) + 1), UNS), (dict(c=(1 << 17) + 1), UNS),
+    (dict(n=1 << 10, r=1 << 12, c=1 << 12), UNS), (dict(steps=0), BAD), (dict(steps=33), BAD),
+    (dict(eps=0.0), BAD), (dict(eps=math.nan), BAD), (dict(co=(4.5, 0.0, 0.0)), BAD),
+    (dict(co=(2.0, 0.0, 0.0)), BAD), (dict(co=(1.0, math.inf, 0.0)), BAD),
+    (dict(co=(3.4445, -4.775, 3.0315)), BAD), (dict(M=FAKE + 4), UNS), (dict(out=FAKE + 8), UNS),
+    (dict(out=FAKE + 16), BAD),
+])
+def test_orthogonalize_refusals(L, case, status):
+    a = dict(M=FAKE, dt=DPF_F32, n=1, r=8, c=8, steps=5, co=NS, eps=1e-7, out=FAR)
+    a.update(case)
+    assert L.dpfused_orthogonalize(a["M"], a["dt"], a["n"], a["r"], a["c"], a["steps"], *a["co"],
+                                   a["eps"], a["out"], None) == status
+
+
+@pytest.mark.parametrize("case,status", [
+    (dict(g=None), BAD), (dict(m=None), BAD), (dict(w=None), BAD), (dict(r=0), BAD), (dict(steps=0), BAD),
+    (dict(co=(9.0, 0.0, 0.0)), BAD), (dict(eps=-1.0), BAD), (dict(lr=math.nan), BAD),
+    (dict(wd=math.inf), BAD), (dict(beta=1.0), BAD), (dict(beta=-0.1), BAD), (dict(scale=math.inf), BAD),
+    (dict(g=FAKE + 4), UNS), (dict(m=FAKE), BAD), (dict(w=FAKE + 64), BAD), (dict(w=FAR + 240), BAD),
+])
+def test_muon_step_refusals(L, case, status):
+    a = dict(g=FAKE, m=FAR, w=FAR + (1 << 20), n=1, r=8, c=8, lr=0.1, beta=0.9, wd=0.0, scale=1.0,
+             steps=5, co=NS, eps=1e-7)
+    a.update(case)
+    assert L.dpfused_muon_step(a["g"], a["m"], a["w"], a["n"], a["r"], a["c"], a["lr"], a["beta"], 1,
+                               a["wd"], a["scale"], a["steps"], *a["co"], a["eps"], None) == status
+
+
+def test_oracle_newton_schulz_by_singular_values():
+    from oracle import optim
+    rng = np.random.default_rng(4)
+    for shape in ((6, 9), (9, 6)):
+        M = rng.standard_normal(shape)
+        u, s, vt = np.linalg.svd(M, full_matrices=False)
+        s = s / np.linalg.norm(s)
+        for _ in range(4):
+            s = NS[0] * s + NS[1] * s ** 3 + NS[2] * s ** 5
+        assert np.abs(optim.newton_schulz(M, 4, NS, 1e-7) - (u * s) @ vt).max() < 1e-12
