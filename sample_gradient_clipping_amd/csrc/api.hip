@@ -1549,7 +1549,8 @@ dpf_status check_embed(const dpf_ids* ids, const dpf_act* G, int64_t V, float sc
 // Workspace of the embedding's gradient: the sort's buffers and what the
 // kernels after it read.
 struct EmbedWs {
-  size_t key[2], pos[2], hist, seg, off, smp, part, sq, c;
+  size_t key[2], pos[2], hist, seg, off, smp, blocks, part, c;
+  bool has_blocks;
 };
 
 dpf::EmbedArgs embed_args(const dpf_ids* ids, const dpf_act* G, const uint8_t* mask, int64_t V,
@@ -1579,6 +1580,9 @@ EmbedWs reserve_embed(const dpf::EmbedArgs& a, Workspace& ws, bool norms) {
   o.seg = ws.reserve((size_t)a.V * sizeof(uint2));
   o.off = ws.reserve(N * sizeof(int64_t));
   o.smp = ws.reserve(N * sizeof(uint32_t));
+  const int64_t blocks = dpf::embed_block_floats(a);
+  o.has_blocks = blocks != 0;
+  if (o.has_blocks) o.blocks = ws.reserve((size_t)blocks * sizeof(float));
   if (norms) {
     o.part = ws.reserve(N * (size_t)dpf::embed_norm_parts(a) * sizeof(double));
     o.c = ws.reserve((size_t)a.B * sizeof(float));
@@ -1595,6 +1599,7 @@ void point_embed(dpf::EmbedArgs& a, const Workspace& ws, const EmbedWs& o, bool 
   a.seg = ws.at<uint2>(o.seg);
   a.off = ws.at<int64_t>(o.off);
   a.smp = ws.at<uint32_t>(o.smp);
+  a.blocks = o.has_blocks ? ws.at<float>(o.blocks) : nullptr;
   if (norms) a.partials = ws.at<double>(o.part);
 }
 

@@ -96,11 +96,12 @@ struct EmbedArgs {
   float scale;
   // workspace
   uint32_t *key[2], *pos[2];   // [N] each: sort buffers, ping and pong
-  uint32_t* hist;              // [sort workgroups, bins]
-  uint2* seg;                  // [V] sorted range of each row
+  uint32_t* hist;              // embed_hist_words
+  uint2* seg;                  // [V] sorted range [x, y) of each row, x > y where it has none
   int64_t* off;                // [N] element offset of each sorted position's row in G
   uint32_t* smp;               // [N] its sample
   double* partials;            // [N, embed_norm_parts] squared run norms
+  float* blocks;               // [N / 16, D] sums of blocks of positions, or null
   // clipped sum
   const float* c;              // [B]
   float noise_std;
@@ -112,12 +113,11 @@ struct EmbedArgs {
 // Launch limits (threads of one grid dimension stay below 2^32).
 constexpr int64_t kEmbedMaxN = (int64_t)1 << 25, kEmbedMaxV = (int64_t)1 << 24;
 constexpr int64_t kEmbedMaxD = (int64_t)1 << 22, kEmbedMaxTable = (int64_t)1 << 33;
-// Elements of a.hist, and partials per sorted position.
+// Elements of a.hist and a.blocks (0: null), partials per sorted position.
 int64_t embed_hist_words(int64_t N, int64_t V);
+int64_t embed_block_floats(const EmbedArgs& a);
 int embed_norm_parts(const EmbedArgs& a);
-// Sorts the positions by (token, sample, position); fills key/pos (the sorted
-// copies are key[embed_sorted], pos[embed_sorted]), seg, off and smp.
-int embed_sorted(int64_t V);
+// Sorts the positions by (token, position); fills seg, off and smp.
 hipError_t launch_embed_sort(const EmbedArgs& a, hipStream_t s);
 hipError_t launch_embed_norm(const EmbedArgs& a, hipStream_t s);
 hipError_t launch_embed_accumulate(const EmbedArgs& a, hipStream_t s);
