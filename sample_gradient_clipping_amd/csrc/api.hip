@@ -1549,7 +1549,7 @@ dpf_status check_embed(const dpf_ids* ids, const dpf_act* G, int64_t V, float sc
 // Workspace of the embedding's gradient: the sort's buffers and what the
 // kernels after it read.
 struct EmbedWs {
-  size_t key[2], pos[2], hist, seg, off, smp, blocks, part, c;
+  size_t key[2], pos[2], hist, seg, rec, blocks, part, c;
   bool has_blocks;
 };
 
@@ -1578,8 +1578,7 @@ EmbedWs reserve_embed(const dpf::EmbedArgs& a, Workspace& ws, bool norms) {
   }
   o.hist = ws.reserve((size_t)dpf::embed_hist_words((int64_t)N, a.V) * sizeof(uint32_t));
   o.seg = ws.reserve((size_t)a.V * sizeof(uint2));
-  o.off = ws.reserve(N * sizeof(int64_t));
-  o.smp = ws.reserve(N * sizeof(uint32_t));
+  o.rec = ws.reserve(N * sizeof(uint4));
   const int64_t blocks = dpf::embed_block_floats(a);
   o.has_blocks = blocks != 0;
   if (o.has_blocks) o.blocks = ws.reserve((size_t)blocks * sizeof(float));
@@ -1597,8 +1596,7 @@ void point_embed(dpf::EmbedArgs& a, const Workspace& ws, const EmbedWs& o, bool 
   }
   a.hist = ws.at<uint32_t>(o.hist);
   a.seg = ws.at<uint2>(o.seg);
-  a.off = ws.at<int64_t>(o.off);
-  a.smp = ws.at<uint32_t>(o.smp);
+  a.rec = ws.at<uint4>(o.rec);
   a.blocks = o.has_blocks ? ws.at<float>(o.blocks) : nullptr;
   if (norms) a.partials = ws.at<double>(o.part);
 }
@@ -1737,6 +1735,7 @@ dpf_status dpfused_embedding_scaled_accumulate(const dpf_ids* ids, const dpf_act
   a.offset = offset;
   a.out = grad_out;
   hipError_t e = dpf::launch_embed_sort(a, s);
+  if (e == hipSuccess) e = dpf::launch_embed_segments(a, s);
   if (e == hipSuccess) e = dpf::launch_embed_accumulate(a, s);
   if (e != hipSuccess) return hip_fail(e, "embedding accumulate launch");
   return ok();

@@ -17,8 +17,11 @@
 //                            significant digit first; inactive positions get
 //                            the id V and end up last; the last pass also
 //                            writes, per position, where its row of G starts
-//                            and its sample, and per table row its segment
-//  embed_blocks            : 16 positions of one run (segment) summed ahead
+//                            and its sample
+//  sort_small              : the same in one workgroup, for a few thousand
+//  embed_segments          : each row's positions (with norms, embed_norm's
+//                            work)
+//  embed_blocks            : 8 positions of one run (segment) summed ahead
 //  embed_norm              : one wave per run and column group
 //  embed_long              : segments that hold such blocks
 //  embed_accumulate        : every row of the result, noise included
@@ -103,11 +106,24 @@ int embed_sorted(int64_t V, int q) {
   return q & 1;
 }
 
+// Mask byte and id are fetched together: both are the caller's memory whatever
+// they hold, and a chain of two loads costs a microsecond more.
 __device__ __forceinline__ uint32_t token_key(const EmbedArgs& a, uint32_t n) {
-  if (a.mask != nullptr && a.mask[n] == 0) return (uint32_t)a.V;
+  const uint8_t m = a.mask != nullptr ? a.mask[n] : 1;
   const uint32_t b = n / (uint32_t)a.T;
   const int64_t id = a.ids.at(b, n - b * (uint32_t)a.T);
-  return id >= 0 && id < a.V ? (uint32_t)id : (uint32_t)a.V;
+  return m != 0 && id >= 0 && id < a.V ? (uint32_t)id : (uint32_t)a.V;
+}
+
+// What the kernels after the sort read of a position, in one load: its token,
+// its sample, and where its row of G starts (elements).
+__device__ __forceinline__ uint4 record(const EmbedArgs& a, uint32_t key, uint32_t n) {
+  const uint32_t b = n / (uint32_t)a.T, t = n - b * (uint32_t)a.T;
+  const int64_t off = (int64_t)b * a.G.stride_b + (int64_t)t * a.G.stride_t;
+  return make_uint4(key, b, (uint32_t)off, (uint32_t)(off >> 32));
+}
+__device__ __forceinline__ int64_t record_off(const uint4& r) {
+  return (int64_t)(((uint64_t)r.w << 32) | r.z);
 }
 
 struct SortPass {
@@ -164,17 +180,19 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* tmp) {
 // workgroups (from the histograms), chunks and waves, and within a wave's 64
 // keys the lanes below it with the same digit (found by ballots on its bits).
 // Each key's digit of the next pass is counted for the workgroup that will
-// read it there.  The last pass writes what the kernels after it read: the
-// row's offset in G and its sample, and the segments (keys that are equal
-// arrive next to each other and in order, so the first and the last of them
-// in a wave give the segment's ends; integer minimum and maximum, the same in
-// any order).
+// read it there: in LDS first (a frequent token would otherwise queue up its
+// global atomics), then added up, integers, so the same in any order.  The last
+// pass writes what the kernels after it read: the row's offset in G and its
+// sample.
 template <int PER, bool FIRST, bool LAST>
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(EmbedArgs a, SortPass p) {
+  extern __shared__ uint32_t next_cnt[];         // [blocks, bins], not in the last pass
   __shared__ uint32_t base[kMaxBins];
   __shared__ uint32_t wcnt[kSortWaves][kMaxBins];
   __shared__ uint32_t tmp[kSortWaves];
   const int bins = 1 << p.digit, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if constexpr (!LAST)
+    for (int i = tid; i < p.blocks * bins; i += kSortThreads) next_cnt[i] = 0u;
   const uint32_t chunk = kSortThreads * PER, len = chunk * p.chunks, n0 = blockIdx.x * len;
   for (int ch = 0; ch < p.chunks; ++ch) {
     const uint32_t c0 = n0 + ch * chunk;
@@ -236,51 +254,183 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(EmbedArgs a,
       const bool in = n < p.N;
       const uint32_t key = k[i];
       const uint32_t to = in ? wcnt[wave][(key >> p.shift) & (uint32_t)(bins - 1)] + r[i] : 0u;
-      const uint32_t prev = __shfl_up(key, 1, 64), next = __shfl_down(key, 1, 64);
       if (!in) continue;
-      p.key_out[to] = key;
       p.pos_out[to] = q[i];
       if constexpr (!LAST) {
+        p.key_out[to] = key;
         const uint32_t nd = (key >> (p.shift + p.digit)) & (uint32_t)(bins - 1);
-        atomicAdd(&p.next_hist[(to / len) * bins + nd], 1u);
+        atomicAdd(&next_cnt[(to / len) * bins + nd], 1u);
       } else {
-        const uint32_t b = q[i] / (uint32_t)a.T, t = q[i] - b * (uint32_t)a.T;
-        a.off[to] = (int64_t)b * a.G.stride_b + (int64_t)t * a.G.stride_t;
-        a.smp[to] = b;
-        if (key < (uint32_t)a.V) {
-          if (lane == 0 || prev != key) atomicMin(&a.seg[key].x, to);
-          if (lane == 63 || n == p.N - 1 || next != key) atomicMax(&a.seg[key].y, to + 1);
-        }
+        a.rec[to] = record(a, key, q[i]);
       }
     }
     __syncthreads();
   }
+  if constexpr (!LAST)
+    for (int i = tid; i < p.blocks * bins; i += kSortThreads)
+      if (const uint32_t n = next_cnt[i]) atomicAdd(&p.next_hist[i], n);
+}
+
+// Up to 2048 positions: every pass in one workgroup, keys and the order so
+// far in LDS, so that a call has one launch instead of one per digit and one
+// more.  The other workgroups empty the segments.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64, kSmallPer = 2;
+constexpr int64_t kSmallN = kSmallThreads * kSmallPer;
+
+template <int PER>
+constexpr int small_lds() {
+  return kSmallThreads * PER * (4 + 2 * 2) + kSmallWaves * kMaxBins * 2 + kSmallWaves * 4;
+}
+
+template <int PER>
+__global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(EmbedArgs a, uint32_t N,
+                                                                   int passes, int digit,
+                                                                   uint32_t* pos_out) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char mem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (blockIdx.x != 0) {
+    for (int64_t v = (int64_t)(blockIdx.x - 1) * kSmallThreads + tid; v < a.V;
+         v += (int64_t)(gridDim.x - 1) * kSmallThreads)
+      a.seg[v] = make_uint2(0xffffffffu, 0u);
+    return;
+  }
+  uint32_t* key = (uint32_t*)mem;                                  // by position
+  uint16_t* perm = (uint16_t*)(key + kSmallThreads * PER);         // two orders
+  uint16_t* wcnt = perm + 2 * kSmallThreads * PER;                 // [wave][bin]
+  uint32_t* tmp = (uint32_t*)(wcnt + kSmallWaves * kMaxBins);
+  const int bins = 1 << digit;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t n = tid + i * kSmallThreads;
+    if (n < N) key[n] = token_key(a, n);
+  }
+  __syncthreads();
+  for (int p = 0; p < passes; ++p) {
+    const uint16_t* from = perm + (p & 1) * kSmallThreads * PER;
+    uint16_t* to = perm + ((p + 1) & 1) * kSmallThreads * PER;
+    for (int d = lane; d < bins; d += 64) wcnt[wave * kMaxBins + d] = 0;
+    __builtin_amdgcn_wave_barrier();
+    uint16_t src[PER], dig[PER], r[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t n = wave * (64 * PER) + i * 64 + lane;
+      src[i] = n >= N ? 0 : p == 0 ? (uint16_t)n : from[n];
+      dig[i] = n >= N ? 0 : (uint16_t)((key[src[i]] >> (p * digit)) & (uint32_t)(bins - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool in = wave * (64 * PER) + i * 64 + lane < N;
+      const uint32_t d = dig[i];
+      uint64_t same = __ballot(in);
+      for (int j = 0; j < digit; ++j) {
+        const uint64_t m = __ballot((d >> j) & 1u);
+        same &= ((d >> j) & 1u) ? m : ~m;
+      }
+      const uint32_t below = (uint32_t)__popcll(same & ((1ull << lane) - 1ull));
+      const uint32_t seen = in ? wcnt[wave * kMaxBins + d] : 0u;
+      r[i] = (uint16_t)(seen + below);
+      __builtin_amdgcn_wave_barrier();
+      if (in && below == 0) wcnt[wave * kMaxBins + d] = (uint16_t)(seen + (uint32_t)__popcll(same));
+      __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    uint32_t total = 0;
+    if (tid < bins)
+      for (int w = 0; w < kSmallWaves; ++w) total += wcnt[w * kMaxBins + tid];
+    uint32_t at = block_exclusive(total, tmp);
+    if (tid < bins)
+      for (int w = 0; w < kSmallWaves; ++w) {
+        const uint32_t c = wcnt[w * kMaxBins + tid];
+        wcnt[w * kMaxBins + tid] = (uint16_t)at;
+        at += c;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (wave * (64 * PER) + i * 64 + lane < N) to[wcnt[wave * kMaxBins + dig[i]] + r[i]] = src[i];
+    __syncthreads();
+  }
+  const uint16_t* order = perm + (passes & 1) * kSmallThreads * PER;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t k = tid + i * kSmallThreads;
+    if (k >= N) break;
+    const uint32_t n = order[k];
+    pos_out[k] = n;
+    a.rec[k] = record(a, key[n], n);
+  }
+}
+
+// The segments, from neighbours' tokens (emptied by the sort).
+__global__ void __launch_bounds__(256) embed_segments_kernel(EmbedArgs a, uint32_t N) {
+  const uint32_t k = blockIdx.x * 256 + threadIdx.x;
+  if (k >= N) return;
+  const uint32_t v = a.rec[k].x;
+  if (v >= (uint32_t)a.V) return;
+  if (k == 0 || a.rec[k - 1].x != v) a.seg[v].x = k;
+  if (k == N - 1 || a.rec[k + 1].x != v) a.seg[v].y = k + 1;
 }
 
 // ---------------------------------------------------------------------------
 // Row sums
 // ---------------------------------------------------------------------------
-// Sorted positions in blocks of 16.  A block that lies inside one run (of one
+// Sorted positions in blocks of 8.  A block that lies inside one run (of one
 // segment, for the clipped sum) is summed by itself first, so that no wave
-// adds more than 30 rows and a partial per 16 others: a token that fills a
+// adds more than 14 rows and a partial per 8 others: a token that fills a
 // tenth of the batch does not leave one wave with all its rows.
-constexpr uint32_t kBlock = 16;
+constexpr uint32_t kBlock = 8;
 // Batches below this many positions go without (two launches less; a wave
 // then adds at most this many rows).
 constexpr int64_t kBlocksFrom = 256;
 
 typedef __attribute__((address_space(4))) const uint32_t c_u32;
-typedef __attribute__((address_space(4))) const int64_t c_i64;
-typedef __attribute__((address_space(4))) const float c_f32;
 
 // Wave-uniform reads of what an earlier kernel wrote, through the scalar cache.
 __device__ __forceinline__ uint32_t su32(const uint32_t* p, uint32_t i) { return ((c_u32*)p)[i]; }
-__device__ __forceinline__ int64_t si64(const int64_t* p, uint32_t i) { return ((c_i64*)p)[i]; }
-__device__ __forceinline__ float sf32(const float* p, uint32_t i) { return ((c_f32*)p)[i]; }
+
+__device__ __forceinline__ int64_t lane_i64(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float lane_f32(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// Rows (or partials) j .. cnt - 1 in batches whose loads are all in flight
+// together: as many of MOST as there are, then the binary rest.
+template <int MOST, class F>
+__device__ __forceinline__ void in_batches(int cnt, F&& f) {
+  int j = 0;
+  for (; j + MOST <= cnt; j += MOST) f(j, std::integral_constant<int, MOST>());
+  if constexpr (MOST >= 8)
+    if (cnt - j >= 4) { f(j, std::integral_constant<int, 4>()); j += 4; }
+  if constexpr (MOST >= 4)
+    if (cnt - j >= 2) { f(j, std::integral_constant<int, 2>()); j += 2; }
+  if (cnt - j >= 1) f(j, std::integral_constant<int, 1>());
+}
+
+// f(offsets, weights, count) for the sorted positions [i, end), 64 at a time,
+// one position's in each lane (to go round by lane reads).  Weights c[sample]
+// * scale, or 1.
+template <bool WEIGHTED, class F>
+__device__ __forceinline__ void over_rows(const EmbedArgs& a, uint32_t i, uint32_t end, F&& f) {
+  const int lane = threadIdx.x & 63;
+  for (; i < end; i += 64) {
+    const int cnt = (int)min(64u, end - i);
+    const uint32_t k = i + min(lane, cnt - 1);
+    const uint4 r = a.rec[k];
+    const int64_t off = record_off(r);
+    const float w = WEIGHTED ? a.c[r.y] * a.scale : 1.f;
+    f(off, w, cnt);
+  }
+}
 
 // One wave's share of a row: U groups of 64 V columns from c0 on.
 template <class E, int V, int U>
 struct RowSum {
+  // Rows loaded ahead: up to 96 registers of them.
+  static constexpr int kMost = U * V * (int)sizeof(typename E::storage) / 4 <= 12 ? 8 : 4;
   float s[U][V];
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -288,31 +438,29 @@ struct RowSum {
 #pragma unroll
       for (int e = 0; e < V; ++e) s[u][e] = 0.f;
   }
-  // += w row; `row` at the wave's first column
-  __device__ __forceinline__ void add(const typename E::storage* row, int64_t left, float w) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t col = (int64_t)(u * 64 + lane) * V;
-      if (col < left) {
-        float x[V];
-        load_f32<E, V>(row + col, x);
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[u][e] += w * x[e];
-      }
-    }
+  // This lane's column of group u, within the row also where the group is
+  // not (what is loaded there is never stored).
+  static __device__ __forceinline__ int64_t column(int u, int64_t left) {
+    const int64_t col = (int64_t)(u * 64 + (threadIdx.x & 63)) * V;
+    return col < left ? col : left - V;
   }
-  __device__ __forceinline__ void add_part(const float* part, int64_t left) {
-    const int lane = threadIdx.x & 63;
+  // += w row, for K rows given at the wave's first column
+  template <class S, int K, class P, class W>
+  __device__ __forceinline__ void add(int64_t left, P&& row, W&& weight) {
+    Raw<S, V> x[K][U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t col = (int64_t)(u * 64 + lane) * V;
-      if (col < left) {
-        float x[V];
-        load_f32<F32, V>(part + col, x);
+    for (int k = 0; k < K; ++k) {
+      const typename S::storage* p = row(k);
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[u][e] += x[e];
-      }
+      for (int u = 0; u < U; ++u) x[k][u] = load_raw<S, V>(p + column(u, left));
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float w = weight(k);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[u][e] += w * raw_f32<S, V>(x[k][u], e);
     }
   }
   __device__ __forceinline__ void store(float* part, int64_t left) const {
@@ -323,24 +471,25 @@ struct RowSum {
       if (col < left) store_f32<F32, V>(part + col, s[u]);
     }
   }
-  // The rows of sorted positions [i, end), whole blocks of 16 from `parts`
-  // (null: none); weights c[sample] * scale, or 1.
-  template <bool WEIGHTED>
-  __device__ __forceinline__ void range(const EmbedArgs& a, const float* parts, int64_t c0,
-                                        uint32_t i, uint32_t end) {
+  // The rows whose offsets and weights the first cnt lanes hold.
+  __device__ __forceinline__ void batch(const EmbedArgs& a, int64_t c0, int64_t off, float w,
+                                        int cnt) {
     const typename E::storage* G = (const typename E::storage*)a.G.data + c0;
-    const int64_t left = a.D - c0;
-    const uint32_t b0 = (i + kBlock - 1) / kBlock, b1 = end / kBlock;
-    const bool blocks = parts != nullptr && b1 > b0;
-    const uint32_t head = blocks ? b0 * kBlock : end;
-#pragma unroll 4
-    for (; i < head; ++i) add(G + si64(a.off, i), left, WEIGHTED ? sf32(a.c, su32(a.smp, i)) * a.scale : 1.f);
-    if (!blocks) return;
-#pragma unroll 4
-    for (uint32_t b = b0; b < b1; ++b) add_part(parts + (int64_t)b * a.D + c0, left);
-#pragma unroll 4
-    for (i = b1 * kBlock; i < end; ++i)
-      add(G + si64(a.off, i), left, WEIGHTED ? sf32(a.c, su32(a.smp, i)) * a.scale : 1.f);
+    in_batches<kMost>(cnt, [&](int j, auto kk) {
+      add<E, decltype(kk)::value>(a.D - c0, [&](int k) { return G + lane_i64(off, j + k); },
+                                  [&](int k) { return lane_f32(w, j + k); });
+    });
+  }
+  template <bool WEIGHTED>
+  __device__ __forceinline__ void rows(const EmbedArgs& a, int64_t c0, uint32_t i, uint32_t end) {
+    over_rows<WEIGHTED>(a, i, end, [&](int64_t off, float w, int cnt) { batch(a, c0, off, w, cnt); });
+  }
+  __device__ __forceinline__ void parts(const EmbedArgs& a, int64_t c0, uint32_t b, uint32_t end) {
+    const float* p = a.blocks + (int64_t)b * a.D + c0;
+    in_batches<U * V <= 16 ? 8 : 4>((int)(end - b), [&](int j, auto kk) {
+      add<F32, decltype(kk)::value>(a.D - c0, [&](int k) { return p + (int64_t)(j + k) * a.D; },
+                                    [](int) { return 1.f; });
+    });
   }
 };
 
@@ -351,73 +500,158 @@ __device__ __forceinline__ uint32_t wave_of_grid() {
 // The blocks inside one run (WEIGHTED: one segment), one wave per block and
 // column group.
 template <class E, int V, int U, bool WEIGHTED>
-__global__ void __launch_bounds__(256) embed_blocks_kernel(EmbedArgs a, const uint32_t* key,
-                                                           uint32_t N) {
+__global__ void __launch_bounds__(256) embed_blocks_kernel(EmbedArgs a, uint32_t N) {
   const uint32_t b = wave_of_grid(), i = b * kBlock;
   if (i + kBlock > N) return;
-  const uint32_t v = su32(key, i);
-  if (v >= (uint32_t)a.V || v != su32(key, i + kBlock - 1)) return;
-  if (!WEIGHTED && su32(a.smp, i) != su32(a.smp, i + kBlock - 1)) return;
+  const uint4 r = a.rec[i + min(threadIdx.x & 63u, kBlock - 1)];
+  const uint32_t v = __builtin_amdgcn_readlane(r.x, 0);
+  if (v >= (uint32_t)a.V || v != __builtin_amdgcn_readlane(r.x, kBlock - 1)) return;
+  if (!WEIGHTED && __builtin_amdgcn_readlane(r.y, 0) != __builtin_amdgcn_readlane(r.y, kBlock - 1)) return;
   const int64_t c0 = (int64_t)blockIdx.y * (64 * V * U);
   RowSum<E, V, U> sum;
   sum.zero();
-  sum.template range<WEIGHTED>(a, nullptr, c0, i, i + kBlock);
+  sum.batch(a, c0, record_off(r), WEIGHTED ? a.c[r.y] * a.scale : 1.f, kBlock);
   sum.store(a.blocks + (int64_t)b * a.D + c0, a.D - c0);
 }
 
 // Segments with a block of their own: their whole sum, in place of the first
-// such block's.
+// such block's.  One workgroup each; its four waves take a quarter of the
+// blocks, the first the rows before them and the last the rows after, and the
+// four sums are added in order.
 template <class E, int V, int U>
-__global__ void __launch_bounds__(256) embed_long_kernel(EmbedArgs a, const uint32_t* key,
-                                                         uint32_t N) {
-  const uint32_t b = wave_of_grid(), i = b * kBlock;
-  if (i + kBlock > N) return;
-  const uint32_t v = su32(key, i);
-  if (v >= (uint32_t)a.V || v != su32(key, i + kBlock - 1)) return;
+__global__ void __launch_bounds__(256) embed_long_kernel(EmbedArgs a, uint32_t N) {
+  __shared__ float part[3][U * V * 64];
+  const uint32_t b = blockIdx.x, i = b * kBlock;
+  const uint32_t v = su32(&a.rec[i].x, 0);
+  if (v >= (uint32_t)a.V || v != su32(&a.rec[i + kBlock - 1].x, 0)) return;
   const uint32_t first = su32(&a.seg[v].x, 0), end = su32(&a.seg[v].y, 0);
   if ((first + kBlock - 1) / kBlock != b) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t b1 = end / kBlock, nb = b1 - b;
   const int64_t c0 = (int64_t)blockIdx.y * (64 * V * U);
   RowSum<E, V, U> sum;
   sum.zero();
-  sum.template range<true>(a, a.blocks, c0, first, end);
+  if (wave == 0) sum.template rows<true>(a, c0, first, i);
+  sum.parts(a, c0, b + nb * wave / 4, b + nb * (wave + 1) / 4);
+  if (wave == 3) sum.template rows<true>(a, c0, b1 * kBlock, end);
+  if (wave > 0)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) part[wave - 1][(u * V + e) * 64 + lane] = sum.s[u][e];
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum.s[u][e] += part[w][(u * V + e) * 64 + lane];
   sum.store(a.blocks + (int64_t)b * a.D + c0, a.D - c0);
 }
 
-// One wave per sorted position and column group.  The first position of a run
-// sums the run's rows (float32, in order) and squares the sum (float64); the
-// others write 0.  partials[position][column group], positions in their
-// original order, so that a sample's are contiguous.
+// One wave per 8 sorted positions and column group, for the runs that start
+// there: the 8 rows are loaded together (most runs have one or two), a run's
+// rows are summed (float32, in order) and the sum squared (float64).  A run
+// that starts before the 8 is skipped, one that goes on past them is followed
+// to its end.  partials[position][column group], positions in their original
+// order, so that a sample's are contiguous; a run's value is written at its
+// last position among the 8, and 0 at the others.
+constexpr int kWindow = kBlock;
 template <class E, int V, int U>
-__global__ void __launch_bounds__(256) embed_norm_kernel(EmbedArgs a, const uint32_t* key,
-                                                         const uint32_t* pos, uint32_t N) {
+__global__ void __launch_bounds__(256) embed_norm_kernel(EmbedArgs a, const uint32_t* pos,
+                                                         uint32_t N) {
   const int lane = threadIdx.x & 63;
-  const uint32_t k = wave_of_grid();
-  if (k >= N) return;
-  double* dst = a.partials + (int64_t)su32(pos, k) * gridDim.y + blockIdx.y;
-  const uint32_t v = su32(key, k), b = su32(a.smp, k);
-  if (v >= (uint32_t)a.V || (k > 0 && su32(key, k - 1) == v && su32(a.smp, k - 1) == b)) {
-    if (lane == 0) *dst = 0.0;
-    return;
+  const uint32_t base = wave_of_grid() * kWindow;
+  if (base >= N) return;
+  // lane l: sorted position base + l - 1
+  const bool in = base + lane >= 1 && base + lane - 1 < N;
+  const uint4 r = a.rec[in ? base + lane - 1 : 0];
+  const uint32_t where = lane < kWindow && base + lane < N ? pos[base + lane] : 0u;
+  const int64_t off = record_off(r);
+  const uint32_t pk = __shfl_up(r.x, 1, 64), pb = __shfl_up(r.y, 1, 64);
+  const bool pin = __shfl_up((int)in, 1, 64) != 0 && lane > 0;
+  // bit l: position base + l - 1 is of the same token (run) as the one before it
+  const uint64_t same = __ballot(in && pin && pk == r.x);
+  const uint64_t cont = same & __ballot(pb == r.y);
+  const uint64_t act = __ballot(in && r.x < (uint32_t)a.V) >> 1;
+  if (blockIdx.y == 0 && lane >= 1 && lane <= kWindow && in && r.x < (uint32_t)a.V) {
+    if (!((same >> lane) & 1)) a.seg[r.x].x = base + lane - 1;
+    if (!((same >> (lane + 1)) & 1)) a.seg[r.x].y = base + lane;
   }
-  uint32_t end = k + 1;
-  for (;;) {                       // the run's end, 64 positions at a time
-    const uint32_t i = end + lane;
-    const uint64_t other = __ballot(i >= N || key[i] != v || a.smp[i] != b);
-    if (other != 0) { end += __builtin_ctzll(other); break; }
-    end += 64;
-  }
-  end = __builtin_amdgcn_readfirstlane(end);
-  const int64_t c0 = (int64_t)blockIdx.y * (64 * V * U);
+  const int lead = __builtin_ctzll(~(cont >> 1));
+  const int64_t c0 = (int64_t)blockIdx.y * (64 * V * U), left = a.D - c0;
+  const typename E::storage* G = (const typename E::storage*)a.G.data + c0;
+  double q[kWindow];
   RowSum<E, V, U> sum;
-  sum.zero();
-  sum.template range<false>(a, a.blocks, c0, k, end);
-  double sq = 0.0;
+  Raw<E, V> x[kWindow][U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int j = 0; j < kWindow; ++j) {
+    q[j] = 0.0;
+    if (j < lead || !((act >> j) & 1)) continue;
+    const typename E::storage* row = G + lane_i64(off, j + 1);
 #pragma unroll
-    for (int e = 0; e < V; ++e) sq += (double)sum.s[u][e] * (double)sum.s[u][e];
-  sq = wave_sum_f64(sq);
-  if (lane == 0) *dst = sq * (double)a.scale * (double)a.scale;
+    for (int u = 0; u < U; ++u) x[j][u] = load_raw<E, V>(row + sum.column(u, left));
+  }
+  // V squares in float32, everything above in float64 (a conversion and a
+  // float64 multiply per value would be as long as the loads).
+  auto squares = [&]() {
+    double s = 0.0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) v += sum.s[u][e] * sum.s[u][e];
+      s += (int64_t)(u * 64 + lane) * V < left ? (double)v : 0.0;
+    }
+    return s;
+  };
+#pragma unroll
+  for (int j = 0; j < kWindow; ++j) {
+    if (j < lead || !((act >> j) & 1)) continue;
+    const bool more = (cont >> (j + 1)) & 1, goes_on = (cont >> (j + 2)) & 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        sum.s[u][e] = (more ? sum.s[u][e] : 0.f) + raw_f32<E, V>(x[j][u], e);
+    if (!goes_on) {
+      q[j] = squares();
+    } else if (j == kWindow - 1) {
+      const uint32_t v = __builtin_amdgcn_readlane(r.x, j + 1), b = __builtin_amdgcn_readlane(r.y, j + 1);
+      const uint32_t i = base + kWindow;
+      uint32_t end = i + (uint32_t)__builtin_ctzll(~(cont >> (kWindow + 1)));
+      while (end >= base + 63 && end < N) {          // past the lanes' positions
+        const uint32_t k = end + lane;
+        const uint4 o = a.rec[min(k, N - 1)];
+        const uint64_t other = __ballot(k >= N || o.x != v || o.y != b);
+        end += other != 0 ? (uint32_t)__builtin_ctzll(other) : 64u;
+        if (other != 0) break;
+      }
+      end = __builtin_amdgcn_readfirstlane(end);
+      uint32_t rest = i;                             // a block starts here
+      if (a.blocks != nullptr) {
+        rest = end / kBlock * kBlock;
+        sum.parts(a, c0, i / kBlock, rest / kBlock);
+      }
+      sum.template rows<false>(a, c0, rest, end);
+      q[j] = squares();
+    }
+  }
+  // all eight sums over the wave: halves of the values change sides while
+  // there are several, then the lanes of one value add up; lane 8 j has q[j]
+#pragma unroll
+  for (int n = kWindow / 2, o = 32; n >= 1; n /= 2, o /= 2)
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const double keep = (lane & o) ? q[j + n] : q[j], give = (lane & o) ? q[j] : q[j + n];
+      q[j] = keep + __shfl_xor(give, o, 64);
+    }
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) q[0] += __shfl_xor(q[0], o, 64);
+  const uint32_t at = __shfl(where, lane >> 3, 64);
+  if ((lane & 7) == 0 && base + (lane >> 3) < N)
+    a.partials[(int64_t)at * gridDim.y + blockIdx.y] = q[0] * (double)a.scale * (double)a.scale;
 }
 
 // One wave per row of the result and U groups of 256 columns (gridDim.y of
@@ -438,58 +672,68 @@ __global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a) {
   const float rd = 1.0f / a.denom;
   for (int64_t g0 = (int64_t)blockIdx.y * (256 * U); start + g0 < row0 + D;
        g0 += (int64_t)gridDim.y * (256 * U)) {
-    int64_t col[U];                // first of the thread's four columns (may be below 0)
+    // First of the thread's four columns (may be below 0), and a place within
+    // the row to load from also where they are not.
+    int64_t col[U], in[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) col[u] = start - row0 + g0 + (u * 64 + lane) * 4;
-    float old[U][4], sum[U][4];
+    for (int u = 0; u < U; ++u) {
+      col[u] = start - row0 + g0 + (u * 64 + lane) * 4;
+      in[u] = AL ? (col[u] < D ? col[u] : D - 4) : col[u];
+    }
+    // Four values of a row of `S`: one load, or (AL false) element by element.
+    auto fetch = [&](auto e, const auto* row, int u) {
+      using S = decltype(e);
+      Raw<S, 4> x;
+      if constexpr (AL) {
+        x = load_raw<S, 4>(row + in[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t c = in[u] + k;
+          x[k] = row[c < 0 ? 0 : c < D ? c : D - 1];
+        }
+      }
+      return x;
+    };
+    f32x4 old[U];
+    float sum[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[u][e] = old[u][e] = 0.f;
-      if (a.beta && col[u] < D) {
-        float* o = a.out + row0 + col[u];
-        if (AL || (col[u] >= 0 && col[u] + 4 <= D)) {
-          load_f32<F32, 4>(o, old[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col[u] + e >= 0 && col[u] + e < D) old[u][e] = o[e];
-        }
-      }
+      for (int e = 0; e < 4; ++e) sum[u][e] = 0.f;
+      old[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    if (a.beta)
+#pragma unroll
+      for (int u = 0; u < U; ++u) old[u] = fetch(F32(), a.out + row0, u);
     if (summed) {
-      const float* part = a.blocks + (int64_t)b0 * D;
+      f32x4 x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (col[u] >= D) continue;
-        if (AL) {
-          load_f32<F32, 4>(part + col[u], sum[u]);
-        } else {
+      for (int u = 0; u < U; ++u) x[u] = fetch(F32(), a.blocks + (int64_t)b0 * D, u);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col[u] + e >= 0 && col[u] + e < D) sum[u][e] = part[col[u] + e];
-        }
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[u][e] = x[u][e];
     } else if (!empty) {
-#pragma unroll 2
-      for (uint32_t i = first; i < end; ++i) {
-        const typename E::storage* row = (const typename E::storage*)a.G.data + si64(a.off, i);
-        const float w = sf32(a.c, su32(a.smp, i)) * a.scale;
+      over_rows<true>(a, first, end, [&](int64_t off, float w, int cnt) {
+        in_batches<4>(cnt, [&](int j, auto kk) {
+          constexpr int K = decltype(kk)::value;
+          Raw<E, 4> x[K][U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (col[u] >= D) continue;
-          if (AL) {
-            float x[4];
-            load_f32<E, 4>(row + col[u], x);
+          for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[u][e] += w * x[e];
-          } else {
+            for (int u = 0; u < U; ++u)
+              x[k][u] = fetch(E(), (const typename E::storage*)a.G.data + lane_i64(off, j + k), u);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (col[u] + e >= 0 && col[u] + e < D) sum[u][e] += w * E::to_float(row[col[u] + e]);
+          for (int k = 0; k < K; ++k) {
+            const float wk = lane_f32(w, j + k);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum[u][e] += wk * raw_f32<E, 4>(x[k][u], e);
           }
-        }
-      }
+        });
+      });
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -559,10 +803,40 @@ void with_rows(const EmbedArgs& a, F&& f) {
 template <int PER>
 void launch_scatter(const EmbedArgs& a, const SortPass& p, bool first, bool last, hipStream_t s) {
   const dim3 grid((unsigned)p.blocks), block(kSortThreads);
-  if (first && last) hipLaunchKernelGGL((sort_scatter_kernel<PER, true, true>), grid, block, 0, s, a, p);
-  else if (first) hipLaunchKernelGGL((sort_scatter_kernel<PER, true, false>), grid, block, 0, s, a, p);
-  else if (last) hipLaunchKernelGGL((sort_scatter_kernel<PER, false, true>), grid, block, 0, s, a, p);
-  else hipLaunchKernelGGL((sort_scatter_kernel<PER, false, false>), grid, block, 0, s, a, p);
+  const unsigned lds = last ? 0u : (unsigned)(p.blocks << p.digit) * 4u;
+  if (first && last) hipLaunchKernelGGL((sort_scatter_kernel<PER, true, true>), grid, block, lds, s, a, p);
+  else if (first) hipLaunchKernelGGL((sort_scatter_kernel<PER, true, false>), grid, block, lds, s, a, p);
+  else if (last) hipLaunchKernelGGL((sort_scatter_kernel<PER, false, true>), grid, block, lds, s, a, p);
+  else hipLaunchKernelGGL((sort_scatter_kernel<PER, false, false>), grid, block, lds, s, a, p);
+}
+
+template <int PER>
+hipError_t launch_small(const EmbedArgs& a, const SortPlan& p, hipStream_t s) {
+  static hipError_t once = hipFuncSetAttribute((const void*)sort_small_kernel<PER>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               small_lds<PER>());
+  if (once != hipSuccess) return once;
+  const int at = embed_sorted(a.V, -1);
+  const int clear = (int)std::min<int64_t>(256, (a.V + kSmallThreads - 1) / kSmallThreads);
+  hipLaunchKernelGGL((sort_small_kernel<PER>), dim3((unsigned)(1 + clear)), dim3(kSmallThreads),
+                     small_lds<PER>(), s, a, (uint32_t)(a.B * a.T), p.passes, p.digit, a.pos[at]);
+  return hipGetLastError();
+}
+
+// More LDS than the default limit, once per scatter kernel that counts the
+// next digit.
+template <int PER>
+hipError_t scatter_attributes() {
+  const int most = kSortBlocks * kMaxBins * 4;
+  static hipError_t once = [&] {
+    hipError_t e = hipFuncSetAttribute((const void*)sort_scatter_kernel<PER, true, false>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == hipSuccess)
+      e = hipFuncSetAttribute((const void*)sort_scatter_kernel<PER, false, false>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, most);
+    return e;
+  }();
+  return once;
 }
 
 }  // namespace
@@ -597,6 +871,14 @@ hipError_t launch_embed_sort(const EmbedArgs& a, hipStream_t s) {
   const SortPlan p = sort_plan(N, a.V);
   const int64_t words = (int64_t)p.blocks << p.digit;
   timing_begin("embed_sort", s);
+  if (N <= kSmallN) {
+    const hipError_t e = N <= kSmallThreads ? launch_small<1>(a, p, s) : launch_small<2>(a, p, s);
+    timing_end("embed_sort", s);
+    return e;
+  }
+  const hipError_t ready = p.per == 1 ? scatter_attributes<1>() : p.per == 2 ? scatter_attributes<2>()
+                         : p.per == 4 ? scatter_attributes<4>() : scatter_attributes<8>();
+  if (ready != hipSuccess) return ready;
   for (int q = 0; q < p.passes; ++q) {
     const bool first = q == 0, last = q + 1 == p.passes;
     SortPass w{};
@@ -630,10 +912,16 @@ hipError_t launch_embed_sort(const EmbedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+hipError_t launch_embed_segments(const EmbedArgs& a, hipStream_t s) {
+  const uint32_t N = (uint32_t)(a.B * a.T);
+  hipLaunchKernelGGL(embed_segments_kernel, dim3((N + 255) / 256), dim3(256), 0, s, a, N);
+  return hipGetLastError();
+}
+
 hipError_t launch_embed_norm(const EmbedArgs& a, hipStream_t s) {
   const uint32_t N = (uint32_t)(a.B * a.T);
   const unsigned parts = (unsigned)embed_norm_parts(a);
-  const uint32_t *key = a.key[embed_sorted(a.V, -1)], *pos = a.pos[embed_sorted(a.V, -1)];
+  const uint32_t* pos = a.pos[embed_sorted(a.V, -1)];
   EmbedArgs q = a;
   if (a.T < (int64_t)kBlock) q.blocks = nullptr;   // no run is as long
   timing_begin("embed_norm", s);
@@ -642,9 +930,9 @@ hipError_t launch_embed_norm(const EmbedArgs& a, hipStream_t s) {
     constexpr int V = decltype(v)::value, U = decltype(u)::value;
     if (q.blocks != nullptr)
       hipLaunchKernelGGL((embed_blocks_kernel<E, V, U, false>), dim3((N / kBlock + 3) / 4, parts),
-                         dim3(256), 0, s, q, key, N);
-    hipLaunchKernelGGL((embed_norm_kernel<E, V, U>), dim3((N + 3) / 4, parts), dim3(256), 0, s, q,
-                       key, pos, N);
+                         dim3(256), 0, s, q, N);
+    hipLaunchKernelGGL((embed_norm_kernel<E, V, U>), dim3((N + 4 * kWindow - 1) / (4 * kWindow), parts),
+                       dim3(256), 0, s, q, pos, N);
   });
   timing_end("embed_norm", s);
   return hipGetLastError();
@@ -668,15 +956,14 @@ void accumulate_u(const EmbedArgs& a, int U, dim3 grid, hipStream_t s) {
 hipError_t launch_embed_accumulate(const EmbedArgs& a, hipStream_t s) {
   const uint32_t N = (uint32_t)(a.B * a.T);
   const unsigned parts = (unsigned)embed_norm_parts(a);
-  const uint32_t* key = a.key[embed_sorted(a.V, -1)];
   timing_begin("embed_accumulate", s);
   if (a.blocks != nullptr)
     with_rows(a, [&](auto e, auto v, auto u) {
       using E = decltype(e);
       constexpr int V = decltype(v)::value, U = decltype(u)::value;
       const dim3 grid((N / kBlock + 3) / 4, parts);
-      hipLaunchKernelGGL((embed_blocks_kernel<E, V, U, true>), grid, dim3(256), 0, s, a, key, N);
-      hipLaunchKernelGGL((embed_long_kernel<E, V, U>), grid, dim3(256), 0, s, a, key, N);
+      hipLaunchKernelGGL((embed_blocks_kernel<E, V, U, true>), grid, dim3(256), 0, s, a, N);
+      hipLaunchKernelGGL((embed_long_kernel<E, V, U>), dim3(N / kBlock, parts), dim3(256), 0, s, a, N);
     });
   const bool al = row_vec(a.G, a.D) >= 4;
   // an unaligned row can touch one Philox block more

@@ -44,6 +44,32 @@ __device__ __forceinline__ void load_f32(const typename E::storage* p, float (&x
   }
 }
 
+// The same elements as they are in memory: a load whose conversion can come
+// later, so that several are in flight (a conversion beside the load waits for
+// it wherever a branch stands between the two and the next).
+template <class E, int V>
+struct RawOf {
+  typedef typename E::storage S;
+  static constexpr int kBytes = V * (int)sizeof(S);
+  typedef S type __attribute__((ext_vector_type(V), aligned(kBytes < 16 ? kBytes : 16)));
+};
+template <class E>
+struct RawOf<E, 1> {
+  typedef typename E::storage type;
+};
+template <class E, int V>
+using Raw = typename RawOf<E, V>::type;
+
+template <class E, int V>
+__device__ __forceinline__ Raw<E, V> load_raw(const typename E::storage* p) {
+  return *(const Raw<E, V>*)p;
+}
+template <class E, int V>
+__device__ __forceinline__ float raw_f32(const Raw<E, V>& r, int k) {
+  if constexpr (V == 1) return E::to_float(r);
+  else return E::to_float(r[k]);
+}
+
 template <class E, int V>
 __device__ __forceinline__ void store_f32(typename E::storage* p, const float (&x)[V]) {
   if constexpr (sizeof(typename E::storage) == 4) {
@@ -98,10 +124,9 @@ struct EmbedArgs {
   uint32_t *key[2], *pos[2];   // [N] each: sort buffers, ping and pong
   uint32_t* hist;              // embed_hist_words
   uint2* seg;                  // [V] sorted range [x, y) of each row, x > y where it has none
-  int64_t* off;                // [N] element offset of each sorted position's row in G
-  uint32_t* smp;               // [N] its sample
+  uint4* rec;                  // [N] each sorted position's token, sample and offset in G
   double* partials;            // [N, embed_norm_parts] squared run norms
-  float* blocks;               // [N / 16, D] sums of blocks of positions, or null
+  float* blocks;               // [N / 8, D] sums of blocks of positions, or null
   // clipped sum
   const float* c;              // [B]
   float noise_std;
@@ -117,8 +142,10 @@ constexpr int64_t kEmbedMaxD = (int64_t)1 << 22, kEmbedMaxTable = (int64_t)1 << 
 int64_t embed_hist_words(int64_t N, int64_t V);
 int64_t embed_block_floats(const EmbedArgs& a);
 int embed_norm_parts(const EmbedArgs& a);
-// Sorts the positions by (token, position); fills seg, off and smp.
+// Sorts the positions by (token, position); fills rec, empties seg.
 hipError_t launch_embed_sort(const EmbedArgs& a, hipStream_t s);
+// Fills seg, for calls that do not take the norms (which fill it too).
+hipError_t launch_embed_segments(const EmbedArgs& a, hipStream_t s);
 hipError_t launch_embed_norm(const EmbedArgs& a, hipStream_t s);
 hipError_t launch_embed_accumulate(const EmbedArgs& a, hipStream_t s);
 
