@@ -1769,7 +1769,15 @@ dpf_status dpfused_token_logprobs(const dpf_act* logits, const dpf_ids* targets,
   a.lse = lse;
   a.top_logp = top_logp;
   a.top_ids = top_ids;
-  const hipError_t e = dpf::launch_token_logprobs(a, static_cast<hipStream_t>(stream));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Workspace ws(s);
+  const size_t bytes = dpf::logprobs_workspace_bytes(a);
+  if (bytes != 0) {
+    const size_t at = ws.reserve(bytes);
+    if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+    a.ws = ws.at<void>(at);
+  }
+  const hipError_t e = dpf::launch_token_logprobs(a, s);
   if (e != hipSuccess) return hip_fail(e, "token log probabilities launch");
   return ok();
 }

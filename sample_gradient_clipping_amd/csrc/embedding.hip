@@ -703,9 +703,13 @@ __global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a) {
       for (int e = 0; e < 4; ++e) sum[u][e] = 0.f;
       old[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    // The result is read and written once: past the caches, which G needs.
     if (a.beta)
 #pragma unroll
-      for (int u = 0; u < U; ++u) old[u] = fetch(F32(), a.out + row0, u);
+      for (int u = 0; u < U; ++u) {
+        if constexpr (AL) old[u] = __builtin_nontemporal_load((const f32x4*)(a.out + row0 + in[u]));
+        else old[u] = fetch(F32(), a.out + row0, u);
+      }
     if (summed) {
       f32x4 x[U];
 #pragma unroll
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a) {
       if (col[u] >= D) continue;
       const int64_t e0 = row0 + col[u];
       if (a.noise_std != 0.0f) {
-        const f32x4 z = normals_of_block(philox_block(a.seed, a.offset + (uint64_t)(e0 >> 2)));
+        const f32x4 z = normals_of_block_hw(philox_block(a.seed, a.offset + (uint64_t)(e0 >> 2)));
         sum[u][0] += a.noise_std * z.x; sum[u][1] += a.noise_std * z.y;
         sum[u][2] += a.noise_std * z.z; sum[u][3] += a.noise_std * z.w;
       }
@@ -748,7 +752,7 @@ __global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a) {
       for (int e = 0; e < 4; ++e) sum[u][e] = old[u][e] + sum[u][e] * rd;
       float* o = a.out + e0;
       if (AL || (col[u] >= 0 && col[u] + 4 <= D)) {
-        store_f32<F32, 4>(o, sum[u]);
+        __builtin_nontemporal_store(f32x4{sum[u][0], sum[u][1], sum[u][2], sum[u][3]}, (f32x4*)o);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)

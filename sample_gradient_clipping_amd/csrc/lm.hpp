@@ -99,6 +99,23 @@ __device__ __forceinline__ void store_f32(typename E::storage* p, const float (&
   }
 }
 
+// The four normals of a Philox block, as normals_of_block, with the radius
+// through the hardware's logarithm and square root: over all 2^23 uniforms it
+// is within 4.9e-7 of the exact value (the library functions: 5.7e-7) in far
+// fewer instructions.  The hardware's sine and cosine are no replacement: near
+// their zeros they are off by 11 units of the last place.
+__device__ __forceinline__ f32x4 normals_of_block_hw(u32x4 w) {
+  constexpr float kM2Ln2 = -1.3862943611198906f;
+  const float r01 = __builtin_amdgcn_sqrtf(kM2Ln2 * __builtin_amdgcn_logf(word_to_uniform(w.x)));
+  const float r23 = __builtin_amdgcn_sqrtf(kM2Ln2 * __builtin_amdgcn_logf(word_to_uniform(w.z)));
+  float s1, c1, s3, c3;
+  sincospif(2.0f * word_to_uniform(w.y), &s1, &c1);
+  sincospif(2.0f * word_to_uniform(w.w), &s3, &c3);
+  f32x4 z;
+  z.x = r01 * c1; z.y = r01 * s1; z.z = r23 * c3; z.w = r23 * s3;
+  return z;
+}
+
 // Embedding (embedding.hip).
 struct LookupArgs {
   Ids ids;
@@ -162,7 +179,10 @@ struct LogprobArgs {
   float *logp, *entropy, *lse;   // [B, T] each, or null
   float* top_logp;          // [B, T, top_k]
   int32_t* top_ids;         // [B, T, top_k]
+  void* ws;                 // logprobs_workspace_bytes(a)
 };
+// Workspace of a call whose rows are split over workgroups (0: none).
+size_t logprobs_workspace_bytes(const LogprobArgs& a);
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s);
 
 struct LogprobGradArgs {
