@@ -645,10 +645,10 @@ __global__ void __launch_bounds__(256) embed_norm_kernel(EmbedArgs a, const uint
 #pragma unroll
     for (int j = 0; j < n; ++j) {
       const double keep = (lane & o) ? q[j + n] : q[j], give = (lane & o) ? q[j] : q[j + n];
-      q[j] = keep + __shfl_xor(give, o, 64);
+      q[j] = keep + lane_xor(give, o);
     }
 #pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) q[0] += __shfl_xor(q[0], o, 64);
+  for (int o = 4; o >= 1; o >>= 1) q[0] += lane_xor(q[0], o);
   const uint32_t at = __shfl(where, lane >> 3, 64);
   if ((lane & 7) == 0 && base + (lane >> 3) < N)
     a.partials[(int64_t)at * gridDim.y + blockIdx.y] = q[0] * (double)a.scale * (double)a.scale;

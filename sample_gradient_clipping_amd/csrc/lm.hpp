@@ -99,6 +99,40 @@ __device__ __forceinline__ void store_f32(typename E::storage* p, const float (&
   }
 }
 
+// The value of lane l ^ j (j a power of two known when compiled, every lane
+// active), without going through LDS as a shuffle does: within 16 lanes by
+// data-parallel moves, across them by gfx950's lane swaps.  A chain of 21
+// such steps sorts a wave, so their latency counts.
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v, int j) {
+  const uint32_t lane = threadIdx.x & 63;
+  switch (j) {
+    case 1: return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, true);   // quad 1 0 3 2
+    case 2: return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xf, 0xf, true);   // quad 2 3 0 1
+    case 4: {                                              // mirrored in 8, then in 4
+      const uint32_t h = __builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, true);
+      return __builtin_amdgcn_update_dpp(0, h, 0x1B, 0xf, 0xf, true);
+    }
+    case 8: return __builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, true);  // 16 rotated by 8
+    case 16: {
+      const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+      return (lane & 16) ? s[0] : s[1];
+    }
+    default: {
+      const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+      return (lane & 32) ? s[0] : s[1];
+    }
+  }
+}
+__device__ __forceinline__ int lane_xor(int v, int j) { return (int)lane_xor((uint32_t)v, j); }
+__device__ __forceinline__ float lane_xor(float v, int j) {
+  return __uint_as_float(lane_xor(__float_as_uint(v), j));
+}
+__device__ __forceinline__ double lane_xor(double v, int j) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = lane_xor((uint32_t)b, j), hi = lane_xor((uint32_t)(b >> 32), j);
+  return __builtin_bit_cast(double, (hi << 32) | lo);
+}
+
 // The four normals of a Philox block, as normals_of_block, with the radius
 // through the hardware's logarithm and square root: over all 2^23 uniforms it
 // is within 4.9e-7 of the exact value (the library functions: 5.7e-7) in far

@@ -87,8 +87,8 @@ __device__ __forceinline__ void sort_lanes(float& v, int& i) {
   for (int k = 2; k <= 64; k *= 2)
 #pragma unroll
     for (int j = k / 2; j >= 1; j /= 2) {
-      const float w = __shfl_xor(v, j, 64);
-      const int o = __shfl_xor(i, j, 64);
+      const float w = lane_xor(v, j);
+      const int o = lane_xor(i, j);
       const bool first = ((lane & j) == 0) == ((lane & k) == 0);   // keep the better one
       if (before(w, o, v, i) == first) { v = w; i = o; }
     }
@@ -101,7 +101,7 @@ __device__ __forceinline__ float kth_of_lanes(float v, int k) {
   for (int n = 2; n <= 64; n *= 2)
 #pragma unroll
     for (int j = n / 2; j >= 1; j /= 2) {
-      const float w = __shfl_xor(v, j, 64);
+      const float w = lane_xor(v, j);
       const bool most = ((lane & j) == 0) == ((lane & n) == 0);
       v = most ? fmaxf(v, w) : fminf(v, w);
     }
@@ -110,12 +110,12 @@ __device__ __forceinline__ float kth_of_lanes(float v, int k) {
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, lane_xor(v, o));
   return v;
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  for (int o = 32; o >= 1; o >>= 1) v += lane_xor(v, o);
   return v;
 }
 
@@ -219,6 +219,11 @@ struct RowPart {
 #pragma unroll
     for (int r = 0; r < kR; ++r)
       if (r < now)
+{
+        float most = raw_f32<E, kVec>(x[r], 0);   // few vectors hold one
+#pragma unroll
+        for (int e = 1; e < kVec; ++e) most = fmaxf(most, raw_f32<E, kVec>(x[r], e));
+        if (__ballot(above ? most > bound : most >= bound) == 0) continue;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           const float v = raw_f32<E, kVec>(x[r], e);
@@ -231,6 +236,7 @@ struct RowPart {
             count += __popcll(hit);
           }
         }
+      }
     if (count <= 64) {
       __builtin_amdgcn_wave_barrier();
       float v = kNegInf;
@@ -264,8 +270,8 @@ struct RowPart {
             }
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) {
-          const float ov = __shfl_xor(cv, o, 64);
-          const int oi = __shfl_xor(ci, o, 64);
+          const float ov = lane_xor(cv, o);
+          const int oi = lane_xor(ci, o);
           if (before(ov, oi, cv, ci)) { cv = ov; ci = oi; }
         }
         if (ci == kNoIndex) break;
