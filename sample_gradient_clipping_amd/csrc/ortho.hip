@@ -23,12 +23,29 @@
 // Layouts.  X stays as U is stored.  With R <= C the products contract X's
 // rows (K-inner operands) for A, and B X contracts over rows of X (K-outer
 // operands, B read as its own transpose).  With R > C it is the other way
-// round, so two kernels serve both shapes and nothing is ever transposed.
+// round, so two kernels serve both shapes and nothing is ever transposed.  In
+// memory the halves alternate, 16 hi and then the same 16 lo, so that a step
+// of 16 along K takes both from one place.  All dimensions are padded with
+// zeros to whole tiles.
+//
+// Product kernel.  Tiles of 256 x 256 on 8 waves (128 x 64 each) or 128 x 128
+// on 4 (64 x 64; two workgroups per compute unit), K in steps of 16.  A step's
+// operands go from memory to LDS directly (16 bytes a lane), into a ring of
+// five slots, four steps ahead; LDS chunks are permuted so that the fragment
+// reads hit every bank once.  Per step a wave reads its fragments one block
+// ahead of the MFMAs, 3 MFMAs per block and half pair: 24 (12) MFMAs on 12 (8)
+// fragments, so LDS is busy for two thirds of the MFMAs' time.  One barrier
+// per step, in its middle: it certifies that the next step has landed and that
+// every wave is done with the step before, whose slot is then refilled.
+//
+// The tiles of a product rarely fill the chip evenly: the workgroups share all
+// tiles' steps evenly instead, and a tile that two of them share is left as
+// float32 parts that a second kernel adds in order.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "lm.hpp"
-#include "tiles.hpp"
 
 namespace dpf {
 namespace {
@@ -36,9 +53,6 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kNT = 256;            // 4 waves, 2 x 2
-constexpr int kKT = 32;             // K per LDS step
-constexpr int kPad = 8;             // LDS row padding (halves)
 constexpr int kSumBlocks = 256;     // most workgroups of one matrix's norm
 
 __device__ __forceinline__ f32x16 mma16(const u16x8& a, const u16x8& b, const f32x16& c) {
@@ -46,27 +60,33 @@ __device__ __forceinline__ f32x16 mma16(const u16x8& a, const u16x8& b, const f3
                                                 __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Two half planes of a matrix, rows ld elements apart; the next matrix of the
-// stack starts `next` elements further.
+// A matrix as pairs of halves: element (r, c) at r ld + 2 (c - c % 16) + c % 16,
+// its lo part 16 further; the next matrix of the stack `next` further.
 struct Pair {
-  uint16_t *hi, *lo;
+  uint16_t* p;
   int64_t ld, next;
-  __device__ __forceinline__ Pair at(int64_t k) const { return Pair{hi + k * next, lo + k * next, ld, next}; }
+  __device__ __forceinline__ Pair at(int64_t k) const { return Pair{p + k * next, ld, next}; }
+  __device__ __forceinline__ uint16_t* elem(int64_t r, int64_t c) const {
+    return p + r * ld + 2 * c - (c & 15);
+  }
 };
 
-__device__ __forceinline__ void store_pair(const Pair& p, int64_t e, const float (&v)[4]) {
+// Four elements of a row (c a multiple of 4).
+__device__ __forceinline__ void store_pair(const Pair& p, int64_t r, int64_t c, const float (&v)[4]) {
   f16x4 h, l;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     h[k] = (_Float16)v[k];
     l[k] = (_Float16)(v[k] - (float)h[k]);
   }
-  *(f16x4*)(p.hi + e) = h;
-  *(f16x4*)(p.lo + e) = l;
+  uint16_t* e = p.elem(r, c);
+  *(f16x4*)e = h;
+  *(f16x4*)(e + 16) = l;
 }
 
-__device__ __forceinline__ void load_pair(const Pair& p, int64_t e, float (&v)[4]) {
-  const f16x4 h = *(const f16x4*)(p.hi + e), l = *(const f16x4*)(p.lo + e);
+__device__ __forceinline__ void load_pair(const Pair& p, int64_t r, int64_t c, float (&v)[4]) {
+  const uint16_t* e = p.elem(r, c);
+  const f16x4 h = *(const f16x4*)e, l = *(const f16x4*)(e + 16);
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = (float)h[k] + (float)l[k];
 }
@@ -107,8 +127,8 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(OrthoArgs a, double* pa
 constexpr int kMaxUnit = 100;
 template <class E, bool MUON>
 __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoArgs a, const double* part, int nb,
-                                                          Pair X, int64_t Rp, float pow_x,
-                                                          float* unit) {
+                                                          Pair X, int64_t Rp, int64_t Cp,
+                                                          float pow_x, float* unit) {
   __shared__ double scale;
   if (threadIdx.x < 64) {
     double sq = 0.0;
@@ -134,16 +154,16 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoArgs a, const dou
   __syncthreads();
   const double f = scale;
   const Pair x = X.at(blockIdx.y);
-  const int64_t total = Rp * X.ld / 4, base = (int64_t)blockIdx.y * a.R * a.C;
+  const int64_t total = Rp * Cp / 4, base = (int64_t)blockIdx.y * a.R * a.C;
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
-    const int64_t r = 4 * q / X.ld, c = 4 * q - r * X.ld;
+    const int64_t r = 4 * q / Cp, c = 4 * q - r * Cp;
     float v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       v[k] = r < a.R && c + k < a.C
                  ? (float)((double)update_at<E, MUON>(a, base + r * a.C + c + k) * f)
                  : 0.f;
-    store_pair(x, 4 * q, v);
+    store_pair(x, r, c, v);
   }
 }
 
@@ -159,8 +179,12 @@ enum Mode {
 };
 struct ProductArgs {
   Pair L, R, add, out;
-  int64_t K;
+  int steps;              // K / 16
   int mt, nt;             // tiles of M and N (symmetric: mt == nt)
+  int tiles;              // per matrix
+  int64_t total;          // steps of all tiles of all matrices
+  int groups;             // workgroups that share them
+  float* parts;           // [2 groups][tile] float32 parts of shared tiles
   int sym, mode, dtype;
   float f0, f1;
   const float* unit;      // [n] 1 / unit of each matrix's X
@@ -172,155 +196,401 @@ struct ProductArgs {
   float decay, size;
 };
 
-// Chunk q of an operand's TILE x kKT slice, in global memory and in LDS.
+constexpr int kSlots = 5;
+constexpr int kAhead = 4;            // steps between a slot's load and its use
+constexpr int kDmaPerStep = 4;       // of one wave: two per operand
+
+template <int TILE>
+struct Shape {
+  static constexpr int kWaves = TILE == 256 ? 8 : 4;
+  static constexpr int kNT = kWaves * 64;
+  static constexpr int kWR = 2, kWC = kWaves / 2;           // wave grid, M by N
+  static constexpr int kBA = TILE / kWR / 32, kBO = TILE / kWC / 32;   // 32 x 32 blocks of a wave
+  static constexpr int kOpBytes = TILE * 64;                // one operand's step
+  static constexpr int kSlotBytes = 2 * kOpBytes;
+  static constexpr int kLds = kSlots * kSlotBytes;
+  static constexpr int kFloats = TILE * TILE;               // one tile's accumulators
+  static_assert(kOpBytes == 2 * 1024 * kWaves, "two 1 KiB loads per wave and operand");
+};
+
+// 16 bytes per lane from rsrc at voffset straight into LDS at m0 + 16 * lane;
+// awaited explicitly (wait_dma).
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voffset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(voffset), "s"(rsrc), "s"(lds)
+               : "memory");
+}
+
+// Until at most `steps` of this wave's latest steps are in flight.
+__device__ __forceinline__ void wait_dma(int steps) {
+  static_assert(kDmaPerStep == 4, "the counts below");
+  if (steps <= 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  else if (steps == 1) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+  else if (steps == 2) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+}
+
+// A barrier without the compiler's wait for every outstanding LDS read: what
+// other waves may overwrite after it has been used by MFMAs before it.
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char*)p;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7fffffff, 0x00020000);
+}
+
+// LDS image of one operand's step, and its loads.
+//   K-inner: [TILE rows][64 bytes]: k 0-7 hi, 8-15 hi, 0-7 lo, 8-15 lo, 16-byte
+//            chunk c of row r at c ^ ((r >> 2) & 3).
+//   K-outer: [16 k][TILE columns, 64 bytes per 16]: the chunk's index with its
+//            bits 2 and 3 inverted by k's low bits (four rows of a transposing
+//            read fall on different banks) and the hi/lo bit by bit 2 (so do
+//            the two 16-column halves of a block).
 template <int TILE, bool KI>
-struct Slice {
-  static constexpr int kCpr = (KI ? kKT : TILE) / 8;
-  static constexpr int kLd = (KI ? kKT : TILE) + kPad;
-  static constexpr int kPlane = (KI ? TILE : kKT) * kLd;     // halves
-  static constexpr int kN = TILE * kKT / 8 / kNT;
-  u32x4 h[kN], l[kN];
-  __device__ __forceinline__ void load(const Pair& p, int64_t m0, int64_t k0) {
+struct Operand {
+  using S = Shape<TILE>;
+  const char* base;               // this tile's next step
+  int64_t step;                   // bytes between steps
+  uint32_t off[2];                // per lane: the wave's two loads
+  __device__ __forceinline__ void start(const Pair& p, int64_t m0, int64_t k0) {
+    const int64_t ldb = p.ld * 2;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    base = (const char*)p.p + (KI ? m0 * ldb + k0 * 64 : m0 * 4 + k0 * 16 * ldb);
+    step = KI ? 64 : 16 * ldb;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int q = threadIdx.x + kNT * i, row = q / kCpr, cc = q % kCpr;
-      const int64_t e = KI ? (m0 + row) * p.ld + k0 + cc * 8 : (k0 + row) * p.ld + m0 + cc * 8;
-      h[i] = *(const u32x4*)(p.hi + e);
-      l[i] = *(const u32x4*)(p.lo + e);
+    for (int j = 0; j < 2; ++j) {
+      const int d = wave * 2 + j;
+      if constexpr (KI) {
+        const int row = d * 16 + (lane >> 2), c = (lane & 3) ^ ((row >> 2) & 3);
+        off[j] = (uint32_t)(row * ldb + c * 16);
+      } else {
+        constexpr int kCpr = TILE / 4;
+        const int k = (d * 64 + lane) / kCpr, q = ((d * 64 + lane) % kCpr) ^ ((k & 3) << 2);
+        off[j] = (uint32_t)(k * ldb + (q ^ (((q >> 2) & 1) << 1)) * 16);
+      }
     }
   }
-  __device__ __forceinline__ void store(uint16_t* lds) const {
+  __device__ __forceinline__ void load(uint32_t lds) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const __amdgpu_buffer_rsrc_t r = rsrc_of(base);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int q = threadIdx.x + kNT * i, row = q / kCpr, cc = q % kCpr;
-      *(u32x4*)(lds + row * kLd + cc * 8) = h[i];
-      *(u32x4*)(lds + kPlane + row * kLd + cc * 8) = l[i];
-    }
-  }
-  static __device__ __forceinline__ u16x8 frag(const uint16_t* plane, int m0, int ks) {
-    if constexpr (KI) return frag_kinner<BF16, kLd>(plane, m0, ks);
-    else return frag_kouter<BF16, kLd>(plane, m0, ks);
+    for (int j = 0; j < 2; ++j) dma16(r, off[j], lds + (uint32_t)(wave * 2 + j) * 1024u);
+    base += step;
   }
 };
 
+// This lane's fragment reads of an operand: blocks of 32 from block `b0` on
+// (even), the hi half at the address and lo at address ^ 32.
 template <int TILE, bool KI>
-constexpr int product_lds() { return 2 * 4 * Slice<TILE, KI>::kPlane * 2; }
+struct FragLane {
+  uint32_t even, odd;             // for blocks b0 + 0, 2, .. and b0 + 1, 3, ..
+  __device__ __forceinline__ void start(int b0) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (KI) {
+      const int c = (lane >> 5) ^ ((lane >> 2) & 3);
+      even = odd = (uint32_t)(b0 * 2048 + (lane & 31) * 64 + c * 16);
+    } else {
+      const int k = 8 * (lane >> 5) + ((lane & 15) >> 2), kb = (k >> 1) & 1;
+      const int lp = ((lane >> 4) & 1) * 4 + ((lane & 3) >> 1);
+      const int c = lp ^ (((lp >> 2) & 1) << 1) ^ ((k & 1) << 2);
+      const uint32_t at = (uint32_t)(k * TILE * 4 + b0 * 128 + c * 16 + (lane & 1) * 8);
+      even = at + (uint32_t)(kb * 128);
+      odd = at - (uint32_t)(kb * 128);
+    }
+  }
+  template <int I>
+  __device__ __forceinline__ u16x8 read(const unsigned char* op, bool lo) const {
+    const uint32_t at = ((I & 1) ? odd : even) ^ (lo ? 32u : 0u);
+    if constexpr (KI) {
+      return *(const u16x8*)(op + at + I * 2048);
+    } else {
+      const u16x4 a = lds_read_tr16((const uint16_t*)(op + at + I * 128));
+      const u16x4 b = lds_read_tr16((const uint16_t*)(op + at + I * 128 + 4 * TILE * 4));
+      u16x8 f;
+      f.s0 = a.s0; f.s1 = a.s1; f.s2 = a.s2; f.s3 = a.s3;
+      f.s4 = b.s0; f.s5 = b.s1; f.s6 = b.s2; f.s7 = b.s3;
+      return f;
+    }
+  }
+};
 
-template <int TILE, bool KI>
-__global__ void __launch_bounds__(kNT) ortho_product_kernel(ProductArgs p) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
-  using S = Slice<TILE, KI>;
-  constexpr int NB = TILE / 64;
-  const int tiles = p.sym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
-  const int64_t mat = blockIdx.x / tiles;
-  int t = blockIdx.x % tiles, ti, tj;
-  if (p.sym) {           // row by row of the upper triangle
-    ti = 0;
-    while (t >= p.mt - ti) { t -= p.mt - ti; ++ti; }
-    tj = ti + t;
-  } else {
-    ti = t / p.nt;
-    tj = t % p.nt;
-  }
-  const Pair Lp = p.L.at(mat), Rp = p.R.at(mat);
-  const int64_t m0 = (int64_t)ti * TILE, n0 = (int64_t)tj * TILE;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, wm = wave >> 1, wn = wave & 1;
-  f32x16 acc[NB][NB];
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  S sl, sr;
-  sl.load(Lp, m0, 0);
-  sr.load(Rp, n0, 0);
-  sl.store(lds);
-  sr.store(lds + 2 * S::kPlane);
-  __syncthreads();
-  const int64_t nk = p.K / kKT;
-  for (int64_t kk = 0; kk < nk; ++kk) {
-    const bool more = kk + 1 < nk;
-    if (more) {
-      sl.load(Lp, m0, (kk + 1) * kKT);
-      sr.load(Rp, n0, (kk + 1) * kKT);
-    }
-    const uint16_t* buf = lds + (kk & 1) * 4 * S::kPlane;
-#pragma unroll
-    for (int ks = 0; ks < kKT / 16; ++ks) {
-      u16x8 lh[NB], ll[NB], rh[NB], rl[NB];
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        lh[i] = S::frag(buf, (wm * NB + i) * 32, ks);
-        ll[i] = S::frag(buf + S::kPlane, (wm * NB + i) * 32, ks);
-        rh[i] = S::frag(buf + 2 * S::kPlane, (wn * NB + i) * 32, ks);
-        rl[i] = S::frag(buf + 3 * S::kPlane, (wn * NB + i) * 32, ks);
+// Tile t of a matrix: groups of four tile rows, within them column by column,
+// so that the tiles in flight on one XCD share operand strips in its L2; with
+// `sym` those on and above the diagonal.
+__device__ __forceinline__ void tile_of(const ProductArgs& p, int t, int* ti, int* tj) {
+  int r0 = 0;
+  for (;;) {
+    const int h = min(4, p.mt - r0);
+    const int count = p.sym ? h * (p.nt - r0) - h * (h - 1) / 2 : h * p.nt;
+    if (t < count) {
+      if (!p.sym) {
+        *ti = r0 + t % h;
+        *tj = t / h;
+        return;
       }
-      // the N side is the MFMA's row operand: a lane's accumulators are then
-      // runs of four columns of one row of D
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          acc[i][j] = mma16(rl[j], lh[i], acc[i][j]);
-          acc[i][j] = mma16(rh[j], ll[i], acc[i][j]);
-          acc[i][j] = mma16(rh[j], lh[i], acc[i][j]);
-        }
+      const int head = h * (h + 1) / 2;          // the triangle at the diagonal
+      if (t < head) {
+        int j = 0;
+        while (t > j) { t -= j + 1; ++j; }
+        *ti = r0 + t;
+        *tj = r0 + j;
+      } else {
+        *ti = r0 + (t - head) % h;
+        *tj = r0 + h + (t - head) / h;
+      }
+      return;
     }
-    if (!more) break;
-    uint16_t* next = lds + ((kk + 1) & 1) * 4 * S::kPlane;
-    sl.store(next);
-    sr.store(next + 2 * S::kPlane);
-    __syncthreads();
+    t -= count;
+    r0 += h;
   }
-  const Pair add = p.add.at(mat), out = p.out.at(mat);
+}
+
+__device__ __forceinline__ int64_t first_step(const ProductArgs& p, int w) {
+  return p.total * w / p.groups;
+}
+
+// Workgroups go round the eight XCDs; each XCD takes a contiguous share.
+__device__ __forceinline__ int logical_group(int id, int groups) {
+  const int q = groups / 8, r = groups % 8, x = id % 8;
+  return x * q + min(x, r) + id / 8;
+}
+
+// Block (i, j) of a wave's part of a tile: scaled, added and stored.
+template <int TILE>
+__device__ __forceinline__ void finish_block(const ProductArgs& p, int64_t mat, int ti, int tj,
+                                             int i, int j, const f32x16& acc) {
+  using S = Shape<TILE>;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wm = wave / S::kWC, wn = wave % S::kWC;
+  const int64_t r = (int64_t)ti * TILE + (wm * S::kBA + i) * 32 + acc_col(lane);
+  const int64_t c0 = (int64_t)tj * TILE + (wn * S::kBO + j) * 32;
   float f0 = p.f0, f1 = p.f1;
   for (int k = 0; k < p.units; ++k) { f0 *= p.unit[mat]; f1 *= p.unit[mat]; }
+  const Pair add = p.add.at(mat), out = p.out.at(mat);
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+  for (int g = 0; g < 4; ++g) {
+    const int64_t c = c0 + acc_row(4 * g, lane);
+    float v[4];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int64_t r = m0 + (wm * NB + i) * 32 + acc_col(lane);
+    for (int k = 0; k < 4; ++k) v[k] = f1 * acc[4 * g + k];
+    if (p.mode != kStore) {
+      float w[4];
+      load_pair(add, r, c, w);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t c = n0 + (wn * NB + j) * 32 + acc_row(4 * g, lane);
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = f1 * acc[i][j][4 * g + k];
-        if (p.mode != kStore) {
-          float w[4];
-          load_pair(add, r * add.ld + c, w);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] += f0 * w[k];
-        }
-        if (p.mode != kFinal) {
-          store_pair(out, r * out.ld + c, v);
-          if (p.sym && ti != tj) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const _Float16 h = (_Float16)v[k], l = (_Float16)(v[k] - (float)h);
-              out.hi[(c + k) * out.ld + r] = __builtin_bit_cast(uint16_t, h);
-              out.lo[(c + k) * out.ld + r] = __builtin_bit_cast(uint16_t, l);
-            }
-          }
-          continue;
-        }
-        if (r >= p.rows) continue;
-        const int64_t e = (mat * p.rows + r) * p.cols + c;
+      for (int k = 0; k < 4; ++k) v[k] += f0 * w[k];
+    }
+    if (p.mode != kFinal) {
+      store_pair(out, r, c, v);
+      if (p.sym && ti != tj) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (c + k >= p.cols) break;
-          if (p.muon) {
-            float* w = (float*)p.dst + e + k;
-            *w = p.decay * *w - p.size * v[k];
-          } else if (p.dtype == kBF16) {
-            ((uint16_t*)p.dst)[e + k] = f32_to_bf16_rne(v[k]);
-          } else {
-            ((float*)p.dst)[e + k] = v[k];
-          }
+          const _Float16 h = (_Float16)v[k], l = (_Float16)(v[k] - (float)h);
+          uint16_t* e = out.elem(c + k, r);
+          e[0] = __builtin_bit_cast(uint16_t, h);
+          e[16] = __builtin_bit_cast(uint16_t, l);
         }
       }
+      continue;
     }
+    if (r >= p.rows) continue;
+    const int64_t e = (mat * p.rows + r) * p.cols + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (c + k >= p.cols) break;
+      if (p.muon) {
+        float* w = (float*)p.dst + e + k;
+        *w = p.decay * *w - p.size * v[k];
+      } else if (p.dtype == kBF16) {
+        ((uint16_t*)p.dst)[e + k] = f32_to_bf16_rne(v[k]);
+      } else {
+        ((float*)p.dst)[e + k] = v[k];
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
+
+template <int TILE, bool KI>
+__global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(ProductArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
+  using S = Shape<TILE>;
+  constexpr int BA = S::kBA, BO = S::kBO;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = logical_group(blockIdx.x, p.groups);
+  const int64_t s0 = first_step(p, w), s1 = first_step(p, w + 1);
+  FragLane<TILE, KI> fl, fr;
+  fl.start(wave / S::kWC * BA);
+  fr.start(wave % S::kWC * BO);
+  const uint32_t lds0 = lds_addr(lds);
+  bool first = true;
+  for (int64_t at = s0; at < s1;) {
+    const int64_t tile = at / p.steps, mat = tile / p.tiles;
+    const int k0 = (int)(at - tile * p.steps);
+    const int n = (int)min((int64_t)(p.steps - k0), s1 - at);    // steps of this piece
+    int ti, tj;
+    tile_of(p, (int)(tile - mat * p.tiles), &ti, &tj);
+    Operand<TILE, KI> ol, orr;
+    ol.start(p.L.at(mat), (int64_t)ti * TILE, k0);
+    orr.start(p.R.at(mat), (int64_t)tj * TILE, k0);
+    f32x16 acc[BA][BO];
+#pragma unroll
+    for (int i = 0; i < BA; ++i)
+#pragma unroll
+      for (int j = 0; j < BO; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    if (!first) __syncthreads();                 // the last piece's slots are read
+    auto issue = [&](int s) {
+      const uint32_t slot = lds0 + (uint32_t)(s % kSlots) * S::kSlotBytes;
+      ol.load(slot);
+      orr.load(slot + S::kOpBytes);
+    };
+    const int ahead = min(kAhead, n);
+    for (int s = 0; s < ahead; ++s) issue(s);
+    wait_dma(ahead - 1);
+    step_barrier();
+    u16x8 L[2][2], R[2][BO][2];                  // [buffer][hi, lo]; R by block
+    int slot = 0;
+    L[0][0] = fl.template read<0>(lds, false);
+    L[0][1] = fl.template read<0>(lds, true);
+    R[0][0][0] = fr.template read<0>(lds + S::kOpBytes, false);
+    R[0][0][1] = fr.template read<0>(lds + S::kOpBytes, true);
+    R[0][1][0] = fr.template read<1>(lds + S::kOpBytes, false);
+    R[0][1][1] = fr.template read<1>(lds + S::kOpBytes, true);
+    // One step; PAR: its buffer of R.  Block row i's products run while block
+    // row i + 1's fragments (from the middle on also the next step's) are read.
+    auto step = [&](int t, auto par) {
+      constexpr int PAR = decltype(par)::value;
+      const unsigned char* cur = lds + slot * S::kSlotBytes;
+      const int nslot = slot + 1 == kSlots ? 0 : slot + 1;
+      const unsigned char* next = lds + nslot * S::kSlotBytes;
+      const bool more = t + 1 < n;
+      auto products = [&](int i, const u16x8 (&l)[2]) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)              // lo hi, hi lo, hi hi
+#pragma unroll
+          for (int j = 0; j < BO; ++j)
+            acc[i][j] = mma16(R[PAR][j][q == 0 ? 1 : 0], l[q == 1 ? 1 : 0], acc[i][j]);
+      };
+      auto middle = [&]() {
+        if (more) {
+          wait_dma(min(n - 2 - t, kAhead - 2));
+          step_barrier();
+          if (t + kAhead < n) issue(t + kAhead);
+        }
+      };
+      if constexpr (BA == 4) {
+        L[1][0] = fl.template read<1>(cur, false);
+        L[1][1] = fl.template read<1>(cur, true);
+        sched_fence();
+        products(0, L[0]);
+        sched_fence();
+        L[0][0] = fl.template read<2>(cur, false);
+        L[0][1] = fl.template read<2>(cur, true);
+        sched_fence();
+        products(1, L[1]);
+        sched_fence();
+        L[1][0] = fl.template read<3>(cur, false);
+        L[1][1] = fl.template read<3>(cur, true);
+        sched_fence();
+        middle();
+        if (more) {
+          R[PAR ^ 1][0][0] = fr.template read<0>(next + S::kOpBytes, false);
+          R[PAR ^ 1][0][1] = fr.template read<0>(next + S::kOpBytes, true);
+        }
+        sched_fence();
+        products(2, L[0]);
+        sched_fence();
+        if (more) {
+          L[0][0] = fl.template read<0>(next, false);
+          L[0][1] = fl.template read<0>(next, true);
+          R[PAR ^ 1][1][0] = fr.template read<1>(next + S::kOpBytes, false);
+          R[PAR ^ 1][1][1] = fr.template read<1>(next + S::kOpBytes, true);
+        }
+        sched_fence();
+        products(3, L[1]);
+        sched_fence();
+      } else {
+        L[1][0] = fl.template read<1>(cur, false);
+        L[1][1] = fl.template read<1>(cur, true);
+        sched_fence();
+        products(0, L[0]);
+        sched_fence();
+        middle();
+        if (more) {
+          L[0][0] = fl.template read<0>(next, false);
+          L[0][1] = fl.template read<0>(next, true);
+          R[PAR ^ 1][0][0] = fr.template read<0>(next + S::kOpBytes, false);
+          R[PAR ^ 1][0][1] = fr.template read<0>(next + S::kOpBytes, true);
+          R[PAR ^ 1][1][0] = fr.template read<1>(next + S::kOpBytes, false);
+          R[PAR ^ 1][1][1] = fr.template read<1>(next + S::kOpBytes, true);
+        }
+        sched_fence();
+        products(1, L[1]);
+        sched_fence();
+      }
+      slot = nslot;
+    };
+    for (int t = 0; t < n; t += 2) {
+      step(t, std::integral_constant<int, 0>());
+      if (t + 1 < n) step(t + 1, std::integral_constant<int, 1>());
+    }
+    if (n == p.steps) {
+#pragma unroll
+      for (int i = 0; i < BA; ++i)
+#pragma unroll
+        for (int j = 0; j < BO; ++j) finish_block<TILE>(p, mat, ti, tj, i, j, acc[i][j]);
+    } else {
+      // part: four accumulators of every thread side by side
+      float* o = p.parts + (int64_t)(2 * w + (first ? 0 : 1)) * S::kFloats + threadIdx.x * 4;
+#pragma unroll
+      for (int i = 0; i < BA; ++i)
+#pragma unroll
+        for (int j = 0; j < BO; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            *(f32x4*)(o + ((i * BO + j) * 4 + g) * S::kNT * 4) =
+                f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    }
+    first = false;
+    at += n;
+  }
+}
+
+// The tiles that workgroups share: their parts in order, then as above.  One
+// workgroup per first inner boundary of a tile and block of its waves.
+template <int TILE>
+__global__ void __launch_bounds__(Shape<TILE>::kNT) ortho_fixup_kernel(ProductArgs p) {
+  using S = Shape<TILE>;
+  const int b = blockIdx.x + 1, block = blockIdx.y;
+  const int64_t s = first_step(p, b), tile = s / p.steps, begin = tile * p.steps;
+  if (s == begin || first_step(p, b - 1) > begin) return;
+  f32x16 acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  for (int w = b - 1; w < p.groups && first_step(p, w) < begin + p.steps; ++w) {
+    const float* o = p.parts + (int64_t)(2 * w + (first_step(p, w) >= begin ? 0 : 1)) * S::kFloats +
+                     threadIdx.x * 4 + (int64_t)block * 4 * S::kNT * 4;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 x = *(const f32x4*)(o + g * S::kNT * 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[4 * g + k] += x[k];
+    }
+  }
+  const int64_t mat = tile / p.tiles;
+  int ti, tj;
+  tile_of(p, (int)(tile - mat * p.tiles), &ti, &tj);
+  finish_block<TILE>(p, mat, ti, tj, block / S::kBO, block % S::kBO, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -369,44 +639,97 @@ struct Plan {
   int tile;
   int64_t m, Rp, Cp, mp;       // padded
   int nb;                      // norm workgroups per matrix
-  size_t x, a, part, unit, total;   // bytes of one X pair, one A pair; offsets
+  int groups_sym, groups_full, groups_square;
+  size_t x, a, part, unit, parts, total;   // bytes of one X pair, one A pair; offsets
 };
 
 int64_t up(int64_t v, int64_t t) { return (v + t - 1) / t * t; }
 
+// Workgroups that run at once.
+int resident(int tile) { return device_cus() * (tile == 256 ? 1 : 2); }
+
+// Workgroups that share `tiles` tiles of `steps` steps: one per tile, or as
+// many as run at once where sharing the tiles' steps evenly is shorter by
+// more than the parts cost (about 12 steps); no fewer than 8 steps each.
+int groups_of(int64_t tiles, int64_t steps, int tile) {
+  const int64_t g = std::min<int64_t>(resident(tile), std::max<int64_t>(1, tiles * steps / 8));
+  const int64_t whole = (tiles + resident(tile) - 1) / resident(tile) * steps;
+  const int64_t shared = (tiles * steps + g - 1) / g + 12;
+  return (int)(shared < whole ? g : tiles);
+}
+
+int64_t sym_tiles(int64_t mt) { return mt * (mt + 1) / 2; }
+
+void plan_tiles(Plan& p, const OrthoArgs& a, int tile) {
+  p.tile = tile;
+  p.Rp = up(a.R, tile);
+  p.Cp = up(a.C, tile);
+  p.mp = up(p.m, tile);
+  const int64_t mt = p.mp / tile, k = (p.flip ? p.Rp : p.Cp) / 16;
+  p.groups_sym = groups_of(a.n * sym_tiles(mt), k, tile);
+  p.groups_square = groups_of(a.n * sym_tiles(mt), p.mp / 16, tile);
+  p.groups_full = groups_of(a.n * (p.Rp / tile) * (p.Cp / tile), p.mp / 16, tile);
+}
+
+// Time of an iteration in steps of a 128 x 128 tile with its neighbour.
+double plan_cost(const Plan& p, const OrthoArgs& a) {
+  const int64_t mt = p.mp / p.tile, k = (p.flip ? p.Rp : p.Cp) / 16, g = resident(p.tile);
+  auto rounds = [&](int64_t tiles, int64_t steps, int groups) {
+    return groups == tiles ? (double)((tiles + g - 1) / g * steps) : (double)(tiles * steps) / groups + 12;
+  };
+  const double steps = rounds(a.n * sym_tiles(mt), k, p.groups_sym) +
+                       rounds(a.n * sym_tiles(mt), p.mp / 16, p.groups_square) +
+                       rounds(a.n * (p.Rp / p.tile) * (p.Cp / p.tile), p.mp / 16, p.groups_full);
+  return steps * (p.tile == 256 ? 1.8 : 1.0);
+}
+
 Plan plan_of(const OrthoArgs& a) {
-  Plan p;
+  Plan p{};
   p.flip = a.R > a.C;
   p.m = std::min(a.R, a.C);
-  const int64_t t128 = up(a.R, 128) / 128 * (up(a.C, 128) / 128) * a.n;
-  p.tile = t128 >= device_cus() ? 128 : 64;
-  p.Rp = up(a.R, p.tile);
-  p.Cp = up(a.C, p.tile);
-  p.mp = up(p.m, p.tile);
+  plan_tiles(p, a, 256);
+  const double large = plan_cost(p, a);
+  plan_tiles(p, a, 128);
+  if (large < plan_cost(p, a)) plan_tiles(p, a, 256);
   p.nb = (int)std::min<int64_t>(kSumBlocks, (a.R * a.C + 4095) / 4096);
   p.x = (size_t)(a.n * p.Rp * p.Cp) * 4;
   p.a = (size_t)(a.n * p.mp * p.mp) * 4;
   p.part = 2 * p.x + 2 * p.a;
   p.unit = p.part + (size_t)a.n * p.nb * sizeof(double);
-  p.total = p.unit + (size_t)a.n * sizeof(float);
+  p.parts = (size_t)up((int64_t)(p.unit + (size_t)a.n * sizeof(float)), 256);
+  const int64_t mt = p.mp / p.tile, full = (p.Rp / p.tile) * (p.Cp / p.tile);
+  int64_t shared = 0;          // the most workgroups of a product that shares tiles
+  if (p.groups_sym != a.n * sym_tiles(mt)) shared = std::max<int64_t>(shared, p.groups_sym);
+  if (p.groups_square != a.n * sym_tiles(mt)) shared = std::max<int64_t>(shared, p.groups_square);
+  if (p.groups_full != a.n * full) shared = std::max<int64_t>(shared, p.groups_full);
+  p.total = p.parts + (size_t)(2 * shared) * p.tile * p.tile * sizeof(float);
   return p;
 }
 
 template <int TILE, bool KI>
-hipError_t launch_product_t(const ProductArgs& p, int64_t n, hipStream_t s) {
+hipError_t launch_product_t(const ProductArgs& p, int64_t tiles, hipStream_t s) {
+  using S = Shape<TILE>;
   static hipError_t once = hipFuncSetAttribute((const void*)ortho_product_kernel<TILE, KI>,
-                                               hipFuncAttributeMaxDynamicSharedMemorySize,
-                                               product_lds<TILE, KI>());
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (once != hipSuccess) return once;
-  const int64_t tiles = p.sym ? (int64_t)p.mt * (p.mt + 1) / 2 : (int64_t)p.mt * p.nt;
-  hipLaunchKernelGGL((ortho_product_kernel<TILE, KI>), dim3((unsigned)(tiles * n)), dim3(kNT),
-                     (product_lds<TILE, KI>()), s, p);
+  hipLaunchKernelGGL((ortho_product_kernel<TILE, KI>), dim3((unsigned)p.groups), dim3(S::kNT), S::kLds,
+                     s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.groups == tiles) return e;
+  hipLaunchKernelGGL(ortho_fixup_kernel<TILE>, dim3((unsigned)(p.groups - 1), S::kBA * S::kBO),
+                     dim3(S::kNT), 0, s, p);
   return hipGetLastError();
 }
 
-hipError_t launch_product(const ProductArgs& p, int tile, bool ki, int64_t n, hipStream_t s) {
-  if (tile == 128) return ki ? launch_product_t<128, true>(p, n, s) : launch_product_t<128, false>(p, n, s);
-  return ki ? launch_product_t<64, true>(p, n, s) : launch_product_t<64, false>(p, n, s);
+hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int groups, hipStream_t s) {
+  p.tiles = p.sym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
+  const int64_t tiles = p.tiles * n;
+  p.total = tiles * p.steps;
+  p.groups = groups;
+  if (groups == 1 && tiles > 1) return hipErrorInvalidValue;
+  if (tile == 256)
+    return ki ? launch_product_t<256, true>(p, tiles, s) : launch_product_t<256, false>(p, tiles, s);
+  return ki ? launch_product_t<128, true>(p, tiles, s) : launch_product_t<128, false>(p, tiles, s);
 }
 
 template <class E, bool MUON>
@@ -418,7 +741,7 @@ hipError_t launch_input(const OrthoArgs& a, const Plan& p, double* part, float* 
   if (e != hipSuccess) return e;
   const int64_t blocks = std::min<int64_t>(2048, (p.Rp * p.Cp / 4 + 255) / 256);
   hipLaunchKernelGGL((ortho_split_kernel<E, MUON>), dim3((unsigned)blocks, (unsigned)a.n), dim3(256),
-                     0, s, a, (const double*)part, p.nb, X, p.Rp, pow_x, unit);
+                     0, s, a, (const double*)part, p.nb, X, p.Rp, p.Cp, pow_x, unit);
   return hipGetLastError();
 }
 
@@ -439,11 +762,10 @@ size_t ortho_workspace_bytes(const OrthoArgs& a) { return plan_of(a).total; }
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   const Plan p = plan_of(a);
   char* ws = (char*)a.ws;
-  auto pair = [&](size_t off, int64_t rows, int64_t ld) {
-    uint16_t* hi = (uint16_t*)(ws + off);
-    return Pair{hi, hi + a.n * rows * ld, ld, rows * ld};
+  auto pair = [&](size_t off, int64_t rows, int64_t cols) {
+    return Pair{(uint16_t*)(ws + off), 2 * cols, 2 * rows * cols};
   };
-  Pair X[2] = {pair(0, p.Rp, p.Cp), pair(p.x, p.Rp, p.Cp)};
+  const Pair X[2] = {pair(0, p.Rp, p.Cp), pair(p.x, p.Rp, p.Cp)};
   const Pair A = pair(2 * p.x, p.mp, p.mp), B = pair(2 * p.x + p.a, p.mp, p.mp);
   double* part = (double*)(ws + p.part);
   float* unit = (float*)(ws + p.unit);
@@ -464,29 +786,30 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     const int sn = last ? 0 : scale_of(kRoom * top);
     ProductArgs q{};
     q.unit = unit;
+    q.parts = (float*)(ws + p.parts);
     // A = X X^T (R <= C: K-inner) or X^T X (K-outer)
     q.L = q.R = Xk;
     q.out = q.add = A;
-    q.K = p.flip ? p.Rp : p.Cp;
+    q.steps = (int)((p.flip ? p.Rp : p.Cp) / 16);
     q.mt = q.nt = mt;
     q.sym = 1;
     q.mode = kStore;
     q.units = 2;
     q.f1 = (float)std::ldexp(1.0, sa - 2 * sx);
     timing_begin("ortho_gram", s);
-    e = launch_product(q, p.tile, !p.flip, a.n, s);
+    e = launch_product(q, p.tile, !p.flip, a.n, p.groups_sym, s);
     timing_end("ortho_gram", s);
     if (e != hipSuccess) break;
     // B = b A + c A A
     q.L = q.R = q.add = A;
     q.out = B;
-    q.K = p.mp;
+    q.steps = (int)(p.mp / 16);
     q.mode = kAddStore;
     q.units = 0;
     q.f0 = (float)(a.b * std::ldexp(1.0, sb - sa));
     q.f1 = (float)(a.c * std::ldexp(1.0, sb - 2 * sa));
     timing_begin("ortho_square", s);
-    e = launch_product(q, p.tile, !p.flip, a.n, s);
+    e = launch_product(q, p.tile, !p.flip, a.n, p.groups_square, s);
     timing_end("ortho_square", s);
     if (e != hipSuccess) break;
     // X <- a X + B X (K-outer) or a X + X B (K-inner)
@@ -509,7 +832,7 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     q.decay = a.decay;
     q.size = a.size;
     timing_begin("ortho_apply", s);
-    e = launch_product(q, p.tile, p.flip, a.n, s);
+    e = launch_product(q, p.tile, p.flip, a.n, p.groups_full, s);
     timing_end("ortho_apply", s);
     sx = sn;
   }
