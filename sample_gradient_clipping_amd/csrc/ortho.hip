@@ -38,9 +38,8 @@
 // per step, in its middle: it certifies that the next step has landed and that
 // every wave is done with the step before, whose slot is then refilled.
 //
-// The tiles of a product rarely fill the chip evenly: the workgroups share all
-// tiles' steps evenly instead, and a tile that two of them share is left as
-// float32 parts that a second kernel adds in order.
+// Where a product has too few tiles for the chip, several workgroups share a
+// tile's steps and leave float32 parts that a second kernel adds in order.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -125,6 +124,22 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(OrthoArgs a, double* pa
 // step can carry past the range (a step takes s to at most |a| s + |b| s^3 +
 // |c| s^5), and A and the result are scaled back.
 constexpr int kMaxUnit = 100;
+__device__ __forceinline__ double input_scale(const OrthoArgs& a, double sq, float pow_x, int* unit) {
+  const double norm = sqrt(sq);
+  int e = 0;
+  if (norm < a.eps && norm > 0.0) {
+    double v = norm / a.eps, most = v;
+    for (int k = 0; k < a.steps && most < 1.0; ++k) {
+      v *= fabs(a.a) + v * v * (fabs(a.b) + v * v * fabs(a.c));
+      most = fmax(most, v);
+    }
+    if (most < 1.0) e = min(kMaxUnit, ilogb(1.0 / most));
+  }
+  *unit = e;
+  return norm < __builtin_huge_val() ? ldexp((double)pow_x, e) / (norm > a.eps ? norm : a.eps)
+                                     : __builtin_nan("");
+}
+
 template <class E, bool MUON>
 __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoArgs a, const double* part, int nb,
                                                           Pair X, int64_t Rp, int64_t Cp,
@@ -135,19 +150,8 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoArgs a, const dou
     for (int k = threadIdx.x; k < nb; k += 64) sq += part[(int64_t)blockIdx.y * nb + k];
     sq = wave_sum_f64(sq);
     if (threadIdx.x == 0) {
-      const double norm = sqrt(sq);
-      int e = 0;
-      if (norm < a.eps && norm > 0.0) {
-        double v = norm / a.eps, most = v;
-        for (int k = 0; k < a.steps && most < 1.0; ++k) {
-          v *= fabs(a.a) + v * v * (fabs(a.b) + v * v * fabs(a.c));
-          most = fmax(most, v);
-        }
-        if (most < 1.0) e = min(kMaxUnit, ilogb(1.0 / most));
-      }
-      scale = norm < __builtin_huge_val()
-                  ? ldexp((double)pow_x, e) / (norm > a.eps ? norm : a.eps)
-                  : __builtin_nan("");
+      int e;
+      scale = input_scale(a, sq, pow_x, &e);
       if (blockIdx.x == 0) unit[blockIdx.y] = ldexpf(1.0f, -e);
     }
   }
@@ -594,6 +598,183 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT) ortho_fixup_kernel(ProductAr
 }
 
 // ---------------------------------------------------------------------------
+// Small matrices
+// ---------------------------------------------------------------------------
+// A matrix whose pairs fit into LDS next to its m x m product: the whole call
+// in one workgroup of 16 waves (a launch per product costs more than the
+// product).  X is kept with its smaller dimension first, A and then B in the
+// same place; each wave computes 32 x 32 blocks in registers and they are
+// stored after a barrier, in place.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallBlocks = 3;                   // blocks of X per wave, at most
+constexpr int kSmallLds = 156 * 1024;
+
+struct StepFactors {
+  float gram, add_b, square, add_x, apply;
+};
+struct SmallArgs {
+  OrthoArgs a;
+  int flip, m, k, mp, kp;                         // X: [m, k], padded to 32
+  float pow_x;
+  StepFactors f[kOrthoMaxSteps];
+};
+
+// One matrix in LDS: hi and lo planes, rows `ld` halves apart.
+struct Planes {
+  uint16_t *hi, *lo;
+  int ld;
+  __device__ __forceinline__ u16x8 inner(bool low, int m0, int k0) const {   // rows m0 .., k0 .. + 15
+    const int lane = threadIdx.x & 63;
+    return *(const u16x8*)((low ? lo : hi) + (m0 + (lane & 31)) * ld + k0 + 8 * (lane >> 5));
+  }
+  __device__ __forceinline__ u16x8 outer(bool low, int m0, int k0) const {   // columns m0 .., rows k0 ..
+    const int lane = threadIdx.x & 63;
+    const uint16_t* p = (low ? lo : hi) + (k0 + 8 * (lane >> 5) + ((lane & 15) >> 2)) * ld + m0 +
+                        16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    const u16x4 a = lds_read_tr16(p), b = lds_read_tr16(p + 4 * ld);
+    u16x8 f;
+    f.s0 = a.s0; f.s1 = a.s1; f.s2 = a.s2; f.s3 = a.s3;
+    f.s4 = b.s0; f.s5 = b.s1; f.s6 = b.s2; f.s7 = b.s3;
+    return f;
+  }
+  __device__ __forceinline__ void put(int r, int c, float v) const {
+    const _Float16 h = (_Float16)v, l = (_Float16)(v - (float)h);
+    hi[r * ld + c] = __builtin_bit_cast(uint16_t, h);
+    lo[r * ld + c] = __builtin_bit_cast(uint16_t, l);
+  }
+  // v = f0 old + f1 acc for this lane's values of a block, in place
+  __device__ __forceinline__ void update(int r0, int c0, float f0, float f1, const f32x16& acc) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int e = (r0 + acc_col(lane)) * ld + c0 + acc_row(4 * g, lane);
+      f16x4 h, l;
+      if (f0 != 0.f) {
+        h = *(const f16x4*)(hi + e);
+        l = *(const f16x4*)(lo + e);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float old = f0 != 0.f ? f0 * ((float)h[k] + (float)l[k]) : 0.f;
+        const float v = old + f1 * acc[4 * g + k];
+        h[k] = (_Float16)v;
+        l[k] = (_Float16)(v - (float)h[k]);
+      }
+      *(f16x4*)(hi + e) = h;
+      *(f16x4*)(lo + e) = l;
+    }
+  }
+};
+
+// Block (r0, c0) of L R^T (fragments from `l` and `r`), K in steps of 16.
+template <class FL, class FR>
+__device__ __forceinline__ f32x16 small_block(int K, FL&& l, FR&& r) {
+  f32x16 acc;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll 2
+  for (int k0 = 0; k0 < K; k0 += 16) {
+    const u16x8 lh = l(false, k0), ll = l(true, k0), rh = r(false, k0), rl = r(true, k0);
+    acc = mma16(rl, lh, acc);
+    acc = mma16(rh, ll, acc);
+    acc = mma16(rh, lh, acc);
+  }
+  return acc;
+}
+
+template <class E, bool MUON>
+__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(SmallArgs p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ double red[kSmallWaves], scale;
+  __shared__ int unit;
+  const OrthoArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int len = p.m * p.k, C = (int)a.C;
+  const int64_t base = (int64_t)blockIdx.x * len;
+  const int ldx = p.kp + 8, lda = p.mp + 8;
+  const Planes X{(uint16_t*)lds, (uint16_t*)lds + p.mp * ldx, ldx};
+  uint16_t* ap = X.lo + p.mp * ldx;
+  const Planes A{ap, ap + p.mp * lda, lda};
+  double sq = 0.0;
+  for (int i = tid; i < len; i += kSmallThreads) {
+    const int64_t e = base + i;
+    if constexpr (MUON) a.momentum[e] = a.beta * a.momentum[e] + a.grad[e];
+    const float u = update_at<E, MUON>(a, e);
+    sq += (double)u * (double)u;
+  }
+  for (int i = tid; i < p.mp * ldx; i += kSmallThreads) ((uint32_t*)lds)[i] = 0u;   // both planes
+  sq = block_sum_f64(sq, red);
+  if (tid == 0) scale = input_scale(a, sq, p.pow_x, &unit);
+  __syncthreads();
+  for (int i = tid; i < len; i += kSmallThreads) {
+    const int r = i / C, c = i - r * C;
+    const float v = (float)((double)update_at<E, MUON>(a, base + i) * scale);
+    if (p.flip) X.put(c, r, v);
+    else X.put(r, c, v);
+  }
+  const float inv = ldexpf(1.0f, -unit);
+  const int mb = p.mp / 32, kb = p.kp / 32;
+  for (int s = 0; s < a.steps; ++s) {
+    const StepFactors f = p.f[s];
+    __syncthreads();
+    // A = X X^T: at most 16 blocks, one per wave
+    const int bi = wave / mb * 32, bj = wave % mb * 32;
+    const bool mine = wave < mb * mb;
+    f32x16 acc;
+    if (mine) {
+      acc = small_block(p.kp, [&](bool low, int k) { return X.inner(low, bi, k); },
+                        [&](bool low, int k) { return X.inner(low, bj, k); });
+      A.update(bi, bj, 0.f, f.gram * inv * inv, acc);
+    }
+    __syncthreads();
+    if (mine)
+      acc = small_block(p.mp, [&](bool low, int k) { return A.inner(low, bi, k); },
+                        [&](bool low, int k) { return A.inner(low, bj, k); });
+    __syncthreads();
+    if (mine) A.update(bi, bj, f.add_b, f.square, acc);     // B
+    __syncthreads();
+    f32x16 x[kSmallBlocks];
+#pragma unroll
+    for (int q = 0; q < kSmallBlocks; ++q) {
+      const int n = wave + q * kSmallWaves;
+      if (n < mb * kb)
+        x[q] = small_block(p.mp, [&](bool low, int k) { return A.inner(low, n / kb * 32, k); },
+                           [&](bool low, int k) { return X.outer(low, n % kb * 32, k); });
+    }
+    __syncthreads();
+    const bool last = s + 1 == a.steps;
+#pragma unroll
+    for (int q = 0; q < kSmallBlocks; ++q) {
+      const int n = wave + q * kSmallWaves;
+      if (n >= mb * kb) continue;
+      const int r0 = n / kb * 32, c0 = n % kb * 32;
+      if (!last) {
+        X.update(r0, c0, f.add_x, f.apply, x[q]);
+        continue;
+      }
+      const int r = r0 + acc_col(lane);
+      if (r >= p.m) continue;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int c = c0 + acc_row(j, lane);
+        if (c >= p.k) continue;
+        const int at = r * ldx + c;
+        const float old = (float)__builtin_bit_cast(_Float16, X.hi[at]) +
+                          (float)__builtin_bit_cast(_Float16, X.lo[at]);
+        const float v = (f.add_x * old + f.apply * x[q][j]) * inv;
+        const int64_t e = base + (p.flip ? (int64_t)c * C + r : (int64_t)r * C + c);
+        if constexpr (MUON) {
+          a.W[e] = a.decay * a.W[e] - a.size * v;
+        } else {
+          float one[1] = {v};
+          store_f32<E, 1>((typename E::storage*)a.out + e, one);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Plan
 // ---------------------------------------------------------------------------
 // The largest |a s + b s^3 + c s^5| over 0 <= s <= top.
@@ -639,23 +820,38 @@ struct Plan {
   int tile;
   int64_t m, Rp, Cp, mp;       // padded
   int nb;                      // norm workgroups per matrix
-  int groups_sym, groups_full, groups_square;
+  int64_t groups_sym, groups_full, groups_square;
+  int small;                   // LDS bytes of the one-workgroup kernel, or 0
   size_t x, a, part, unit, parts, total;   // bytes of one X pair, one A pair; offsets
 };
 
 int64_t up(int64_t v, int64_t t) { return (v + t - 1) / t * t; }
 
-// Workgroups that run at once.
-int resident(int tile) { return device_cus() * (tile == 256 ? 1 : 2); }
+// Microseconds of a product on `groups` workgroups, measured: a step of a
+// 128 x 128 tile takes 0.55 with the compute unit to itself and 1.0 next to
+// another, of a 256 x 256 tile 1.6; shared tiles cost their parts' way through
+// memory and a launch.
+double product_us(int64_t tiles, int64_t steps, int tile, int64_t groups) {
+  const int64_t cus = device_cus();
+  if (groups != tiles)
+    return (double)(tiles * steps) / groups * (groups <= cus ? 0.55 : 1.0) + 5.0 + 0.033 * groups;
+  if (tile == 256) return (double)((tiles + cus - 1) / cus * steps) * 1.6;
+  if (tiles <= cus) return steps * 0.55;
+  return (double)((tiles + 2 * cus - 1) / (2 * cus) * steps);
+}
 
-// Workgroups that share `tiles` tiles of `steps` steps: one per tile, or as
-// many as run at once where sharing the tiles' steps evenly is shorter by
-// more than the parts cost (about 12 steps); no fewer than 8 steps each.
-int groups_of(int64_t tiles, int64_t steps, int tile) {
-  const int64_t g = std::min<int64_t>(resident(tile), std::max<int64_t>(1, tiles * steps / 8));
-  const int64_t whole = (tiles + resident(tile) - 1) / resident(tile) * steps;
-  const int64_t shared = (tiles * steps + g - 1) / g + 12;
-  return (int)(shared < whole ? g : tiles);
+// Workgroups for `tiles` tiles of `steps` steps: one per tile, or, where there
+// are too few tiles for the compute units, 2 or more that share each (at
+// least 8 steps each).  Tiles of 256 are taken where there are enough of them;
+// sharing those was measured slower even with a fifth of the chip idle (the
+// clock rises when units idle: 5120 x 5120 7.8 ms whole, 8.5 shared).
+int64_t groups_of(int64_t tiles, int64_t steps, int tile) {
+  int64_t best = tiles;
+  if (tile == 256) return best;
+  for (int64_t share = 2; share * 8 <= steps && tiles * share <= 2 * device_cus(); ++share)
+    if (product_us(tiles, steps, tile, tiles * share) < product_us(tiles, steps, tile, best))
+      best = tiles * share;
+  return best;
 }
 
 int64_t sym_tiles(int64_t mt) { return mt * (mt + 1) / 2; }
@@ -671,22 +867,27 @@ void plan_tiles(Plan& p, const OrthoArgs& a, int tile) {
   p.groups_full = groups_of(a.n * (p.Rp / tile) * (p.Cp / tile), p.mp / 16, tile);
 }
 
-// Time of an iteration in steps of a 128 x 128 tile with its neighbour.
+// Time of an iteration.
 double plan_cost(const Plan& p, const OrthoArgs& a) {
-  const int64_t mt = p.mp / p.tile, k = (p.flip ? p.Rp : p.Cp) / 16, g = resident(p.tile);
-  auto rounds = [&](int64_t tiles, int64_t steps, int groups) {
-    return groups == tiles ? (double)((tiles + g - 1) / g * steps) : (double)(tiles * steps) / groups + 12;
-  };
-  const double steps = rounds(a.n * sym_tiles(mt), k, p.groups_sym) +
-                       rounds(a.n * sym_tiles(mt), p.mp / 16, p.groups_square) +
-                       rounds(a.n * (p.Rp / p.tile) * (p.Cp / p.tile), p.mp / 16, p.groups_full);
-  return steps * (p.tile == 256 ? 1.8 : 1.0);
+  const int64_t mt = p.mp / p.tile, k = (p.flip ? p.Rp : p.Cp) / 16;
+  return product_us(a.n * sym_tiles(mt), k, p.tile, p.groups_sym) +
+         product_us(a.n * sym_tiles(mt), p.mp / 16, p.tile, p.groups_square) +
+         product_us(a.n * (p.Rp / p.tile) * (p.Cp / p.tile), p.mp / 16, p.tile, p.groups_full);
+}
+
+// The small kernel's LDS for X [mp, kp] (0: does not fit).
+int small_lds(int64_t mp, int64_t kp) {
+  if (mp > 128 || mp / 32 * (kp / 32) > kSmallWaves * kSmallBlocks) return 0;
+  const int64_t bytes = 4 * mp * (kp + 8) + 4 * mp * (mp + 8);
+  return bytes <= kSmallLds ? (int)bytes : 0;
 }
 
 Plan plan_of(const OrthoArgs& a) {
   Plan p{};
   p.flip = a.R > a.C;
   p.m = std::min(a.R, a.C);
+  p.small = small_lds(up(p.m, 32), up(std::max(a.R, a.C), 32));
+  if (p.small != 0) return p;
   plan_tiles(p, a, 256);
   const double large = plan_cost(p, a);
   plan_tiles(p, a, 128);
@@ -716,16 +917,18 @@ hipError_t launch_product_t(const ProductArgs& p, int64_t tiles, hipStream_t s) 
                      s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups == tiles) return e;
-  hipLaunchKernelGGL(ortho_fixup_kernel<TILE>, dim3((unsigned)(p.groups - 1), S::kBA * S::kBO),
+  if constexpr (TILE == 128)
+    hipLaunchKernelGGL(ortho_fixup_kernel<TILE>, dim3((unsigned)(p.groups - 1), S::kBA * S::kBO),
                      dim3(S::kNT), 0, s, p);
   return hipGetLastError();
 }
 
-hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int groups, hipStream_t s) {
+hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int64_t groups,
+                          hipStream_t s) {
   p.tiles = p.sym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
   const int64_t tiles = p.tiles * n;
   p.total = tiles * p.steps;
-  p.groups = groups;
+  p.groups = (int)groups;
   if (groups == 1 && tiles > 1) return hipErrorInvalidValue;
   if (tile == 256)
     return ki ? launch_product_t<256, true>(p, tiles, s) : launch_product_t<256, false>(p, tiles, s);
@@ -759,8 +962,65 @@ bool ortho_coeffs_ok(const OrthoArgs& a) {
 
 size_t ortho_workspace_bytes(const OrthoArgs& a) { return plan_of(a).total; }
 
+namespace {
+
+// The powers of two that X, A and B are kept with in each step, and what the
+// products' results are multiplied by.
+struct StepScale {
+  int x, a, b, next;
+  StepFactors f;
+};
+StepScale step_scale(const OrthoArgs& a, double* top, int sx, bool last) {
+  StepScale s;
+  s.x = sx;
+  s.a = scale_of(kRoom * *top * *top);
+  s.b = scale_of(kRoom * quad_bound(a.b, a.c, *top * *top));
+  *top = kRoom * poly_bound(a.a, a.b, a.c, *top);
+  s.next = last ? 0 : scale_of(kRoom * *top);
+  s.f.gram = (float)std::ldexp(1.0, s.a - 2 * s.x);
+  s.f.add_b = (float)(a.b * std::ldexp(1.0, s.b - s.a));
+  s.f.square = (float)(a.c * std::ldexp(1.0, s.b - 2 * s.a));
+  s.f.add_x = (float)(a.a * std::ldexp(1.0, s.next - s.x));
+  s.f.apply = (float)std::ldexp(1.0, s.next - s.b - s.x);
+  return s;
+}
+
+template <class E, bool MUON>
+hipError_t launch_small(const SmallArgs& q, int lds, hipStream_t s) {
+  static hipError_t once = hipFuncSetAttribute((const void*)ortho_small_kernel<E, MUON>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
+  if (once != hipSuccess) return once;
+  hipLaunchKernelGGL((ortho_small_kernel<E, MUON>), dim3((unsigned)q.a.n), dim3(kSmallThreads), lds, s, q);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   const Plan p = plan_of(a);
+  double top = 1.0;
+  int sx = scale_of(top * kRoom);
+  if (p.small != 0) {
+    SmallArgs q{};
+    q.a = a;
+    q.flip = p.flip ? 1 : 0;
+    q.m = (int)p.m;
+    q.k = (int)std::max(a.R, a.C);
+    q.mp = (int)up(q.m, 32);
+    q.kp = (int)up(q.k, 32);
+    q.pow_x = std::ldexp(1.f, sx);
+    for (int k = 0; k < a.steps; ++k) {
+      const StepScale c = step_scale(a, &top, sx, k + 1 == a.steps);
+      q.f[k] = c.f;
+      sx = c.next;
+    }
+    timing_begin("ortho_small", s);
+    const hipError_t e = a.W != nullptr       ? launch_small<F32, true>(q, p.small, s)
+                         : a.dtype == kBF16 ? launch_small<BF16, false>(q, p.small, s)
+                                            : launch_small<F32, false>(q, p.small, s);
+    timing_end("ortho_small", s);
+    return e;
+  }
   char* ws = (char*)a.ws;
   auto pair = [&](size_t off, int64_t rows, int64_t cols) {
     return Pair{(uint16_t*)(ws + off), 2 * cols, 2 * rows * cols};
@@ -769,8 +1029,6 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   const Pair A = pair(2 * p.x, p.mp, p.mp), B = pair(2 * p.x + p.a, p.mp, p.mp);
   double* part = (double*)(ws + p.part);
   float* unit = (float*)(ws + p.unit);
-  double top = 1.0;
-  int sx = scale_of(top * kRoom);
   timing_begin("ortho_input", s);
   hipError_t e;
   if (a.W != nullptr) e = launch_input<F32, true>(a, p, part, unit, X[0], std::ldexp(1.f, sx), s);
@@ -780,10 +1038,8 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   const int mt = (int)(p.mp / p.tile);
   for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
     const Pair& Xk = X[k & 1];
-    const int sa = scale_of(kRoom * top * top), sb = scale_of(kRoom * quad_bound(a.b, a.c, top * top));
-    top = kRoom * poly_bound(a.a, a.b, a.c, top);
     const bool last = k + 1 == a.steps;
-    const int sn = last ? 0 : scale_of(kRoom * top);
+    const StepScale c = step_scale(a, &top, sx, last);
     ProductArgs q{};
     q.unit = unit;
     q.parts = (float*)(ws + p.parts);
@@ -795,7 +1051,7 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     q.sym = 1;
     q.mode = kStore;
     q.units = 2;
-    q.f1 = (float)std::ldexp(1.0, sa - 2 * sx);
+    q.f1 = c.f.gram;
     timing_begin("ortho_gram", s);
     e = launch_product(q, p.tile, !p.flip, a.n, p.groups_sym, s);
     timing_end("ortho_gram", s);
@@ -806,8 +1062,8 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     q.steps = (int)(p.mp / 16);
     q.mode = kAddStore;
     q.units = 0;
-    q.f0 = (float)(a.b * std::ldexp(1.0, sb - sa));
-    q.f1 = (float)(a.c * std::ldexp(1.0, sb - 2 * sa));
+    q.f0 = c.f.add_b;
+    q.f1 = c.f.square;
     timing_begin("ortho_square", s);
     e = launch_product(q, p.tile, !p.flip, a.n, p.groups_square, s);
     timing_end("ortho_square", s);
@@ -822,8 +1078,8 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     q.sym = 0;
     q.mode = last ? kFinal : kAddStore;
     q.units = last ? 1 : 0;
-    q.f0 = (float)(a.a * std::ldexp(1.0, sn - sx));
-    q.f1 = (float)std::ldexp(1.0, sn - sb - sx);
+    q.f0 = c.f.add_x;
+    q.f1 = c.f.apply;
     q.rows = a.R;
     q.cols = a.C;
     q.dst = a.W != nullptr ? (void*)a.W : a.out;
@@ -834,7 +1090,7 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     timing_begin("ortho_apply", s);
     e = launch_product(q, p.tile, p.flip, a.n, p.groups_full, s);
     timing_end("ortho_apply", s);
-    sx = sn;
+    sx = c.next;
   }
   return e;
 }
