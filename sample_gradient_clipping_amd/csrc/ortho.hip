@@ -4,7 +4,12 @@
 //   X <- a X + (b A + c A^2) X,  A = X X^T      (R <= C; else X (b A + c A^2), A = X^T X)
 //
 // `steps` times: each singular value s of X goes to a s + b s^3 + c s^5, which
-// the coefficients drive towards 1, and the singular vectors stay.  The
+// the coefficients drive towards 1, and the singular vectors stay.  Computed as
+//
+//   A' = A + (b / 2c) I,  B = c A'^2 + (a - b^2 / 4c) I,  X <- B X
+//
+// so that every product's result is only scaled, shifted on its diagonal and
+// stored: nothing is read back (with c = 0: B = b A + a I, and no square).  The
 // optimizer step forms U from the gradient and the momentum, and subtracts the
 // result from the weight.
 //
@@ -17,7 +22,7 @@
 // them by up to a, and an error in X as large as bfloat16's rounding would be
 // multiplied with them.
 //
-// A and B = b A + c A^2 are symmetric: only the tiles on and above the
+// A and B are symmetric: only the tiles on and above the
 // diagonal are computed, and stored twice.
 //
 // Layouts.  X stays as U is stored.  With R <= C the products contract X's
@@ -52,7 +57,7 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kSumBlocks = 256;     // most workgroups of one matrix's norm
+constexpr int kSumBlocks = 2048;    // most workgroups of one matrix's norm
 
 __device__ __forceinline__ f32x16 mma16(const u16x8& a, const u16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
@@ -83,13 +88,6 @@ __device__ __forceinline__ void store_pair(const Pair& p, int64_t r, int64_t c, 
   *(f16x4*)(e + 16) = l;
 }
 
-__device__ __forceinline__ void load_pair(const Pair& p, int64_t r, int64_t c, float (&v)[4]) {
-  const uint16_t* e = p.elem(r, c);
-  const f16x4 h = *(const f16x4*)e, l = *(const f16x4*)(e + 16);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = (float)h[k] + (float)l[k];
-}
-
 // ---------------------------------------------------------------------------
 // Momentum and norm
 // ---------------------------------------------------------------------------
@@ -103,16 +101,38 @@ __device__ __forceinline__ float update_at(const OrthoArgs& a, int64_t e) {
   }
 }
 
-template <class E, bool MUON>
+// V consecutive elements of the update from element e on; `first` pass: the
+// momentum is moved on.
+template <class E, bool MUON, int V, bool FIRST>
+__device__ __forceinline__ void update_from(const OrthoArgs& a, int64_t e, float (&u)[V]) {
+  if constexpr (MUON) {
+    float g[V], m[V];
+    load_f32<F32, V>(a.grad + e, g);
+    load_f32<F32, V>(a.momentum + e, m);
+    if constexpr (FIRST) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) m[k] = a.beta * m[k] + g[k];
+      store_f32<F32, V>(a.momentum + e, m);
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) u[k] = a.nesterov ? g[k] + a.beta * m[k] : m[k];
+  } else {
+    load_f32<E, V>((const typename E::storage*)a.in + e, u);
+  }
+}
+
+// V: 4 where a matrix's elements are a multiple of 4, else 1.
+template <class E, bool MUON, int V>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(OrthoArgs a, double* part) {
   __shared__ double red[4];
   const int64_t len = a.R * a.C, base = (int64_t)blockIdx.y * len;
   double sq = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < len; i += (int64_t)gridDim.x * 256) {
-    const int64_t e = base + i;
-    if constexpr (MUON) a.momentum[e] = a.beta * a.momentum[e] + a.grad[e];
-    const float u = update_at<E, MUON>(a, e);
-    sq += (double)u * (double)u;
+#pragma unroll 4
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < len; i += (int64_t)gridDim.x * 256 * V) {
+    float u[V];
+    update_from<E, MUON, V, true>(a, base + i, u);
+#pragma unroll
+    for (int k = 0; k < V; ++k) sq += (double)u[k] * (double)u[k];
   }
   sq = block_sum_f64(sq, red);
   if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sq;
@@ -140,10 +160,11 @@ __device__ __forceinline__ double input_scale(const OrthoArgs& a, double sq, flo
                                      : __builtin_nan("");
 }
 
-template <class E, bool MUON>
+// V: 4 where C is a multiple of 4, else 1.
+template <class E, bool MUON, int V>
 __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoArgs a, const double* part, int nb,
-                                                          Pair X, int64_t Rp, int64_t Cp,
-                                                          float pow_x, float* unit) {
+                                                          Pair X, int Rp, int Cp, float pow_x,
+                                                          float* unit) {
   __shared__ double scale;
   if (threadIdx.x < 64) {
     double sq = 0.0;
@@ -158,31 +179,48 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(OrthoArgs a, const dou
   __syncthreads();
   const double f = scale;
   const Pair x = X.at(blockIdx.y);
-  const int64_t total = Rp * Cp / 4, base = (int64_t)blockIdx.y * a.R * a.C;
-  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
-    const int64_t r = 4 * q / Cp, c = 4 * q - r * Cp;
-    float v[4];
+  const int64_t base = (int64_t)blockIdx.y * a.R * a.C;
+  const int per = Cp / 4, R = (int)a.R, C = (int)a.C;   // lanes of a row
+  // rows in steps of the grid's, a row's groups of four side by side
+  const int64_t total = (int64_t)Rp * per, step = (int64_t)gridDim.x * 256;
+  const int64_t q0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  int r = (int)(q0 / per), c4 = (int)(q0 - (int64_t)r * per);
+  const int dr = (int)(step / per), dc = (int)(step - (int64_t)dr * per);
+#pragma unroll 2
+  for (int64_t q = q0; q < total; q += step) {
+    const int c = 4 * c4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < R && c < C) {
+      const int64_t e = base + (int64_t)r * C + c;
+      if constexpr (V == 4) {
+        update_from<E, MUON, 4, false>(a, e, v);
+      } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = r < a.R && c + k < a.C
-                 ? (float)((double)update_at<E, MUON>(a, base + r * a.C + c + k) * f)
-                 : 0.f;
+        for (int k = 0; k < 4; ++k)
+          if (c + k < C) {
+            float one[1];
+            update_from<E, MUON, 1, false>(a, e + k, one);
+            v[k] = one[0];
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = r < R && c + k < C ? (float)((double)v[k] * f) : 0.f;
     store_pair(x, r, c, v);
+    r += dr;
+    c4 += dc;
+    if (c4 >= per) { c4 -= per; ++r; }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Products
 // ---------------------------------------------------------------------------
-// D[M][N] = sum_k L(M, k) R(N, k); then, by mode, with f0, f1 powers of two
-// times coefficients:
-enum Mode {
-  kStore = 0,    // out = f1 D
-  kAddStore = 1, // out = f0 add + f1 D
-  kFinal = 2     // result = f0 add + f1 D, to the caller's matrix
-};
+// D[M][N] = f sum_k L(M, k) R(N, k), symmetric ones plus `shift` on the
+// diagonal; stored as pairs, or (the last one) to the caller's matrix.
+enum Mode { kStore = 0, kFinal = 1 };
 struct ProductArgs {
-  Pair L, R, add, out;
+  Pair L, R, out;
   int steps;              // K / 16
   int mt, nt;             // tiles of M and N (symmetric: mt == nt)
   int tiles;              // per matrix
@@ -190,9 +228,9 @@ struct ProductArgs {
   int groups;             // workgroups that share them
   float* parts;           // [2 groups][tile] float32 parts of shared tiles
   int sym, mode, dtype;
-  float f0, f1;
+  float f, shift;
   const float* unit;      // [n] 1 / unit of each matrix's X
-  int units;              // power of it that scales f1 D (kStore) or the result (kFinal)
+  int units;              // power of it that is part of f
   // kFinal
   int64_t rows, cols;
   void* dst;              // [rows, cols] of dtype, or the weight (float32)
@@ -284,7 +322,13 @@ struct Operand {
   }
   __device__ __forceinline__ void load(uint32_t lds) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const __amdgpu_buffer_rsrc_t r = rsrc_of(base);
+    // The same in every lane; the compiler computes tile indices in vector
+    // registers and has to be told.
+    const uint64_t at = (uint64_t)base;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+    const __amdgpu_buffer_rsrc_t r = rsrc_of((const void*)(((uint64_t)hi << 32) | lo));
+    lds = __builtin_amdgcn_readfirstlane(lds);
 #pragma unroll
     for (int j = 0; j < 2; ++j) dma16(r, off[j], lds + (uint32_t)(wave * 2 + j) * 1024u);
     base += step;
@@ -367,55 +411,130 @@ __device__ __forceinline__ int logical_group(int id, int groups) {
   return x * q + min(x, r) + id / 8;
 }
 
-// Block (i, j) of a wave's part of a tile: scaled, added and stored.
+// Block row i of every wave of a tile (64 rows of the result), scaled, shifted
+// on the diagonal, and stored.  The accumulators hold 8 bytes of each of 32
+// rows; they go through LDS, so that memory sees whole lines.
+constexpr int kStageRows = 64;
 template <int TILE>
-__device__ __forceinline__ void finish_block(const ProductArgs& p, int64_t mat, int ti, int tj,
-                                             int i, int j, const f32x16& acc) {
+constexpr int stage_bytes() {
+  const int rows = kStageRows * (TILE * 4 + 16), mirror = TILE * (kStageRows * 4 + 16);
+  return rows > mirror ? rows : mirror;
+}
+
+template <int TILE>
+__device__ __forceinline__ void store_rows(const ProductArgs& p, int64_t mat, int ti, int tj, int i,
+                                           const f32x16 (&acc)[Shape<TILE>::kBO],
+                                           unsigned char* lds) {
   using S = Shape<TILE>;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  static_assert(S::kWR * 32 == kStageRows, "two blocks of 32 rows");
+  static_assert(stage_bytes<TILE>() <= S::kLds, "the stage fits into the ring");
+  constexpr int kLine = TILE * 4 + 16, kMirrorLine = kStageRows * 4 + 16;
+  // Hidden from the optimiser, which would otherwise keep these addresses in
+  // registers through the main loop.
+  int tid = (int)threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int wave = tid >> 6, lane = tid & 63;
   const int wm = wave / S::kWC, wn = wave % S::kWC;
-  const int64_t r = (int64_t)ti * TILE + (wm * S::kBA + i) * 32 + acc_col(lane);
-  const int64_t c0 = (int64_t)tj * TILE + (wn * S::kBO + j) * 32;
-  float f0 = p.f0, f1 = p.f1;
-  for (int k = 0; k < p.units; ++k) { f0 *= p.unit[mat]; f1 *= p.unit[mat]; }
-  const Pair add = p.add.at(mat), out = p.out.at(mat);
+  const int64_t m0 = (int64_t)ti * TILE, n0 = (int64_t)tj * TILE;
+  // stage row s holds row m0 + (s / 32) * kBA * 32 + i * 32 + s % 32
+  const int srow = wm * 32 + (lane & 31);
+  const int64_t r = m0 + (wm * S::kBA + i) * 32 + (lane & 31);
+  float f = p.f;
+  for (int k = 0; k < p.units; ++k) f *= p.unit[mat];
+  const bool mirror = p.sym && ti != tj;
+  __syncthreads();                                  // the ring, or the last rows, are read
+  if (p.mode == kFinal) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int64_t c = c0 + acc_row(4 * g, lane);
-    float v[4];
+    for (int j = 0; j < S::kBO; ++j)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = f1 * acc[4 * g + k];
-    if (p.mode != kStore) {
-      float w[4];
-      load_pair(add, r, c, w);
+      for (int g = 0; g < 4; ++g)
+        *(f32x4*)(lds + srow * kLine + ((wn * S::kBO + j) * 32 + (8 * g + 4 * (lane >> 5))) * 4) =
+            f32x4{f * acc[j][4 * g], f * acc[j][4 * g + 1], f * acc[j][4 * g + 2], f * acc[j][4 * g + 3]};
+  } else {
+    // the tile column of this lane's diagonal element, if it has one
+    const int diag = p.sym && ti == tj ? (int)(r - n0) : -1;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += f0 * w[k];
-    }
-    if (p.mode != kFinal) {
-      store_pair(out, r, c, v);
-      if (p.sym && ti != tj) {
+    for (int j = 0; j < S::kBO; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = (wn * S::kBO + j) * 32 + (8 * g + 4 * (lane >> 5));
+        f16x4 h, l;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const _Float16 h = (_Float16)v[k], l = (_Float16)(v[k] - (float)h);
-          uint16_t* e = out.elem(c + k, r);
-          e[0] = __builtin_bit_cast(uint16_t, h);
-          e[16] = __builtin_bit_cast(uint16_t, l);
+          const float x = f * acc[j][4 * g + k] + (c + k == diag ? p.shift : 0.f);
+          h[k] = (_Float16)x;
+          l[k] = (_Float16)(x - (float)h[k]);
         }
+        unsigned char* e = lds + srow * kLine + (2 * c - (c & 15)) * 2;
+        *(f16x4*)e = h;
+        *(f16x4*)(e + 32) = l;
+      }
+  }
+  __syncthreads();
+  constexpr int kChunks = TILE / 4;                 // 16-byte chunks of a stage row
+  if (p.mode == kStore) {
+    const Pair out = p.out.at(mat);
+#pragma unroll 4
+    for (int q = tid; q < kStageRows * kChunks; q += S::kNT) {
+      const int s = q / kChunks, c = q % kChunks;
+      const int64_t row = m0 + (s >> 5) * (S::kBA * 32) + i * 32 + (s & 31);
+      *(u32x4*)((char*)(out.p + row * out.ld) + n0 * 4 + c * 16) = *(const u32x4*)(lds + s * kLine + c * 16);
+    }
+    if (!mirror) return;
+    // the same values as columns: row n0 + c of the result, 32 of its columns
+    // (128 bytes) per block of rows
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < S::kBO; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int c = (wn * S::kBO + j) * 32 + acc_row(k, lane), q = (lane & 31);
+        const float x = f * acc[j][k];
+        const _Float16 h = (_Float16)x, l = (_Float16)(x - (float)h);
+        unsigned char* e = lds + c * kMirrorLine + wm * 128 + (2 * q - (q & 15)) * 2;
+        *(_Float16*)e = h;
+        *(_Float16*)(e + 32) = l;
+      }
+    __syncthreads();
+#pragma unroll 4
+    for (int q = tid; q < TILE * 16; q += S::kNT) {
+      const int c = q >> 4, half = (q >> 3) & 1, x = q & 7;
+      const int64_t col = m0 + half * (S::kBA * 32) + i * 32;
+      *(u32x4*)((char*)(out.p + (n0 + c) * out.ld) + col * 4 + x * 16) =
+          *(const u32x4*)(lds + c * kMirrorLine + half * 128 + x * 16);
+    }
+    return;
+  }
+  for (int q = tid; q < kStageRows * kChunks; q += S::kNT) {
+    const int s = q / kChunks;
+    const int64_t row = m0 + (s >> 5) * (S::kBA * 32) + i * 32 + (s & 31), c = n0 + (q % kChunks) * 4;
+    if (row >= p.rows || c >= p.cols) continue;
+    const f32x4 x = *(const f32x4*)(lds + s * kLine + (q % kChunks) * 16);
+    const int64_t e = (mat * p.rows + row) * p.cols + c;
+    if (p.cols % 4 == 0) {                          // whole and aligned
+      if (p.muon) {
+        f32x4* w = (f32x4*)((float*)p.dst + e);
+        f32x4 old = *w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) old[k] = p.decay * old[k] - p.size * x[k];
+        *w = old;
+      } else {
+        float y[4] = {x[0], x[1], x[2], x[3]};
+        if (p.dtype == kBF16) store_f32<BF16, 4>((uint16_t*)p.dst + e, y);
+        else store_f32<F32, 4>((float*)p.dst + e, y);
       }
       continue;
     }
-    if (r >= p.rows) continue;
-    const int64_t e = (mat * p.rows + r) * p.cols + c;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (c + k >= p.cols) break;
       if (p.muon) {
         float* w = (float*)p.dst + e + k;
-        *w = p.decay * *w - p.size * v[k];
+        *w = p.decay * *w - p.size * x[k];
       } else if (p.dtype == kBF16) {
-        ((uint16_t*)p.dst)[e + k] = f32_to_bf16_rne(v[k]);
+        ((uint16_t*)p.dst)[e + k] = f32_to_bf16_rne(x[k]);
       } else {
-        ((float*)p.dst)[e + k] = v[k];
+        ((float*)p.dst)[e + k] = x[k];
       }
     }
   }
@@ -437,11 +556,14 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(Prod
   const uint32_t lds0 = lds_addr(lds);
   bool first = true;
   for (int64_t at = s0; at < s1;) {
-    const int64_t tile = at / p.steps, mat = tile / p.tiles;
-    const int k0 = (int)(at - tile * p.steps);
-    const int n = (int)min((int64_t)(p.steps - k0), s1 - at);    // steps of this piece
+    const int64_t tile = at / p.steps;
+    const int mat = __builtin_amdgcn_readfirstlane((int)(tile / p.tiles));
+    const int k0 = __builtin_amdgcn_readfirstlane((int)(at - tile * p.steps));
+    const int n = __builtin_amdgcn_readfirstlane((int)min((int64_t)(p.steps - k0), s1 - at));   // steps of this piece
     int ti, tj;
-    tile_of(p, (int)(tile - mat * p.tiles), &ti, &tj);
+    tile_of(p, (int)(tile - (int64_t)mat * p.tiles), &ti, &tj);
+    ti = __builtin_amdgcn_readfirstlane(ti);
+    tj = __builtin_amdgcn_readfirstlane(tj);
     Operand<TILE, KI> ol, orr;
     ol.start(p.L.at(mat), (int64_t)ti * TILE, k0);
     orr.start(p.R.at(mat), (int64_t)tj * TILE, k0);
@@ -550,9 +672,7 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(Prod
     }
     if (n == p.steps) {
 #pragma unroll
-      for (int i = 0; i < BA; ++i)
-#pragma unroll
-        for (int j = 0; j < BO; ++j) finish_block<TILE>(p, mat, ti, tj, i, j, acc[i][j]);
+      for (int i = 0; i < BA; ++i) store_rows<TILE>(p, mat, ti, tj, i, acc[i], lds);
     } else {
       // part: four accumulators of every thread side by side
       float* o = p.parts + (int64_t)(2 * w + (first ? 0 : 1)) * S::kFloats + threadIdx.x * 4;
@@ -571,52 +691,65 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(Prod
 }
 
 // The tiles that workgroups share: their parts in order, then as above.  One
-// workgroup per first inner boundary of a tile and block of its waves.
+// workgroup per first inner boundary of a tile and block row of its waves.
 template <int TILE>
 __global__ void __launch_bounds__(Shape<TILE>::kNT) ortho_fixup_kernel(ProductArgs p) {
   using S = Shape<TILE>;
-  const int b = blockIdx.x + 1, block = blockIdx.y;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
+  const int b = blockIdx.x + 1, i = blockIdx.y;
   const int64_t s = first_step(p, b), tile = s / p.steps, begin = tile * p.steps;
   if (s == begin || first_step(p, b - 1) > begin) return;
-  f32x16 acc;
+  f32x16 acc[S::kBO];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  for (int j = 0; j < S::kBO; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
   for (int w = b - 1; w < p.groups && first_step(p, w) < begin + p.steps; ++w) {
     const float* o = p.parts + (int64_t)(2 * w + (first_step(p, w) >= begin ? 0 : 1)) * S::kFloats +
-                     threadIdx.x * 4 + (int64_t)block * 4 * S::kNT * 4;
+                     threadIdx.x * 4 + (int64_t)i * S::kBO * 4 * S::kNT * 4;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 x = *(const f32x4*)(o + g * S::kNT * 4);
+    for (int j = 0; j < S::kBO; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[4 * g + k] += x[k];
-    }
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 x = *(const f32x4*)(o + (j * 4 + g) * S::kNT * 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[j][4 * g + k] += x[k];
+      }
   }
   const int64_t mat = tile / p.tiles;
   int ti, tj;
   tile_of(p, (int)(tile - mat * p.tiles), &ti, &tj);
-  finish_block<TILE>(p, mat, ti, tj, block / S::kBO, block % S::kBO, acc);
+  store_rows<TILE>(p, mat, ti, tj, i, acc, lds);
 }
 
 // ---------------------------------------------------------------------------
 // Small matrices
 // ---------------------------------------------------------------------------
 // A matrix whose pairs fit into LDS next to its m x m product: the whole call
-// in one workgroup of 16 waves (a launch per product costs more than the
+// in one workgroup of 8 waves (a launch per product costs more than the
 // product).  X is kept with its smaller dimension first, A and then B in the
 // same place; each wave computes 32 x 32 blocks in registers and they are
-// stored after a barrier, in place.
-constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
-constexpr int kSmallBlocks = 3;                   // blocks of X per wave, at most
+// stored after a barrier, in place.  Here B = b A + c A^2 and X <- a X + B X as
+// they stand: reading back costs nothing in LDS, and a few large entries (a
+// row, a number) do not average out what the shifted diagonals round off.
+constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallBlocks = 5;                   // blocks of X per wave, at most
+constexpr int kSmallSquare = 2;                   // and of A
 constexpr int kSmallLds = 156 * 1024;
 
+// What the products' results are multiplied by, and the diagonal shifts.
 struct StepFactors {
+  float gram, gram_shift, square, square_shift, apply;
+};
+// The same for B = b A + c A^2 and X <- a X + B X.
+struct AddFactors {
   float gram, add_b, square, add_x, apply;
 };
 struct SmallArgs {
   OrthoArgs a;
   int flip, m, k, mp, kp;                         // X: [m, k], padded to 32
   float pow_x;
-  StepFactors f[kOrthoMaxSteps];
+  AddFactors f[kOrthoMaxSteps];
 };
 
 // One matrix in LDS: hi and lo planes, rows `ld` halves apart.
@@ -642,12 +775,12 @@ struct Planes {
     hi[r * ld + c] = __builtin_bit_cast(uint16_t, h);
     lo[r * ld + c] = __builtin_bit_cast(uint16_t, l);
   }
-  // v = f0 old + f1 acc for this lane's values of a block, in place
+  // old f0 + f1 acc for this lane's values of a block, in place
   __device__ __forceinline__ void update(int r0, int c0, float f0, float f1, const f32x16& acc) const {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, r = r0 + acc_col(lane);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int e = (r0 + acc_col(lane)) * ld + c0 + acc_row(4 * g, lane);
+      const int e = r * ld + c0 + acc_row(4 * g, lane);
       f16x4 h, l;
       if (f0 != 0.f) {
         h = *(const f16x4*)(hi + e);
@@ -715,44 +848,51 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(SmallArgs p)
   const float inv = ldexpf(1.0f, -unit);
   const int mb = p.mp / 32, kb = p.kp / 32;
   for (int s = 0; s < a.steps; ++s) {
-    const StepFactors f = p.f[s];
+    const AddFactors f = p.f[s];
     __syncthreads();
-    // A = X X^T: at most 16 blocks, one per wave
-    const int bi = wave / mb * 32, bj = wave % mb * 32;
-    const bool mine = wave < mb * mb;
-    f32x16 acc;
-    if (mine) {
-      acc = small_block(p.kp, [&](bool low, int k) { return X.inner(low, bi, k); },
-                        [&](bool low, int k) { return X.inner(low, bj, k); });
-      A.update(bi, bj, 0.f, f.gram * inv * inv, acc);
-    }
-    __syncthreads();
-    if (mine)
-      acc = small_block(p.mp, [&](bool low, int k) { return A.inner(low, bi, k); },
-                        [&](bool low, int k) { return A.inner(low, bj, k); });
-    __syncthreads();
-    if (mine) A.update(bi, bj, f.add_b, f.square, acc);     // B
-    __syncthreads();
-    f32x16 x[kSmallBlocks];
+    f32x16 acc[kSmallSquare];
+    // f(q, r0, c0) for this wave's blocks of A
+    auto squares = [&](auto&& g) {
 #pragma unroll
-    for (int q = 0; q < kSmallBlocks; ++q) {
-      const int n = wave + q * kSmallWaves;
-      if (n < mb * kb)
-        x[q] = small_block(p.mp, [&](bool low, int k) { return A.inner(low, n / kb * 32, k); },
-                           [&](bool low, int k) { return X.outer(low, n % kb * 32, k); });
-    }
-    __syncthreads();
-    const bool last = s + 1 == a.steps;
-#pragma unroll
-    for (int q = 0; q < kSmallBlocks; ++q) {
-      const int n = wave + q * kSmallWaves;
-      if (n >= mb * kb) continue;
-      const int r0 = n / kb * 32, c0 = n % kb * 32;
-      if (!last) {
-        X.update(r0, c0, f.add_x, f.apply, x[q]);
-        continue;
+      for (int q = 0; q < kSmallSquare; ++q) {
+        const int n = wave + q * kSmallWaves;
+        if (n < mb * mb) g(q, n / mb * 32, n % mb * 32);
       }
-      const int r = r0 + acc_col(lane);
+    };
+    squares([&](int q, int r0, int c0) {                    // A
+      acc[q] = small_block(p.kp, [&](bool low, int k) { return X.inner(low, r0, k); },
+                           [&](bool low, int k) { return X.inner(low, c0, k); });
+      A.update(r0, c0, 0.f, f.gram * inv * inv, acc[q]);
+    });
+    __syncthreads();
+    squares([&](int q, int r0, int c0) {                    // B
+      acc[q] = small_block(p.mp, [&](bool low, int k) { return A.inner(low, r0, k); },
+                           [&](bool low, int k) { return A.inner(low, c0, k); });
+    });
+    __syncthreads();
+    squares([&](int q, int r0, int c0) { A.update(r0, c0, f.add_b, f.square, acc[q]); });
+    __syncthreads();
+    auto block = [&](int n) {
+      return small_block(p.mp, [&](bool low, int k) { return A.inner(low, n / kb * 32, k); },
+                         [&](bool low, int k) { return X.outer(low, n % kb * 32, k); });
+    };
+    if (s + 1 < a.steps) {
+      f32x16 x[kSmallBlocks];
+#pragma unroll
+      for (int q = 0; q < kSmallBlocks; ++q)
+        if (wave + q * kSmallWaves < mb * kb) x[q] = block(wave + q * kSmallWaves);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kSmallBlocks; ++q) {
+        const int n = wave + q * kSmallWaves;
+        if (n < mb * kb) X.update(n / kb * 32, n % kb * 32, f.add_x, f.apply, x[q]);
+      }
+      continue;
+    }
+#pragma unroll 1
+    for (int n = wave; n < mb * kb; n += kSmallWaves) {       // the result
+      const f32x16 x = block(n);
+      const int r = n / kb * 32 + acc_col(lane), c0 = n % kb * 32;
       if (r >= p.m) continue;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -761,8 +901,8 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(SmallArgs p)
         const int at = r * ldx + c;
         const float old = (float)__builtin_bit_cast(_Float16, X.hi[at]) +
                           (float)__builtin_bit_cast(_Float16, X.lo[at]);
-        const float v = (f.add_x * old + f.apply * x[q][j]) * inv;
-        const int64_t e = base + (p.flip ? (int64_t)c * C + r : (int64_t)r * C + c);
+        const float v = (f.add_x * old + f.apply * x[j]) * inv;
+        const int64_t e = base + (p.flip ? c * C + r : r * C + c);
         if constexpr (MUON) {
           a.W[e] = a.decay * a.W[e] - a.size * v;
         } else {
@@ -796,12 +936,12 @@ double poly_bound(double a, double b, double c, double top) {
   return most;
 }
 
-// The largest |b q + c q^2| over 0 <= q <= top.
-double quad_bound(double b, double c, double top) {
-  auto f = [&](double q) { return std::fabs(q * (b + q * c)); };
-  double most = f(top);
-  if (c != 0.0) {
-    const double q = -b / (2 * c);
+// The largest |x + y q + z q^2| over 0 <= q <= top.
+double quad_bound(double x, double y, double z, double top) {
+  auto f = [&](double q) { return std::fabs(x + q * (y + q * z)); };
+  double most = std::max(f(0.0), f(top));
+  if (z != 0.0) {
+    const double q = -y / (2 * z);
     if (q > 0.0 && q < top) most = std::max(most, f(q));
   }
   return most;
@@ -918,8 +1058,8 @@ hipError_t launch_product_t(const ProductArgs& p, int64_t tiles, hipStream_t s) 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups == tiles) return e;
   if constexpr (TILE == 128)
-    hipLaunchKernelGGL(ortho_fixup_kernel<TILE>, dim3((unsigned)(p.groups - 1), S::kBA * S::kBO),
-                     dim3(S::kNT), 0, s, p);
+    hipLaunchKernelGGL(ortho_fixup_kernel<TILE>, dim3((unsigned)(p.groups - 1), S::kBA), dim3(S::kNT),
+                       stage_bytes<TILE>(), s, p);
   return hipGetLastError();
 }
 
@@ -938,13 +1078,18 @@ hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int64_t g
 template <class E, bool MUON>
 hipError_t launch_input(const OrthoArgs& a, const Plan& p, double* part, float* unit, Pair X,
                         float pow_x, hipStream_t s) {
-  hipLaunchKernelGGL((ortho_norm_kernel<E, MUON>), dim3((unsigned)p.nb, (unsigned)a.n), dim3(256), 0,
-                     s, a, part);
+  const dim3 grid((unsigned)p.nb, (unsigned)a.n);
+  if (a.R * a.C % 4 == 0) hipLaunchKernelGGL((ortho_norm_kernel<E, MUON, 4>), grid, dim3(256), 0, s, a, part);
+  else hipLaunchKernelGGL((ortho_norm_kernel<E, MUON, 1>), grid, dim3(256), 0, s, a, part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t blocks = std::min<int64_t>(2048, (p.Rp * p.Cp / 4 + 255) / 256);
-  hipLaunchKernelGGL((ortho_split_kernel<E, MUON>), dim3((unsigned)blocks, (unsigned)a.n), dim3(256),
-                     0, s, a, (const double*)part, p.nb, X, p.Rp, p.Cp, pow_x, unit);
+  const dim3 blocks((unsigned)std::min<int64_t>(8192, (p.Rp * p.Cp / 4 + 1023) / 1024), (unsigned)a.n);
+  if (a.C % 4 == 0)
+    hipLaunchKernelGGL((ortho_split_kernel<E, MUON, 4>), blocks, dim3(256), 0, s, a, (const double*)part,
+                       p.nb, X, (int)p.Rp, (int)p.Cp, pow_x, unit);
+  else
+    hipLaunchKernelGGL((ortho_split_kernel<E, MUON, 1>), blocks, dim3(256), 0, s, a, (const double*)part,
+                       p.nb, X, (int)p.Rp, (int)p.Cp, pow_x, unit);
   return hipGetLastError();
 }
 
@@ -955,7 +1100,8 @@ bool ortho_coeffs_ok(const OrthoArgs& a) {
   for (int k = 0; k < a.steps; ++k) {
     top = kRoom * poly_bound(a.a, a.b, a.c, top);
     if (!(top <= 4.0)) return false;
-    if (!(quad_bound(a.b, a.c, top * top) <= 1e4)) return false;
+    if (!(quad_bound(a.a, a.b, a.c, top * top) <= 1e4)) return false;
+    if (a.c != 0.0 && !(std::fabs(a.b / (2 * a.c)) <= 1e4)) return false;
   }
   return true;
 }
@@ -964,25 +1110,42 @@ size_t ortho_workspace_bytes(const OrthoArgs& a) { return plan_of(a).total; }
 
 namespace {
 
-// The powers of two that X, A and B are kept with in each step, and what the
-// products' results are multiplied by.
-struct StepScale {
-  int x, a, b, next;
-  StepFactors f;
-};
-StepScale step_scale(const OrthoArgs& a, double* top, int sx, bool last) {
-  StepScale s;
-  s.x = sx;
-  s.a = scale_of(kRoom * *top * *top);
-  s.b = scale_of(kRoom * quad_bound(a.b, a.c, *top * *top));
+// The factors of a step whose X is kept times 2^sx with singular values up to
+// *top; *top and the power of the next X come back.  A' and B are kept times
+// the powers that their largest values allow.
+StepFactors step_factors(const OrthoArgs& a, double* top, int* sx, bool last) {
+  const double most = *top * *top;                // of A's eigenvalues
+  const bool square = a.c != 0.0;
+  const double shift = square ? a.b / (2 * a.c) : 0.0;
+  const int sb = scale_of(kRoom * quad_bound(a.a, a.b, a.c, most));
+  const int sa = square ? scale_of(kRoom * quad_bound(shift, 1.0, 0.0, most)) : sb;
   *top = kRoom * poly_bound(a.a, a.b, a.c, *top);
-  s.next = last ? 0 : scale_of(kRoom * *top);
-  s.f.gram = (float)std::ldexp(1.0, s.a - 2 * s.x);
-  s.f.add_b = (float)(a.b * std::ldexp(1.0, s.b - s.a));
-  s.f.square = (float)(a.c * std::ldexp(1.0, s.b - 2 * s.a));
-  s.f.add_x = (float)(a.a * std::ldexp(1.0, s.next - s.x));
-  s.f.apply = (float)std::ldexp(1.0, s.next - s.b - s.x);
-  return s;
+  const int next = last ? 0 : scale_of(kRoom * *top);
+  StepFactors f;
+  f.gram = (float)((square ? 1.0 : a.b) * std::ldexp(1.0, sa - 2 * *sx));
+  f.gram_shift = (float)((square ? shift : a.a) * std::ldexp(1.0, sa));
+  f.square = (float)(a.c * std::ldexp(1.0, sb - 2 * sa));
+  // from the shift as it was rounded, so that the two cancel in full
+  const double rounded = std::ldexp((double)f.gram_shift, -sa);
+  f.square_shift = square ? (float)((a.a - a.c * rounded * rounded) * std::ldexp(1.0, sb)) : 0.f;
+  f.apply = (float)std::ldexp(1.0, next - sb - *sx);
+  *sx = next;
+  return f;
+}
+
+AddFactors add_factors(const OrthoArgs& a, double* top, int* sx, bool last) {
+  const double most = *top * *top;
+  const int sa = scale_of(kRoom * most), sb = scale_of(kRoom * quad_bound(0.0, a.b, a.c, most));
+  *top = kRoom * poly_bound(a.a, a.b, a.c, *top);
+  const int next = last ? 0 : scale_of(kRoom * *top);
+  AddFactors f;
+  f.gram = (float)std::ldexp(1.0, sa - 2 * *sx);
+  f.add_b = (float)(a.b * std::ldexp(1.0, sb - sa));
+  f.square = (float)(a.c * std::ldexp(1.0, sb - 2 * sa));
+  f.add_x = (float)(a.a * std::ldexp(1.0, next - *sx));
+  f.apply = (float)std::ldexp(1.0, next - sb - *sx);
+  *sx = next;
+  return f;
 }
 
 template <class E, bool MUON>
@@ -1009,11 +1172,7 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     q.mp = (int)up(q.m, 32);
     q.kp = (int)up(q.k, 32);
     q.pow_x = std::ldexp(1.f, sx);
-    for (int k = 0; k < a.steps; ++k) {
-      const StepScale c = step_scale(a, &top, sx, k + 1 == a.steps);
-      q.f[k] = c.f;
-      sx = c.next;
-    }
+    for (int k = 0; k < a.steps; ++k) q.f[k] = add_factors(a, &top, &sx, k + 1 == a.steps);
     timing_begin("ortho_small", s);
     const hipError_t e = a.W != nullptr       ? launch_small<F32, true>(q, p.small, s)
                          : a.dtype == kBF16 ? launch_small<BF16, false>(q, p.small, s)
@@ -1039,47 +1198,48 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
     const Pair& Xk = X[k & 1];
     const bool last = k + 1 == a.steps;
-    const StepScale c = step_scale(a, &top, sx, last);
+    const StepFactors f = step_factors(a, &top, &sx, last);
     ProductArgs q{};
     q.unit = unit;
     q.parts = (float*)(ws + p.parts);
-    // A = X X^T (R <= C: K-inner) or X^T X (K-outer)
+    // A' from X X^T (R <= C: K-inner) or X^T X (K-outer)
     q.L = q.R = Xk;
-    q.out = q.add = A;
+    q.out = A;
     q.steps = (int)((p.flip ? p.Rp : p.Cp) / 16);
     q.mt = q.nt = mt;
     q.sym = 1;
     q.mode = kStore;
     q.units = 2;
-    q.f1 = c.f.gram;
+    q.f = f.gram;
+    q.shift = f.gram_shift;
     timing_begin("ortho_gram", s);
     e = launch_product(q, p.tile, !p.flip, a.n, p.groups_sym, s);
     timing_end("ortho_gram", s);
     if (e != hipSuccess) break;
-    // B = b A + c A A
-    q.L = q.R = q.add = A;
-    q.out = B;
-    q.steps = (int)(p.mp / 16);
-    q.mode = kAddStore;
-    q.units = 0;
-    q.f0 = c.f.add_b;
-    q.f1 = c.f.square;
-    timing_begin("ortho_square", s);
-    e = launch_product(q, p.tile, !p.flip, a.n, p.groups_square, s);
-    timing_end("ortho_square", s);
-    if (e != hipSuccess) break;
-    // X <- a X + B X (K-outer) or a X + X B (K-inner)
-    q.L = p.flip ? Xk : B;
-    q.R = p.flip ? B : Xk;
-    q.add = Xk;
+    const bool square = a.c != 0.0;
+    if (square) {
+      q.L = q.R = A;
+      q.out = B;
+      q.steps = (int)(p.mp / 16);
+      q.units = 0;
+      q.f = f.square;
+      q.shift = f.square_shift;
+      timing_begin("ortho_square", s);
+      e = launch_product(q, p.tile, !p.flip, a.n, p.groups_square, s);
+      timing_end("ortho_square", s);
+      if (e != hipSuccess) break;
+    }
+    // X <- B X (K-outer) or X B (K-inner)
+    q.L = p.flip ? Xk : square ? B : A;
+    q.R = p.flip ? (square ? B : A) : Xk;
     q.out = X[(k + 1) & 1];
+    q.steps = (int)(p.mp / 16);
     q.mt = (int)(p.Rp / p.tile);
     q.nt = (int)(p.Cp / p.tile);
     q.sym = 0;
-    q.mode = last ? kFinal : kAddStore;
+    q.mode = last ? kFinal : kStore;
     q.units = last ? 1 : 0;
-    q.f0 = c.f.add_x;
-    q.f1 = c.f.apply;
+    q.f = f.apply;
     q.rows = a.R;
     q.cols = a.C;
     q.dst = a.W != nullptr ? (void*)a.W : a.out;
@@ -1090,7 +1250,6 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     timing_begin("ortho_apply", s);
     e = launch_product(q, p.tile, p.flip, a.n, p.groups_full, s);
     timing_end("ortho_apply", s);
-    sx = c.next;
   }
   return e;
 }
