@@ -240,11 +240,10 @@ struct ProductArgs {
 
 constexpr int kSlots = 5;
 constexpr int kAhead = 4;            // steps between a slot's load and its use
-constexpr int kDmaPerStep = 4;       // of one wave: two per operand
 
-template <int TILE>
+template <int TILE, int WAVES>
 struct Shape {
-  static constexpr int kWaves = TILE == 256 ? 8 : 4;
+  static constexpr int kTile = TILE, kWaves = WAVES;
   static constexpr int kNT = kWaves * 64;
   static constexpr int kWR = 2, kWC = kWaves / 2;           // wave grid, M by N
   static constexpr int kBA = TILE / kWR / 32, kBO = TILE / kWC / 32;   // 32 x 32 blocks of a wave
@@ -252,7 +251,8 @@ struct Shape {
   static constexpr int kSlotBytes = 2 * kOpBytes;
   static constexpr int kLds = kSlots * kSlotBytes;
   static constexpr int kFloats = TILE * TILE;               // one tile's accumulators
-  static_assert(kOpBytes == 2 * 1024 * kWaves, "two 1 KiB loads per wave and operand");
+  static constexpr int kDma = kOpBytes / 1024 / kWaves;     // loads of a wave per operand and step
+  static_assert(kOpBytes == kDma * 1024 * kWaves, "whole 1 KiB loads");
 };
 
 // 16 bytes per lane from rsrc at voffset straight into LDS at m0 + 16 * lane;
@@ -264,13 +264,15 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff
                : "memory");
 }
 
-// Until at most `steps` of this wave's latest steps are in flight.
+// Until at most `steps` of this wave's latest steps (of LOADS loads) are in
+// flight.
+template <int LOADS>
 __device__ __forceinline__ void wait_dma(int steps) {
-  static_assert(kDmaPerStep == 4, "the counts below");
+  static_assert(LOADS == 4 || LOADS == 2, "the counts below");
   if (steps <= 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  else if (steps == 1) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-  else if (steps == 2) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-  else asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+  else if (steps == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+  else if (steps == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * LOADS) : "memory");
+  else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * LOADS) : "memory");
 }
 
 // A barrier without the compiler's wait for every outstanding LDS read: what
@@ -296,20 +298,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
 //            bits 2 and 3 inverted by k's low bits (four rows of a transposing
 //            read fall on different banks) and the hi/lo bit by bit 2 (so do
 //            the two 16-column halves of a block).
-template <int TILE, bool KI>
+template <class S, bool KI>
 struct Operand {
-  using S = Shape<TILE>;
+  static constexpr int TILE = S::kTile;
   const char* base;               // this tile's next step
   int64_t step;                   // bytes between steps
-  uint32_t off[2];                // per lane: the wave's two loads
+  uint32_t off[S::kDma];          // per lane: the wave's loads
   __device__ __forceinline__ void start(const Pair& p, int64_t m0, int64_t k0) {
     const int64_t ldb = p.ld * 2;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     base = (const char*)p.p + (KI ? m0 * ldb + k0 * 64 : m0 * 4 + k0 * 16 * ldb);
     step = KI ? 64 : 16 * ldb;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int d = wave * 2 + j;
+    for (int j = 0; j < S::kDma; ++j) {
+      const int d = wave * S::kDma + j;
       if constexpr (KI) {
         const int row = d * 16 + (lane >> 2), c = (lane & 3) ^ ((row >> 2) & 3);
         off[j] = (uint32_t)(row * ldb + c * 16);
@@ -320,23 +322,16 @@ struct Operand {
       }
     }
   }
-  __device__ __forceinline__ void load(uint32_t lds) {
+  // Load j of the next step into its slot; the last one moves on.
+  __device__ __forceinline__ void load(int j, uint32_t lds) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // The same in every lane; the compiler computes tile indices in vector
-    // registers and has to be told.
-    const uint64_t at = (uint64_t)base;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-    const __amdgpu_buffer_rsrc_t r = rsrc_of((const void*)(((uint64_t)hi << 32) | lo));
-    lds = __builtin_amdgcn_readfirstlane(lds);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) dma16(r, off[j], lds + (uint32_t)(wave * 2 + j) * 1024u);
-    base += step;
+    dma16(rsrc_of(base), off[j], lds + (uint32_t)(wave * S::kDma + j) * 1024u);
+    if (j + 1 == S::kDma) base += step;
   }
 };
 
-// This lane's fragment reads of an operand: blocks of 32 from block `b0` on
-// (even), the hi half at the address and lo at address ^ 32.
+// This lane's fragment reads of an operand: blocks of 32 from block `b0` on, the
+// hi half at the address and lo at address ^ 32.
 template <int TILE, bool KI>
 struct FragLane {
   uint32_t even, odd;             // for blocks b0 + 0, 2, .. and b0 + 1, 3, ..
@@ -350,8 +345,9 @@ struct FragLane {
       const int lp = ((lane >> 4) & 1) * 4 + ((lane & 3) >> 1);
       const int c = lp ^ (((lp >> 2) & 1) << 1) ^ ((k & 1) << 2);
       const uint32_t at = (uint32_t)(k * TILE * 4 + b0 * 128 + c * 16 + (lane & 1) * 8);
-      even = at + (uint32_t)(kb * 128);
-      odd = at - (uint32_t)(kb * 128);
+      const uint32_t swap = (uint32_t)(kb * 128);      // an even block and the next change places
+      even = (b0 & 1) ? at - swap : at + swap;
+      odd = (b0 & 1) ? at + swap : at - swap;
     }
   }
   template <int I>
@@ -421,11 +417,11 @@ constexpr int stage_bytes() {
   return rows > mirror ? rows : mirror;
 }
 
-template <int TILE>
+template <class S>
 __device__ __forceinline__ void store_rows(const ProductArgs& p, int64_t mat, int ti, int tj, int i,
-                                           const f32x16 (&acc)[Shape<TILE>::kBO],
+                                           const f32x16 (&acc)[S::kBO],
                                            unsigned char* lds) {
-  using S = Shape<TILE>;
+  constexpr int TILE = S::kTile;
   static_assert(S::kWR * 32 == kStageRows, "two blocks of 32 rows");
   static_assert(stage_bytes<TILE>() <= S::kLds, "the stage fits into the ring");
   constexpr int kLine = TILE * 4 + 16, kMirrorLine = kStageRows * 4 + 16;
@@ -542,10 +538,11 @@ __device__ __forceinline__ void store_rows(const ProductArgs& p, int64_t mat, in
 
 __device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-template <int TILE, bool KI>
-__global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(ProductArgs p) {
+template <int TILE, int WAVES, bool KI>
+__global__ void __launch_bounds__(WAVES * 64, 2) ortho_product_kernel(ProductArgs p) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
-  using S = Shape<TILE>;
+  using S = Shape<TILE, WAVES>;
+  constexpr int kLoads = 2 * S::kDma;
   constexpr int BA = S::kBA, BO = S::kBO;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = logical_group(blockIdx.x, p.groups);
@@ -564,7 +561,7 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(Prod
     tile_of(p, (int)(tile - (int64_t)mat * p.tiles), &ti, &tj);
     ti = __builtin_amdgcn_readfirstlane(ti);
     tj = __builtin_amdgcn_readfirstlane(tj);
-    Operand<TILE, KI> ol, orr;
+    Operand<S, KI> ol, orr;
     ol.start(p.L.at(mat), (int64_t)ti * TILE, k0);
     orr.start(p.R.at(mat), (int64_t)tj * TILE, k0);
     f32x16 acc[BA][BO];
@@ -575,104 +572,123 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(Prod
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     if (!first) __syncthreads();                 // the last piece's slots are read
-    auto issue = [&](int s) {
-      const uint32_t slot = lds0 + (uint32_t)(s % kSlots) * S::kSlotBytes;
-      ol.load(slot);
-      orr.load(slot + S::kOpBytes);
+    // Load d (operand d % 2) of a step, into the slot at `to`.
+    auto dma = [&](int d, uint32_t to) {
+      if (d & 1) orr.load(d >> 1, to + S::kOpBytes);
+      else ol.load(d >> 1, to);
     };
     const int ahead = min(kAhead, n);
-    for (int s = 0; s < ahead; ++s) issue(s);
-    wait_dma(ahead - 1);
+    for (int s = 0; s < ahead; ++s)
+#pragma unroll
+      for (int d = 0; d < kLoads; ++d) dma(d, lds0 + (uint32_t)s * S::kSlotBytes);
+    wait_dma<kLoads>(ahead - 1);
     step_barrier();
-    u16x8 L[2][2], R[2][BO][2];                  // [buffer][hi, lo]; R by block
+    // Fragments [.. block][hi, lo]: of the step at hand and, as they are used
+    // up, of the next.
+    constexpr int NL = BA == 4 ? 1 : 2;
+    u16x8 L[NL][BA][2], R[2][BO][2];
+    auto read_l = [&](auto buf, auto i, int lo, const unsigned char* slot) {
+      L[decltype(buf)::value][decltype(i)::value][lo] = fl.template read<decltype(i)::value>(slot, lo != 0);
+    };
+    auto read_r = [&](auto buf, auto j, int lo, const unsigned char* slot) {
+      R[decltype(buf)::value][decltype(j)::value][lo] =
+          fr.template read<decltype(j)::value>(slot + S::kOpBytes, lo != 0);
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+#pragma unroll
+    for (int lo = 0; lo < 2; ++lo) {
+      read_r(I0(), I0(), lo, lds);
+      if constexpr (BO > 1) read_r(I0(), I1(), lo, lds);
+      read_l(I0(), I0(), lo, lds);
+      read_l(I0(), I1(), lo, lds);
+    }
     int slot = 0;
-    L[0][0] = fl.template read<0>(lds, false);
-    L[0][1] = fl.template read<0>(lds, true);
-    R[0][0][0] = fr.template read<0>(lds + S::kOpBytes, false);
-    R[0][0][1] = fr.template read<0>(lds + S::kOpBytes, true);
-    R[0][1][0] = fr.template read<1>(lds + S::kOpBytes, false);
-    R[0][1][1] = fr.template read<1>(lds + S::kOpBytes, true);
-    // One step; PAR: its buffer of R.  Block row i's products run while block
-    // row i + 1's fragments (from the middle on also the next step's) are read.
+    uint32_t fill = lds0 + kAhead * S::kSlotBytes;      // where step t + kAhead goes
+    // One step.  Between any two MFMAs at most one fragment read or one load is
+    // issued: all waves pass the barrier together, and a burst of them there
+    // would leave the matrix units waiting.
     auto step = [&](int t, auto par) {
-      constexpr int PAR = decltype(par)::value;
+      using P = decltype(par);
+      using Q = std::integral_constant<int, P::value ^ 1>;
       const unsigned char* cur = lds + slot * S::kSlotBytes;
-      const int nslot = slot + 1 == kSlots ? 0 : slot + 1;
-      const unsigned char* next = lds + nslot * S::kSlotBytes;
-      const bool more = t + 1 < n;
-      auto products = [&](int i, const u16x8 (&l)[2]) {
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+      const unsigned char* next = lds + slot * S::kSlotBytes;
+      const bool more = t + 1 < n, load = t + kAhead < n;
+      // Block row i: lo hi, hi lo, hi hi; `then(k)` after MFMA k.
+      auto products = [&](int i, const u16x8 (&l)[2], auto&& then) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q)              // lo hi, hi lo, hi hi
-#pragma unroll
-          for (int j = 0; j < BO; ++j)
-            acc[i][j] = mma16(R[PAR][j][q == 0 ? 1 : 0], l[q == 1 ? 1 : 0], acc[i][j]);
+        for (int k = 0; k < 3 * BO; ++k) {
+          const int q = k / BO, j = k % BO;
+          acc[i][j] = mma16(R[P::value][j][q == 0 ? 1 : 0], l[q == 1 ? 1 : 0], acc[i][j]);
+          sched_fence();
+          then(k);
+          sched_fence();
+        }
       };
-      auto middle = [&]() {
+      auto barrier = [&]() {
         if (more) {
-          wait_dma(min(n - 2 - t, kAhead - 2));
+          wait_dma<kLoads>(min(n - 2 - t, kAhead - 2));
           step_barrier();
-          if (t + kAhead < n) issue(t + kAhead);
         }
       };
       if constexpr (BA == 4) {
-        L[1][0] = fl.template read<1>(cur, false);
-        L[1][1] = fl.template read<1>(cur, true);
-        sched_fence();
-        products(0, L[0]);
-        sched_fence();
-        L[0][0] = fl.template read<2>(cur, false);
-        L[0][1] = fl.template read<2>(cur, true);
-        sched_fence();
-        products(1, L[1]);
-        sched_fence();
-        L[1][0] = fl.template read<3>(cur, false);
-        L[1][1] = fl.template read<3>(cur, true);
-        sched_fence();
-        middle();
-        if (more) {
-          R[PAR ^ 1][0][0] = fr.template read<0>(next + S::kOpBytes, false);
-          R[PAR ^ 1][0][1] = fr.template read<0>(next + S::kOpBytes, true);
-        }
-        sched_fence();
-        products(2, L[0]);
-        sched_fence();
-        if (more) {
-          L[0][0] = fl.template read<0>(next, false);
-          L[0][1] = fl.template read<0>(next, true);
-          R[PAR ^ 1][1][0] = fr.template read<1>(next + S::kOpBytes, false);
-          R[PAR ^ 1][1][1] = fr.template read<1>(next + S::kOpBytes, true);
-        }
-        sched_fence();
-        products(3, L[1]);
-        sched_fence();
+        products(0, L[0][0], [&](int k) {
+          if (k < 2) read_l(I0(), I2(), k, cur);
+        });
+        products(1, L[0][1], [&](int k) {
+          if (k < 2) read_l(I0(), I3(), k, cur);
+        });
+        barrier();
+        products(2, L[0][2], [&](int k) {
+          if (k == 0 || k == 2) {
+            if (load) dma(k / 2, fill);
+          } else if (more) {
+            if (k == 1 || k == 3) read_r(Q(), I0(), k >> 1, next);
+            else read_r(Q(), I1(), k & 1, next);
+          }
+        });
+        products(3, L[0][3], [&](int k) {
+          if (k == 0 || k == 2) {
+            if (load) dma(2 + k / 2, fill);
+          } else if (more) {
+            if (k == 1 || k == 3) read_l(I0(), I0(), k >> 1, next);
+            else read_l(I0(), I1(), k & 1, next);
+          }
+        });
       } else {
-        L[1][0] = fl.template read<1>(cur, false);
-        L[1][1] = fl.template read<1>(cur, true);
-        sched_fence();
-        products(0, L[0]);
-        sched_fence();
-        middle();
-        if (more) {
-          L[0][0] = fl.template read<0>(next, false);
-          L[0][1] = fl.template read<0>(next, true);
-          R[PAR ^ 1][0][0] = fr.template read<0>(next + S::kOpBytes, false);
-          R[PAR ^ 1][0][1] = fr.template read<0>(next + S::kOpBytes, true);
-          R[PAR ^ 1][1][0] = fr.template read<1>(next + S::kOpBytes, false);
-          R[PAR ^ 1][1][1] = fr.template read<1>(next + S::kOpBytes, true);
-        }
-        sched_fence();
-        products(1, L[1]);
-        sched_fence();
+        // everything of the next step is read during this one
+        barrier();
+        products(0, L[P::value][0], [&](int k) {
+          if (more) {
+            if (k < 2) read_r(Q(), I0(), k, next);
+            if constexpr (BO > 1)
+              if (k == 2 || k == 3) read_r(Q(), I1(), k & 1, next);
+          }
+          if (load && k >= 3 * BO - kLoads / 2) dma(k - (3 * BO - kLoads / 2), fill);
+        });
+        products(1, L[P::value][1], [&](int k) {
+          if (more) {
+            if (k < 2) read_l(Q(), I0(), k, next);
+            if (BO > 1 ? (k == 2 || k == 3) : k == 2) {
+              read_l(Q(), I1(), BO > 1 ? k & 1 : 0, next);
+              if (BO == 1) read_l(Q(), I1(), 1, next);
+            }
+          }
+          if (load && k >= 3 * BO - kLoads / 2) dma(kLoads / 2 + k - (3 * BO - kLoads / 2), fill);
+        });
       }
-      slot = nslot;
+      fill = fill == lds0 + (kSlots - 1) * S::kSlotBytes ? lds0 : fill + S::kSlotBytes;
     };
     for (int t = 0; t < n; t += 2) {
-      step(t, std::integral_constant<int, 0>());
-      if (t + 1 < n) step(t + 1, std::integral_constant<int, 1>());
+      step(t, I0());
+      if (t + 1 < n) step(t + 1, I1());
     }
     if (n == p.steps) {
 #pragma unroll
-      for (int i = 0; i < BA; ++i) store_rows<TILE>(p, mat, ti, tj, i, acc[i], lds);
+      for (int i = 0; i < BA; ++i) store_rows<S>(p, mat, ti, tj, i, acc[i], lds);
     } else {
       // part: four accumulators of every thread side by side
       float* o = p.parts + (int64_t)(2 * w + (first ? 0 : 1)) * S::kFloats + threadIdx.x * 4;
@@ -692,9 +708,9 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT, 2) ortho_product_kernel(Prod
 
 // The tiles that workgroups share: their parts in order, then as above.  One
 // workgroup per first inner boundary of a tile and block row of its waves.
-template <int TILE>
-__global__ void __launch_bounds__(Shape<TILE>::kNT) ortho_fixup_kernel(ProductArgs p) {
-  using S = Shape<TILE>;
+template <int TILE, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64) ortho_fixup_kernel(ProductArgs p) {
+  using S = Shape<TILE, WAVES>;
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   const int b = blockIdx.x + 1, i = blockIdx.y;
   const int64_t s = first_step(p, b), tile = s / p.steps, begin = tile * p.steps;
@@ -719,7 +735,7 @@ __global__ void __launch_bounds__(Shape<TILE>::kNT) ortho_fixup_kernel(ProductAr
   const int64_t mat = tile / p.tiles;
   int ti, tj;
   tile_of(p, (int)(tile - mat * p.tiles), &ti, &tj);
-  store_rows<TILE>(p, mat, ti, tj, i, acc, lds);
+  store_rows<S>(p, mat, ti, tj, i, acc, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -1047,20 +1063,26 @@ Plan plan_of(const OrthoArgs& a) {
   return p;
 }
 
-template <int TILE, bool KI>
+template <int TILE, int WAVES, bool KI>
 hipError_t launch_product_t(const ProductArgs& p, int64_t tiles, hipStream_t s) {
-  using S = Shape<TILE>;
-  static hipError_t once = hipFuncSetAttribute((const void*)ortho_product_kernel<TILE, KI>,
+  using S = Shape<TILE, WAVES>;
+  static hipError_t once = hipFuncSetAttribute((const void*)ortho_product_kernel<TILE, WAVES, KI>,
                                                hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (once != hipSuccess) return once;
-  hipLaunchKernelGGL((ortho_product_kernel<TILE, KI>), dim3((unsigned)p.groups), dim3(S::kNT), S::kLds,
-                     s, p);
+  hipLaunchKernelGGL((ortho_product_kernel<TILE, WAVES, KI>), dim3((unsigned)p.groups), dim3(S::kNT),
+                     S::kLds, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups == tiles) return e;
   if constexpr (TILE == 128)
-    hipLaunchKernelGGL(ortho_fixup_kernel<TILE>, dim3((unsigned)(p.groups - 1), S::kBA), dim3(S::kNT),
-                       stage_bytes<TILE>(), s, p);
+    hipLaunchKernelGGL((ortho_fixup_kernel<TILE, WAVES>), dim3((unsigned)(p.groups - 1), S::kBA),
+                       dim3(S::kNT), stage_bytes<TILE>(), s, p);
   return hipGetLastError();
+}
+
+template <int TILE, int WAVES>
+hipError_t launch_product_w(const ProductArgs& p, bool ki, int64_t tiles, hipStream_t s) {
+  return ki ? launch_product_t<TILE, WAVES, true>(p, tiles, s)
+            : launch_product_t<TILE, WAVES, false>(p, tiles, s);
 }
 
 hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int64_t groups,
@@ -1069,10 +1091,10 @@ hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int64_t g
   const int64_t tiles = p.tiles * n;
   p.total = tiles * p.steps;
   p.groups = (int)groups;
-  if (groups == 1 && tiles > 1) return hipErrorInvalidValue;
-  if (tile == 256)
-    return ki ? launch_product_t<256, true>(p, tiles, s) : launch_product_t<256, false>(p, tiles, s);
-  return ki ? launch_product_t<128, true>(p, tiles, s) : launch_product_t<128, false>(p, tiles, s);
+  if (tile == 256) return launch_product_w<256, 8>(p, ki, tiles, s);
+  static const int w8 = getenv("ORTHO_W8") ? atoi(getenv("ORTHO_W8")) : 0;
+  if (w8) return launch_product_w<128, 8>(p, ki, tiles, s);
+  return launch_product_w<128, 4>(p, ki, tiles, s);
 }
 
 template <class E, bool MUON>
