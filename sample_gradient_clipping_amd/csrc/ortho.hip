@@ -238,12 +238,10 @@ struct ProductArgs {
   float decay, size;
 };
 
-constexpr int kSlots = 5;
-constexpr int kAhead = 4;            // steps between a slot's load and its use
-
-template <int TILE, int WAVES>
+template <int TILE, int WAVES, int SLOTS>
 struct Shape {
-  static constexpr int kTile = TILE, kWaves = WAVES;
+  static constexpr int kTile = TILE, kWaves = WAVES, kSlots = SLOTS;
+  static constexpr int kAhead = kSlots - 1;                 // steps between a slot's load and its use
   static constexpr int kNT = kWaves * 64;
   static constexpr int kWR = 2, kWC = kWaves / 2;           // wave grid, M by N
   static constexpr int kBA = TILE / kWR / 32, kBO = TILE / kWC / 32;   // 32 x 32 blocks of a wave
@@ -252,7 +250,7 @@ struct Shape {
   static constexpr int kLds = kSlots * kSlotBytes;
   static constexpr int kFloats = TILE * TILE;               // one tile's accumulators
   static constexpr int kDma = kOpBytes / 1024 / kWaves;     // loads of a wave per operand and step
-  static_assert(kOpBytes == kDma * 1024 * kWaves, "whole 1 KiB loads");
+  static_assert(kOpBytes == 2 * 1024 * kWaves && kBO == 2, "the main loop's order of reads and loads");
 };
 
 // 16 bytes per lane from rsrc at voffset straight into LDS at m0 + 16 * lane;
@@ -264,15 +262,11 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff
                : "memory");
 }
 
-// Until at most `steps` of this wave's latest steps (of LOADS loads) are in
-// flight.
+// Until at most LOADS of this wave's latest loads are in flight.
 template <int LOADS>
-__device__ __forceinline__ void wait_dma(int steps) {
-  static_assert(LOADS == 4 || LOADS == 2, "the counts below");
-  if (steps <= 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  else if (steps == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
-  else if (steps == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * LOADS) : "memory");
-  else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * LOADS) : "memory");
+__device__ __forceinline__ void wait_dma() {
+  static_assert(LOADS < 64, "the counter's range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
 }
 
 // A barrier without the compiler's wait for every outstanding LDS read: what
@@ -287,8 +281,9 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char*)p;
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7fffffff, 0x00020000);
+// `live` false: a buffer of no bytes, whose loads touch no memory and give 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, bool live) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, live ? 0x7fffffff : 0, 0x00020000);
 }
 
 // LDS image of one operand's step, and its loads.
@@ -323,9 +318,8 @@ struct Operand {
     }
   }
   // Load j of the next step into its slot; the last one moves on.
-  __device__ __forceinline__ void load(int j, uint32_t lds) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    dma16(rsrc_of(base), off[j], lds + (uint32_t)(wave * S::kDma + j) * 1024u);
+  __device__ __forceinline__ void load(int j, uint32_t lds, int wave, bool live) {
+    dma16(rsrc_of(base, live), off[j], lds + (uint32_t)(wave * S::kDma + j) * 1024u);
     if (j + 1 == S::kDma) base += step;
   }
 };
@@ -538,11 +532,10 @@ __device__ __forceinline__ void store_rows(const ProductArgs& p, int64_t mat, in
 
 __device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-template <int TILE, int WAVES, bool KI>
-__global__ void __launch_bounds__(WAVES * 64, 2) ortho_product_kernel(ProductArgs p) {
+template <class S, bool KI>
+__global__ void __launch_bounds__(S::kNT, 2) ortho_product_kernel(ProductArgs p) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
-  using S = Shape<TILE, WAVES>;
-  constexpr int kLoads = 2 * S::kDma;
+  constexpr int TILE = S::kTile, kLoads = 2 * S::kDma, kAhead = S::kAhead, kSlots = S::kSlots;
   constexpr int BA = S::kBA, BO = S::kBO;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = logical_group(blockIdx.x, p.groups);
@@ -572,16 +565,17 @@ __global__ void __launch_bounds__(WAVES * 64, 2) ortho_product_kernel(ProductArg
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     if (!first) __syncthreads();                 // the last piece's slots are read
-    // Load d (operand d % 2) of a step, into the slot at `to`.
-    auto dma = [&](int d, uint32_t to) {
-      if (d & 1) orr.load(d >> 1, to + S::kOpBytes);
-      else ol.load(d >> 1, to);
+    // Load d (operand d % 2) of a step, into the slot at `to`.  Steps past the
+    // last are loaded too, as nothing (`live`): the loop has no branch then,
+    // and a wave always has the same number of loads in flight.
+    auto dma = [&](int d, uint32_t to, bool live) {
+      if (d & 1) orr.load(d >> 1, to + S::kOpBytes, wave, live);
+      else ol.load(d >> 1, to, wave, live);
     };
-    const int ahead = min(kAhead, n);
-    for (int s = 0; s < ahead; ++s)
+    for (int s = 0; s < kAhead; ++s)
 #pragma unroll
-      for (int d = 0; d < kLoads; ++d) dma(d, lds0 + (uint32_t)s * S::kSlotBytes);
-    wait_dma<kLoads>(ahead - 1);
+      for (int d = 0; d < kLoads; ++d) dma(d, lds0 + (uint32_t)s * S::kSlotBytes, s < n);
+    wait_dma<kLoads * (kAhead - 1)>();
     step_barrier();
     // Fragments [.. block][hi, lo]: of the step at hand and, as they are used
     // up, of the next.
@@ -616,7 +610,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) ortho_product_kernel(ProductArg
       const unsigned char* cur = lds + slot * S::kSlotBytes;
       slot = slot + 1 == kSlots ? 0 : slot + 1;
       const unsigned char* next = lds + slot * S::kSlotBytes;
-      const bool more = t + 1 < n, load = t + kAhead < n;
+      const bool live = t + kAhead < n;
       // Block row i: lo hi, hi lo, hi hi; `then(k)` after MFMA k.
       auto products = [&](int i, const u16x8 (&l)[2], auto&& then) {
 #pragma unroll
@@ -629,10 +623,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) ortho_product_kernel(ProductArg
         }
       };
       auto barrier = [&]() {
-        if (more) {
-          wait_dma<kLoads>(min(n - 2 - t, kAhead - 2));
-          step_barrier();
-        }
+        wait_dma<kLoads * (kAhead - 2)>();
+        step_barrier();
       };
       if constexpr (BA == 4) {
         products(0, L[0][0], [&](int k) {
@@ -643,49 +635,38 @@ __global__ void __launch_bounds__(WAVES * 64, 2) ortho_product_kernel(ProductArg
         });
         barrier();
         products(2, L[0][2], [&](int k) {
-          if (k == 0 || k == 2) {
-            if (load) dma(k / 2, fill);
-          } else if (more) {
-            if (k == 1 || k == 3) read_r(Q(), I0(), k >> 1, next);
-            else read_r(Q(), I1(), k & 1, next);
-          }
+          if (k == 0 || k == 2) dma(k / 2, fill, live);
+          else if (k == 1 || k == 3) read_r(Q(), I0(), k >> 1, next);
+          else read_r(Q(), I1(), k & 1, next);
         });
         products(3, L[0][3], [&](int k) {
-          if (k == 0 || k == 2) {
-            if (load) dma(2 + k / 2, fill);
-          } else if (more) {
-            if (k == 1 || k == 3) read_l(I0(), I0(), k >> 1, next);
-            else read_l(I0(), I1(), k & 1, next);
-          }
+          if (k == 0 || k == 2) dma(2 + k / 2, fill, live);
+          else if (k == 1 || k == 3) read_l(I0(), I0(), k >> 1, next);
+          else read_l(I0(), I1(), k & 1, next);
         });
       } else {
         // everything of the next step is read during this one
         barrier();
         products(0, L[P::value][0], [&](int k) {
-          if (more) {
-            if (k < 2) read_r(Q(), I0(), k, next);
-            if constexpr (BO > 1)
-              if (k == 2 || k == 3) read_r(Q(), I1(), k & 1, next);
-          }
-          if (load && k >= 3 * BO - kLoads / 2) dma(k - (3 * BO - kLoads / 2), fill);
+          if (k < 2) read_r(Q(), I0(), k, next);
+          else if (k < 4) read_r(Q(), I1(), k & 1, next);
+          else dma(k - 4, fill, live);
         });
         products(1, L[P::value][1], [&](int k) {
-          if (more) {
-            if (k < 2) read_l(Q(), I0(), k, next);
-            if (BO > 1 ? (k == 2 || k == 3) : k == 2) {
-              read_l(Q(), I1(), BO > 1 ? k & 1 : 0, next);
-              if (BO == 1) read_l(Q(), I1(), 1, next);
-            }
-          }
-          if (load && k >= 3 * BO - kLoads / 2) dma(kLoads / 2 + k - (3 * BO - kLoads / 2), fill);
+          if (k < 2) read_l(Q(), I0(), k, next);
+          else if (k < 4) read_l(Q(), I1(), k & 1, next);
+          else dma(k - 2, fill, live);
         });
       }
       fill = fill == lds0 + (kSlots - 1) * S::kSlotBytes ? lds0 : fill + S::kSlotBytes;
     };
-    for (int t = 0; t < n; t += 2) {
+    int t = 0;
+    for (; t + 1 < n; t += 2) {
       step(t, I0());
-      if (t + 1 < n) step(t + 1, I1());
+      step(t + 1, I1());
     }
+    if (t < n) step(t, I0());
+    wait_dma<0>();                               // nothing is left in flight into LDS
     if (n == p.steps) {
 #pragma unroll
       for (int i = 0; i < BA; ++i) store_rows<S>(p, mat, ti, tj, i, acc[i], lds);
@@ -708,9 +689,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) ortho_product_kernel(ProductArg
 
 // The tiles that workgroups share: their parts in order, then as above.  One
 // workgroup per first inner boundary of a tile and block row of its waves.
-template <int TILE, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64) ortho_fixup_kernel(ProductArgs p) {
-  using S = Shape<TILE, WAVES>;
+template <class S>
+__global__ void __launch_bounds__(S::kNT) ortho_fixup_kernel(ProductArgs p) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   const int b = blockIdx.x + 1, i = blockIdx.y;
   const int64_t s = first_step(p, b), tile = s / p.steps, begin = tile * p.steps;
@@ -1063,26 +1043,23 @@ Plan plan_of(const OrthoArgs& a) {
   return p;
 }
 
-template <int TILE, int WAVES, bool KI>
-hipError_t launch_product_t(const ProductArgs& p, int64_t tiles, hipStream_t s) {
-  using S = Shape<TILE, WAVES>;
-  static hipError_t once = hipFuncSetAttribute((const void*)ortho_product_kernel<TILE, WAVES, KI>,
+template <class S, bool KI>
+hipError_t launch_product_k(const ProductArgs& p, int64_t tiles, hipStream_t s) {
+  static hipError_t once = hipFuncSetAttribute((const void*)ortho_product_kernel<S, KI>,
                                                hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (once != hipSuccess) return once;
-  hipLaunchKernelGGL((ortho_product_kernel<TILE, WAVES, KI>), dim3((unsigned)p.groups), dim3(S::kNT),
-                     S::kLds, s, p);
+  hipLaunchKernelGGL((ortho_product_kernel<S, KI>), dim3((unsigned)p.groups), dim3(S::kNT), S::kLds, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.groups == tiles) return e;
-  if constexpr (TILE == 128)
-    hipLaunchKernelGGL((ortho_fixup_kernel<TILE, WAVES>), dim3((unsigned)(p.groups - 1), S::kBA),
-                       dim3(S::kNT), stage_bytes<TILE>(), s, p);
+  if constexpr (S::kTile == 128)
+    hipLaunchKernelGGL((ortho_fixup_kernel<S>), dim3((unsigned)(p.groups - 1), S::kBA), dim3(S::kNT),
+                       stage_bytes<S::kTile>(), s, p);
   return hipGetLastError();
 }
 
-template <int TILE, int WAVES>
-hipError_t launch_product_w(const ProductArgs& p, bool ki, int64_t tiles, hipStream_t s) {
-  return ki ? launch_product_t<TILE, WAVES, true>(p, tiles, s)
-            : launch_product_t<TILE, WAVES, false>(p, tiles, s);
+template <class S>
+hipError_t launch_product_s(const ProductArgs& p, bool ki, int64_t tiles, hipStream_t s) {
+  return ki ? launch_product_k<S, true>(p, tiles, s) : launch_product_k<S, false>(p, tiles, s);
 }
 
 hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int64_t groups,
@@ -1091,10 +1068,9 @@ hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int64_t g
   const int64_t tiles = p.tiles * n;
   p.total = tiles * p.steps;
   p.groups = (int)groups;
-  if (tile == 256) return launch_product_w<256, 8>(p, ki, tiles, s);
-  static const int w8 = getenv("ORTHO_W8") ? atoi(getenv("ORTHO_W8")) : 0;
-  if (w8) return launch_product_w<128, 8>(p, ki, tiles, s);
-  return launch_product_w<128, 4>(p, ki, tiles, s);
+  if (tile == 256) return launch_product_s<Shape<256, 8, 5>>(p, ki, tiles, s);
+  if (groups <= device_cus()) return launch_product_s<Shape<128, 4, 10>>(p, ki, tiles, s);
+  return launch_product_s<Shape<128, 4, 5>>(p, ki, tiles, s);
 }
 
 template <class E, bool MUON>
