@@ -964,23 +964,26 @@ struct Plan {
 int64_t up(int64_t v, int64_t t) { return (v + t - 1) / t * t; }
 
 // Microseconds of a product on `groups` workgroups, measured: a step of a
-// 128 x 128 tile takes 0.55 with the compute unit to itself and 1.0 next to
-// another, of a 256 x 256 tile 1.6; shared tiles cost their parts' way through
-// memory and a launch.
+// 128 x 128 tile takes 0.37 with the compute unit to itself and 0.75 next to
+// another, of a 256 x 256 tile 1.05; shared tiles cost a launch and their
+// parts' way through memory.
 double product_us(int64_t tiles, int64_t steps, int tile, int64_t groups) {
   const int64_t cus = device_cus();
   if (groups != tiles)
-    return (double)(tiles * steps) / groups * (groups <= cus ? 0.55 : 1.0) + 5.0 + 0.033 * groups;
-  if (tile == 256) return (double)((tiles + cus - 1) / cus * steps) * 1.6;
-  if (tiles <= cus) return steps * 0.55;
-  return (double)((tiles + 2 * cus - 1) / (2 * cus) * steps);
+    return (double)(tiles * steps) / groups * (groups <= cus ? 0.37 : 0.75) + 5.0 + 0.06 * groups;
+  if (tile == 256) return (double)((tiles + cus - 1) / cus * steps) * 1.05;
+  if (tiles <= cus) return steps * 0.37;
+  return (double)((tiles + 2 * cus - 1) / (2 * cus) * steps) * 0.75;
 }
 
 // Workgroups for `tiles` tiles of `steps` steps: one per tile, or, where there
-// are too few tiles for the compute units, 2 or more that share each (at
-// least 8 steps each).  Tiles of 256 are taken where there are enough of them;
-// sharing those was measured slower even with a fifth of the chip idle (the
-// clock rises when units idle: 5120 x 5120 7.8 ms whole, 8.5 shared).
+// are too few tiles for the compute units, several that share each (at least 8
+// steps each): one 768 x 768 matrix takes 287 us with three to a tile, 355
+// whole; twelve of them 528 whole, 586 with two to a tile.  Tiles of 256 are
+// taken where there are enough of them (4096 x 4096: 3.87 ms, 4.05 with 128;
+// 3000 x 3000: 2.50 against 2.17), and never shared: that was slower even with
+// a fifth of the chip idle (5120 x 5120 7.8 ms whole, 8.5 shared; the clock
+// rises when units idle).
 int64_t groups_of(int64_t tiles, int64_t steps, int tile) {
   int64_t best = tiles;
   if (tile == 256) return best;
