@@ -15,9 +15,13 @@
 // several workgroups share a row and a second kernel joins their parts.
 //
 // The alternatives come from the same registers.  The K-th largest of a wave's
-// 64 lane maxima is a bound that at least K of its logits reach and few others
-// do; those are put in order by a sort over the lanes.  Where more than 64
-// reach it (equal logits), the K best are picked one after another.
+// 64 lane maxima is a bound that at least K of its logits reach; the largest
+// bound of any wave so far is in LDS, and the few logits that reach it are
+// listed there.  What reaches the last bound of all is put in order by a sort
+// over the lanes.  Which logits are listed on the way depends on the waves'
+// pace, the result does not.  Where more than 64 of a chunk reach the bound
+// (equal logits), the chunk is read again and the K best are picked one after
+// another.
 //
 // Rows may start anywhere: the 16-byte loads are aligned, and the vectors
 // that reach past either end of the row are read element by element.
@@ -31,10 +35,10 @@ namespace {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kNoIndex = 0x7fffffff;
 constexpr int kR = 8;                       // 16-byte vectors per lane and chunk
 constexpr int kWaves = 8;                   // waves that share a long row
-constexpr int kTopLanes = 32;               // lanes that hold the alternatives so far
+constexpr int kTopLanes = 32;               // lanes that hold the best so far in a sort of many
+constexpr int kListed = 128;                // a wave's list: up to 64 entries and a chunk's 64
 constexpr float kFloor2 = -1000.f;          // below the least exponent: e = 0 there
 
 static_assert(kMaxTopK <= kTopLanes, "one lane per alternative");
@@ -75,36 +79,64 @@ __device__ __forceinline__ Stats merge(Stats a, Stats b) {
   return Stats{m, a.s + b.s, a.s1 + b.s1};
 }
 
-// Larger value first, then the lower index; (-inf, kNoIndex) is no entry.
-__device__ __forceinline__ bool before(float v, int i, float w, int j) {
-  return v > w || (v == w && i < j);
+// Unsigned integers in the order of the floats (no NaN; -0 as 0).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u ^ (u >> 31 != 0 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u ^ (u >> 31 != 0 ? 0x80000000u : 0xffffffffu));
+}
+
+// An alternative as one number: the larger logit is the larger, and of equal
+// ones that with the lower index.  0 is no alternative.
+__device__ __forceinline__ uint64_t entry(float v, int i) {
+  return (uint64_t)ordered(v) << 32 | (uint32_t)~i;
+}
+__device__ __forceinline__ float value_of(uint64_t e) { return from_ordered((uint32_t)(e >> 32)); }
+__device__ __forceinline__ int index_of(uint64_t e) { return (int)~(uint32_t)e; }
+
+__device__ __forceinline__ uint64_t entry_xor(uint64_t e, int o) {
+  const uint32_t hi = (uint32_t)lane_xor((int)(e >> 32), o), lo = (uint32_t)lane_xor((int)(uint32_t)e, o);
+  return (uint64_t)hi << 32 | lo;
 }
 
 // The 64 lanes' entries in order, lane 0 the first.
-__device__ __forceinline__ void sort_lanes(float& v, int& i) {
+__device__ __forceinline__ uint64_t sort_lanes(uint64_t e) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int k = 2; k <= 64; k *= 2)
 #pragma unroll
     for (int j = k / 2; j >= 1; j /= 2) {
-      const float w = lane_xor(v, j);
-      const int o = lane_xor(i, j);
-      const bool first = ((lane & j) == 0) == ((lane & k) == 0);   // keep the better one
-      if (before(w, o, v, i) == first) { v = w; i = o; }
+      const uint64_t o = entry_xor(e, j);
+      const bool most = ((lane & j) == 0) == ((lane & k) == 0);   // keep the better one
+      e = (o > e) == most ? o : e;
     }
+  return e;
 }
 
-// The k-th largest of 64 lanes' values.
+// A value that at least k of the 64 lanes' reach, k <= 32: the k-th largest of
+// the 64, or for k <= 8 of the maxima of four lanes each, in half the steps.
 __device__ __forceinline__ float kth_of_lanes(float v, int k) {
   const int lane = threadIdx.x & 63;
+  const auto step = [&](int j, int n) {
+    const float w = lane_xor(v, j);
+    const bool most = ((lane & j) == 0) == ((lane & n) == 0);
+    v = most ? fmaxf(v, w) : fminf(v, w);
+  };
+  if (k <= 8) {
+    v = fmaxf(v, lane_xor(v, 32));
+    v = fmaxf(v, lane_xor(v, 16));
 #pragma unroll
-  for (int n = 2; n <= 64; n *= 2)
+    for (int n = 2; n <= 16; n *= 2)
 #pragma unroll
-    for (int j = n / 2; j >= 1; j /= 2) {
-      const float w = lane_xor(v, j);
-      const bool most = ((lane & j) == 0) == ((lane & n) == 0);
-      v = most ? fmaxf(v, w) : fminf(v, w);
-    }
+      for (int j = n / 2; j >= 1; j /= 2) step(j, n == 16 ? 64 : n);
+  } else {
+#pragma unroll
+    for (int n = 2; n <= 64; n *= 2)
+#pragma unroll
+      for (int j = n / 2; j >= 1; j /= 2) step(j, n);
+  }
   return __shfl(v, k - 1, 64);
 }
 
@@ -127,6 +159,20 @@ __device__ __forceinline__ void as_loaded(Vec (&x)[kR]) {
   for (int r = 0; r < kR; ++r) asm volatile("" : "+v"(x[r]));
 }
 
+// The best of `n` entries in memory, in order, by one wave: the first 32 lanes'.
+__device__ __forceinline__ uint64_t best_of(const uint64_t* of, int n) {
+  const int lane = threadIdx.x & 63;
+  uint64_t e = lane < n ? of[lane] : 0;
+  int at = 64;
+  for (;;) {
+    e = sort_lanes(e);
+    if (at >= n) return e;
+    const int k = at + lane - kTopLanes;
+    if (lane >= kTopLanes) e = k < n ? of[k] : 0;
+    at += 64 - kTopLanes;
+  }
+}
+
 // What one wave finds in its part of a row.
 template <class E, bool TOP>
 struct RowPart {
@@ -134,41 +180,44 @@ struct RowPart {
   using S = typename E::storage;
   typedef Raw<E, kVec> Vec;
 
+  const S* z;                                     // the row's first aligned vector,
+  int pre, V, v1;                                 // `pre` elements before the row
+  int step;                                       // vectors from one of a lane's to its next
+  int top_k;
+  uint64_t* list;                                 // kListed entries of this wave's own
+  uint32_t* bound;                                // ordered(the row's bound so far)
+
   Stats st;
-  float tv;                                       // lanes 0 .. 31: alternatives so far
-  int ti;
-  // The vectors [v0, v1) of the row whose first aligned vector is at `z`
-  // (`pre` elements before the row), this wave's share of them: vectors
-  // v0 + `wave` * 64 + lane and so on, in steps of `waves` * 64.
-  // `list`: 64 entries of LDS of this wave's own.
-  __device__ __forceinline__ void run(const S* z, int pre, int V, int v0, int v1, int wave,
-                                      int waves, int top_k, float2* list) {
+  int count;                                      // entries in the list, <= 64 between chunks
+  float kth;                                      // top_k of them reach this,
+  bool full;                                      // if there are so many
+
+  // This wave's share of the vectors [v0, v1): v0 + `wave` * 64 + lane and so
+  // on, in steps of `waves` * 64.
+  __device__ __forceinline__ void run(int v0, int wave, int waves) {
     const int lane = threadIdx.x & 63;
     st = Stats{kNegInf, 0.f, 0.f};
-    tv = kNegInf;
-    ti = kNoIndex;
-    float kth = kNegInf;                          // the top_k-th so far
-    bool full = false;                            // there are top_k
-    const int step = waves * 64;
+    count = 0;
+    kth = kNegInf;
+    full = false;
+    step = waves * 64;
     const int n = max(0, (v1 - v0 - wave * 64 + step - 1) / step);   // vectors of lane 0
     const int chunks = (n + kR - 1) / kR;
     int done = 0;
     for (int c = 0; c < chunks; ++c) {
       const int now = (n - done + (chunks - c) - 1) / (chunks - c);    // even chunks, <= kR
+      const int first = v0 + wave * 64 + done * step + lane;
       Vec x[kR];
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         if (r >= now) continue;
-        const int v = v0 + wave * 64 + (done + r) * step + lane;
+        const int v = first + r * step;
         const int j = v * kVec - pre;             // first index of the vector
         if (v < v1 && j >= 0 && j + kVec <= V) {
           x[r] = load_raw<E, kVec>(z + (int64_t)v * kVec);
         } else {
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            const bool in = v < v1 && j + e >= 0 && j + e < V;
-            x[r][e] = in ? z[(int64_t)v * kVec + e] : lowest();
-          }
+          for (int e = 0; e < kVec; ++e) x[r][e] = inside(v, e) ? z[(int64_t)v * kVec + e] : lowest();
         }
       }
       float lm = kNegInf;
@@ -177,7 +226,7 @@ struct RowPart {
         if (r < now)
 #pragma unroll
           for (int e = 0; e < kVec; ++e) lm = fmaxf(lm, raw_f32<E, kVec>(x[r], e));
-      const float m = fmaxf(st.m, wave_max(lm));
+      const float most = wave_max(lm), m = fmaxf(st.m, most);
       as_loaded(x);
       rebase(st.m, m, st.s, st.s1);
       const float at = m == kNegInf ? 0.f : m;    // -inf - -inf would be NaN
@@ -191,12 +240,20 @@ struct RowPart {
             st.s1 += p * fmaxf(d, kFloor2);       // NaN is kept by s
           }
       st.m = m;
-      as_loaded(x);
-      if constexpr (TOP) alternatives(x, now, lm, pre, V, v0 + wave * 64 + done * step, v1, step, top_k, list, kth, full);
+      if constexpr (TOP) {
+        as_loaded(x);
+        alternatives(x, now, lm, most, first);
+      }
       done += now;
     }
     st.s = wave_sum(st.s);
     st.s1 = wave_sum(st.s1);
+  }
+
+  // Element e of vector v is this part's.
+  __device__ __forceinline__ bool inside(int v, int e) const {
+    const int j = v * kVec - pre + e;
+    return v < v1 && j >= 0 && j < V;
   }
 
   static __device__ __forceinline__ S lowest() {
@@ -204,127 +261,111 @@ struct RowPart {
     else return kNegInf;
   }
 
-  // Adds a chunk's best logits to the alternatives.  Later chunks hold higher
-  // indices, so a logit equal to the last alternative comes after it.
-  __device__ __forceinline__ void alternatives(const Vec (&x)[kR], int now, float lm, int pre, int V,
-                                               int first, int v1, int step, int top_k,
-                                               float2* list, float& kth, bool& full) {
+  __device__ __forceinline__ float bound_now() const {
+    return from_ordered(*(volatile const uint32_t*)bound);
+  }
+  __device__ __forceinline__ void raise_bound(float b) {
+    if ((threadIdx.x & 63) == 0) atomicMax(bound, ordered(b));
+  }
+
+  // Lists a chunk's logits that reach the bound.  Later chunks hold higher
+  // indices, so where top_k entries of this wave's reach it already, a logit
+  // equal to it comes after them.
+  __device__ __forceinline__ void alternatives(const Vec (&x)[kR], int now, float lm, float most,
+                                               int first) {
     const int lane = threadIdx.x & 63;
-    if (full && !(wave_max(lm) > kth)) return;
-    float bound = kth_of_lanes(lm, top_k);
-    // strictly above the last alternative, if there are enough of them
-    const bool above = full && kth >= bound;
-    if (above) bound = kth;
-    int count = 0;
+    float b = bound_now();
+    if (most < b || (full && kth == b && !(most > b))) return;
+    const float of_chunk = kth_of_lanes(lm, top_k);
+    if (of_chunk > b) {
+      b = of_chunk;
+      raise_bound(b);
+    }
+    const bool above = full && kth == b;
+    int n = 0;                                    // that reach it
 #pragma unroll
     for (int r = 0; r < kR; ++r)
-      if (r < now)
-{
-        float most = raw_f32<E, kVec>(x[r], 0);   // few vectors hold one
+      if (r < now) {
+        float vm = raw_f32<E, kVec>(x[r], 0);     // few vectors hold one
 #pragma unroll
-        for (int e = 1; e < kVec; ++e) most = fmaxf(most, raw_f32<E, kVec>(x[r], e));
-        if (__ballot(above ? most > bound : most >= bound) == 0) continue;
+        for (int e = 1; e < kVec; ++e) vm = fmaxf(vm, raw_f32<E, kVec>(x[r], e));
+        if (__ballot(above ? vm > b : vm >= b) == 0) continue;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           const float v = raw_f32<E, kVec>(x[r], e);
-          uint64_t hit = __ballot(above ? v > bound : v >= bound);
+          uint64_t hit = __ballot(above ? v > b : v >= b);
           if (hit != 0) {
-            const int w = first + r * step + lane, j = w * kVec - pre + e;
-            hit &= __ballot(w < v1 && j >= 0 && j < V);     // not the padding's -inf
-            const int to = count + __popcll(hit & ((1ull << lane) - 1ull));
-            if (((hit >> lane) & 1) && to < 64) list[to] = make_float2(v, __int_as_float(j));
-            count += __popcll(hit);
+            hit &= __ballot(inside(first + r * step, e));     // not the padding's -inf
+            const int to = n + __popcll(hit & ((1ull << lane) - 1ull));
+            if (((hit >> lane) & 1) && to < 64)
+              list[count + to] = entry(v, (first + r * step) * kVec - pre + e);
+            n += __popcll(hit);
           }
         }
       }
-    if (count <= 64) {
-      __builtin_amdgcn_wave_barrier();
-      float v = kNegInf;
-      int i = kNoIndex;
-      if (lane < count) {
-        const float2 c = list[lane];
-        v = c.x;
-        i = __float_as_int(c.y);
-      }
-      __builtin_amdgcn_wave_barrier();
-      if (ti_any()) sort_lanes(v, i);             // the best 32 of these first
-      join(v, i);
-    } else {
-      // Too many equal ones: the best, then the best after it, and so on.
-      float bv = 0.f, mv = kNegInf;
-      int bi = -1, mi = kNoIndex;
-      for (int k = 0; k < top_k; ++k) {
-        float cv = kNegInf;
-        int ci = kNoIndex;
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
-          if (r < now)
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-              const float v = raw_f32<E, kVec>(x[r], e);
-              const int w = first + r * step + lane, j = w * kVec - pre + e;
-              if (v == v && w < v1 && j >= 0 && j < V && (k == 0 || before(bv, bi, v, j)) && before(v, j, cv, ci)) {
-                cv = v;
-                ci = j;
-              }
-            }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-          const float ov = lane_xor(cv, o);
-          const int oi = lane_xor(ci, o);
-          if (before(ov, oi, cv, ci)) { cv = ov; ci = oi; }
-        }
-        if (ci == kNoIndex) break;
-        bv = cv;
-        bi = ci;
-        if (lane == k) { mv = cv; mi = ci; }
-      }
-      join(mv, mi);
+    __builtin_amdgcn_wave_barrier();
+    const bool fits = n <= 64;
+    if (fits) {
+      count += n;
+      if (n >= top_k) { full = true; kth = b; }
     }
-    full = __shfl(ti, top_k - 1, 64) != kNoIndex;
-    if (full) kth = __shfl(tv, top_k - 1, 64);
+    if (count > (fits ? 64 : 64 - top_k)) keep_best();
+    if (!fits) pick(now, first);
   }
 
-  __device__ __forceinline__ bool ti_any() const { return __ballot((threadIdx.x & 63) < kTopLanes && ti != kNoIndex) != 0; }
-
-  // Takes the entries of all lanes (where there are alternatives already, only
-  // the first 32 lanes', the best of them).
-  __device__ __forceinline__ void join(float v, int i) {
+  // Shortens the list to its best top_k entries.
+  __device__ __forceinline__ void keep_best() {
     const int lane = threadIdx.x & 63;
-    if (!ti_any()) {
-      tv = v;
-      ti = i;
-    } else {
-      const float up = __shfl(v, lane - kTopLanes, 64);
-      const int ui = __shfl(i, lane - kTopLanes, 64);
-      if (lane >= kTopLanes) { tv = up; ti = ui; }
+    const uint64_t e = best_of(list, count);
+    __builtin_amdgcn_wave_barrier();
+    if (lane < top_k) list[lane] = e;
+    __builtin_amdgcn_wave_barrier();
+    count = top_k;                                // it was longer
+    full = true;
+    kth = __shfl(value_of(e), top_k - 1, 64);
+    raise_bound(kth);
+  }
+
+  // Too many equal ones: the best of the chunk, then the best after it, and so on.
+  __device__ __forceinline__ void pick(int now, int first) {
+    const int lane = threadIdx.x & 63;
+    uint64_t last = ~0ull;
+    int k = 0;
+    for (; k < top_k; ++k) {
+      uint64_t c = 0;
+      for (int r = 0; r < now; ++r) {
+        const int w = first + r * step;
+#pragma unroll 1
+        for (int e = 0; e < kVec; ++e) {
+          if (!inside(w, e)) continue;
+          const float v = E::to_float(z[(int64_t)w * kVec + e]);
+          const uint64_t o = v == v ? entry(v, w * kVec - pre + e) : 0;
+          if (o < last && o > c) c = o;
+        }
+      }
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) {
+        const uint64_t w = entry_xor(c, o);
+        c = w > c ? w : c;
+      }
+      if (c == 0) break;
+      last = c;
+      if (lane == 0) list[count + k] = c;
     }
-    sort_lanes(tv, ti);
-    if (lane >= kTopLanes) { tv = kNegInf; ti = kNoIndex; }
+    __builtin_amdgcn_wave_barrier();
+    count += k;
+    if (k == top_k) {
+      full = true;
+      kth = value_of(last);
+      raise_bound(kth);
+    }
   }
 };
 
-// The best of `n` entries in memory, by one wave, into lanes 0 .. 31.
-__device__ __forceinline__ void best_of(const float2* e, int n, float& v, int& i) {
-  const int lane = threadIdx.x & 63;
-  v = kNegInf;
-  i = kNoIndex;
-  if (lane < n) { v = e[lane].x; i = __float_as_int(e[lane].y); }
-  sort_lanes(v, i);
-  for (int at = 64; at < n; at += 64 - kTopLanes) {
-    const int k = at + lane - kTopLanes;
-    if (lane >= kTopLanes) {
-      v = k < n ? e[k].x : kNegInf;
-      i = k < n ? __float_as_int(e[k].y) : kNoIndex;
-    }
-    sort_lanes(v, i);
-  }
-}
-
 // One wave writes a row's results (entries in lanes 0 ..).
 template <class E>
-__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t n, const Stats& st, float v,
-                                          int i, const typename E::storage* z) {
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t n, const Stats& st, uint64_t e,
+                                          const typename E::storage* z) {
   const int lane = threadIdx.x & 63;
   const float log_s = logf(st.s), lse = st.m + log_s;
   if (lane == 0) {
@@ -336,8 +377,8 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t n, const
     }
   }
   if (lane < a.top_k) {
-    a.top_logp[n * a.top_k + lane] = i != kNoIndex ? v - lse : __builtin_nanf("");
-    a.top_ids[n * a.top_k + lane] = i != kNoIndex ? i : -1;
+    a.top_logp[n * a.top_k + lane] = e != 0 ? value_of(e) - lse : __builtin_nanf("");
+    a.top_ids[n * a.top_k + lane] = e != 0 ? index_of(e) : -1;
   }
 }
 
@@ -374,7 +415,10 @@ template <class E, int WAVES, bool TOP>
 __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) logprobs_kernel(LogprobArgs a,
                                                                                  int splits) {
   constexpr int kLists = WAVES == 1 ? 4 : WAVES;
-  __shared__ float2 lists[kLists][64];
+  __shared__ uint64_t lists[TOP ? kLists : 1][TOP ? kListed : 1];
+  __shared__ uint64_t best[TOP && WAVES > 1 ? WAVES * 64 : 1];
+  __shared__ uint32_t bounds[kLists];
+  __shared__ int listed;
   __shared__ Stats stats[kLists];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int64_t n;
@@ -390,35 +434,55 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) logprobs_kernel
     if ((WAVES == 1 || wave == 0) && part == 0) write_masked(a, n);
     return;
   }
+  if constexpr (TOP) {
+    if (lane == 0) bounds[wave] = ordered(kNegInf);
+    if constexpr (WAVES == 1) {
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      if (threadIdx.x == 0) listed = 0;
+      __syncthreads();
+    }
+  }
   const typename E::storage* z = row_of<E>(a.Z, a.T, n);
-  const int pre = before_aligned<E>(z), V = (int)a.V;
-  const int vecs = (V + pre + E::kVec - 1) / E::kVec;
-  const int v0 = (int)((int64_t)vecs * part / splits), v1 = (int)((int64_t)vecs * (part + 1) / splits);
   RowPart<E, TOP> p;
-  p.run(z - pre, pre, V, v0, v1, WAVES == 1 ? 0 : wave, WAVES, a.top_k, lists[wave]);
+  p.pre = before_aligned<E>(z);
+  p.z = z - p.pre;
+  p.V = (int)a.V;
+  p.top_k = a.top_k;
+  p.list = lists[TOP ? wave : 0];
+  p.bound = &bounds[WAVES == 1 ? wave : 0];
+  const int vecs = (p.V + p.pre + E::kVec - 1) / E::kVec;
+  p.v1 = (int)((int64_t)vecs * (part + 1) / splits);
+  p.run((int)((int64_t)vecs * part / splits), WAVES == 1 ? 0 : wave, WAVES);
+  uint64_t top = 0;
   if constexpr (WAVES == 1) {
-    write_row<E>(a, n, p.st, p.tv, p.ti, z);
+    if constexpr (TOP) top = best_of(p.list, p.count);
+    write_row<E>(a, n, p.st, top, z);
   } else {
     if (lane == 0) stats[wave] = p.st;
-    float2* best = &lists[0][0];
-    __syncthreads();                             // the lists are free
+    __syncthreads();
     if constexpr (TOP) {
-      if (lane < a.top_k) best[wave * a.top_k + lane] = make_float2(p.tv, __int_as_float(p.ti));
+      const uint64_t c = lane < p.count ? p.list[lane] : 0;
+      const uint64_t hit = __ballot((uint32_t)(c >> 32) >= *p.bound);
+      if (hit != 0) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&listed, __popcll(hit));
+        at = __shfl(at, 0, 64);
+        if ((hit >> lane) & 1) best[at + __popcll(hit & ((1ull << lane) - 1ull))] = c;
+      }
       __syncthreads();
     }
     if (wave != 0) return;
     Stats st = stats[0];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) st = merge(st, stats[w]);
-    float v = kNegInf;
-    int i = kNoIndex;
-    if constexpr (TOP) best_of(best, WAVES * a.top_k, v, i);
+    if constexpr (TOP) top = best_of(best, listed);
     if (splits == 1) {
-      write_row<E>(a, n, st, v, i, z);
+      write_row<E>(a, n, st, top, z);
     } else {
       float* o = (float*)a.ws + (n * splits + part) * part_words(a.top_k);
       if (lane == 0) { o[0] = st.m; o[1] = st.s; o[2] = st.s1; }
-      if (lane < a.top_k) ((float2*)(o + 4))[lane] = make_float2(v, __int_as_float(i));
+      if (lane < a.top_k) ((uint64_t*)(o + 4))[lane] = top;
     }
   }
 }
@@ -427,7 +491,7 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) logprobs_kernel
 // order, the alternatives by order.
 template <class E>
 __global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobArgs a, int splits) {
-  __shared__ float2 best[kTopLanes * 64];
+  __shared__ uint64_t best[kTopLanes * 64];
   const int64_t n = blockIdx.x;
   const int lane = threadIdx.x;
   if (a.mask != nullptr && a.mask[n] == 0) return;
@@ -436,15 +500,13 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobArgs a, int sp
   Stats mine = {kNegInf, 0.f, 0.f};
   if (lane < splits) mine = Stats{o[lane * words], o[lane * words + 1], o[lane * words + 2]};
   for (int k = lane; k < splits * a.top_k; k += 64)
-    best[k] = ((const float2*)(o + (k / a.top_k) * words + 4))[k % a.top_k];
+    best[k] = ((const uint64_t*)(o + (k / a.top_k) * words + 4))[k % a.top_k];
   Stats st = {__shfl(mine.m, 0, 64), __shfl(mine.s, 0, 64), __shfl(mine.s1, 0, 64)};
   for (int w = 1; w < splits; ++w)
     st = merge(st, Stats{__shfl(mine.m, w, 64), __shfl(mine.s, w, 64), __shfl(mine.s1, w, 64)});
   __syncthreads();
-  float v = kNegInf;
-  int i = kNoIndex;
-  if (a.top_k > 0) best_of(best, splits * a.top_k, v, i);
-  write_row<E>(a, n, st, v, i, row_of<E>(a.Z, a.T, n));
+  const uint64_t top = a.top_k > 0 ? best_of(best, splits * a.top_k) : 0;
+  write_row<E>(a, n, st, top, row_of<E>(a.Z, a.T, n));
 }
 
 // ---------------------------------------------------------------------------
