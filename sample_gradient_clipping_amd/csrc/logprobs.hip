@@ -278,8 +278,9 @@ struct RowPart {
     if (most < b || (full && kth == b && !(most > b))) return;
     const float of_chunk = kth_of_lanes(lm, top_k);
     if (of_chunk > b) {
-      b = of_chunk;
-      raise_bound(b);
+      raise_bound(of_chunk);
+      b = bound_now();                            // another wave's may be higher by now
+      if (most < b) return;
     }
     const bool above = full && kth == b;
     int n = 0;                                    // that reach it
