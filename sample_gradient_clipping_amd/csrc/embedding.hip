@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a) {
   const uint32_t first = su32(&a.seg[v].x, 0), end = su32(&a.seg[v].y, 0);
   const uint32_t b0 = (first + kBlock - 1) / kBlock;
   const bool empty = first >= end;
+  if (empty && a.beta && a.noise_std == 0.0f) return;       // nothing is added to it
   const bool summed = !empty && a.blocks != nullptr && (b0 + 1) * kBlock <= end;
   const int64_t row0 = (int64_t)v * a.D, start = AL ? row0 : row0 & ~(int64_t)3;
   const int64_t D = a.D;
