@@ -18,13 +18,23 @@
 //                            the id V and end up last; the last pass also
 //                            writes, per position, where its row of G starts
 //                            and its sample
-//  sort_small              : the same in one workgroup, for a few thousand
+//  sort_small              : the same in one workgroup, up to 2048 positions
 //  embed_segments          : each row's positions (with norms, embed_norm's
 //                            work)
 //  embed_blocks            : 8 positions of one run (segment) summed ahead
-//  embed_norm              : one wave per run and column group
-//  embed_long              : segments that hold such blocks
+//  embed_norm              : one wave per 8 sorted positions and column group
 //  embed_accumulate        : every row of the result, noise included
+//
+// What it costs (MI355X).  Lookup of 16384 rows of 5120 bf16: 52 us, 4.3 TB/s of
+// distinct rows read and rows written; of 16: 3.3 us.  Gradient of 16384
+// positions, 8.7 thousand active, 5120 bf16 columns, added into 32000 rows of
+// which 3.4 thousand have a token: 120 us.  The norms read G (89 MB) in 25 us,
+// the result takes 54 (G again, 140 MB of rows read and written: 4.2 TB/s); the
+// sort's three launches 16, the block sums 10 twice, the clip factors 5: a few
+// thousand rows each, bound by the latency of dependent loads.  Of 32 x 512
+// positions, 768 columns, 50257 rows with noise: 85 us, 50 of them the result,
+// which the noise's arithmetic bounds (39 million normals; 154 MB written).
+// Of 132 positions in 99 float32 columns: 16 us in four launches, 22 a call.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,7 +46,9 @@ namespace {
 // ---------------------------------------------------------------------------
 // Lookup
 // ---------------------------------------------------------------------------
-// L lanes per position (a power of two up to 64), V elements per lane and step.
+// L lanes per position (a power of two up to 64), V elements per lane and step:
+// a row is one or a few 16-byte loads of each lane, all in flight together, and
+// a wave's stores are whole lines.
 template <class EI, class EO, int V>
 __global__ void __launch_bounds__(256) lookup_kernel(LookupArgs a, int L) {
   const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
@@ -379,8 +391,8 @@ __global__ void __launch_bounds__(256) embed_segments_kernel(EmbedArgs a, uint32
 // adds more than 14 rows and a partial per 8 others: a token that fills a
 // tenth of the batch does not leave one wave with all its rows.
 constexpr uint32_t kBlock = 8;
-// Batches below this many positions go without (two launches less; a wave
-// then adds at most this many rows).
+// Batches below this many positions go without (two launches less, 4 to 5 us
+// each; a wave then adds at most this many rows, 32 batches of loads).
 constexpr int64_t kBlocksFrom = 256;
 
 typedef __attribute__((address_space(4))) const uint32_t c_u32;
@@ -514,42 +526,6 @@ __global__ void __launch_bounds__(256) embed_blocks_kernel(EmbedArgs a, uint32_t
   sum.store(a.blocks + (int64_t)b * a.D + c0, a.D - c0);
 }
 
-// Segments with a block of their own: their whole sum, in place of the first
-// such block's.  One workgroup each; its four waves take a quarter of the
-// blocks, the first the rows before them and the last the rows after, and the
-// four sums are added in order.
-template <class E, int V, int U>
-__global__ void __launch_bounds__(256) embed_long_kernel(EmbedArgs a, uint32_t N) {
-  __shared__ float part[3][U * V * 64];
-  const uint32_t b = blockIdx.x, i = b * kBlock;
-  const uint32_t v = su32(&a.rec[i].x, 0);
-  if (v >= (uint32_t)a.V || v != su32(&a.rec[i + kBlock - 1].x, 0)) return;
-  const uint32_t first = su32(&a.seg[v].x, 0), end = su32(&a.seg[v].y, 0);
-  if ((first + kBlock - 1) / kBlock != b) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const uint32_t b1 = end / kBlock, nb = b1 - b;
-  const int64_t c0 = (int64_t)blockIdx.y * (64 * V * U);
-  RowSum<E, V, U> sum;
-  sum.zero();
-  if (wave == 0) sum.template rows<true>(a, c0, first, i);
-  sum.parts(a, c0, b + nb * wave / 4, b + nb * (wave + 1) / 4);
-  if (wave == 3) sum.template rows<true>(a, c0, b1 * kBlock, end);
-  if (wave > 0)
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < V; ++e) part[wave - 1][(u * V + e) * 64 + lane] = sum.s[u][e];
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int w = 0; w < 3; ++w)
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < V; ++e) sum.s[u][e] += part[w][(u * V + e) * 64 + lane];
-  sum.store(a.blocks + (int64_t)b * a.D + c0, a.D - c0);
-}
-
 // One wave per 8 sorted positions and column group, for the runs that start
 // there: the 8 rows are loaded together (most runs have one or two), a run's
 // rows are summed (float32, in order) and the sum squared (float64).  A run
@@ -654,20 +630,44 @@ __global__ void __launch_bounds__(256) embed_norm_kernel(EmbedArgs a, const uint
     a.partials[(int64_t)at * gridDim.y + blockIdx.y] = q[0] * (double)a.scale * (double)a.scale;
 }
 
-// One wave per row of the result and U groups of 256 columns (gridDim.y of
-// them at a time).  A thread's four values are one Philox block: with D % 4
-// != 0 (AL false) the groups start at the block that holds the row's first
-// value, and each row keeps its own part of a shared block.
+// The rows of the result in U groups of 256 columns (gridDim.y of them at a
+// time).  A thread's four values are one Philox block: with D % 4 != 0 (AL
+// false) the groups start at the block that holds the row's first value, and
+// each row keeps its own part of a shared block.
+//
+// The first `shared` workgroups look for segments with a block of their own,
+// one candidate each.  There the four waves take a quarter of the blocks, the
+// first the rows before them too and the last the rows after, and the four
+// sums are added in order.  The other rows get one wave each, so that the
+// longest segments are summed next to them and not before them.
 template <class E, int U, bool AL>
-__global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t v = wave_of_grid();
-  if (v >= (uint32_t)a.V) return;
+__global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a, uint32_t shared) {
+  __shared__ f32x4 part[3][U][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool share = blockIdx.x < shared;
+  uint32_t v, b0, b1 = 0;
+  if (share) {
+    b0 = blockIdx.x;
+    v = su32(&a.rec[b0 * kBlock].x, 0);
+    if (v >= (uint32_t)a.V || v != su32(&a.rec[b0 * kBlock + kBlock - 1].x, 0)) return;
+  } else {
+    v = (blockIdx.x - shared) * 4 + wave;
+    if (v >= (uint32_t)a.V) return;
+  }
   const uint32_t first = su32(&a.seg[v].x, 0), end = su32(&a.seg[v].y, 0);
-  const uint32_t b0 = (first + kBlock - 1) / kBlock;
   const bool empty = first >= end;
-  if (empty && a.beta && a.noise_std == 0.0f) return;       // nothing is added to it
-  const bool summed = !empty && a.blocks != nullptr && (b0 + 1) * kBlock <= end;
+  if (share) {
+    if ((first + kBlock - 1) / kBlock != b0) return;         // not its first block
+    b1 = end / kBlock;
+  } else {
+    if (empty && a.beta && a.noise_std == 0.0f) return;      // nothing is added to it
+    b0 = (first + kBlock - 1) / kBlock;
+    if (shared != 0 && !empty && (b0 + 1) * kBlock <= end) return;   // done by a workgroup
+  }
+  // this wave's rows, and after them its blocks [pb, pe)
+  const uint32_t r0 = share && wave == 3 ? b1 * kBlock : first;
+  const uint32_t r1 = !share || wave == 3 ? end : wave == 0 ? b0 * kBlock : first;
+  const uint32_t pb = b0 + (b1 - b0) * wave / 4, pe = b0 + (b1 - b0) * (wave + 1) / 4;
   const int64_t row0 = (int64_t)v * a.D, start = AL ? row0 : row0 & ~(int64_t)3;
   const int64_t D = a.D;
   const float rd = 1.0f / a.denom;
@@ -705,40 +705,62 @@ __global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a) {
       old[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     // The result is read and written once: past the caches, which G needs.
-    if (a.beta)
+    if (a.beta && (!share || wave == 0))
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if constexpr (AL) old[u] = __builtin_nontemporal_load((const f32x4*)(a.out + row0 + in[u]));
         else old[u] = fetch(F32(), a.out + row0, u);
       }
-    if (summed) {
-      f32x4 x[U];
+    over_rows<true>(a, r0, r1, [&](int64_t off, float w, int cnt) {
+      in_batches<4>(cnt, [&](int j, auto kk) {
+        constexpr int K = decltype(kk)::value;
+        Raw<E, 4> x[K][U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = fetch(F32(), a.blocks + (int64_t)b0 * D, u);
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+          for (int u = 0; u < U; ++u)
+            x[k][u] = fetch(E(), (const typename E::storage*)a.G.data + lane_i64(off, j + k), u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[u][e] = x[u][e];
-    } else if (!empty) {
-      over_rows<true>(a, first, end, [&](int64_t off, float w, int cnt) {
-        in_batches<4>(cnt, [&](int j, auto kk) {
-          constexpr int K = decltype(kk)::value;
-          Raw<E, 4> x[K][U];
+        for (int k = 0; k < K; ++k) {
+          const float wk = lane_f32(w, j + k);
 #pragma unroll
-          for (int k = 0; k < K; ++k)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-              x[k][u] = fetch(E(), (const typename E::storage*)a.G.data + lane_i64(off, j + k), u);
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            const float wk = lane_f32(w, j + k);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sum[u][e] += wk * raw_f32<E, 4>(x[k][u], e);
-          }
-        });
+            for (int e = 0; e < 4; ++e) sum[u][e] += wk * raw_f32<E, 4>(x[k][u], e);
+        }
       });
+    });
+    if (share) {
+      in_batches<sizeof(typename E::storage)>((int)(pe - pb), [&](int j, auto kk) {
+        constexpr int K = decltype(kk)::value;
+        f32x4 x[K][U];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int u = 0; u < U; ++u) x[k][u] = fetch(F32(), a.blocks + (int64_t)(pb + j + k) * D, u);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[u][e] += x[k][u][e];
+      });
+      if (wave > 0)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          part[wave - 1][u][lane] = f32x4{sum[u][0], sum[u][1], sum[u][2], sum[u][3]};
+      __syncthreads();
+      if (wave == 0)
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const f32x4 x = part[w][u][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[u][e] += x[e];
+          }
+      __syncthreads();                           // before the next columns' parts
+      if (wave > 0) continue;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -946,13 +968,13 @@ hipError_t launch_embed_norm(const EmbedArgs& a, hipStream_t s) {
 namespace {
 
 template <class E, bool AL>
-void accumulate_u(const EmbedArgs& a, int U, dim3 grid, hipStream_t s) {
+void accumulate_u(const EmbedArgs& a, int U, dim3 grid, uint32_t shared, hipStream_t s) {
   switch (U) {
-    case 1: hipLaunchKernelGGL((embed_accumulate_kernel<E, 1, AL>), grid, dim3(256), 0, s, a); break;
-    case 2: hipLaunchKernelGGL((embed_accumulate_kernel<E, 2, AL>), grid, dim3(256), 0, s, a); break;
-    case 3: hipLaunchKernelGGL((embed_accumulate_kernel<E, 3, AL>), grid, dim3(256), 0, s, a); break;
-    case 4: hipLaunchKernelGGL((embed_accumulate_kernel<E, 4, AL>), grid, dim3(256), 0, s, a); break;
-    default: hipLaunchKernelGGL((embed_accumulate_kernel<E, 5, AL>), grid, dim3(256), 0, s, a);
+    case 1: hipLaunchKernelGGL((embed_accumulate_kernel<E, 1, AL>), grid, dim3(256), 0, s, a, shared); break;
+    case 2: hipLaunchKernelGGL((embed_accumulate_kernel<E, 2, AL>), grid, dim3(256), 0, s, a, shared); break;
+    case 3: hipLaunchKernelGGL((embed_accumulate_kernel<E, 3, AL>), grid, dim3(256), 0, s, a, shared); break;
+    case 4: hipLaunchKernelGGL((embed_accumulate_kernel<E, 4, AL>), grid, dim3(256), 0, s, a, shared); break;
+    default: hipLaunchKernelGGL((embed_accumulate_kernel<E, 5, AL>), grid, dim3(256), 0, s, a, shared);
   }
 }
 
@@ -961,6 +983,7 @@ void accumulate_u(const EmbedArgs& a, int U, dim3 grid, hipStream_t s) {
 hipError_t launch_embed_accumulate(const EmbedArgs& a, hipStream_t s) {
   const uint32_t N = (uint32_t)(a.B * a.T);
   const unsigned parts = (unsigned)embed_norm_parts(a);
+  const uint32_t shared = a.blocks != nullptr ? N / kBlock : 0;
   timing_begin("embed_accumulate", s);
   if (a.blocks != nullptr)
     with_rows(a, [&](auto e, auto v, auto u) {
@@ -968,7 +991,6 @@ hipError_t launch_embed_accumulate(const EmbedArgs& a, hipStream_t s) {
       constexpr int V = decltype(v)::value, U = decltype(u)::value;
       const dim3 grid((N / kBlock + 3) / 4, parts);
       hipLaunchKernelGGL((embed_blocks_kernel<E, V, U, true>), grid, dim3(256), 0, s, a, N);
-      hipLaunchKernelGGL((embed_long_kernel<E, V, U>), dim3(N / kBlock, parts), dim3(256), 0, s, a, N);
     });
   const bool al = row_vec(a.G, a.D) >= 4;
   // an unaligned row can touch one Philox block more
@@ -979,13 +1001,13 @@ hipError_t launch_embed_accumulate(const EmbedArgs& a, hipStream_t s) {
   // Column groups side by side only where the rows alone leave the chip idle.
   const int64_t groups = (steps + U - 1) / U, want = (int64_t)device_cus() * 32;
   const int64_t gy = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(groups, 65535), want / a.V));
-  const dim3 grid((unsigned)((a.V + 3) / 4), (unsigned)gy);
+  const dim3 grid((unsigned)(shared + (a.V + 3) / 4), (unsigned)gy);
   if (a.dtype == kBF16) {
-    if (al) accumulate_u<BF16, true>(a, U, grid, s);
-    else accumulate_u<BF16, false>(a, U, grid, s);
+    if (al) accumulate_u<BF16, true>(a, U, grid, shared, s);
+    else accumulate_u<BF16, false>(a, U, grid, shared, s);
   } else {
-    if (al) accumulate_u<F32, true>(a, U, grid, s);
-    else accumulate_u<F32, false>(a, U, grid, s);
+    if (al) accumulate_u<F32, true>(a, U, grid, shared, s);
+    else accumulate_u<F32, false>(a, U, grid, shared, s);
   }
   timing_end("embed_accumulate", s);
   return hipGetLastError();
