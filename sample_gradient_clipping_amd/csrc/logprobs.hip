@@ -25,6 +25,15 @@
 //
 // Rows may start anywhere: the 16-byte loads are aligned, and the vectors
 // that reach past either end of the row are read element by element.
+//
+// What it costs (MI355X).  16384 rows of 32000 bf16 logits: 193 to 205 us, 5.1 to
+// 5.4 TB/s; with five alternatives 345 (their instructions bound it then: two
+// bounds, a scan and a sort per chunk of a wave), 2052 float32 rows of 50257 with
+// eight 104 (4.0 TB/s).  15600 rows of 3128 with one alternative: 39 us.  One row of
+// 32000 with five: 11 us in one workgroup, most of it the latency of a chain
+// of loads, maximum, bound, list and sort.  The gradient: 16384 x 32000 bf16
+// 424 us (4.9 TB/s read and written, a copy's rate), 2052 x 50257 float32, half
+// the rows masked, 127 (5.0 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -595,7 +604,8 @@ void grad_v(const LogprobGradArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((logprobs_grad_kernel<E, EO, false>), grid, dim3(256), 0, s, a);
 }
 
-// One wave per row up to this many logits (one chunk of a wave).
+// One wave per row up to this many logits (one chunk of a wave): no barrier, and
+// four rows per workgroup.
 template <class E>
 constexpr int64_t wave_row() { return 64 * kR * E::kVec; }
 

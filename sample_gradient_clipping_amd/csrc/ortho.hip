@@ -36,7 +36,9 @@
 // Product kernel.  Tiles of 256 x 256 on 8 waves (128 x 64 each) or 128 x 128
 // on 4 (64 x 64; two workgroups per compute unit), K in steps of 16.  A step's
 // operands go from memory to LDS directly (16 bytes a lane), into a ring of
-// five slots, four steps ahead; LDS chunks are permuted so that the fragment
+// five slots, four steps ahead (ten slots and nine steps where the grid leaves a
+// compute unit to one workgroup of 4 waves: a step is then shorter than a load
+// takes); LDS chunks are permuted so that the fragment
 // reads hit every bank once.  Per step a wave reads its fragments one block
 // ahead of the MFMAs, 3 MFMAs per block and half pair: 24 (12) MFMAs on 12 (8)
 // fragments, so LDS is busy for two thirds of the MFMAs' time.  One barrier
@@ -45,6 +47,18 @@
 //
 // Where a product has too few tiles for the chip, several workgroups share a
 // tile's steps and leave float32 parts that a second kernel adds in order.
+// Matrices that fit into LDS take one workgroup for the whole call.
+//
+// What it costs (MI355X).  The MFMAs bound it.  A 13824 x 5120 step takes 15.9
+// ms: five times X^T X 0.91 ms (1250 TFLOP/s of half-precision products), the
+// square 0.34 (1210), B X 1.89 (1150), where a large half-precision library
+// product reaches 1170; norm and split 0.15 and 0.18 (1.1 and 0.7 GB: 7 and 4
+// TB/s).  The clock falls to 2.0 to 2.1 GHz under these, so that keeping the
+// MFMAs busier than half the cycles buys little.  Twelve 768 x 768 take 475 us:
+// per step 31 each for the symmetric products (600 TFLOP/s: 252 tiles of 128 on
+// 256 compute units, one wave per SIMD) and 41 for B X (790: 432 tiles on 512
+// places).  One 768 x 768 takes 295, 1024 x 4096 450 us, 4096 x 4096 3.9 ms;
+// 64 x 32 20 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -725,7 +739,8 @@ __global__ void __launch_bounds__(S::kNT) ortho_fixup_kernel(ProductArgs p) {
 // in one workgroup of 8 waves (a launch per product costs more than the
 // product).  X is kept with its smaller dimension first, A and then B in the
 // same place; each wave computes 32 x 32 blocks in registers and they are
-// stored after a barrier, in place.  Here B = b A + c A^2 and X <- a X + B X as
+// stored after a barrier, in place: 64 x 32 20 us, 128 x 128 75 (latency of LDS
+// reads and barriers; 182 for 64 x 32 with a launch per product).  Here B = b A + c A^2 and X <- a X + B X as
 // they stand: reading back costs nothing in LDS, and a few large entries (a
 // row, a number) do not average out what the shifted diagonals round off.
 constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / 64;
