@@ -467,7 +467,8 @@ dpf_status dpfused_embedding_lookup(const dpf_ids* ids, const void* table, int32
  * The positions are sorted by token (a stable sort on the device); equal
  * tokens of a sample are summed before they are squared, equal tokens of the
  * batch are one row of the result.  No per-sample gradient is stored.
- * Sums in float32, norms in float64, in a fixed order.
+ * Sums in float32, norms in float64, in a fixed order.  Accumulated without
+ * noise (sigma 0), rows that no active position adds to are not touched.
  *
  *   ids, G       [B, T] and [B, T, D] (bf16 or f32)
  *   V            rows of the table
@@ -581,7 +582,8 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  * for an unknown dtype, pointers not 16-byte aligned, n > 65535, rows or cols
  * > 2^17 or n * rows * cols > 2^33; DPF_ERR_OUT_OF_MEMORY when the workspace
  * (8 bytes per element, and 8 per element of the [n, m, m] products, m =
- * min(rows, cols)) cannot be allocated. */
+ * min(rows, cols), dimensions rounded up to 128 or 256; none for matrices
+ * that fit into one workgroup's LDS) cannot be allocated. */
 dpf_status dpfused_orthogonalize(const void* M, int32_t dtype, int64_t n, int64_t rows,
                                  int64_t cols, int32_t steps, float a, float b, float c, float eps,
                                  void* out, void* stream);

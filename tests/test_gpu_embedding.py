@@ -207,6 +207,40 @@ def test_micro_batches_add_up(D):
     _check(torch, dp, tok, G, 120, "bf16", None, 1.0, 0.2, 0.9, denom=16.0, base=base)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [4, 97, 1282, 1300, 2564])
+def test_long_segments_in_several_column_groups(D, dtype):
+    """Few tokens, many positions: most of a row's positions come in whole blocks."""
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(D)
+    tok, G = _case(rng, 5, 131, 4, D, dtype)
+    base = rng.standard_normal((9, D)).astype(np.float32)
+    for m, sigma in (("holes", 0.0), ("prefix", 0.6)):
+        _check(torch, dp, tok, G, 9, dtype, _mask(rng, 5, 131, m), 1.0, 0.3, sigma, denom=7.0, base=base)
+
+
+@pytest.mark.parametrize("D", [8, 13])
+@pytest.mark.parametrize("T", [10, 400])
+def test_accumulating_without_noise_leaves_other_rows(T, D):
+    """Rows that no active position adds to keep their bits, NaN and -0 among them."""
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(T)
+    tok, G = _case(rng, 2, T, 20, D, "f32")
+    tok[tok == 7] = 8
+    base = rng.standard_normal((30, D)).astype(np.float32)
+    base[7], base[25], base[26] = -0.0, np.nan, np.inf
+    out = torch.from_numpy(base).cuda()
+    dp.embedding_clip_accumulate(torch.from_numpy(tok).cuda(), to_dev(G, "f32", torch), 30, C=1.0,
+                                 grad_out=out, accumulate=True)
+    got = out.cpu().numpy()
+    rest = np.setdiff1d(np.arange(30), tok)
+    assert {7, 25, 26} <= set(rest)
+    assert np.array_equal(got[rest].view(np.uint32), base[rest].view(np.uint32))
+    assert (got[np.unique(tok)] != base[np.unique(tok)]).any(axis=1).all()
+
+
 def test_group_clipping_with_a_linear_layer():
     """One factor per sample over the embedding and a linear, from the building blocks."""
     torch = need_gpu()

@@ -110,6 +110,41 @@ def test_equal_logits_go_to_the_lowest_index(V):
     _check(torch, dp, z, y, None, "f32", 32, _forward(torch, dp, z, y, None, "f32", 32))
 
 
+@pytest.mark.parametrize("top_k", [1, 3, 32])
+@pytest.mark.parametrize("V", [700, 4096, 16385, 32769, 70001])
+def test_ordered_and_nearly_equal_logits(V, top_k):
+    """Alternatives that keep being replaced (rising logits), that come first, that sit in one
+    wave's part, and more candidates than a list holds."""
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(V + top_k)
+    rise = np.arange(V, dtype=np.float32) / V
+    z = np.empty((2, 4, V), np.float32)
+    z[0, 0], z[0, 1] = rise, rise[::-1]
+    z[0, 2] = np.floor(rise * 40)                      # steps of equal ones, rising
+    z[0, 3] = np.floor(rise[::-1] * 40)
+    z[1, 0] = rng.integers(0, 50, V)
+    z[1, 1] = np.where(np.arange(V) % 512 < 8, 1.0, 0.0) + rng.integers(0, 2, V)
+    z[1, 2] = -1e4
+    z[1, 2, V // 2: V // 2 + 5] = rng.standard_normal(5)
+    z[1, 3] = rng.standard_normal(V)
+    y = rng.integers(0, V, (2, 4))
+    y[1, 2] = V // 2
+    for dtype in ("f32", "bf16"):
+        x = f32_to_bf16_bits(z) if dtype == "bf16" else z
+        _check(torch, dp, x, y, None, dtype, top_k, _forward(torch, dp, x, y, None, dtype, top_k))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [16383, 16384, 32767, 32768, 32776, 65535, 65545])
+def test_rows_at_the_edges_of_parts(V, dtype):
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(V)
+    z, y = _case(rng, 1, 3, V, dtype)
+    _check(torch, dp, z, y, None, dtype, 8, _forward(torch, dp, z, y, None, dtype, 8))
+
+
 @pytest.mark.parametrize("V", [50, 4100, 50257])
 def test_masked_vocabulary_and_large_logits(V):
     """-inf logits are tokens of probability 0; the type's lowest value and +-1e4 stay finite."""
