@@ -517,7 +517,8 @@ def embedding_lookup(ids, table, mask=None, scale: float = 1.0, out_dtype=None, 
         out_dtype = table.dtype if out is None else out.dtype
     if out is None:
         out = torch.empty((*ids.shape, D), dtype=out_dtype, device=ids.device)
-    _check_out(out, (*ids.shape, D), "out", ids.device, dtype=out_dtype)
+    else:
+        _check_out(out, (*ids.shape, D), "out", ids.device, dtype=out_dtype)
     st = _lib.lib().dpfused_embedding_lookup(
         ctypes.byref(ia), table.data_ptr(), _dtype_code(table), int(V), int(D),
         int(table.stride(0)) if V > 1 else int(D), _mask_ptr(mask, *ids.shape, ids.device),
@@ -543,11 +544,12 @@ def embedding_clip_accumulate(ids, G, V: int, mask=None, scale: float = 1.0, C: 
         raise ValueError("accumulate=True needs grad_out")
     if grad_out is None:
         grad_out = torch.empty((int(V), D), dtype=torch.float32, device=G.device)
-    _check_out(grad_out, (int(V), D), "grad_out", G.device)
-    if norms_out is None and want_norms:
-        norms_out = torch.empty((B,), dtype=torch.float32, device=G.device)
+    else:
+        _check_out(grad_out, (int(V), D), "grad_out", G.device)
     if norms_out is not None:
         _check_out(norms_out, (B,), "norms_out", G.device)
+    elif want_norms:
+        norms_out = torch.empty((B,), dtype=torch.float32, device=G.device)
     st = _lib.lib().dpfused_embedding_clip_accumulate(
         ctypes.byref(ia), ctypes.byref(ga), _mask_ptr(mask, B, T, G.device), int(V), float(scale),
         float(C), float(sigma), int(seed), int(offset), float(B if denom is None else denom),
@@ -620,11 +622,13 @@ def token_logprobs(logits, targets=None, mask=None, top_k: int = 0, stream=None)
         ta = _ids(targets, "targets")
         _same_device(targets, dev, "targets")
     top_k = int(top_k)
-    f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
-    logp = f32(B, T) if targets is not None else None
-    entropy, lse = f32(B, T), f32(B, T)
-    top_logp = f32(B, T, top_k) if top_k > 0 else None
-    top_ids = torch.empty((B, T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
+    # one allocation for the rows' values: a call for a few rows costs what its host side does
+    rows = torch.empty((2 if targets is None else 3, B, T), dtype=torch.float32, device=dev).unbind(0)
+    entropy, lse, logp = rows if targets is not None else (*rows, None)
+    top_logp = top_ids = None
+    if top_k > 0:
+        top_logp = torch.empty((B, T, top_k), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((B, T, top_k), dtype=torch.int32, device=dev)
     st = _lib.lib().dpfused_token_logprobs(
         ctypes.byref(za), None if ta is None else ctypes.byref(ta), _mask_ptr(mask, B, T, dev),
         top_k, _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(top_logp), _ptr(top_ids),

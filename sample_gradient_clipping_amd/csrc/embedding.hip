@@ -32,7 +32,7 @@
 // the result takes 54 (G again, 140 MB of rows read and written: 4.2 TB/s); the
 // sort's three launches 16, the block sums 10 twice, the clip factors 5: a few
 // thousand rows each, bound by the latency of dependent loads.  Of 32 x 512
-// positions, 768 columns, 50257 rows with noise: 85 us, 50 of them the result,
+// positions, 768 columns, 50257 rows with noise: 80 us, 47 of them the result,
 // which the noise's arithmetic bounds (39 million normals; 154 MB written).
 // Of 132 positions in 99 float32 columns: 16 us in four launches, 22 a call.
 #include <algorithm>
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(256) embed_accumulate_kernel(EmbedArgs a, uint
       if (col[u] >= D) continue;
       const int64_t e0 = row0 + col[u];
       if (a.noise_std != 0.0f) {
-        const f32x4 z = normals_of_block_hw(philox_block(a.seed, a.offset + (uint64_t)(e0 >> 2)));
+        const f32x4 z = normals_of_block_hw(philox_block_xor3(a.seed, a.offset + (uint64_t)(e0 >> 2)));
         sum[u][0] += a.noise_std * z.x; sum[u][1] += a.noise_std * z.y;
         sum[u][2] += a.noise_std * z.z; sum[u][3] += a.noise_std * z.w;
       }

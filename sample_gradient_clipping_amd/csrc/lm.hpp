@@ -133,6 +133,26 @@ __device__ __forceinline__ double lane_xor(double v, int j) {
   return __builtin_bit_cast(double, (hi << 32) | lo);
 }
 
+// philox_block's words, with gfx950's three-way xor: 20 instructions of a block's
+// 100 less.
+__device__ __forceinline__ u32x4 philox_block_xor3(uint64_t seed, uint64_t block) {
+  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = 0u, c3 = 0u;
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = (uint64_t)kPhiloxM0 * c0, p1 = (uint64_t)kPhiloxM1 * c2;
+    c0 = __builtin_amdgcn_bitop3_b32((uint32_t)(p1 >> 32), c1, k0, 0x96);
+    c2 = __builtin_amdgcn_bitop3_b32((uint32_t)(p0 >> 32), c3, k1, 0x96);
+    c1 = (uint32_t)p1;
+    c3 = (uint32_t)p0;
+    k0 += kPhiloxW0;
+    k1 += kPhiloxW1;
+  }
+  u32x4 w;
+  w.x = c0; w.y = c1; w.z = c2; w.w = c3;
+  return w;
+}
+
 // The four normals of a Philox block, as normals_of_block, with the radius
 // through the hardware's logarithm and square root: over all 2^23 uniforms it
 // is within 4.9e-7 of the exact value (the library functions: 5.7e-7) in far
