@@ -10,7 +10,7 @@
 // wave holds a chunk of it in registers (64 bf16 or 32 float32 logits a lane),
 // takes the chunk's maximum, and adds to S and S1 relative to the largest
 // maximum so far: where that moves by d = m - m', S' = e^d S and S1' =
-// e^d (S1 + d S).  A wave does short rows alone; the eight waves of a
+// e^d (S1 + d S).  A wave does short rows alone, four or eight waves of a
 // workgroup share long ones, and where there are too few rows for the chip,
 // several workgroups share a row and a second kernel joins their parts.
 //
@@ -26,10 +26,10 @@
 // Rows may start anywhere: the 16-byte loads are aligned, and the vectors
 // that reach past either end of the row are read element by element.
 //
-// What it costs (MI355X).  16384 rows of 32000 bf16 logits: 193 to 205 us, 5.1 to
-// 5.4 TB/s; with five alternatives 345 (their instructions bound it then: two
-// bounds, a scan and a sort per chunk of a wave), 2052 float32 rows of 50257 with
-// eight 104 (4.0 TB/s).  15600 rows of 3128 with one alternative: 39 us.  One row of
+// What it costs (MI355X).  16384 rows of 32000 bf16 logits: 181 to 186 us, 5.7 TB/s;
+// with five alternatives 267 (their instructions bound it then: a bound and a
+// scan per chunk of a wave), 2052 float32 rows of 50257 with eight 104 (4.0
+// TB/s).  16384 float32 rows of 4096: 44, with five 59 us.  One row of
 // 32000 with five: 11 us in one workgroup, most of it the latency of a chain
 // of loads, maximum, bound, list and sort.  The gradient: 16384 x 32000 bf16
 // 424 us (4.9 TB/s read and written, a copy's rate), 2052 x 50257 float32, half
@@ -45,7 +45,7 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kR = 8;                       // 16-byte vectors per lane and chunk
-constexpr int kWaves = 8;                   // waves that share a long row
+constexpr int kWaves = 8;                   // waves that share a long row, at most
 constexpr int kTopLanes = 32;               // lanes that hold the best so far in a sort of many
 constexpr int kListed = 128;                // a wave's list: up to 64 entries and a chunk's 64
 constexpr float kFloor2 = -1000.f;          // below the least exponent: e = 0 there
@@ -604,10 +604,24 @@ void grad_v(const LogprobGradArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((logprobs_grad_kernel<E, EO, false>), grid, dim3(256), 0, s, a);
 }
 
-// One wave per row up to this many logits (one chunk of a wave): no barrier, and
-// four rows per workgroup.
+// Waves per row.  A wave alone needs no barrier and one bound, list and sort per
+// row, but the chip needs rows for it; eight hold a long row at once.  In
+// chunks of a wave (64 kR vectors, 8 KB), N rows, microseconds for 1, 4, 8 waves:
+//   without alternatives  N 16384, 1.5 chunks 33 39 70; 4 105 100 125; 8 198 185 191
+//                         N 1024, 6 chunks 20 14 14; 24 63 40 40
+//   five alternatives     N 16384, 1.5 chunks 68 106 186; 4 146 154 258; 12 384 400 479
+//                         N 4096, 2 chunks 30 35 55; 12 129 115 129; 24 220 201 200
+//                         N 1024, 4 chunks 31 18 21; 24 126 67 61
 template <class E>
-constexpr int64_t wave_row() { return 64 * kR * E::kVec; }
+int waves_of(const LogprobArgs& a) {
+  const int64_t chunk = 64 * kR * E::kVec, chunks = (a.V + chunk - 1) / chunk;
+  const int64_t alone = a.top_k > 0 ? a.N / 2048 : std::min<int64_t>(2, a.N / 2048);
+  if (chunks <= std::max<int64_t>(1, alone)) return 1;
+  return chunks <= a.N / 128 ? 4 : kWaves;
+}
+int waves_of(const LogprobArgs& a) {
+  return a.dtype == kBF16 ? waves_of<BF16>(a) : waves_of<F32>(a);
+}
 
 // Workgroups per row: 1, or enough for half the compute units where the rows
 // are fewer, parts of at least one chunk of each wave.  (Smaller parts are read
@@ -623,8 +637,13 @@ int splits_of(const LogprobArgs& a) {
 
 template <class E, bool TOP>
 hipError_t logprobs_e(const LogprobArgs& a, hipStream_t s) {
-  if (a.V <= wave_row<E>()) {
+  const int waves = waves_of<E>(a);
+  if (waves == 1) {
     hipLaunchKernelGGL((logprobs_kernel<E, 1, TOP>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a, 1);
+    return hipGetLastError();
+  }
+  if (waves == 4) {
+    hipLaunchKernelGGL((logprobs_kernel<E, 4, TOP>), dim3((unsigned)a.N), dim3(256), 0, s, a, 1);
     return hipGetLastError();
   }
   const int splits = splits_of(a);
@@ -639,7 +658,7 @@ hipError_t logprobs_e(const LogprobArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t logprobs_workspace_bytes(const LogprobArgs& a) {
-  const int splits = a.V <= (a.dtype == kBF16 ? wave_row<BF16>() : wave_row<F32>()) ? 1 : splits_of(a);
+  const int splits = waves_of(a) < kWaves ? 1 : splits_of(a);
   return splits == 1 ? 0 : (size_t)a.N * splits * part_words(a.top_k) * sizeof(float);
 }
 

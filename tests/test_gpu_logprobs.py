@@ -135,6 +135,29 @@ def test_ordered_and_nearly_equal_logits(V, top_k):
         _check(torch, dp, x, y, None, dtype, top_k, _forward(torch, dp, x, y, None, dtype, top_k))
 
 
+@pytest.mark.parametrize("top_k", [0, 5, 32])
+@pytest.mark.parametrize("dtype,V", [("f32", 2049), ("f32", 4001), ("f32", 7000), ("bf16", 4097),
+                                     ("bf16", 8003), ("bf16", 12345)])
+def test_many_rows(V, dtype, top_k):
+    """Rows of two or more chunks by one wave, or by four: where there are many.  The same rows
+    over and over (at other alignments, so not bit for bit), in two calls alike."""
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(V + top_k)
+    z, y = _case(rng, 4, 75, V, dtype)
+    few = _forward(torch, dp, z, y, None, dtype, top_k)                  # 300 rows
+    _check(torch, dp, z, y, None, dtype, top_k, few)
+    reps = 4200 // 75 + 1
+    zs = to_dev(z[:1], dtype, torch).repeat(reps, 1, 1)
+    ys = torch.from_numpy(y[:1]).cuda().repeat(reps, 1)
+    many, again = (dp.token_logprobs(zs, ys, top_k=top_k) for _ in range(2))
+    for a, b in zip(many, again):
+        assert a is None or torch.equal(a, b)
+    for k in (0, 1, reps // 2, reps - 1):
+        part = type(many)(*(None if x is None else x[k:k + 1] for x in many))
+        _check(torch, dp, z[:1], y[:1], None, dtype, top_k, part)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("V", [16383, 16384, 32767, 32768, 32776, 65535, 65545])
 def test_rows_at_the_edges_of_parts(V, dtype):
