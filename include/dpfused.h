@@ -582,8 +582,8 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  * for an unknown dtype, pointers not 16-byte aligned, n > 65535, rows or cols
  * > 2^17 or n * rows * cols > 2^33; DPF_ERR_OUT_OF_MEMORY when the workspace
  * (8 bytes per element, and 8 per element of the [n, m, m] products, m =
- * min(rows, cols), dimensions rounded up to 128 or 256; none for matrices
- * that fit into one workgroup's LDS) cannot be allocated. */
+ * min(rows, cols), dimensions rounded up to 128 or 256; less for matrices of
+ * at most 96 rows or columns, none where one fits into a workgroup's LDS) cannot be allocated. */
 dpf_status dpfused_orthogonalize(const void* M, int32_t dtype, int64_t n, int64_t rows,
                                  int64_t cols, int32_t steps, float a, float b, float c, float eps,
                                  void* out, void* stream);

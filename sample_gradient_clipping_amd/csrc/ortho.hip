@@ -47,7 +47,8 @@
 //
 // Where a product has too few tiles for the chip, several workgroups share a
 // tile's steps and leave float32 parts that a second kernel adds in order.
-// Matrices that fit into LDS take one workgroup for the whole call.
+// Matrices that fit into LDS take one workgroup for the whole call, other
+// thin ones (up to 96 rows or columns) two launches a step.
 //
 // What it costs (MI355X).  The MFMAs bound it.  A 13824 x 5120 step takes 15.9
 // ms: five times X^T X 0.91 ms (1250 TFLOP/s of half-precision products), the
@@ -810,12 +811,16 @@ struct Planes {
   }
 };
 
-// Block (r0, c0) of L R^T (fragments from `l` and `r`), K in steps of 16.
-template <class FL, class FR>
-__device__ __forceinline__ f32x16 small_block(int K, FL&& l, FR&& r) {
+__device__ __forceinline__ f32x16 zero16() {
   f32x16 acc;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  return acc;
+}
+
+// acc + block (r0, c0) of L R^T (fragments from `l` and `r`), K in steps of 16.
+template <class FL, class FR>
+__device__ __forceinline__ f32x16 small_block(int K, FL&& l, FR&& r, f32x16 acc = zero16()) {
 #pragma unroll 2
   for (int k0 = 0; k0 < K; k0 += 16) {
     const u16x8 lh = l(false, k0), ll = l(true, k0), rh = r(false, k0), rl = r(true, k0);
@@ -926,6 +931,226 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(SmallArgs p)
 }
 
 // ---------------------------------------------------------------------------
+// Thin matrices
+// ---------------------------------------------------------------------------
+// m x k with m <= 96 and too long for one workgroup: two launches a step in
+// place of four.  X is cut into strips of 128 columns, each kept as the image of
+// its planes in LDS.  A workgroup takes a strip (or several) through X <- a X +
+// B X and at once adds its X X^T to the next step's A, of which it leaves a part
+// (the 32 x 32 blocks on and above the diagonal); one workgroup per matrix adds
+// the parts in order and makes B = b A + c A^2.  Bound by the latency of its
+// twelve launches' short chains (memory, LDS, barrier, store), 5 to 8 us each.
+// Against the tiles of 128: 16 x 5120 65 us (250), 35 x 4850 105 (247), 5120 x 64
+// 94 (257), 90 x 600 115 (164), 96 x 20000 297 (395), stacks of 256 64 x 1000 285
+// (576), of 64 90 x 1000 216 (258).  With m = 128 it was no faster (128 x 5120
+// 280 against 254: the parts of A, and one workgroup per compute unit).
+constexpr int kThinCols = 128, kThinMost = 96;    // columns of a strip, rows of X at most
+constexpr int kThinX = (kThinMost / 32 * (kThinCols / 32) + kSmallWaves - 1) / kSmallWaves;   // blocks of X per wave
+constexpr int kThinLd = kThinCols + 8;
+
+struct ThinArgs {
+  OrthoArgs a;
+  int flip, m, k, mp;             // X: [m, k], m padded to 32
+  int strips, parts;              // strips, and workgroups that share them
+  int nb;                         // norm partials per matrix
+  const double* sq;
+  float* unit;                    // [n]
+  uint16_t* X;                    // [n][strips][hi, lo][mp][kThinCols]
+  uint16_t* B;                    // [n][hi, lo][mp][mp]
+  float* part;                    // [n][parts][blocks][32 * 32]
+  float pow_x;
+  AddFactors f;
+};
+
+__host__ __device__ constexpr int tri_blocks(int mb) { return mb * (mb + 1) / 2; }
+// Block q on or above the diagonal, row by row.
+__device__ __forceinline__ void tri_block(int q, int mb, int* r0, int* c0) {
+  int r = 0;
+  while (q >= mb - r) q -= mb - r++;
+  *r0 = 32 * r;
+  *c0 = 32 * (r + q);
+}
+
+// `rows` rows of `cols` halves between memory (contiguous, the lo plane after the
+// hi plane) and planes in LDS, 16 bytes a lane.
+template <bool STORE>
+__device__ __forceinline__ void copy_planes(const Planes& x, uint16_t* g, int rows, int cols) {
+  const int per = cols / 8, plane = rows * per;
+  for (int i = threadIdx.x; i < 2 * plane; i += kSmallThreads) {
+    const int j = i < plane ? i : i - plane, r = j / per, c = (j - r * per) * 8;
+    u16x8* l = (u16x8*)((i < plane ? x.hi : x.lo) + r * x.ld + c);
+    u16x8* m = (u16x8*)g + i;
+    if constexpr (STORE) *m = *l;
+    else *l = *m;
+  }
+}
+
+enum ThinStage { kThinFirst = 0, kThinStep = 1, kThinLast = 2 };
+
+template <class E, bool MUON, int STAGE>
+__global__ void __launch_bounds__(kSmallThreads) ortho_strip_kernel(ThinArgs p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ double scale;
+  const OrthoArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int mp = p.mp, mb = mp / 32, kb = kThinCols / 32, C = (int)a.C;
+  const int64_t n = blockIdx.y, base = n * p.m * p.k;
+  const Planes X{(uint16_t*)lds, (uint16_t*)lds + mp * kThinLd, kThinLd};
+  uint16_t* bp = X.lo + mp * kThinLd;
+  const Planes B{bp, bp + mp * (mp + 8), mp + 8};
+  if constexpr (STAGE == kThinFirst) {
+    if (tid < 64) {
+      double sq = 0.0;
+      for (int i = tid; i < p.nb; i += 64) sq += p.sq[n * p.nb + i];
+      sq = wave_sum_f64(sq);
+      if (tid == 0) {
+        int e;
+        scale = input_scale(a, sq, p.pow_x, &e);
+        if (blockIdx.x == 0) p.unit[n] = ldexpf(1.0f, -e);
+      }
+    }
+  } else {
+    copy_planes<false>(B, p.B + n * 2 * mp * mp, mp, mp);
+  }
+  f32x16 sums[kSmallSquare];
+#pragma unroll
+  for (int q = 0; q < kSmallSquare; ++q) sums[q] = zero16();
+  const int s0 = (int)((int64_t)p.strips * blockIdx.x / p.parts);
+  const int s1 = (int)((int64_t)p.strips * (blockIdx.x + 1) / p.parts);
+  for (int strip = s0; strip < s1; ++strip) {
+    uint16_t* image = p.X + (n * p.strips + strip) * (2 * mp * kThinCols);
+    const int col0 = strip * kThinCols;
+    __syncthreads();                              // the last strip is done with
+    if constexpr (STAGE == kThinFirst) {
+      for (int i = tid; i < mp * kThinCols; i += kSmallThreads) {
+        // along the input's rows
+        const int r = p.flip ? i % mp : i / kThinCols, c = p.flip ? i / mp : i % kThinCols;
+        float v = 0.f;
+        if (r < p.m && col0 + c < p.k) {
+          const int64_t e = base + (p.flip ? (int64_t)(col0 + c) * C + r : (int64_t)r * C + col0 + c);
+          v = (float)((double)update_at<E, MUON>(a, e) * scale);
+        }
+        X.put(r, c, v);
+      }
+      __syncthreads();
+    } else {
+      copy_planes<false>(X, image, mp, kThinCols);
+      __syncthreads();
+      f32x16 x[kThinX];
+#pragma unroll
+      for (int q = 0; q < kThinX; ++q) {
+        const int i = wave + q * kSmallWaves;
+        if (i < mb * kb)
+          x[q] = small_block(mp, [&](bool low, int k) { return B.inner(low, i / kb * 32, k); },
+                             [&](bool low, int k) { return X.outer(low, i % kb * 32, k); });
+      }
+      __syncthreads();
+      if constexpr (STAGE == kThinStep) {
+#pragma unroll
+        for (int q = 0; q < kThinX; ++q) {
+          const int i = wave + q * kSmallWaves;
+          if (i < mb * kb) X.update(i / kb * 32, i % kb * 32, p.f.add_x, p.f.apply, x[q]);
+        }
+        __syncthreads();
+      } else {
+        const float inv = p.unit[n];
+#pragma unroll
+        for (int q = 0; q < kThinX; ++q) {
+          const int i = wave + q * kSmallWaves;
+          const int r = i / kb * 32 + acc_col(lane), c0 = i % kb * 32;
+          if (i >= mb * kb || r >= p.m) continue;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int c = c0 + acc_row(j, lane);
+            if (col0 + c >= p.k) continue;
+            const int at = r * kThinLd + c;
+            const float old = (float)__builtin_bit_cast(_Float16, X.hi[at]) +
+                              (float)__builtin_bit_cast(_Float16, X.lo[at]);
+            const float v = (p.f.add_x * old + p.f.apply * x[q][j]) * inv;
+            const int64_t e = base + (p.flip ? (int64_t)(col0 + c) * C + r : (int64_t)r * C + col0 + c);
+            if constexpr (MUON) {
+              a.W[e] = a.decay * a.W[e] - a.size * v;
+            } else {
+              float one[1] = {v};
+              store_f32<E, 1>((typename E::storage*)a.out + e, one);
+            }
+          }
+        }
+      }
+    }
+    if constexpr (STAGE != kThinLast) {
+      copy_planes<true>(X, image, mp, kThinCols);
+#pragma unroll
+      for (int q = 0; q < kSmallSquare; ++q) {
+        const int i = wave + q * kSmallWaves;
+        if (i >= tri_blocks(mb)) continue;
+        int r0, c0;
+        tri_block(i, mb, &r0, &c0);
+        sums[q] = small_block(kThinCols, [&](bool low, int k) { return X.inner(low, r0, k); },
+                              [&](bool low, int k) { return X.inner(low, c0, k); }, sums[q]);
+      }
+    }
+  }
+  if constexpr (STAGE != kThinLast) {
+    float* part = p.part + (n * p.parts + blockIdx.x) * (tri_blocks(mb) * 1024);
+#pragma unroll
+    for (int q = 0; q < kSmallSquare; ++q) {
+      const int i = wave + q * kSmallWaves;
+      if (i >= tri_blocks(mb)) continue;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        ((f32x4*)part)[i * 256 + g * 64 + lane] =
+            f32x4{sums[q][4 * g], sums[q][4 * g + 1], sums[q][4 * g + 2], sums[q][4 * g + 3]};
+    }
+  }
+}
+
+// B of one matrix from the strips' parts of A.
+__global__ void __launch_bounds__(kSmallThreads) ortho_thin_square_kernel(ThinArgs p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int tid = threadIdx.x, wave = tid >> 6, mp = p.mp, mb = mp / 32, ld = mp + 8;
+  const int64_t n = blockIdx.x;
+  const Planes A{(uint16_t*)lds, (uint16_t*)lds + mp * ld, ld};
+  const int values = tri_blocks(mb) * 256;        // four of each part
+  const f32x4* part = (const f32x4*)p.part + n * p.parts * values;
+  const float inv = p.unit[n], f = p.f.gram * inv * inv;
+  for (int i = tid; i < values; i += kSmallThreads) {
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = 0; k < p.parts; ++k) {
+      const f32x4 v = part[(int64_t)k * values + i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += v[e];
+    }
+    int r0, c0;
+    tri_block(i / 256, mb, &r0, &c0);
+    const int lane = i & 63, r = r0 + acc_col(lane), c = c0 + acc_row(4 * (i >> 6 & 3), lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      A.put(r, c + e, f * sum[e]);
+      if (r0 != c0) A.put(c + e, r, f * sum[e]);
+    }
+  }
+  __syncthreads();
+  f32x16 acc[kSmallSquare];
+#pragma unroll
+  for (int q = 0; q < kSmallSquare; ++q) {
+    const int i = wave + q * kSmallWaves;
+    if (i < mb * mb)
+      acc[q] = small_block(mp, [&](bool low, int k) { return A.inner(low, i / mb * 32, k); },
+                           [&](bool low, int k) { return A.inner(low, i % mb * 32, k); });
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kSmallSquare; ++q) {
+    const int i = wave + q * kSmallWaves;
+    if (i < mb * mb) A.update(i / mb * 32, i % mb * 32, p.f.add_b, p.f.square, acc[q]);
+  }
+  __syncthreads();
+  copy_planes<true>(A, p.B + n * 2 * mp * mp, mp, mp);
+}
+
+// ---------------------------------------------------------------------------
 // Plan
 // ---------------------------------------------------------------------------
 // The largest |a s + b s^3 + c s^5| over 0 <= s <= top.
@@ -973,6 +1198,7 @@ struct Plan {
   int nb;                      // norm workgroups per matrix
   int64_t groups_sym, groups_full, groups_square;
   int small;                   // LDS bytes of the one-workgroup kernel, or 0
+  int strips, thin_parts;      // of a thin matrix, or 0
   size_t x, a, part, unit, parts, total;   // bytes of one X pair, one A pair; offsets
 };
 
@@ -1036,17 +1262,38 @@ int small_lds(int64_t mp, int64_t kp) {
   return bytes <= kSmallLds ? (int)bytes : 0;
 }
 
+// Workgroups that share a thin matrix's strips: enough for two per compute
+// unit over the stack, and few enough that the one workgroup which adds their
+// parts does not take longer than the strips (192 blocks of 4 KB).
+int thin_parts(int64_t n, int strips, int blocks) {
+  const int64_t want = std::max<int64_t>(1, 2 * device_cus() / n);
+  return (int)std::min<int64_t>({strips, want, std::max(16, 192 / blocks), 64});
+}
+
 Plan plan_of(const OrthoArgs& a) {
   Plan p{};
   p.flip = a.R > a.C;
   p.m = std::min(a.R, a.C);
   p.small = small_lds(up(p.m, 32), up(std::max(a.R, a.C), 32));
   if (p.small != 0) return p;
+  p.nb = (int)std::min<int64_t>(kSumBlocks, (a.R * a.C + 4095) / 4096);
+  if (p.m <= kThinMost) {
+    p.mp = up(p.m, 32);
+    p.strips = (int)((std::max(a.R, a.C) + kThinCols - 1) / kThinCols);
+    const int blocks = tri_blocks((int)(p.mp / 32));
+    p.thin_parts = thin_parts(a.n, p.strips, blocks);
+    p.x = (size_t)a.n * p.strips * (size_t)p.mp * kThinCols * 4;
+    p.a = (size_t)(a.n * p.mp * p.mp) * 4;
+    p.part = p.x + p.a;
+    p.unit = p.part + (size_t)a.n * p.nb * sizeof(double);
+    p.parts = (size_t)up((int64_t)(p.unit + (size_t)a.n * sizeof(float)), 256);
+    p.total = p.parts + (size_t)a.n * p.thin_parts * blocks * 1024 * sizeof(float);
+    return p;
+  }
   plan_tiles(p, a, 256);
   const double large = plan_cost(p, a);
   plan_tiles(p, a, 128);
   if (large < plan_cost(p, a)) plan_tiles(p, a, 256);
-  p.nb = (int)std::min<int64_t>(kSumBlocks, (a.R * a.C + 4095) / 4096);
   p.x = (size_t)(a.n * p.Rp * p.Cp) * 4;
   p.a = (size_t)(a.n * p.mp * p.mp) * 4;
   p.part = 2 * p.x + 2 * p.a;
@@ -1092,12 +1339,17 @@ hipError_t launch_product(ProductArgs p, int tile, bool ki, int64_t n, int64_t g
 }
 
 template <class E, bool MUON>
-hipError_t launch_input(const OrthoArgs& a, const Plan& p, double* part, float* unit, Pair X,
-                        float pow_x, hipStream_t s) {
+hipError_t launch_norm(const OrthoArgs& a, const Plan& p, double* part, hipStream_t s) {
   const dim3 grid((unsigned)p.nb, (unsigned)a.n);
   if (a.R * a.C % 4 == 0) hipLaunchKernelGGL((ortho_norm_kernel<E, MUON, 4>), grid, dim3(256), 0, s, a, part);
   else hipLaunchKernelGGL((ortho_norm_kernel<E, MUON, 1>), grid, dim3(256), 0, s, a, part);
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+template <class E, bool MUON>
+hipError_t launch_input(const OrthoArgs& a, const Plan& p, double* part, float* unit, Pair X,
+                        float pow_x, hipStream_t s) {
+  const hipError_t e = launch_norm<E, MUON>(a, p, part, s);
   if (e != hipSuccess) return e;
   const dim3 blocks((unsigned)std::min<int64_t>(8192, (p.Rp * p.Cp / 4 + 1023) / 1024), (unsigned)a.n);
   if (a.C % 4 == 0)
@@ -1173,6 +1425,52 @@ hipError_t launch_small(const SmallArgs& q, int lds, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class E, bool MUON, int STAGE>
+hipError_t launch_strips(const ThinArgs& q, hipStream_t s) {
+  static hipError_t once = hipFuncSetAttribute((const void*)ortho_strip_kernel<E, MUON, STAGE>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
+  if (once != hipSuccess) return once;
+  const int lds = 4 * q.mp * kThinLd + 4 * q.mp * (q.mp + 8);
+  hipLaunchKernelGGL((ortho_strip_kernel<E, MUON, STAGE>), dim3((unsigned)q.parts, (unsigned)q.a.n),
+                     dim3(kSmallThreads), lds, s, q);
+  return hipGetLastError();
+}
+
+template <class E, bool MUON>
+hipError_t launch_thin(const OrthoArgs& a, const Plan& p, hipStream_t s) {
+  static hipError_t once = hipFuncSetAttribute((const void*)ortho_thin_square_kernel,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
+  if (once != hipSuccess) return once;
+  char* ws = (char*)a.ws;
+  double top = 1.0;
+  int sx = scale_of(top * kRoom);
+  ThinArgs q{};
+  q.a = a;
+  q.flip = p.flip ? 1 : 0;
+  q.m = (int)p.m;
+  q.k = (int)std::max(a.R, a.C);
+  q.mp = (int)p.mp;
+  q.strips = p.strips;
+  q.parts = p.thin_parts;
+  q.nb = p.nb;
+  q.sq = (const double*)(ws + p.part);
+  q.unit = (float*)(ws + p.unit);
+  q.X = (uint16_t*)ws;
+  q.B = (uint16_t*)(ws + p.x);
+  q.part = (float*)(ws + p.parts);
+  q.pow_x = std::ldexp(1.f, sx);
+  hipError_t e = launch_norm<E, MUON>(a, p, (double*)(ws + p.part), s);
+  if (e == hipSuccess) e = launch_strips<E, MUON, kThinFirst>(q, s);
+  for (int k = 0; k < a.steps && e == hipSuccess; ++k) {
+    q.f = add_factors(a, &top, &sx, k + 1 == a.steps);
+    hipLaunchKernelGGL(ortho_thin_square_kernel, dim3((unsigned)a.n), dim3(kSmallThreads),
+                       4 * q.mp * (q.mp + 8), s, q);
+    if ((e = hipGetLastError()) != hipSuccess) break;
+    e = k + 1 < a.steps ? launch_strips<E, MUON, kThinStep>(q, s) : launch_strips<E, MUON, kThinLast>(q, s);
+  }
+  return e;
+}
+
 }  // namespace
 
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
@@ -1194,6 +1492,14 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
                          : a.dtype == kBF16 ? launch_small<BF16, false>(q, p.small, s)
                                             : launch_small<F32, false>(q, p.small, s);
     timing_end("ortho_small", s);
+    return e;
+  }
+  if (p.strips != 0) {
+    timing_begin("ortho_thin", s);
+    const hipError_t e = a.W != nullptr       ? launch_thin<F32, true>(a, p, s)
+                         : a.dtype == kBF16 ? launch_thin<BF16, false>(a, p, s)
+                                            : launch_thin<F32, false>(a, p, s);
+    timing_end("ortho_thin", s);
     return e;
   }
   char* ws = (char*)a.ws;

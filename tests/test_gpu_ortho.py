@@ -168,6 +168,88 @@ def test_optimizer_step_scale_and_repeat():
     assert torch.equal(W, W2) and torch.equal(m, m2)
 
 
+# Matrices of at most 96 rows or columns, too long for one workgroup.
+@pytest.mark.parametrize("kind", ["full", "lowrank", "spike"])
+@pytest.mark.parametrize("shape", [(1, 6000), (6000, 1), (17, 2000), (32, 1409), (1409, 33), (64, 700),
+                                   (65, 650), (650, 65), (96, 417), (3001, 96), (90, 8200)])
+def test_thin_matrices(shape, kind):
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(sum(shape))
+    M = _matrix(rng, *shape, kind)
+    for steps, coeffs in ((1, COEFFS), (5, COEFFS), (4, (1.5, -0.5, 0.0))):
+        t = torch.from_numpy(M).cuda()
+        out = dp.orthogonalize(t, steps=steps, coeffs=coeffs)
+        ref, bar = _bar(M, steps, coeffs, 1e-7)
+        err = np.linalg.norm(out.cpu().numpy() - ref)
+        assert err <= bar, (steps, err, bar)
+        assert torch.equal(out, dp.orthogonalize(t, steps=steps, coeffs=coeffs))
+        assert torch.equal(out, dp.orthogonalize(t, steps=steps, coeffs=coeffs, out=t))     # in place
+
+
+@pytest.mark.parametrize("shape", [(70, 900), (900, 40)])
+@pytest.mark.parametrize("n", [2, 150])
+def test_stacks_of_thin_matrices(n, shape):
+    """Each matrix with its own norm; zero, tiny, huge and not finite ones among them."""
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(n)
+    M = np.stack([_matrix(rng, *shape, "full") * np.float32(10.0 ** (k % 5)) for k in range(n)])
+    if n > 8:
+        M[1] = 0.0
+        M[2] *= np.float32(1e-27)                 # below eps: stays small
+        M[3] *= np.float32(1e36)
+        M[4, 3, 5] = np.nan
+        M[5, 7, 1] = np.inf
+    t = torch.from_numpy(M).cuda()
+    out = dp.orthogonalize(t).cpu().numpy()
+    for k in range(n):
+        if n > 8 and k in (1, 4, 5):
+            assert (out[k] == 0).all() if k == 1 else np.isnan(out[k]).all()
+            continue
+        ref, bar = _bar(M[k], 5, COEFFS, 1e-7)
+        assert np.linalg.norm(out[k] - ref) <= bar, k
+    if n > 8:
+        t16 = t[6:].bfloat16()
+        a, b = dp.orthogonalize(t16), dp.orthogonalize(t16.float())
+        assert torch.equal(a, b.bfloat16())
+
+
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("shape", [(60, 1000), (2000, 17), (3, 96, 500)])
+def test_optimizer_step_of_thin_matrices(shape, nesterov):
+    test_optimizer_step(shape, nesterov)
+
+
+def test_thin_matrices_on_streams_in_graphs_and_buffers():
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    for shape in ((50, 1303), (1303, 50)):
+        M = torch.randn(shape, device="cuda")
+        ref = dp.orthogonalize(M)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            other = dp.orthogonalize(M)
+        s.synchronize()
+        assert torch.equal(ref, other)
+        n = M.numel()
+        buf = torch.full((n + 512,), 7.0, device="cuda")
+        out = buf[256:256 + n].view(shape)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            dp.orthogonalize(M, out=out)
+        for _ in range(4):
+            M.copy_(torch.randn(shape, device="cuda"))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            eager = dp.orthogonalize(M)
+            torch.cuda.synchronize()
+            assert torch.equal(out, eager)
+        assert (buf[:256] == 7).all() and (buf[256 + n:] == 7).all()
+
+
 def test_in_place_streams_and_graphs():
     torch = need_gpu()
     import sample_gradient_clipping_amd as dp
