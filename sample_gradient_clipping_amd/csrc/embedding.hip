@@ -394,6 +394,11 @@ constexpr uint32_t kBlock = 8;
 // Batches below this many positions go without (two launches less, 4 to 5 us
 // each; a wave then adds at most this many rows, 32 batches of loads).
 constexpr int64_t kBlocksFrom = 256;
+// Samples of at most this many positions have no runs worth summing ahead for
+// the norms: norms of 256 x 64 positions of 768 columns 29.3 us without, 30.9
+// with (one token throughout: 34.1 and 33.5); of 32 x 512 31.0 and 31.6 (86.5 and
+// 42.1); of 8 x 2048 of 5120 columns 69.6 and 64.5 (546 and 161).
+constexpr int64_t kShortRuns = 64;
 
 typedef __attribute__((address_space(4))) const uint32_t c_u32;
 
@@ -950,7 +955,7 @@ hipError_t launch_embed_norm(const EmbedArgs& a, hipStream_t s) {
   const unsigned parts = (unsigned)embed_norm_parts(a);
   const uint32_t* pos = a.pos[embed_sorted(a.V, -1)];
   EmbedArgs q = a;
-  if (a.T < (int64_t)kBlock) q.blocks = nullptr;   // no run is as long
+  if (a.T <= kShortRuns) q.blocks = nullptr;
   timing_begin("embed_norm", s);
   with_rows(a, [&](auto e, auto v, auto u) {
     using E = decltype(e);

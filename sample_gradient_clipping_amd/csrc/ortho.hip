@@ -142,8 +142,9 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(OrthoArgs a, double* pa
   __shared__ double red[4];
   const int64_t len = a.R * a.C, base = (int64_t)blockIdx.y * len;
   double sq = 0.0;
+  const int64_t step = (int64_t)gridDim.x * 256 * V;
 #pragma unroll 4
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < len; i += (int64_t)gridDim.x * 256 * V) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < len; i += step) {
     float u[V];
     update_from<E, MUON, V, true>(a, base + i, u);
 #pragma unroll
@@ -564,7 +565,8 @@ __global__ void __launch_bounds__(S::kNT, 2) ortho_product_kernel(ProductArgs p)
     const int64_t tile = at / p.steps;
     const int mat = __builtin_amdgcn_readfirstlane((int)(tile / p.tiles));
     const int k0 = __builtin_amdgcn_readfirstlane((int)(at - tile * p.steps));
-    const int n = __builtin_amdgcn_readfirstlane((int)min((int64_t)(p.steps - k0), s1 - at));   // steps of this piece
+    // steps of this piece
+    const int n = __builtin_amdgcn_readfirstlane((int)min((int64_t)(p.steps - k0), s1 - at));
     int ti, tj;
     tile_of(p, (int)(tile - (int64_t)mat * p.tiles), &ti, &tj);
     ti = __builtin_amdgcn_readfirstlane(ti);
@@ -945,7 +947,8 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(SmallArgs p)
 // (576), of 64 90 x 1000 216 (258).  With m = 128 it was no faster (128 x 5120
 // 280 against 254: the parts of A, and one workgroup per compute unit).
 constexpr int kThinCols = 128, kThinMost = 96;    // columns of a strip, rows of X at most
-constexpr int kThinX = (kThinMost / 32 * (kThinCols / 32) + kSmallWaves - 1) / kSmallWaves;   // blocks of X per wave
+// blocks of X per wave
+constexpr int kThinX = (kThinMost / 32 * (kThinCols / 32) + kSmallWaves - 1) / kSmallWaves;
 constexpr int kThinLd = kThinCols + 8;
 
 struct ThinArgs {
