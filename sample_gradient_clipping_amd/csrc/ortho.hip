@@ -9,9 +9,11 @@
 //   A' = A + (b / 2c) I,  B = c A'^2 + (a - b^2 / 4c) I,  X <- B X
 //
 // so that every product's result is only scaled, shifted on its diagonal and
-// stored: nothing is read back (with c = 0: B = b A + a I, and no square).  The
-// optimizer step forms U from the gradient and the momentum, and subtracts the
-// result from the weight.
+// stored: nothing is read back (with c = 0: B = b A + a I, and no square).  A
+// shift that is large beside A's eigenvalues would take A's low bits with it:
+// then the square is c A^2, and a pass over it adds b A + a I (completed_square
+// below).  The optimizer step forms U from the gradient and the momentum, and
+// subtracts the result from the weight.
 //
 // Products.  Every operand is kept as two half-precision matrices hi + lo
 // (hi = half(v), lo = half(v - hi), 22 bits together), scaled by a power of two
@@ -735,6 +737,32 @@ __global__ void __launch_bounds__(S::kNT) ortho_fixup_kernel(ProductArgs p) {
   store_rows<S>(p, mat, ti, tj, i, acc, lds);
 }
 
+// B += add A, plus `shift` on the diagonal: 8 elements of n matrices [mp, mp] a
+// thread, hi and lo of both in one 16-byte load each.  Bound by memory (201 MB
+// for 4096 x 4096), below that by its launch: five steps of 768 x 768 take 304 us
+// with it and 292 with the completed square, of 1920 x 1920 655 and 625, of
+// 4096 x 4096 3.95 and 3.83 ms.
+__global__ void __launch_bounds__(256) ortho_add_kernel(Pair A, Pair B, int64_t n, int mp, float add,
+                                                        float shift) {
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (e >= n * mp * mp) return;
+  const int64_t row = e / mp;                       // of all matrices
+  const int c = (int)(e - row * mp), diag = (int)(row % mp) - c;
+  const int64_t at = row * A.ld + 2 * c - (c & 15);
+  typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+  const half8 ah = *(const half8*)(A.p + at), al = *(const half8*)(A.p + at + 16);
+  half8 bh = *(const half8*)(B.p + at), bl = *(const half8*)(B.p + at + 16);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float x = ((float)bh[k] + (float)bl[k]) + add * ((float)ah[k] + (float)al[k]) +
+                    (k == diag ? shift : 0.f);
+    bh[k] = (_Float16)x;
+    bl[k] = (_Float16)(x - (float)bh[k]);
+  }
+  *(half8*)(B.p + at) = bh;
+  *(half8*)(B.p + at + 16) = bl;
+}
+
 // ---------------------------------------------------------------------------
 // Small matrices
 // ---------------------------------------------------------------------------
@@ -754,6 +782,7 @@ constexpr int kSmallLds = 156 * 1024;
 // What the products' results are multiplied by, and the diagonal shifts.
 struct StepFactors {
   float gram, gram_shift, square, square_shift, apply;
+  float add_b, add_shift;                         // of the pass after the square, or 0
 };
 // The same for B = b A + c A^2 and X <- a X + B X.
 struct AddFactors {
@@ -1371,8 +1400,6 @@ bool ortho_coeffs_ok(const OrthoArgs& a) {
   for (int k = 0; k < a.steps; ++k) {
     top = kRoom * poly_bound(a.a, a.b, a.c, top);
     if (!(top <= 4.0)) return false;
-    if (!(quad_bound(a.a, a.b, a.c, top * top) <= 1e4)) return false;
-    if (a.c != 0.0 && !(std::fabs(a.b / (2 * a.c)) <= 1e4)) return false;
   }
   return true;
 }
@@ -1381,24 +1408,43 @@ size_t ortho_workspace_bytes(const OrthoArgs& a) { return plan_of(a).total; }
 
 namespace {
 
+// Whether the square is completed.  A' is rounded at the shift's size, 2^-23
+// |b / 2c|, which B takes times b; in b A + c A^2 the rounding of A, whose
+// eigenvalues are at most about 1, stands there instead.  So the shift may be
+// little more than that (the limit of 3/2 has (2, -1.5, 0.5) at it), and what
+// the diagonal takes back, b^2 / 4c, no larger than a.  Error against float64
+// after 5 steps of a 160 x 200 matrix (these roundings in numpy), completed and
+// not: (3.4445, -4.775, 2.0315) 1.3e-6 and 1.4e-6 (plain float32 products
+// 1.6e-6), (2, -1.5, 0.5) 6e-7 and 6e-7 (2.3e-7), (1.5, -0.5, 0.01) 7.5e-6 and
+// 5.4e-7 (9.3e-8), (1.5, -0.5, 1e-6) 6.0e-3 and 5.4e-7 (9.4e-8).
+bool completed_square(const OrthoArgs& a) {
+  return std::fabs(a.b) <= 3 * std::fabs(a.c) && a.b * a.b <= 4 * std::fabs(a.a * a.c);
+}
+
 // The factors of a step whose X is kept times 2^sx with singular values up to
 // *top; *top and the power of the next X come back.  A' and B are kept times
 // the powers that their largest values allow.
 StepFactors step_factors(const OrthoArgs& a, double* top, int* sx, bool last) {
   const double most = *top * *top;                // of A's eigenvalues
-  const bool square = a.c != 0.0;
-  const double shift = square ? a.b / (2 * a.c) : 0.0;
-  const int sb = scale_of(kRoom * quad_bound(a.a, a.b, a.c, most));
+  const bool square = a.c != 0.0, completed = square && completed_square(a);
+  const double shift = completed ? a.b / (2 * a.c) : 0.0;
+  int sb = scale_of(kRoom * quad_bound(a.a, a.b, a.c, most));
+  if (square && !completed) sb = std::min(sb, scale_of(kRoom * std::fabs(a.c) * most * most));
   const int sa = square ? scale_of(kRoom * quad_bound(shift, 1.0, 0.0, most)) : sb;
   *top = kRoom * poly_bound(a.a, a.b, a.c, *top);
   const int next = last ? 0 : scale_of(kRoom * *top);
-  StepFactors f;
+  StepFactors f{};
   f.gram = (float)((square ? 1.0 : a.b) * std::ldexp(1.0, sa - 2 * *sx));
   f.gram_shift = (float)((square ? shift : a.a) * std::ldexp(1.0, sa));
   f.square = (float)(a.c * std::ldexp(1.0, sb - 2 * sa));
-  // from the shift as it was rounded, so that the two cancel in full
-  const double rounded = std::ldexp((double)f.gram_shift, -sa);
-  f.square_shift = square ? (float)((a.a - a.c * rounded * rounded) * std::ldexp(1.0, sb)) : 0.f;
+  if (completed) {
+    // from the shift as it was rounded, so that the two cancel in full
+    const double rounded = std::ldexp((double)f.gram_shift, -sa);
+    f.square_shift = (float)((a.a - a.c * rounded * rounded) * std::ldexp(1.0, sb));
+  } else if (square) {
+    f.add_b = (float)(a.b * std::ldexp(1.0, sb - sa));
+    f.add_shift = (float)(a.a * std::ldexp(1.0, sb));
+  }
   f.apply = (float)std::ldexp(1.0, next - sb - *sx);
   *sx = next;
   return f;
@@ -1553,6 +1599,14 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
       e = launch_product(q, p.tile, !p.flip, a.n, p.groups_square, s);
       timing_end("ortho_square", s);
       if (e != hipSuccess) break;
+      if (!completed_square(a)) {
+        const int64_t threads = a.n * p.mp * p.mp / 8;
+        timing_begin("ortho_add", s);
+        hipLaunchKernelGGL(ortho_add_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, A, B,
+                           a.n, (int)p.mp, f.add_b, f.add_shift);
+        timing_end("ortho_add", s);
+        if ((e = hipGetLastError()) != hipSuccess) break;
+      }
     }
     // X <- B X (K-outer) or X B (K-inner)
     q.L = p.flip ? Xk : square ? B : A;

@@ -1,0 +1,19 @@
+"""Argument checks of the language-model entry points (CPU: they run before anything is queued)."""
+import pytest
+
+from sample_gradient_clipping_amd import _lib
+from sample_gradient_clipping_amd._lib import DPF_ERR_INVALID_ARGUMENT, DPF_ERR_UNSUPPORTED, DPF_F32
+
+FAKE, FAR = 0x10000, 0x10000 + (1 << 20)   # aligned, never dereferenced
+BAD, UNS = DPF_ERR_INVALID_ARGUMENT, DPF_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("coeffs,steps,status", [
+    ((1.5, -0.5, 1e-6), 5, UNS), ((1.5, -0.5, 1e-42), 5, UNS), ((1.5, -0.5, -1e-6), 5, UNS),
+    ((19.0, -76.0, 60.8), 1, UNS),           # 3.8 times the fifth Chebyshev polynomial
+    ((19.0, -76.0, 60.8), 2, BAD), ((4.5, 0.0, 1e-6), 1, BAD),
+])
+def test_only_growth_refuses_coefficients(coeffs, steps, status):
+    """Accepted ones get as far as the misaligned pointer."""
+    L = _lib.lib()
+    assert L.dpfused_orthogonalize(FAKE + 4, DPF_F32, 1, 8, 8, steps, *coeffs, 1e-7, FAR, None) == status
