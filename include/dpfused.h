@@ -467,8 +467,10 @@ dpf_status dpfused_embedding_lookup(const dpf_ids* ids, const void* table, int32
  * The positions are sorted by token (a stable sort on the device); equal
  * tokens of a sample are summed before they are squared, equal tokens of the
  * batch are one row of the result.  No per-sample gradient is stored.
- * Sums in float32, norms in float64, in a fixed order.  Accumulated without
- * noise (sigma 0), rows that no active position adds to are not touched.
+ * Sums in float32, in a fixed order; their squares in float32 over at most 8
+ * neighbouring columns (in float64 where one would leave float32's range) and
+ * in float64 from there on.  Accumulated without noise (sigma 0), rows that no
+ * active position adds to are not touched.
  *
  *   ids, G       [B, T] and [B, T, D] (bf16 or f32)
  *   V            rows of the table
