@@ -512,7 +512,9 @@ dpf_status dpfused_embedding_scaled_accumulate(const dpf_ids* ids, const dpf_act
  *   top_ids, top_logp   the top_k largest z_j and their z_j - lse, the
  *             largest first, equal values by the lower index first
  *
- * all in float32.  A logit of -inf is a token of probability 0.  A row that
+ * all in float32; logp and top_logp from the difference to the row's largest
+ * logit, so an offset that its logits have in common costs only lse its last
+ * bits.  A logit of -inf is a token of probability 0.  A row that
  * holds NaN or +inf, or only -inf, has NaN logp, entropy and top_logp (and
  * lse, but for the -inf row's -inf); top_ids then still orders the entries
  * that are not NaN, and is -1 past them.  A masked row is not read: its
@@ -543,7 +545,9 @@ dpf_status dpfused_token_logprobs(const dpf_act* logits, const dpf_ids* targets,
  * per-sample loss keeps its rows apart (dlogp = -1 / T_i, not -1 / (B T)).
  *
  *   lse, entropy     what the forward call gave for the same logits;
- *                    entropy may be NULL where dentropy is
+ *                    entropy may be NULL where dentropy is.  lse is rounded at
+ *                    the logits' size, and p with it: by up to 2^-24 |lse| of
+ *                    its value
  *   dlogp, dentropy  [B, T] float32; either may be NULL (taken as 0), not both
  *   dlogits          [B, T, V] bf16 or f32, strided; may be the logits
  *                    themselves (same dtype and strides), else must not

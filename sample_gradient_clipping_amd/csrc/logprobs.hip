@@ -2,7 +2,7 @@
 // logits, and the gradient to the logits.  For a row z of V logits, target y:
 //
 //   lse  = m + log S,  S = sum_j e_j,  e_j = exp(z_j - m),  m = max_j z_j
-//   logp = z_y - lse
+//   logp = z_y - lse = (z_y - m) - log S
 //   H    = -sum_j p_j log p_j = log S - S1 / S,  S1 = sum_j e_j (z_j - m)
 //   dz_j = dlogp (1[j = y] - p_j) - dH p_j (log p_j + H),  p_j = exp(z_j - lse)
 //
@@ -372,22 +372,24 @@ struct RowPart {
   }
 };
 
-// One wave writes a row's results (entries in lanes 0 ..).
+// One wave writes a row's results (entries in lanes 0 ..).  Log probabilities are
+// taken from the maximum, not from lse: that is rounded at the logits' size, and
+// an offset common to a row's logits would show in them.
 template <class E>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t n, const Stats& st, uint64_t e,
                                           const typename E::storage* z) {
   const int lane = threadIdx.x & 63;
-  const float log_s = logf(st.s), lse = st.m + log_s;
+  const float log_s = logf(st.s);
   if (lane == 0) {
-    if (a.lse != nullptr) a.lse[n] = lse;
+    if (a.lse != nullptr) a.lse[n] = st.m + log_s;
     if (a.entropy != nullptr) a.entropy[n] = log_s - kLn2 * (st.s1 / st.s);
     if (a.logp != nullptr) {
       const int64_t b = n / a.T, y = a.targets.at(b, n - b * a.T);
-      a.logp[n] = y >= 0 && y < a.V ? E::to_float(z[y]) - lse : 0.f;
+      a.logp[n] = y >= 0 && y < a.V ? (E::to_float(z[y]) - st.m) - log_s : 0.f;
     }
   }
   if (lane < a.top_k) {
-    a.top_logp[n * a.top_k + lane] = e != 0 ? value_of(e) - lse : __builtin_nanf("");
+    a.top_logp[n * a.top_k + lane] = e != 0 ? (value_of(e) - st.m) - log_s : __builtin_nanf("");
     a.top_ids[n * a.top_k + lane] = e != 0 ? index_of(e) : -1;
   }
 }
