@@ -607,7 +607,8 @@ dpf_status dpfused_orthogonalize(const void* M, int32_t dtype, int64_t n, int64_
  *   grad           [n, dout, din] float32, read
  *   momentum, W    [n, dout, din] float32, updated in place
  *   lr, weight_decay   finite; beta in [0, 1)
- *   scale          finite; NaN or <= 0: sqrt(max(1, dout / din))
+ *   scale          finite and >= 0 (0: only the momentum and the decay), or NaN
+ *                  for sqrt(max(1, dout / din))
  *
  * All pointers 16-byte aligned, none overlapping another.  Other arguments
  * and errors as above; nothing is written on error. */

@@ -704,7 +704,8 @@ def muon_step(grad, momentum, W, lr: float, beta: float = 0.95, nesterov: bool =
         momentum <- beta momentum + grad;  U = grad + beta momentum (nesterov) or momentum
         W <- (1 - lr weight_decay) W - lr scale orthogonalize(U)
 
-    scale=None takes sqrt(max(1, dout / din)).  Returns (momentum, W)."""
+    scale=None takes sqrt(max(1, dout / din)); 0 moves the momentum and decays W, a negative one
+    is refused.  Returns (momentum, W)."""
     torch = _torch()
     for t, name in ((grad, "grad"), (momentum, "momentum"), (W, "W")):
         if t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:

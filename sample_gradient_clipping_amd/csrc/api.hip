@@ -1914,16 +1914,16 @@ dpf_status dpfused_muon_step(const float* grad, float* momentum, float* W, int64
   if (!std::isfinite(lr) || !std::isfinite(weight_decay))
     return fail(DPF_ERR_INVALID_ARGUMENT, "lr and weight_decay must be finite");
   if (!(beta >= 0.0f && beta < 1.0f)) return fail(DPF_ERR_INVALID_ARGUMENT, "beta must be in [0, 1)");
-  if (std::isinf(scale)) return fail(DPF_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (std::isinf(scale) || scale < 0.0f)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "scale must be finite and >= 0 (or NaN for the default)");
   if (!aligned16(grad) || !aligned16(momentum) || !aligned16(W))
     return fail(DPF_ERR_UNSUPPORTED, "grad, momentum and W must be 16-byte aligned");
   const size_t bytes = (size_t)(n * dout * din) * sizeof(float);
   if (ranges_overlap(grad, bytes, momentum, bytes) || ranges_overlap(grad, bytes, W, bytes) ||
       ranges_overlap(momentum, bytes, W, bytes))
     return fail(DPF_ERR_INVALID_ARGUMENT, "grad, momentum and W must not overlap");
-  const double by = std::isnan(scale) || scale <= 0.0f
-                        ? std::sqrt(std::max(1.0, (double)dout / (double)din))
-                        : (double)scale;
+  const double by = std::isnan(scale) ? std::sqrt(std::max(1.0, (double)dout / (double)din))
+                                      : (double)scale;
   o.beta = beta;
   o.nesterov = nesterov != 0 ? 1 : 0;
   o.decay = (float)(1.0 - (double)lr * (double)weight_decay);

@@ -66,3 +66,20 @@ def test_small_last_coefficient_below_eps_and_in_stacks():
         ref, bar = _bar(M[k], 5, (1.5, -0.5, 1e-4))
         assert np.linalg.norm(out[k] - ref) <= bar
     assert np.count_nonzero(out[2]) == 0 and np.isnan(out[3]).all()
+
+
+def test_update_size_of_zero():
+    """scale 0 is a step of size 0, not the default one: the momentum moves, the weight decays."""
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(11)
+    for shape in ((40, 24), (90, 900), (200, 180)):          # one workgroup, strips, tiles
+        g, m, w = (torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).cuda() for _ in range(3))
+        m0, w0 = m.clone(), w.clone()
+        dp.muon_step(g, m, w, lr=0.5, beta=0.5, weight_decay=0.5, scale=0.0)
+        assert torch.equal(w, w0 * 0.75)
+        assert torch.equal(m, m0 * 0.5 + g)
+        for bad in (-1.0, -1e-30, float("-inf")):
+            with pytest.raises(dp.DpfError):
+                dp.muon_step(g, m, w, lr=0.5, scale=bad)
+        assert torch.equal(w, w0 * 0.75)

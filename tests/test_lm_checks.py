@@ -17,3 +17,12 @@ def test_only_growth_refuses_coefficients(coeffs, steps, status):
     """Accepted ones get as far as the misaligned pointer."""
     L = _lib.lib()
     assert L.dpfused_orthogonalize(FAKE + 4, DPF_F32, 1, 8, 8, steps, *coeffs, 1e-7, FAR, None) == status
+
+
+@pytest.mark.parametrize("scale,status", [(0.0, UNS), (2.0, UNS), (float("nan"), UNS), (-1.0, BAD),
+                                          (-1e-30, BAD), (float("-inf"), BAD)])
+def test_update_size(scale, status):
+    """0 is a size like any other, NaN asks for the default, negative ones are refused."""
+    L = _lib.lib()
+    assert L.dpfused_muon_step(FAKE + 4, FAR, FAR + (1 << 20), 1, 8, 8, 0.1, 0.9, 1, 0.0, scale, 5,
+                               3.4445, -4.775, 2.0315, 1e-7, None) == status
