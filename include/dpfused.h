@@ -701,6 +701,11 @@ uint64_t dpfused_noise_blocks(int64_t n_elements);
  *                on the same tiles (2); the 256 x 256 tiles (0).  Results
  *                agree within rounding (a different summation order), and
  *                each setting is deterministic.
+ *   "ortho_tile" orthogonalised update: 128 or 256 = its products on tiles of
+ *                that width wherever the matrices are too large for the
+ *                kernels of small and thin ones; 0 (default) = the width that
+ *                a cost rule expects to be faster.  Results agree within
+ *                rounding, and each setting is deterministic.
  *   "trace"      1 = push a roctx range named after the entry point around
  *                every call, for rocprofv3 --marker-trace; 0 = off (default)
  *   "debug"      1 = synchronise the launch stream after every kernel and

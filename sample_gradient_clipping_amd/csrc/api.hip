@@ -1850,7 +1850,11 @@ dpf_status check_ortho(const dpf::OrthoArgs& a) {
   return DPF_OK;
 }
 
+// Width of the product tiles, 0: chosen by their cost ("ortho_tile").
+std::atomic<int> g_ortho_tile{0};
+
 dpf_status queue_ortho(dpf::OrthoArgs& a, hipStream_t s, const char* where) {
+  a.tile = g_ortho_tile.load();
   Workspace ws(s);
   const size_t at = ws.reserve(dpf::ortho_workspace_bytes(a));
   if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
@@ -2015,6 +2019,12 @@ dpf_status dpfused_set_option(const char* name, int64_t value) {
     g_rspace_tiles.store((int)value);
     return ok();
   }
+  if (std::strcmp(name, "ortho_tile") == 0) {
+    if (value != 0 && value != 128 && value != 256)
+      return fail(DPF_ERR_INVALID_ARGUMENT, "ortho_tile must be 0, 128 or 256");
+    g_ortho_tile.store((int)value);
+    return ok();
+  }
   if (std::strcmp(name, "p_in_kernels") == 0) {
     if (value != 0 && value != 1) return fail(DPF_ERR_INVALID_ARGUMENT, "p_in_kernels must be 0 or 1");
     dpf::set_p_in_kernels(value != 0);
@@ -2047,6 +2057,7 @@ int64_t dpfused_get_option(const char* name) {
   if (std::strcmp(name, "p_in_kernels") == 0) return dpf::p_in_kernels() ? 1 : 0;
   if (std::strcmp(name, "side_streams") == 0) return g_side_streams.load();
   if (std::strcmp(name, "rspace_tiles") == 0) return g_rspace_tiles.load();
+  if (std::strcmp(name, "ortho_tile") == 0) return g_ortho_tile.load();
   if (std::strcmp(name, "trace") == 0) return g_trace.load();
   if (std::strcmp(name, "debug") == 0) return g_debug.load();
   // Read-only: memory the current device's workspace pool holds now, and the

@@ -266,6 +266,7 @@ struct OrthoArgs {
   float *momentum, *W;
   float beta, decay, size;
   int nesterov;
+  int tile;                 // 128 or 256 wide products, 0: the faster by their cost
   void* ws;                 // ortho_workspace_bytes(a)
 };
 // False where the coefficients let a singular value grow past 4 within the

@@ -1322,10 +1322,14 @@ Plan plan_of(const OrthoArgs& a) {
     p.total = p.parts + (size_t)a.n * p.thin_parts * blocks * 1024 * sizeof(float);
     return p;
   }
-  plan_tiles(p, a, 256);
-  const double large = plan_cost(p, a);
-  plan_tiles(p, a, 128);
-  if (large < plan_cost(p, a)) plan_tiles(p, a, 256);
+  if (a.tile != 0) {
+    plan_tiles(p, a, a.tile);
+  } else {
+    plan_tiles(p, a, 256);
+    const double large = plan_cost(p, a);
+    plan_tiles(p, a, 128);
+    if (large < plan_cost(p, a)) plan_tiles(p, a, 256);
+  }
   p.x = (size_t)(a.n * p.Rp * p.Cp) * 4;
   p.a = (size_t)(a.n * p.mp * p.mp) * 4;
   p.part = 2 * p.x + 2 * p.a;

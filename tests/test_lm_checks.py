@@ -26,3 +26,14 @@ def test_update_size(scale, status):
     L = _lib.lib()
     assert L.dpfused_muon_step(FAKE + 4, FAR, FAR + (1 << 20), 1, 8, 8, 0.1, 0.9, 1, 0.0, scale, 5,
                                3.4445, -4.775, 2.0315, 1e-7, None) == status
+
+
+def test_tile_option():
+    L = _lib.lib()
+    assert L.dpfused_get_option(b"ortho_tile") == 0
+    for v in (128, 256, 0):
+        assert L.dpfused_set_option(b"ortho_tile", v) == 0
+        assert L.dpfused_get_option(b"ortho_tile") == v
+    for v in (-1, 1, 64, 512):
+        assert L.dpfused_set_option(b"ortho_tile", v) == BAD
+    assert L.dpfused_get_option(b"ortho_tile") == 0
