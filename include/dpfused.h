@@ -429,9 +429,9 @@ typedef struct {
   int64_t stride_b;
 } dpf_ids;
 
-/* out[b][t] = scale * table[ids[b][t]], rounded once to out_dtype (nearest
- * even for bf16); 0 where the position is inactive (mask byte 0, or an id
- * outside [0, V)).
+/* out[b][t] = scale * table[ids[b][t]], a float32 product, rounded to out_dtype
+ * (nearest even for bf16); 0 where the position is inactive (mask byte 0, or
+ * an id outside [0, V)).
  *
  *   table      [V, D], table_dtype, rows contiguous, stride_v >= D elements
  *              apart, 16-byte aligned
@@ -462,7 +462,9 @@ dpf_status dpfused_embedding_lookup(const dpf_ids* ids, const void* table, int32
  * xi over the row-major [V, D] result as for dpfused_linear_clip_accumulate
  * (every row gets noise, also those whose token does not occur: which tokens
  * occurred is itself private).  A call consumes dpfused_noise_blocks(V * D)
- * blocks.
+ * blocks.  The words are the same as there; the normals made of them go through
+ * the hardware's logarithm and square root, so they equal that call's to
+ * float32 rounding (1e-6), not bit for bit.
  *
  * The positions are sorted by token (a stable sort on the device); equal
  * tokens of a sample are summed before they are squared, equal tokens of the
@@ -494,7 +496,12 @@ dpf_status dpfused_embedding_clip_accumulate(const dpf_ids* ids, const dpf_act* 
  * dpfused_clip_factors): ||g_i||^2 in float64, added to sqnorms_out with
  * accumulate != 0; and (sum_i c[i] g_i + noise_std * xi) / B for given
  * factors c[B] (device float32, each finite and > 0; noise_std finite and
- * >= 0). */
+ * >= 0).
+ * The squared norms of layers add up where their parameters are different
+ * ones.  A table that is the output layer's weight too has ONE gradient per
+ * sample, the sum of both layers', whose squared norm has their inner product
+ * in it: factors from the sum of the two squared norms do not bound it by C
+ * (only by sqrt(2) C), and noise for C is then too little. */
 dpf_status dpfused_embedding_sqnorms(const dpf_ids* ids, const dpf_act* G, const uint8_t* mask,
                                      int64_t V, float scale, double* sqnorms_out,
                                      int32_t accumulate, void* stream);

@@ -502,8 +502,8 @@ def _ids(t, name: str) -> DpfIds:
 
 def embedding_lookup(ids, table, mask=None, scale: float = 1.0, out_dtype=None, out=None,
                      stream=None):
-    """out[b, t] = scale * table[ids[b, t]] as [B, T, D] in out_dtype (default: the table's),
-    rounded once; 0 where the mask is 0 or the id is outside [0, V).
+    """out[b, t] = scale * table[ids[b, t]] as [B, T, D], a float32 product rounded to out_dtype
+    (default: the table's); 0 where the mask is 0 or the id is outside [0, V).
 
     ids [B, T] int32 or int64; table [V, D] bf16 or fp32, rows contiguous (a float32 master
     table can give bf16 activations directly)."""
@@ -561,7 +561,10 @@ def embedding_clip_accumulate(ids, G, V: int, mask=None, scale: float = 1.0, C: 
 def embedding_sqnorms(ids, G, V: int, mask=None, scale: float = 1.0, out=None,
                       accumulate: bool = False, stream=None):
     """||g_i||^2 of the embedding's per-sample gradients (fp64 [B]); with accumulate=True added
-    into ``out``, for clipping the embedding together with other layers."""
+    into ``out``, for clipping the embedding together with other layers.
+
+    Not with an output layer that shares the table: the gradient of the shared weight is the sum
+    of the two, and the sum of their squared norms does not bound it."""
     torch = _torch()
     ia, ga = _ids(ids, "ids"), _act(G)
     _same_device(G, ids.device, "G")

@@ -1,6 +1,6 @@
 // Embedding rows: the lookup, and the per-sample clipped gradient of the table.
 //
-//   out[b][t]  = scale * table[id_bt]
+//   out[b][t]  = scale * table[id_bt]                    (float32, then rounded)
 //   g_i[v]     = scale * sum over the active t of sample i with id_it = v of G_i[t]
 //   n_i^2      = sum_v ||g_i[v]||^2
 //   grad[v]    = (sum_i c_i g_i[v] + noise_std xi_v) / denom
@@ -28,8 +28,8 @@
 // What it costs (MI355X).  Lookup of 16384 rows of 5120 bf16: 52 us, 4.3 TB/s of
 // distinct rows read and rows written; of 16: 3.3 us.  Gradient of 16384
 // positions, 8.7 thousand active, 5120 bf16 columns, added into 32000 rows of
-// which 3.4 thousand have a token: 120 us.  The norms read G (89 MB) in 25 us,
-// the result takes 54 (G again, 140 MB of rows read and written: 4.2 TB/s); the
+// which 3.4 thousand have a token: 125 us.  The norms read G (89 MB) in 25 us,
+// the result takes 51 (G again, 140 MB of rows read and written: 4.5 TB/s); the
 // sort's three launches 16, the block sums 10 twice, the clip factors 5: a few
 // thousand rows each, bound by the latency of dependent loads.  Of 32 x 512
 // positions, 768 columns, 50257 rows with noise: 80 us, 47 of them the result,

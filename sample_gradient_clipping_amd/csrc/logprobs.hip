@@ -28,7 +28,7 @@
 //
 // What it costs (MI355X).  16384 rows of 32000 bf16 logits: 181 to 186 us, 5.7 TB/s;
 // with five alternatives 267 (their instructions bound it then: a bound and a
-// scan per chunk of a wave), 2052 float32 rows of 50257 with eight 104 (4.0
+// scan per chunk of a wave), 2052 float32 rows of 50257 with eight 101 (4.1
 // TB/s).  16384 float32 rows of 4096: 44, with five 59 us.  One row of
 // 32000 with five: 11 us in one workgroup, most of it the latency of a chain
 // of loads, maximum, bound, list and sort.  The gradient: 16384 x 32000 bf16

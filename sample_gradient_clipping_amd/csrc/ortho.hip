@@ -52,12 +52,12 @@
 // Matrices that fit into LDS take one workgroup for the whole call, other
 // thin ones (up to 96 rows or columns) two launches a step.
 //
-// What it costs (MI355X).  The MFMAs bound it.  A 13824 x 5120 step takes 15.9
-// ms: five times X^T X 0.91 ms (1250 TFLOP/s of half-precision products), the
-// square 0.34 (1210), B X 1.89 (1150), where a large half-precision library
+// What it costs (MI355X).  The MFMAs bound it.  A 13824 x 5120 step takes 15.6
+// to 16.4 ms: five times X^T X 0.91 ms (1250 TFLOP/s of half-precision products),
+// the square 0.34 (1210), B X 1.89 (1150), where a large half-precision library
 // product reaches 1170; norm and split 0.15 and 0.18 (1.1 and 0.7 GB: 7 and 4
 // TB/s).  The clock falls to 2.0 to 2.1 GHz under these, so that keeping the
-// MFMAs busier than half the cycles buys little.  Twelve 768 x 768 take 475 us:
+// MFMAs busier than half the cycles buys little.  Twelve 768 x 768 take 490 us:
 // per step 31 each for the symmetric products (600 TFLOP/s: 252 tiles of 128 on
 // 256 compute units, one wave per SIMD) and 41 for B X (790: 432 tiles on 512
 // places).  One 768 x 768 takes 295, 1024 x 4096 450 us, 4096 x 4096 3.9 ms;
