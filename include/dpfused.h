@@ -98,6 +98,22 @@ typedef struct {
   int64_t stride_b, stride_t;
 } dpf_act;
 
+/* One [B, T, H, D] tensor of heads in device memory: queries, keys, values, an
+ * attention's output.  D is contiguous, the strides are in ELEMENTS and may be
+ * in any order: [B, T, H, D] and [B, H, T, D] arrays and the parts of a fused
+ * projection's rows are all described so.  `data` must be aligned to its
+ * elements; where it is 16-byte aligned and D and the strides are whole 16-byte
+ * pieces the rows are read 16 bytes at a time, else element by element.
+ * stride_t >= D where T > 1; no stride is negative.  An output's elements must
+ * not overlap each other. */
+typedef struct {
+  void* data;
+  int32_t dtype;     /* dpf_dtype */
+  int32_t reserved;  /* must be 0 */
+  int64_t B, T, H, D;
+  int64_t stride_b, stride_t, stride_h;
+} dpf_heads;
+
 /* The fused per-layer DP step for one linear layer (FlashDP abstract: one
  * fused per-layer task; the clip rule, noise law and orientation follow the
  * contract above).
@@ -567,6 +583,160 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
                                            const float* entropy, const float* dlogp,
                                            const float* dentropy, const dpf_act* dlogits,
                                            void* stream);
+
+/* Attention of each sample's positions, forward, in one pass over the keys:
+ *
+ *   p(i)    = Tk - Tq + i: the queries are those of the last Tq positions
+ *   A(i)    = the positions j with mask[j] != 0 and segments[j] ==
+ *             segments[p(i)], and j <= p(i) if causal; none where mask[p(i)]
+ *             is 0
+ *   s_ij    = scale q_i . k_j,  lse_i = log sum over A(i) of e^{s_ij}
+ *   out_i   = sum over A(i) of e^{s_ij - lse_i} v_j
+ *
+ * for each head; head h of the Hq queries' heads uses head h / (Hq / Hkv) of
+ * the keys and values.  A query with an empty A(i) has out 0 and lse 0.  Tq = Tk
+ * trains or scores a batch; a small Tq answers for new positions over those
+ * before them (the keys are then split over workgroups).
+ *
+ * Scores, softmax and sums are float32; for bf16 inputs the weights
+ * e^{s_ij - m} are rounded to bf16 for their product with the values.  bf16
+ * products run on bf16 matrix cores, float32 ones on float32 ones.
+ *
+ * A NaN or infinity in an active position reaches the outputs of its own
+ * sample (of any of its positions that share a tile of keys, also those that
+ * do not attend to it), never another sample's; masked positions are never
+ * read into the arithmetic.
+ *
+ *   q          [B, Tq, Hq, D];  k, v  [B, Tk, Hkv, D]; bf16 or f32, all alike
+ *   mask       [B, Tk] uint8, contiguous, or NULL (all active)
+ *   segments   [B, Tk] int32, contiguous, or NULL: the document of each
+ *              position, not decreasing along T (else some pairs of equal
+ *              numbers do not see each other; nothing worse)
+ *   causal     0 or 1
+ *   scale      finite and > 0, or NaN for 1 / sqrt(D)
+ *   out        like q; must not overlap an input
+ *   lse        [B, Hq, Tq] float32, contiguous (the backward call's input)
+ *
+ * Errors: DPF_ERR_INVALID_ARGUMENT for NULL pointers, a dimension < 1, shapes
+ * that disagree, Tq > Tk, Hq not a multiple of Hkv, bad strides, causal or
+ * scale, overlapping outputs; DPF_ERR_UNSUPPORTED for an unknown dtype, mixed
+ * dtypes, a misaligned pointer, a non-zero reserved field, D > 128, Tk > 2^22 or
+ * B * Hq * ceil(Tk / 32) > 2^22; DPF_ERR_OUT_OF_MEMORY where the workspace (12
+ * bytes per position with mask or segments; 4 (D + 2) bytes, D rounded up to 64 or
+ * 128, per query, head and split of the keys) cannot be had. */
+dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v,
+                             const uint8_t* mask, const int32_t* segments, int32_t causal,
+                             float scale, const dpf_heads* out, float* lse, void* stream);
+
+/* The gradients of the above, given what it returned:
+ *
+ *   P_ij = e^{s_ij - lse_i},  delta_i = dout_i . out_i
+ *   dS_ij = P_ij (dout_i . v_j - delta_i)
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i
+ *   dv_j = sum_i P_ij dout_i
+ *
+ * dk and dv are summed over the heads of a group (and the queries) in a fixed
+ * order: no atomics.  Masked positions get 0.  P and dS are rounded to bf16 for
+ * their products where the inputs are bf16; sums are float32.  No gradient flows
+ * through lse.
+ *
+ *   dout, out      like q;  dq like q, dk like k, dv like v; the gradients may
+ *                  be parts of one array (the G of a fused projection's clip
+ *                  call) but must not overlap an input or each other
+ *   other arguments and errors as above; the workspace holds 4 bytes per query
+ *   and head more. */
+dpf_status dpfused_attention_backward(const dpf_heads* dout, const dpf_heads* q,
+                                      const dpf_heads* k, const dpf_heads* v,
+                                      const dpf_heads* out, const float* lse,
+                                      const uint8_t* mask, const int32_t* segments,
+                                      int32_t causal, float scale, const dpf_heads* dq,
+                                      const dpf_heads* dk, const dpf_heads* dv, void* stream);
+
+/* Norms of queries and keys per head, and their rotation by position, in one
+ * pass over both:
+ *
+ *   n = w x / sqrt(mean(x^2) + eps)                        w NULL: n = x
+ *   (a, b) -> amplitude (a cos t - b sin t, b cos t + a sin t),
+ *             t = position * freqs[j]
+ *
+ * on the pairs j < pairs of every head: entries (j, j + pairs), or
+ * (2 j, 2 j + 1) with interleaved = 1; entries from 2 * pairs on pass through.
+ * Angles in float64, reduced, everything else float32, rounded once.  Masked
+ * positions are not read and give 0.
+ *
+ *   q, k       [B, T, Hq, D] and [B, T, Hk, D], bf16 or f32, alike
+ *   q_weight, k_weight   [D] float32 each, or both NULL (no norm)
+ *   eps        finite and > 0 (with weights)
+ *   freqs      [pairs] float64 on the device, radians per position; NULL with
+ *              pairs = 0 (no rotation)
+ *   amplitude  finite (1: a plain rotation)
+ *   positions  [B, T] ids, or NULL for 0 .. T - 1; any value, negative ones too
+ *   q_out, k_out   like q and k; each may be its input itself (same pointer and
+ *              strides), else must not overlap q or k
+ *
+ * Errors: DPF_ERR_INVALID_ARGUMENT for NULL tensors, shapes that disagree,
+ * one weight without the other, neither weights nor pairs, pairs < 0 or
+ * 2 * pairs > D, freqs NULL where pairs > 0, eps, amplitude or interleaved out of
+ * range, overlapping outputs; DPF_ERR_UNSUPPORTED for dtypes, alignment (freqs:
+ * 8 bytes, weights: 4), D > 256, B * T > 2^24 or B * T * (Hq + Hk) > 2^31. */
+dpf_status dpfused_qk_norm_rotary(const dpf_heads* q, const dpf_heads* k, const float* q_weight,
+                                  const float* k_weight, float eps, const double* freqs,
+                                  int64_t pairs, float amplitude, int32_t interleaved,
+                                  const dpf_ids* positions, const uint8_t* mask,
+                                  const dpf_heads* q_out, const dpf_heads* k_out, void* stream);
+
+/* The gradients of the above: to q and k, and to the norms' weights PER SAMPLE
+ * (per-sample clipping, FlashDP abstract: a layer of D parameters whose
+ * gradients of all samples fit in B * D values).  With d the transposed rotation of
+ * the output's gradient and r = 1 / sqrt(mean(x^2) + eps):
+ *
+ *   dx = r (d w - x r mean(d w x r)),   dweight[b] = sum of d x r over sample b's
+ *                                       positions and heads
+ *
+ * in float32, the sums in a fixed order.  dweight[b] is the G of a linear of one
+ * input and T = 1: dpfused_per_sample_sqnorms and dpfused_scaled_accumulate with
+ * X = 1 clip, sum and noise it.
+ *
+ *   dq_out, dk_out   the gradients of q_out and k_out
+ *   q, k             the forward call's inputs (read only with weights)
+ *   dq, dk           like q and k; each may be its dq_out / dk_out itself, else
+ *                    must not overlap an input
+ *   dq_weight, dk_weight   [B, D] float32, 0 or more; NULL without weights
+ *   other arguments and errors as above; DPF_ERR_OUT_OF_MEMORY where the
+ *   workspace (8 D bytes per 1 to 8 positions) cannot be had. */
+dpf_status dpfused_qk_norm_rotary_backward(
+    const dpf_heads* dq_out, const dpf_heads* dk_out, const dpf_heads* q, const dpf_heads* k,
+    const float* q_weight, const float* k_weight, float eps, const double* freqs, int64_t pairs,
+    float amplitude, int32_t interleaved, const dpf_ids* positions, const uint8_t* mask,
+    const dpf_heads* dq, const dpf_heads* dk, float* dq_weight, float* dk_weight, void* stream);
+
+/* Dropout whose mask is drawn again wherever it is needed, never stored:
+ *
+ *   y_e = residual_e + x_e / (1 - p')   where bits_e >= 65536 p', else residual_e
+ *   p'  = round(65536 p) / 65536
+ *
+ * with e the row-major index in [B, T, D] and bits_e the 16-bit half e mod 8
+ * (the low half of each word first) of block offset + e / 8 of the noise's
+ * generator with counter (lo32(block), hi32(block), 1, 0): dropout's blocks are
+ * never the noise's.  A call consumes dpfused_dropout_blocks(B * T * D) blocks.
+ * Masked rows are not read and give 0.  The backward pass is the same call on y's
+ * gradient without a residual; the residual's gradient is y's.
+ *
+ *   x, y, residual   [B, T, D] alike, bf16 or f32, strided as any dpf_act but
+ *                    aligned to their elements only (16 bytes and D a multiple
+ *                    of 8 for the wide path); residual may be NULL; y may be x
+ *                    or the residual itself (same pointer and strides), else must
+ *                    not overlap them
+ *   p                in [0, 1); p' = 1 is refused
+ *
+ * Errors: DPF_ERR_INVALID_ARGUMENT for NULL x or y, shapes that disagree, bad
+ * strides, p out of range, overlap; DPF_ERR_UNSUPPORTED for dtypes, alignment or
+ * B * T * D > 2^34. */
+dpf_status dpfused_dropout(const dpf_act* x, const dpf_act* residual, const uint8_t* mask, float p,
+                           uint64_t seed, uint64_t offset, const dpf_act* y, void* stream);
+
+/* Blocks that dropout of n entries consumes: ceil(n / 8); 0 for n <= 0. */
+uint64_t dpfused_dropout_blocks(int64_t n_elements);
 
 /* The orthogonal factor of each of n matrices, approximately, by Newton-Schulz
  * products (the orthogonalised update of the Muon optimizer):

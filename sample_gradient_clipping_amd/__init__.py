@@ -13,12 +13,14 @@ and the pre-clip per-sample norms.  See include/dpfused.h for the contract.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import NamedTuple, Optional, Tuple
 
 from . import _lib
-from ._lib import DpfAct, DpfError, DpfIds, DPF_BF16, DPF_F32, DPF_I32, DPF_I64  # noqa: F401
+from ._lib import (DpfAct, DpfError, DpfHeads, DpfIds, DPF_BF16, DPF_F32, DPF_I32,  # noqa: F401
+                   DPF_I64)
 
 __all__ = [
     "linear_clip_accumulate", "linear_clip_accumulate_noalloc", "linear_clip_accumulate_projected",
@@ -27,6 +29,8 @@ __all__ = [
     "linear_clip_accumulate_projected_many",
     "embedding_lookup", "embedding_clip_accumulate", "embedding_sqnorms",
     "embedding_scaled_accumulate", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
+    "attention", "attention_backward", "AttentionOutput", "qk_norm_rotary",
+    "qk_norm_rotary_backward", "QkGradients", "rotary_frequencies", "dropout", "dropout_blocks",
     "orthogonalize", "muon_step", "NEWTON_SCHULZ",
     "per_sample_sqnorms",
     "clip_factors", "scaled_accumulate", "philox4x32_10", "gaussian_fill", "noise_blocks",
@@ -670,6 +674,284 @@ def token_logprobs_backward(logits, targets, lse, dlogp, entropy=None, dentropy=
         _stream(logits, stream))
     _lib.check(st)
     return out
+
+
+def _on(device):
+    """Makes ``device`` the current one for a call whose stream is that device's."""
+    torch = _torch()
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _heads(t, name: str) -> DpfHeads:
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, T, heads, D]")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    B, T, H, D = t.shape
+    if D > 1 and t.stride(3) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return DpfHeads(t.data_ptr(), _dtype_code(t), 0, B, T, H, D, t.stride(0), t.stride(1), t.stride(2))
+
+
+def _check_heads_out(t, like, name: str) -> None:
+    """A caller-supplied output of heads: ``like``'s shape, dtype and device, any strides."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype}")
+    _same_device(t, like.device, name)
+
+
+def _segments_ptr(segments, B, T, device) -> Optional[int]:
+    if segments is None:
+        return None
+    torch = _torch()
+    if segments.dtype != torch.int32:
+        raise TypeError("segments must be int32")
+    if tuple(segments.shape) != (B, T) or not segments.is_contiguous() or not segments.is_cuda:
+        raise ValueError("segments must be a contiguous [B, T] GPU tensor")
+    _same_device(segments, device, "segments")
+    return segments.data_ptr()
+
+
+class AttentionOutput(NamedTuple):
+    """What attention returns: out [B, Tq, Hq, D] in q's dtype, lse [B, Hq, Tq] float32."""
+    out: object
+    lse: object
+
+
+def attention(q, k, v, mask=None, segments=None, causal: bool = True,
+              scale: Optional[float] = None, out=None, stream=None) -> AttentionOutput:
+    """softmax(scale q k^T) v of each sample and head, in one pass; q [B, Tq, Hq, D] are the
+    queries of the last Tq of the Tk positions of k and v [B, Tk, Hkv, D] (bf16 or fp32, any
+    strides; Hq a multiple of Hkv, D up to 128).
+
+    A query attends to the positions of its own segment (segments [B, Tk] int32, not decreasing:
+    the documents packed into a row) with a non-zero mask byte (mask [B, Tk]), up to its own if
+    causal; one whose own mask byte is 0 gives out 0 and lse 0.  scale=None takes 1 / sqrt(D)."""
+    torch = _torch()
+    qa, ka, va = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    dev = q.device
+    _same_device(k, dev, "k")
+    _same_device(v, dev, "v")
+    B, T = k.shape[0], k.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _check_heads_out(out, q, "out")
+    lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=dev)
+    oa = _heads(out, "out")
+    with _on(dev):
+        st = _lib.lib().dpfused_attention(
+            ctypes.byref(qa), ctypes.byref(ka), ctypes.byref(va), _mask_ptr(mask, B, T, dev),
+            _segments_ptr(segments, B, T, dev), int(bool(causal)),
+            math.nan if scale is None else float(scale), ctypes.byref(oa), lse.data_ptr(),
+            _stream(q, stream))
+    _lib.check(st)
+    return AttentionOutput(out, lse)
+
+
+def attention_backward(dout, q, k, v, out, lse, mask=None, segments=None, causal: bool = True,
+                       scale: Optional[float] = None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of attention from its output's gradient, given what it returned.
+
+    dq, dk and dv may be given, with any strides: as parts of one [B, T, (Hq + 2 Hkv) D] array
+    they are the G of the fused projection's linear_clip_accumulate."""
+    torch = _torch()
+    dev = q.device
+    args = [_heads(t, name) for t, name in ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"))]
+    for t, name in ((dout, "dout"), (k, "k"), (v, "v"), (out, "out")):
+        _same_device(t, dev, name)
+    _check_out(lse, (q.shape[0], q.shape[2], q.shape[1]), "lse", dev)
+    B, T = k.shape[0], k.shape[1]
+    grads = []
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        if t is None:
+            t = torch.empty(like.shape, dtype=like.dtype, device=dev)
+        else:
+            _check_heads_out(t, like, name)
+        grads.append(t)
+    outs = [_heads(t, name) for t, name in zip(grads, ("dq", "dk", "dv"))]
+    with _on(dev):
+        st = _lib.lib().dpfused_attention_backward(
+            *[ctypes.byref(a) for a in args], lse.data_ptr(), _mask_ptr(mask, B, T, dev),
+            _segments_ptr(segments, B, T, dev), int(bool(causal)),
+            math.nan if scale is None else float(scale), *[ctypes.byref(a) for a in outs],
+            _stream(q, stream))
+    _lib.check(st)
+    return tuple(grads)
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                       factor: float = 1.0, length: Optional[int] = None,
+                       beta: Tuple[float, float] = (32.0, 1.0), device="cuda"):
+    """(freqs [dim / 2] float64 in radians per position, amplitude) for qk_norm_rotary:
+    freqs[j] = base^(-2 j / dim), for contexts ``factor`` times the trained length scaled by
+
+    "linear"  position interpolation: every frequency divided by factor
+    "ntk"     a larger base, base factor^(dim / (dim - 2)): the slowest frequency divided by
+              factor, the fastest kept
+    "yarn"    frequencies that turn more than beta[0] times in the trained ``length`` kept, those
+              that turn less than beta[1] times divided, a linear ramp over j between;
+              amplitude 0.1 ln(factor) + 1"""
+    torch = _torch()
+    if dim < 2 or dim % 2 != 0:
+        raise ValueError("dim must be even and >= 2")
+    if not (base > 1.0 and math.isfinite(base)) or not (factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("base must be > 1 and factor >= 1")
+    pairs, amplitude = dim // 2, 1.0
+    if scaling == "ntk" and dim > 2:
+        base = base * factor ** (dim / (dim - 2))
+    freqs = [base ** (-2.0 * j / dim) for j in range(pairs)]
+    if scaling == "linear":
+        freqs = [f / factor for f in freqs]
+    elif scaling == "yarn":
+        if length is None or length < 1:
+            raise ValueError("yarn scaling needs the trained length")
+        if not beta[0] > beta[1] > 0:
+            raise ValueError("beta must be (fast, slow) with fast > slow > 0")
+        # index of the frequency that turns n times in the trained length
+        at = [dim * math.log(length / (n * 2.0 * math.pi)) / (2.0 * math.log(base)) for n in beta]
+        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), dim - 1)
+        width = max(last - first, 1e-3)
+        divided = [min(max((j - first) / width, 0.0), 1.0) for j in range(pairs)]
+        freqs = [f * (1.0 - d) + f / factor * d for f, d in zip(freqs, divided)]
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    return torch.tensor(freqs, dtype=torch.float64, device=device), amplitude
+
+
+def _rotary_args(q, k, q_weight, k_weight, freqs, positions, mask):
+    """The C arguments that both directions share: descriptors and pointers."""
+    torch = _torch()
+    dev = q.device
+    _same_device(k, dev, "k")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _check_out(t, (q.shape[-1],), name, dev)
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be [pairs]")
+        _check_out(freqs, freqs.shape, "freqs", dev, torch.float64)
+    pa = None
+    if positions is not None:
+        pa = _ids(positions, "positions")
+        _same_device(positions, dev, "positions")
+    return (_ptr(q_weight), _ptr(k_weight), _ptr(freqs), 0 if freqs is None else int(freqs.shape[0]),
+            None if pa is None else ctypes.byref(pa), _mask_ptr(mask, q.shape[0], q.shape[1], dev))
+
+
+def qk_norm_rotary(q, k, q_weight=None, k_weight=None, freqs=None, positions=None, mask=None,
+                   interleaved: bool = False, amplitude: float = 1.0, eps: float = 1e-6,
+                   q_out=None, k_out=None, stream=None):
+    """Queries [B, T, Hq, D] and keys [B, T, Hk, D] (bf16 or fp32, any strides, D up to 256), each
+    head normalised by its root mean square and multiplied by the weight (float32 [D]; None for
+    both: no norm), then its first 2 len(freqs) entries rotated by position: pairs (j, j + pairs),
+    or (2 j, 2 j + 1) when interleaved.  Returns (q, k); q_out and k_out may be q and k.
+
+    freqs: float64 [pairs], see rotary_frequencies (None: no rotation); positions [B, T] int32 or
+    int64 (default 0 .. T - 1); rows whose mask byte is 0 give 0."""
+    torch = _torch()
+    qa, ka = _heads(q, "q"), _heads(k, "k")
+    qw, kw, fr, pairs, pos, mp = _rotary_args(q, k, q_weight, k_weight, freqs, positions, mask)
+    outs = []
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is None:
+            t = torch.empty(like.shape, dtype=like.dtype, device=q.device)
+        else:
+            _check_heads_out(t, like, name)
+        outs.append(t)
+    oq, ok = _heads(outs[0], "q_out"), _heads(outs[1], "k_out")
+    with _on(q.device):
+        st = _lib.lib().dpfused_qk_norm_rotary(
+            ctypes.byref(qa), ctypes.byref(ka), qw, kw, float(eps), fr, pairs, float(amplitude),
+            int(bool(interleaved)), pos, mp, ctypes.byref(oq), ctypes.byref(ok), _stream(q, stream))
+    _lib.check(st)
+    return outs[0], outs[1]
+
+
+class QkGradients(NamedTuple):
+    """What qk_norm_rotary_backward returns: dq and dk like q and k, and the weights' gradients
+    PER SAMPLE, float32 [B, 1, D] (None without weights)."""
+    dq: object
+    dk: object
+    dq_weight: object
+    dk_weight: object
+
+
+def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, freqs=None,
+                            positions=None, mask=None, interleaved: bool = False,
+                            amplitude: float = 1.0, eps: float = 1e-6, dq=None, dk=None,
+                            stream=None) -> QkGradients:
+    """Gradients of qk_norm_rotary from those of its outputs, with the forward call's inputs and
+    arguments.  dq and dk may be given (parts of one array, or dq_out and dk_out themselves).
+
+    The weights' gradients are the G [B, 1, D] of a linear of one input: with X = ones [B, 1, 1]
+    per_sample_sqnorms, linear_clip_accumulate and scaled_accumulate clip, sum and noise them."""
+    torch = _torch()
+    qa, ka = _heads(q, "q"), _heads(k, "k")
+    ga, gb = _heads(dq_out, "dq_out"), _heads(dk_out, "dk_out")
+    dev = q.device
+    _same_device(dq_out, dev, "dq_out")
+    _same_device(dk_out, dev, "dk_out")
+    qw, kw, fr, pairs, pos, mp = _rotary_args(q, k, q_weight, k_weight, freqs, positions, mask)
+    grads = []
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk")):
+        if t is None:
+            t = torch.empty(like.shape, dtype=like.dtype, device=dev)
+        else:
+            _check_heads_out(t, like, name)
+        grads.append(t)
+    dqw = dkw = None
+    if q_weight is not None and k_weight is not None:
+        dqw, dkw = torch.empty((2, q.shape[0], 1, q.shape[3]), dtype=torch.float32, device=dev).unbind(0)
+    oq, ok = _heads(grads[0], "dq"), _heads(grads[1], "dk")
+    with _on(dev):
+        st = _lib.lib().dpfused_qk_norm_rotary_backward(
+            ctypes.byref(ga), ctypes.byref(gb), ctypes.byref(qa), ctypes.byref(ka), qw, kw, float(eps),
+            fr, pairs, float(amplitude), int(bool(interleaved)), pos, mp, ctypes.byref(oq),
+            ctypes.byref(ok), _ptr(dqw), _ptr(dkw), _stream(q, stream))
+    _lib.check(st)
+    return QkGradients(grads[0], grads[1], dqw, dkw)
+
+
+def dropout(x, p: float, seed: int = 0, offset: int = 0, residual=None, mask=None, out=None,
+            stream=None):
+    """residual + dropout(x) for x [B, T, D] (bf16 or fp32), the mask drawn from (seed, offset)
+    and never stored: an entry is dropped with probability p (held in 16 bits), kept ones are
+    divided by 1 - p.  Rows whose mask byte is 0 give 0; out may be x or the residual.
+
+    The gradient to x is dropout(dy, p, seed, offset), to the residual dy.  A call consumes
+    dropout_blocks(x.numel()) blocks of the seed: advance offset by as much.  They are apart from
+    the noise's blocks."""
+    torch = _torch()
+    xa = _act(x)
+    B, T, D = x.shape
+    if out is None:
+        out = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
+    for t, name in ((out, "out"), (residual, "residual")):
+        if t is None:
+            continue
+        if t.dtype != x.dtype or t.shape != x.shape:
+            raise ValueError(f"{name} must be {tuple(x.shape)} of {x.dtype}")
+        _same_device(t, x.device, name)
+    ra = None if residual is None else _act(residual)
+    oa = _act(out)
+    with _on(x.device):
+        st = _lib.lib().dpfused_dropout(
+            ctypes.byref(xa), None if ra is None else ctypes.byref(ra),
+            _mask_ptr(mask, B, T, x.device), float(p), int(seed), int(offset), ctypes.byref(oa),
+            _stream(x, stream))
+    _lib.check(st)
+    return out
+
+
+def dropout_blocks(n_elements: int) -> int:
+    return int(_lib.lib().dpfused_dropout_blocks(int(n_elements)))
 
 
 # Coefficients (a, b, c) that take a singular value s to a s + b s^3 + c s^5 in each step.

@@ -49,6 +49,22 @@ class DpfIds(ctypes.Structure):
     ]
 
 
+class DpfHeads(ctypes.Structure):
+    """Mirror of dpf_heads: one [B, T, H, D] tensor, last dim contiguous, strides in elements."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("B", ctypes.c_int64),
+        ("T", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("stride_b", ctypes.c_int64),
+        ("stride_t", ctypes.c_int64),
+        ("stride_h", ctypes.c_int64),
+    ]
+
+
 class DpfError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{status_name(status)}: {message}")
@@ -129,6 +145,30 @@ _SIGNATURES = {
         ctypes.POINTER(DpfAct), ctypes.POINTER(DpfIds), ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(DpfAct),
         ctypes.c_void_p]),
+    "dpfused_attention": (ctypes.c_int, [
+        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.POINTER(DpfHeads),
+        ctypes.c_void_p, ctypes.c_void_p]),
+    "dpfused_attention_backward": (ctypes.c_int, [
+        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
+        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.POINTER(DpfHeads),
+        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p]),
+    "dpfused_qk_norm_rotary": (ctypes.c_int, [
+        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int32,
+        ctypes.POINTER(DpfIds), ctypes.c_void_p, ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
+        ctypes.c_void_p]),
+    "dpfused_qk_norm_rotary_backward": (ctypes.c_int, [
+        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
+        ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
+        ctypes.c_int64, ctypes.c_float, ctypes.c_int32, ctypes.POINTER(DpfIds), ctypes.c_void_p,
+        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p]),
+    "dpfused_dropout": (ctypes.c_int, [
+        ctypes.POINTER(DpfAct), ctypes.POINTER(DpfAct), ctypes.c_void_p, ctypes.c_float,
+        ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(DpfAct), ctypes.c_void_p]),
+    "dpfused_dropout_blocks": (ctypes.c_uint64, [ctypes.c_int64]),
     "dpfused_orthogonalize": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
         ctypes.c_int32, ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,

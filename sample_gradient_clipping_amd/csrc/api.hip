@@ -25,6 +25,7 @@
 #include "dpfused.h"
 #include "kernels.hpp"
 #include "lm.hpp"
+#include "attn.hpp"
 
 // Static scratch of dpfused_linear_clip_accumulate_noalloc, for callers that
 // cannot allocate (graph capture, tight serving loops): 80 MiB, which holds
@@ -1825,7 +1826,7 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
 }
 
 // ---------------------------------------------------------------------------
-// Orthogonalised update
+// Attention, norms and rotation of queries and keys, dropout
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -1833,6 +1834,446 @@ bool ranges_overlap(const void* p, size_t np, const void* q, size_t nq) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
   return a < b + nq && b < a + np;
 }
+
+// Largest extent of a tensor of heads or of an activation here, in elements: byte
+// offsets of any element fit in 63 bits many times over.
+constexpr int64_t kMaxExtent = (int64_t)1 << 42;
+
+// Elements from the first to past the last one.
+int64_t heads_extent(const dpf_heads* a) {
+  return (a->B - 1) * a->stride_b + (a->T - 1) * a->stride_t + (a->H - 1) * a->stride_h + a->D;
+}
+
+dpf_status check_heads(const dpf_heads* a, const char* name, bool output) {
+  const std::string n(name);
+  if (a == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, n + " is NULL");
+  if (a->data == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, n + ".data is NULL");
+  if (a->dtype != DPF_F32 && a->dtype != DPF_BF16)
+    return fail(DPF_ERR_UNSUPPORTED, n + ".dtype is not DPF_F32 or DPF_BF16");
+  if (a->reserved != 0) return fail(DPF_ERR_UNSUPPORTED, n + ".reserved must be 0");
+  if (a->B < 1 || a->T < 1 || a->H < 1 || a->D < 1)
+    return fail(DPF_ERR_INVALID_ARGUMENT, n + ": B, T, H and D must be >= 1");
+  const int64_t dims[3] = {a->B, a->T, a->H}, strides[3] = {a->stride_b, a->stride_t, a->stride_h};
+  for (int k = 0; k < 3; ++k) {
+    if (dims[k] > kMaxDim) return fail(DPF_ERR_UNSUPPORTED, n + ": dimension too large");
+    if (strides[k] < 0) return fail(DPF_ERR_INVALID_ARGUMENT, n + ": a stride is negative");
+    if (dims[k] > 1 && strides[k] > kMaxExtent / dims[k])
+      return fail(DPF_ERR_UNSUPPORTED, n + ": the strides reach too far");
+  }
+  if (a->T > 1 && a->stride_t < a->D)
+    return fail(DPF_ERR_INVALID_ARGUMENT, n + ".stride_t < D (rows overlap)");
+  if ((reinterpret_cast<uintptr_t>(a->data) & (elem_size(a->dtype) - 1)) != 0)
+    return fail(DPF_ERR_UNSUPPORTED, n + ".data is not aligned to its elements");
+  if (output) {
+    // every dimension steps past what those of smaller strides span
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int x, int y) { return strides[x] < strides[y]; });
+    int64_t span = a->D;
+    for (int k : order) {
+      if (dims[k] == 1) continue;
+      if (strides[k] < span)
+        return fail(DPF_ERR_INVALID_ARGUMENT, n + ": elements of an output overlap");
+      span += (dims[k] - 1) * strides[k];
+    }
+  }
+  return DPF_OK;
+}
+
+bool heads_alike(const dpf_heads* a, const dpf_heads* b) {
+  return a->B == b->B && a->T == b->T && a->H == b->H && a->D == b->D;
+}
+bool heads_same(const dpf_heads* a, const dpf_heads* b) {
+  return a->data == b->data && a->dtype == b->dtype && heads_alike(a, b) &&
+         (a->B == 1 || a->stride_b == b->stride_b) && (a->T == 1 || a->stride_t == b->stride_t) &&
+         (a->H == 1 || a->stride_h == b->stride_h);
+}
+
+// Whether two tensors of heads share no element, as far as this can be seen:
+// their ranges are apart, or both step through the same rows (equal stride_t, and
+// stride_b a multiple of it) and take different parts of each.
+bool heads_apart(const dpf_heads* a, const dpf_heads* b) {
+  const int64_t ea = (int64_t)elem_size(a->dtype), eb = (int64_t)elem_size(b->dtype);
+  if (!ranges_overlap(a->data, (size_t)(heads_extent(a) * ea), b->data, (size_t)(heads_extent(b) * eb)))
+    return true;
+  const int64_t row = a->stride_t * ea;
+  if (a->dtype != b->dtype || a->T == 1 || b->T == 1 || a->stride_t != b->stride_t) return false;
+  if ((a->B > 1 && a->stride_b % a->stride_t != 0) || (b->B > 1 && b->stride_b % b->stride_t != 0))
+    return false;
+  const int64_t na = ((a->H - 1) * a->stride_h + a->D) * ea, nb = ((b->H - 1) * b->stride_h + b->D) * eb;
+  int64_t at = (int64_t)((intptr_t)a->data - (intptr_t)b->data) % row;
+  if (at < 0) at += row;
+  return at >= nb && at + na <= row;
+}
+
+// Strides as the kernels take them: those of dimensions of one entry are free, and
+// a row's is made to step past it.
+dpf::Heads to_heads(const dpf_heads* a) {
+  return dpf::Heads{a->data, a->B > 1 ? a->stride_b : 0, a->T > 1 ? a->stride_t : a->D,
+                    a->H > 1 ? a->stride_h : 0};
+}
+
+// Rows of whole 16-byte pieces, read through buffers whose tiles of 64 rows stay
+// below 2^31 bytes.
+bool heads_vec(const dpf_heads* a) {
+  const dpf::Heads h = to_heads(a);
+  const int64_t es = (int64_t)elem_size(a->dtype);
+  return aligned16(a->data) && (a->D * es) % 16 == 0 && (h.sb * es) % 16 == 0 &&
+         (h.st * es) % 16 == 0 && (h.sh * es) % 16 == 0 && h.st * es <= ((int64_t)1 << 24);
+}
+
+dpf_status check_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v, int32_t causal,
+                           float scale) {
+  dpf_status st = check_heads(q, "q", false);
+  if (st == DPF_OK) st = check_heads(k, "k", false);
+  if (st == DPF_OK) st = check_heads(v, "v", false);
+  if (st != DPF_OK) return st;
+  if (q->dtype != k->dtype || q->dtype != v->dtype)
+    return fail(DPF_ERR_UNSUPPORTED, "q, k and v have different dtypes");
+  if (!heads_alike(k, v)) return fail(DPF_ERR_INVALID_ARGUMENT, "k and v have different shapes");
+  if (q->B != k->B || q->D != k->D)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "q and k disagree on B or D");
+  if (q->T > k->T)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "more queries than positions (Tq > Tk)");
+  if (q->H % k->H != 0)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "the queries' heads are not a multiple of the keys'");
+  if (causal != 0 && causal != 1) return fail(DPF_ERR_INVALID_ARGUMENT, "causal must be 0 or 1");
+  if (!std::isnan(scale) && !(scale > 0.0f && std::isfinite(scale)))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "scale must be finite and > 0 (or NaN for the default)");
+  if (q->D > dpf::kAttnMaxD) return fail(DPF_ERR_UNSUPPORTED, "heads are wider than 128");
+  if (k->T > dpf::kAttnMaxT || q->B > dpf::kAttnMaxTiles || q->H > dpf::kAttnMaxTiles ||
+      q->B * q->H > dpf::kAttnMaxTiles / ((k->T + 31) / 32))
+    return fail(DPF_ERR_UNSUPPORTED, "too many positions (Tk <= 2^22, B * Hq * ceil(Tk / 32) <= 2^22)");
+  return DPF_OK;
+}
+
+dpf::AttnArgs attention_args(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v,
+                             const dpf_heads* out, const uint8_t* mask, const int32_t* segments,
+                             int32_t causal, float scale, float* lse) {
+  dpf::AttnArgs a{};
+  a.q = to_heads(q);
+  a.k = to_heads(k);
+  a.v = to_heads(v);
+  a.o = to_heads(out);
+  a.lse = lse;
+  a.dtype = q->dtype;
+  a.B = (int)q->B;
+  a.Tq = (int)q->T;
+  a.Tk = (int)k->T;
+  a.Hq = (int)q->H;
+  a.Hkv = (int)k->H;
+  a.D = (int)q->D;
+  a.causal = causal;
+  a.scale = std::isnan(scale) ? (float)(1.0 / std::sqrt((double)q->D)) : scale;
+  a.mask = mask;
+  a.segments = segments;
+  a.nwords = dpf::attn_words(k->T);
+  a.vec = heads_vec(q) && heads_vec(k) && heads_vec(v) && heads_vec(out);
+  return a;
+}
+
+struct AttnWs {
+  size_t lo, end, bits;
+};
+AttnWs reserve_ranges(const dpf::AttnArgs& a, Workspace& ws) {
+  AttnWs o{};
+  if (a.mask == nullptr && a.segments == nullptr) return o;
+  const size_t n = (size_t)a.B * a.Tk;
+  o.lo = ws.reserve(n * sizeof(int32_t));
+  o.end = ws.reserve(n * sizeof(int32_t));
+  o.bits = ws.reserve((size_t)a.B * a.nwords * sizeof(uint32_t));
+  return o;
+}
+hipError_t queue_ranges(dpf::AttnArgs& a, const Workspace& ws, const AttnWs& o, hipStream_t s) {
+  if (a.mask == nullptr && a.segments == nullptr) return hipSuccess;
+  a.lo = ws.at<int32_t>(o.lo);
+  a.end = ws.at<int32_t>(o.end);
+  a.bits = ws.at<uint32_t>(o.bits);
+  return dpf::launch_attn_ranges(a, s);
+}
+
+dpf_status check_apart(const dpf_heads* out, const char* out_name, const dpf_heads* in,
+                       const char* in_name) {
+  if (heads_apart(out, in)) return DPF_OK;
+  return fail(DPF_ERR_INVALID_ARGUMENT, std::string(out_name) + " overlaps " + in_name);
+}
+
+dpf_status check_rotary(const dpf_heads* q, const dpf_heads* k, const float* qw, const float* kw,
+                        float eps, const double* freqs, int64_t pairs, float amplitude,
+                        int32_t interleaved, const dpf_ids* positions) {
+  dpf_status st = check_heads(q, "q", false);
+  if (st == DPF_OK) st = check_heads(k, "k", false);
+  if (st != DPF_OK) return st;
+  if (q->dtype != k->dtype) return fail(DPF_ERR_UNSUPPORTED, "q and k have different dtypes");
+  if (q->B != k->B || q->T != k->T || q->D != k->D)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "q and k disagree on B, T or D");
+  if (q->D > dpf::kRotaryMaxD) return fail(DPF_ERR_UNSUPPORTED, "heads are wider than 256");
+  if ((qw == nullptr) != (kw == nullptr))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "the norms' weights are given together or not at all");
+  if (qw != nullptr && !(eps > 0.0f && std::isfinite(eps)))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "eps must be finite and > 0");
+  if (pairs < 0 || 2 * pairs > q->D)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "pairs must be in 0 .. D / 2");
+  if (pairs > 0 && freqs == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "freqs is NULL");
+  if (pairs == 0 && qw == nullptr)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "neither weights nor freqs were given");
+  if (!std::isfinite(amplitude)) return fail(DPF_ERR_INVALID_ARGUMENT, "amplitude must be finite");
+  if (interleaved != 0 && interleaved != 1)
+    return fail(DPF_ERR_INVALID_ARGUMENT, "interleaved must be 0 or 1");
+  if (((uintptr_t)freqs & 7u) != 0 || ((uintptr_t)qw & 3u) != 0 || ((uintptr_t)kw & 3u) != 0)
+    return fail(DPF_ERR_UNSUPPORTED, "freqs or a weight is not aligned to its elements");
+  if (positions != nullptr) {
+    if ((st = check_ids(positions, "positions")) != DPF_OK) return st;
+    if (positions->B != q->B || positions->T != q->T)
+      return fail(DPF_ERR_INVALID_ARGUMENT, "q and positions disagree on B or T");
+  }
+  const int64_t most = (int64_t)1 << 31;
+  if (q->H > most || k->H > most || q->B > ((int64_t)1 << 24) / q->T ||
+      q->B * q->T > most / (q->H + k->H))
+    return fail(DPF_ERR_UNSUPPORTED, "too many rows (B * T <= 2^24, B * T * (Hq + Hk) <= 2^31)");
+  return DPF_OK;
+}
+
+dpf::RotaryArgs rotary_args(const dpf_heads* q, const dpf_heads* k, const float* qw, const float* kw,
+                            float eps, const double* freqs, int64_t pairs, float amplitude,
+                            int32_t interleaved, const dpf_ids* positions, const uint8_t* mask,
+                            const dpf_heads* oq, const dpf_heads* ok) {
+  dpf::RotaryArgs a{};
+  a.q = to_heads(q);
+  a.k = to_heads(k);
+  a.oq = to_heads(oq);
+  a.ok = to_heads(ok);
+  a.dtype = q->dtype;
+  a.B = q->B;
+  a.T = q->T;
+  a.Hq = (int)q->H;
+  a.Hk = (int)k->H;
+  a.D = (int)q->D;
+  a.wq = qw;
+  a.wk = kw;
+  a.eps = eps;
+  a.freqs = freqs;
+  a.pairs = (int)pairs;
+  a.amplitude = amplitude;
+  a.interleaved = interleaved;
+  if (positions != nullptr) a.positions = to_ids(positions);
+  a.mask = mask;
+  return a;
+}
+
+// An output that is one of the inputs itself, or shares nothing with any.
+dpf_status check_in_place(const dpf_heads* out, const char* name, const dpf_heads* own,
+                          std::initializer_list<const dpf_heads*> others) {
+  if (!heads_same(out, own) && !heads_apart(out, own))
+    return fail(DPF_ERR_INVALID_ARGUMENT, std::string(name) + " overlaps its input without being it");
+  for (const dpf_heads* o : others)
+    if (!heads_apart(out, o))
+      return fail(DPF_ERR_INVALID_ARGUMENT, std::string(name) + " overlaps another tensor of the call");
+  return DPF_OK;
+}
+
+// An activation whose rows need no alignment.
+dpf_status check_rows(const dpf_act* a, const char* name) {
+  if (a == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, std::string(name) + " is NULL");
+  dpf_act aligned = *a;   // the shared checks, less the pointer's alignment
+  if (a->data != nullptr) aligned.data = reinterpret_cast<const void*>((uintptr_t)16);
+  const dpf_status st = check_act(&aligned, name);
+  if (st != DPF_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(a->data) & (elem_size(a->dtype) - 1)) != 0)
+    return fail(DPF_ERR_UNSUPPORTED, std::string(name) + ".data is not aligned to its elements");
+  return DPF_OK;
+}
+
+}  // namespace
+
+dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v,
+                             const uint8_t* mask, const int32_t* segments, int32_t causal,
+                             float scale, const dpf_heads* out, float* lse, void* stream) {
+  CallScope call_("dpfused_attention");
+  dpf_status st = check_attention(q, k, v, causal, scale);
+  if (st == DPF_OK) st = check_heads(out, "out", true);
+  if (st != DPF_OK) return st;
+  if (lse == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "lse is NULL");
+  if (out->dtype != q->dtype) return fail(DPF_ERR_UNSUPPORTED, "q and out have different dtypes");
+  if (!heads_alike(q, out)) return fail(DPF_ERR_INVALID_ARGUMENT, "q and out have different shapes");
+  if ((st = check_apart(out, "out", q, "q")) != DPF_OK) return st;
+  if ((st = check_apart(out, "out", k, "k")) != DPF_OK) return st;
+  if ((st = check_apart(out, "out", v, "v")) != DPF_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  dpf::AttnArgs a = attention_args(q, k, v, out, mask, segments, causal, scale, lse);
+  Workspace ws(s);
+  const AttnWs o = reserve_ranges(a, ws);
+  const size_t floats = dpf::attention_part_floats(a);
+  const size_t part = floats != 0 ? ws.reserve(floats * sizeof(float)) : 0;
+  if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+  if (floats != 0) a.part = ws.at<float>(part);
+  hipError_t e = queue_ranges(a, ws, o, s);
+  if (e == hipSuccess) e = dpf::launch_attention(a, s);
+  if (e != hipSuccess) return hip_fail(e, "attention launch");
+  return ok();
+}
+
+dpf_status dpfused_attention_backward(const dpf_heads* dout, const dpf_heads* q,
+                                      const dpf_heads* k, const dpf_heads* v,
+                                      const dpf_heads* out, const float* lse,
+                                      const uint8_t* mask, const int32_t* segments,
+                                      int32_t causal, float scale, const dpf_heads* dq,
+                                      const dpf_heads* dk, const dpf_heads* dv, void* stream) {
+  CallScope call_("dpfused_attention_backward");
+  dpf_status st = check_attention(q, k, v, causal, scale);
+  if (st == DPF_OK) st = check_heads(dout, "dout", false);
+  if (st == DPF_OK) st = check_heads(out, "out", false);
+  if (st == DPF_OK) st = check_heads(dq, "dq", true);
+  if (st == DPF_OK) st = check_heads(dk, "dk", true);
+  if (st == DPF_OK) st = check_heads(dv, "dv", true);
+  if (st != DPF_OK) return st;
+  if (lse == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "lse is NULL");
+  for (const dpf_heads* h : {dout, out, dq, dk, dv})
+    if (h->dtype != q->dtype) return fail(DPF_ERR_UNSUPPORTED, "the tensors have different dtypes");
+  if (!heads_alike(q, dout) || !heads_alike(q, out) || !heads_alike(q, dq))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "dout, out and dq must have q's shape");
+  if (!heads_alike(k, dk) || !heads_alike(k, dv))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "dk and dv must have k's shape");
+  const dpf_heads* outs[3] = {dq, dk, dv};
+  const char* names[3] = {"dq", "dk", "dv"};
+  for (int x = 0; x < 3; ++x) {
+    for (const dpf_heads* in : {dout, q, k, v, out})
+      if ((st = check_apart(outs[x], names[x], in, "an input")) != DPF_OK) return st;
+    for (int y = 0; y < x; ++y)
+      if ((st = check_apart(outs[x], names[x], outs[y], names[y])) != DPF_OK) return st;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  dpf::AttnArgs a = attention_args(q, k, v, out, mask, segments, causal, scale, const_cast<float*>(lse));
+  a.dout = to_heads(dout);
+  a.dq = to_heads(dq);
+  a.dk = to_heads(dk);
+  a.dv = to_heads(dv);
+  a.vec = a.vec && heads_vec(dout) && heads_vec(dq) && heads_vec(dk) && heads_vec(dv);
+  Workspace ws(s);
+  const AttnWs o = reserve_ranges(a, ws);
+  const size_t delta = ws.reserve((size_t)(q->B * q->H * q->T) * sizeof(float));
+  if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+  a.delta = ws.at<float>(delta);
+  hipError_t e = queue_ranges(a, ws, o, s);
+  if (e == hipSuccess) e = dpf::launch_attention_backward(a, s);
+  if (e != hipSuccess) return hip_fail(e, "attention gradient launch");
+  return ok();
+}
+
+dpf_status dpfused_qk_norm_rotary(const dpf_heads* q, const dpf_heads* k, const float* q_weight,
+                                  const float* k_weight, float eps, const double* freqs,
+                                  int64_t pairs, float amplitude, int32_t interleaved,
+                                  const dpf_ids* positions, const uint8_t* mask,
+                                  const dpf_heads* q_out, const dpf_heads* k_out, void* stream) {
+  CallScope call_("dpfused_qk_norm_rotary");
+  dpf_status st = check_rotary(q, k, q_weight, k_weight, eps, freqs, pairs, amplitude, interleaved,
+                               positions);
+  if (st == DPF_OK) st = check_heads(q_out, "q_out", true);
+  if (st == DPF_OK) st = check_heads(k_out, "k_out", true);
+  if (st != DPF_OK) return st;
+  if (q_out->dtype != q->dtype || k_out->dtype != q->dtype)
+    return fail(DPF_ERR_UNSUPPORTED, "the tensors have different dtypes");
+  if (!heads_alike(q, q_out) || !heads_alike(k, k_out))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "q_out and k_out must have the shapes of q and k");
+  if ((st = check_in_place(q_out, "q_out", q, {k, k_out})) != DPF_OK) return st;
+  if ((st = check_in_place(k_out, "k_out", k, {q})) != DPF_OK) return st;
+  dpf::RotaryArgs a = rotary_args(q, k, q_weight, k_weight, eps, freqs, pairs, amplitude, interleaved,
+                                  positions, mask, q_out, k_out);
+  dpf::rotary_plan(a, false);
+  const hipError_t e = dpf::launch_qk_norm_rotary(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "norm and rotation launch");
+  return ok();
+}
+
+dpf_status dpfused_qk_norm_rotary_backward(
+    const dpf_heads* dq_out, const dpf_heads* dk_out, const dpf_heads* q, const dpf_heads* k,
+    const float* q_weight, const float* k_weight, float eps, const double* freqs, int64_t pairs,
+    float amplitude, int32_t interleaved, const dpf_ids* positions, const uint8_t* mask,
+    const dpf_heads* dq, const dpf_heads* dk, float* dq_weight, float* dk_weight, void* stream) {
+  CallScope call_("dpfused_qk_norm_rotary_backward");
+  dpf_status st = check_rotary(q, k, q_weight, k_weight, eps, freqs, pairs, amplitude, interleaved,
+                               positions);
+  if (st == DPF_OK) st = check_heads(dq_out, "dq_out", false);
+  if (st == DPF_OK) st = check_heads(dk_out, "dk_out", false);
+  if (st == DPF_OK) st = check_heads(dq, "dq", true);
+  if (st == DPF_OK) st = check_heads(dk, "dk", true);
+  if (st != DPF_OK) return st;
+  for (const dpf_heads* h : {dq_out, dk_out, dq, dk})
+    if (h->dtype != q->dtype) return fail(DPF_ERR_UNSUPPORTED, "the tensors have different dtypes");
+  if (!heads_alike(q, dq_out) || !heads_alike(q, dq) || !heads_alike(k, dk_out) || !heads_alike(k, dk))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "the gradients must have the shapes of q and k");
+  if ((dq_weight == nullptr) != (q_weight == nullptr) || (dk_weight == nullptr) != (k_weight == nullptr))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "the weights' gradients are given exactly where the weights are");
+  if (((uintptr_t)dq_weight & 3u) != 0 || ((uintptr_t)dk_weight & 3u) != 0)
+    return fail(DPF_ERR_UNSUPPORTED, "a weight's gradient is not aligned to its elements");
+  if ((st = check_in_place(dq, "dq", dq_out, {dk_out, q, k, dk})) != DPF_OK) return st;
+  if ((st = check_in_place(dk, "dk", dk_out, {dq_out, q, k})) != DPF_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  dpf::RotaryArgs a = rotary_args(q, k, q_weight, k_weight, eps, freqs, pairs, amplitude, interleaved,
+                                  positions, mask, dq, dk);
+  a.gq = to_heads(dq_out);
+  a.gk = to_heads(dk_out);
+  a.dwq = dq_weight;
+  a.dwk = dk_weight;
+  const size_t floats = dpf::rotary_plan(a, true);
+  Workspace ws(s);
+  const size_t part = floats != 0 ? ws.reserve(floats * sizeof(float)) : 0;
+  if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
+  if (floats != 0) a.part = ws.at<float>(part);
+  const hipError_t e = dpf::launch_qk_norm_rotary_backward(a, s);
+  if (e != hipSuccess) return hip_fail(e, "norm and rotation gradient launch");
+  return ok();
+}
+
+dpf_status dpfused_dropout(const dpf_act* x, const dpf_act* residual, const uint8_t* mask, float p,
+                           uint64_t seed, uint64_t offset, const dpf_act* y, void* stream) {
+  CallScope call_("dpfused_dropout");
+  dpf_status st = check_rows(x, "x");
+  if (st == DPF_OK) st = check_rows(y, "y");
+  if (st == DPF_OK && residual != nullptr) st = check_rows(residual, "residual");
+  if (st != DPF_OK) return st;
+  for (const dpf_act* t : {y, residual}) {
+    if (t == nullptr) continue;
+    if (t->dtype != x->dtype) return fail(DPF_ERR_UNSUPPORTED, "x, y and residual have different dtypes");
+    if (t->B != x->B || t->T != x->T || t->D != x->D)
+      return fail(DPF_ERR_INVALID_ARGUMENT, "x, y and residual have different shapes");
+  }
+  if (!(p >= 0.0f && p < 1.0f)) return fail(DPF_ERR_INVALID_ARGUMENT, "p must be in [0, 1)");
+  const uint32_t limit = (uint32_t)std::nearbyint((double)p * 65536.0);
+  if (limit >= 65536u) return fail(DPF_ERR_INVALID_ARGUMENT, "p rounds to 1 (16 bits)");
+  if (x->B * x->T > ((int64_t)1 << 34) / x->D) return fail(DPF_ERR_UNSUPPORTED, "B * T * D > 2^34");
+  for (const dpf_act* t : {x, residual}) {
+    if (t == nullptr) continue;
+    const bool same = t->data == y->data && t->stride_b == y->stride_b && t->stride_t == y->stride_t;
+    if (!same && ranges_overlap(t->data, (size_t)act_bytes(t), y->data, (size_t)act_bytes(y)))
+      return fail(DPF_ERR_INVALID_ARGUMENT, "y overlaps an input without being it");
+  }
+  dpf::DropoutArgs a{};
+  a.X = to_act(x);
+  a.Y = to_act(y);
+  if (residual != nullptr) a.R = to_act(residual);
+  a.dtype = x->dtype;
+  a.B = x->B;
+  a.T = x->T;
+  a.D = x->D;
+  a.mask = mask;
+  a.limit = limit;
+  a.factor = (float)(65536.0 / (65536.0 - (double)limit));
+  a.seed = seed;
+  a.offset = offset;
+  a.vec = x->D % 8 == 0 && vec_ok(x) && vec_ok(y) && (residual == nullptr || vec_ok(residual));
+  const hipError_t e = dpf::launch_dropout(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "dropout launch");
+  return ok();
+}
+
+uint64_t dpfused_dropout_blocks(int64_t n_elements) {
+  return n_elements <= 0 ? 0 : (uint64_t)((n_elements - 1) / 8 + 1);
+}
+
+// ---------------------------------------------------------------------------
+// Orthogonalised update
+// ---------------------------------------------------------------------------
+namespace {
 
 dpf_status check_ortho(const dpf::OrthoArgs& a) {
   if (a.n < 1 || a.R < 1 || a.C < 1)

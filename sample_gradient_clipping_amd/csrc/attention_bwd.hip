@@ -1,0 +1,331 @@
+// Attention over the positions of each sample, backward.
+//
+//   P_ij = e^{s_ij - lse_i},  delta_i = dO_i . O_i
+//   dS_ij = P_ij (dO_i . v_j - delta_i)
+//   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i
+//
+// Two kernels, each a pass with sums of its own in registers, so that nothing is
+// added to memory in an order that changes: one over the keys for dq (which
+// takes delta too), one over the queries of all heads of a group for dk and dv.
+// Both form S and dO V^T again: seven products for the five of the formula, in
+// exchange for no atomics and no array of queries by keys.  P and dS lie in the
+// accumulators as the right operands of the products that sum over their rows;
+// they are rounded to bf16 there (what the operand type holds), all sums are
+// float32.
+//
+// A query that sees one key only has P = 1 and dS = 0 exactly; its delta comes
+// from the rounded output and would leave a difference that is all rounding, so
+// such a pair's dS is set to 0.
+#include "attn.hpp"
+
+namespace dpf {
+namespace attn {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kNT = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;      // queries (keys) of a workgroup
+
+template <class E> struct StepOf;       // keys (queries) of a tile
+template <> struct StepOf<BF16> { static constexpr int kN = 64; };
+template <> struct StepOf<F32> { static constexpr int kN = 32; };
+
+// ---------------------------------------------------------------------------
+// dq and delta: as the forward pass, each wave 32 queries (its lanes), tiles of
+// keys and values through LDS.
+// ---------------------------------------------------------------------------
+template <class E, int DP, bool VEC>
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 ? 2 : 1) void
+attention_dq_kernel(AttnArgs a) {
+  typedef Shape<E, DP> Sh;
+  typedef typename E::storage S;
+  constexpr int KEYS = StepOf<E>::kN;
+  constexpr int kTile = KEYS * Sh::kRowBytes;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][K, V] tiles
+  __shared__ int bound[2][kWaves];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
+  const int tiles = (a.Tq + kRows - 1) / kRows;
+  int head, tile;
+  if (!place(a.B * a.Hq, tiles, &head, &tile)) return;
+  tile = tiles - 1 - tile;
+  const int b = head / a.Hq, hq = head % a.Hq, hk = hq / (a.Hq / a.Hkv);
+  const int i = tile * kRows + wave * 32 + (lane & 31), p = a.Tk - a.Tq + i;
+  const bool valid = i < a.Tq;
+  Span keys = valid ? span_of(a, b, p) : Span{0, 0};
+  if (a.causal && valid) keys.end = min(keys.end, p + 1);
+  const bool some = keys.lo < keys.end, lone = keys.end - keys.lo == 1;
+  const int wlo = wave_min(some ? keys.lo : INT32_MAX), wend = wave_max(some ? keys.end : 0);
+  const int full_lo = wave_max(some ? keys.lo : 0), full_end = wave_min(some ? keys.end : INT32_MAX);
+  if (lane == 0) {
+    bound[0][wave] = wlo;
+    bound[1][wave] = wend;
+  }
+  __syncthreads();
+  int lo = bound[0][0], end = bound[1][0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    lo = min(lo, bound[0][w]);
+    end = max(end, bound[1][w]);
+  }
+  lo = uniform(lo);
+  end = uniform(end);
+  f32x16 dq[Sh::kDB];
+#pragma unroll
+  for (int db = 0; db < Sh::kDB; ++db) dq[db] = f32x16{};
+  const int64_t at = ((int64_t)b * a.Hq + hq) * a.Tq + i;
+  if (lo < end) {
+    const int64_t kat = b * a.k.sb + hk * a.k.sh, vat = b * a.v.sb + hk * a.v.sh;
+    uint32_t live[KEYS / 32], next[KEYS / 32];
+    int k0 = lo / KEYS * KEYS;
+    uint64_t m = live_keys<KEYS>(a, b, k0, live);
+    load_tile<E, DP, KEYS, kWaves, VEC>(smem, a.k, kat, k0, a.Tk, a.D, m, wave, lane);
+    load_tile<E, DP, KEYS, kWaves, VEC>(smem + kTile, a.v, vat, k0, a.Tk, a.D, m, wave, lane);
+    Chunk<E> qf[Sh::kG], gf[Sh::kG];
+    row_frags_from<E, DP, VEC>((const S*)a.o.data + b * a.o.sb + hq * a.o.sh + (int64_t)i * a.o.st, some,
+                               a.D, lane, qf);
+    row_frags_from<E, DP, VEC>((const S*)a.dout.data + b * a.dout.sb + hq * a.dout.sh +
+                               (int64_t)i * a.dout.st, some, a.D, lane, gf);
+    float delta = 0.0f;
+#pragma unroll
+    for (int g = 0; g < Sh::kG; ++g)
+#pragma unroll
+      for (int k = 0; k < 16 / Sh::kES; ++k)
+        delta = fmaf(E::to_float(qf[g][k]), E::to_float(gf[g][k]), delta);
+    delta += lane_xor(delta, 32);
+    row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
+                               a.D, lane, qf);
+    const float lse = some ? a.lse[at] * kLog2e : 0.0f;
+    if (valid && h == 0) a.delta[at] = delta;
+    const float c = a.scale * kLog2e;
+    int buf = 0;
+    for (; k0 < end; k0 += KEYS, buf ^= 1) {
+      const unsigned char* kt = smem + buf * 2 * kTile;
+      const unsigned char* vt = kt + kTile;
+      unsigned char* there = smem + (buf ^ 1) * 2 * kTile;
+      if constexpr (VEC) wait_loads();
+      tile_barrier();        // this tile is there; the other one has been read
+      if (k0 + KEYS < end) {
+        m = live_keys<KEYS>(a, b, k0 + KEYS, next);
+        load_tile<E, DP, KEYS, kWaves, VEC>(there, a.k, kat, k0 + KEYS, a.Tk, a.D, m, wave, lane);
+        load_tile<E, DP, KEYS, kWaves, VEC>(there + kTile, a.v, vat, k0 + KEYS, a.Tk, a.D, m, wave, lane);
+      }
+      if (k0 < wend && k0 + KEYS > wlo) {
+        const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
+#pragma unroll
+        for (int n = 0; n < KEYS / 32; ++n) {
+          f32x16 s = {}, ds = {};
+#pragma unroll
+          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(kt, 32 * n, g, lane), qf[g], s);
+#pragma unroll
+          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(vt, 32 * n, g, lane), gf[g], ds);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            ds[j] = __builtin_amdgcn_exp2f(fmaf(s[j], c, -lse)) * (ds[j] - delta);
+          if (!full) {
+            const uint32_t w = live[n] >> (4 * h);
+            const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int r = 8 * (j >> 2) + (j & 3);
+              const bool in = r >= first && r < past && ((w >> r) & 1) && !lone;
+              ds[j] = in ? ds[j] : 0.0f;
+            }
+          }
+          Weights<E> wt;
+          wt.set(ds);
+#pragma unroll
+          for (int db = 0; db < Sh::kDB; ++db)
+            dq[db] = mma_columns<E, DP>(kt, 32 * n, db, wt, dq[db], lane);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < KEYS / 32; ++n) live[n] = next[n];
+    }
+  } else if (valid && h == 0) {
+    a.delta[at] = 0.0f;
+  }
+  if (!valid) return;
+  store_row<E, DP, VEC>((S*)a.dq.data + b * a.dq.sb + hq * a.dq.sh + (int64_t)i * a.dq.st, dq,
+                        some ? a.scale : 0.0f, a.D, lane);
+}
+
+// ---------------------------------------------------------------------------
+// dk and dv: each wave 32 keys (its lanes), whose rows of K and V it holds in
+// registers; tiles of queries and of their output gradients go through LDS, for
+// each head of the group in turn.
+// ---------------------------------------------------------------------------
+template <class E, int DP, bool VEC>
+__global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
+  typedef Shape<E, DP> Sh;
+  typedef typename E::storage S;
+  constexpr int N = StepOf<E>::kN;
+  constexpr int kTile = N * Sh::kRowBytes;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][Q, dO] tiles
+  __shared__ int bound[2][kWaves];
+  __shared__ __attribute__((aligned(16))) float row_lse[2][N], row_delta[2][N];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
+  const int tiles = (a.Tk + kRows - 1) / kRows, group = a.Hq / a.Hkv, off = a.Tk - a.Tq;
+  int head, tile;
+  if (!place(a.B * a.Hkv, tiles, &head, &tile)) return;
+  const int b = head / a.Hkv, hk = head % a.Hkv;
+  const int j0 = tile * kRows + wave * 32 + (lane & 31);
+  const bool valid = j0 < a.Tk;
+  const Span sp = valid ? span_of(a, b, j0) : Span{0, 0};
+  // positions whose queries see this key: [from, past), active
+  int from = a.causal ? j0 : sp.lo;
+  const int past = sp.end;
+  const bool lone = a.causal ? sp.lo == j0 : sp.end - sp.lo == 1;   // position j0 sees only this key
+  from = max(from, off);
+  const bool some = from < past && sp.lo < sp.end;
+  const int wlo = wave_min(some ? from : INT32_MAX), wend = wave_max(some ? past : 0);
+  const int full_lo = wave_max(some ? from : 0), full_end = wave_min(some ? past : INT32_MAX);
+  if (lane == 0) {
+    bound[0][wave] = wlo;
+    bound[1][wave] = wend;
+  }
+  __syncthreads();
+  int lo = bound[0][0], end = bound[1][0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    lo = min(lo, bound[0][w]);
+    end = max(end, bound[1][w]);
+  }
+  lo = uniform(lo);
+  end = uniform(end);
+  f32x16 dk[Sh::kDB], dv[Sh::kDB];
+#pragma unroll
+  for (int db = 0; db < Sh::kDB; ++db) dk[db] = dv[db] = f32x16{};
+  if (lo < end) {
+    const int p_first = lo / N * N, steps = (end - p_first + N - 1) / N;
+    const float c = a.scale * kLog2e;
+    Chunk<E> kf[Sh::kG], vf[Sh::kG];
+    row_frags_from<E, DP, VEC>((const S*)a.k.data + b * a.k.sb + hk * a.k.sh + (int64_t)j0 * a.k.st, some,
+                               a.D, lane, kf);
+    row_frags_from<E, DP, VEC>((const S*)a.v.data + b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st, some,
+                               a.D, lane, vf);
+    uint32_t live[N / 32], next[N / 32];
+    float value = 0.0f;                   // of the next tile's lse (threads 0 ..) or delta (64 ..)
+    const int row = threadIdx.x & 63;
+    const auto fetch = [&](int p0, int hq, int buf) {
+      const uint64_t m = live_keys<N>(a, b, p0, next);
+      load_tile<E, DP, N, kWaves, VEC>(smem + buf * 2 * kTile, a.q, b * a.q.sb + hq * a.q.sh, p0 - off,
+                                       a.Tq, a.D, m, wave, lane);
+      load_tile<E, DP, N, kWaves, VEC>(smem + buf * 2 * kTile + kTile, a.dout,
+                                       b * a.dout.sb + hq * a.dout.sh, p0 - off, a.Tq, a.D, m, wave, lane);
+      const int i = p0 - off + row;
+      value = 0.0f;
+      if (wave < 2 && row < N && i >= 0 && i < a.Tq) {
+        const int64_t e = ((int64_t)b * a.Hq + hq) * a.Tq + i;
+        value = wave == 0 ? a.lse[e] * kLog2e : a.delta[e];
+      }
+    };
+    const auto keep = [&](int buf) {
+      if (wave < 2 && row < N) (wave == 0 ? row_lse : row_delta)[buf][row] = value;
+    };
+    fetch(p_first, hk * group, 0);
+    keep(0);
+    int buf = 0, p0 = p_first, hq = hk * group;
+    for (int it = 0; it < steps * group; ++it, buf ^= 1) {
+#pragma unroll
+      for (int n = 0; n < N / 32; ++n) live[n] = next[n];
+      int p1 = p0 + N, hq1 = hq;
+      if (p1 >= end) {
+        p1 = p_first;
+        ++hq1;
+      }
+      if constexpr (VEC) wait_loads();
+      tile_barrier();        // this tile is there; the other one has been read
+      const bool more = it + 1 < steps * group;
+      if (more) fetch(p1, hq1, buf ^ 1);
+      if (p0 < wend && p0 + N > wlo) {
+        const unsigned char* qt = smem + buf * 2 * kTile;
+        const unsigned char* gt = qt + kTile;
+        const bool full = p0 >= full_lo && p0 + N <= full_end && all_live<N>(live);
+#pragma unroll
+        for (int n = 0; n < N / 32; ++n) {
+          f32x16 s = {}, ds = {};
+#pragma unroll
+          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(qt, 32 * n, g, lane), kf[g], s);
+#pragma unroll
+          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(gt, 32 * n, g, lane), vf[g], ds);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 l4 = *(const f32x4*)&row_lse[buf][32 * n + 8 * q + 4 * h];
+            const f32x4 d4 = *(const f32x4*)&row_delta[buf][32 * n + 8 * q + 4 * h];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = 4 * q + k;
+              s[j] = __builtin_amdgcn_exp2f(fmaf(s[j], c, -l4[k]));
+              ds[j] = s[j] * (ds[j] - d4[k]);
+            }
+          }
+          if (!full) {
+            const uint32_t w = live[n] >> (4 * h);
+            const int base = p0 + 32 * n + 4 * h;
+            const int first = from - base, stop = past - base, self = lone ? j0 - base : -1;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int r = 8 * (j >> 2) + (j & 3);
+              const bool in = r >= first && r < stop && ((w >> r) & 1);
+              s[j] = in ? s[j] : 0.0f;
+              ds[j] = in && r != self ? ds[j] : 0.0f;
+            }
+          }
+          Weights<E> pw, dw;
+          pw.set(s);
+          dw.set(ds);
+#pragma unroll
+          for (int db = 0; db < Sh::kDB; ++db) {
+            dv[db] = mma_columns<E, DP>(gt, 32 * n, db, pw, dv[db], lane);
+            dk[db] = mma_columns<E, DP>(qt, 32 * n, db, dw, dk[db], lane);
+          }
+        }
+      }
+      if (more) keep(buf ^ 1);
+      p0 = p1;
+      hq = hq1;
+    }
+  }
+  if (!valid) return;
+  store_row<E, DP, VEC>((S*)a.dk.data + b * a.dk.sb + hk * a.dk.sh + (int64_t)j0 * a.dk.st, dk,
+                        some ? a.scale : 0.0f, a.D, lane);
+  store_row<E, DP, VEC>((S*)a.dv.data + b * a.dv.sb + hk * a.dv.sh + (int64_t)j0 * a.dv.st, dv,
+                        some ? 1.0f : 0.0f, a.D, lane);
+}
+
+template <class E, int DP, bool VEC>
+hipError_t backward(const AttnArgs& a, hipStream_t s) {
+  typedef Shape<E, DP> Sh;
+  constexpr int lds = 4 * StepOf<E>::kN * Sh::kRowBytes;
+  static hipError_t once[2] = {
+      hipFuncSetAttribute((const void*)attention_dq_kernel<E, DP, VEC>,
+                          hipFuncAttributeMaxDynamicSharedMemorySize, lds),
+      hipFuncSetAttribute((const void*)attention_dkv_kernel<E, DP, VEC>,
+                          hipFuncAttributeMaxDynamicSharedMemorySize, lds)};
+  if (once[0] != hipSuccess) return once[0];
+  if (once[1] != hipSuccess) return once[1];
+  const int64_t qt = (a.Tq + kRows - 1) / kRows, kt = (a.Tk + kRows - 1) / kRows;
+  const int64_t qh = ((int64_t)a.B * a.Hq + 7) / 8 * 8, kh = ((int64_t)a.B * a.Hkv + 7) / 8 * 8;
+  timing_begin("attention_dq", s);
+  hipLaunchKernelGGL((attention_dq_kernel<E, DP, VEC>), dim3((unsigned)(qh * qt)), dim3(kNT), lds, s, a);
+  timing_end("attention_dq", s);
+  timing_begin("attention_dkv", s);
+  hipLaunchKernelGGL((attention_dkv_kernel<E, DP, VEC>), dim3((unsigned)(kh * kt)), dim3(kNT), lds, s, a);
+  timing_end("attention_dkv", s);
+  return hipGetLastError();
+}
+
+template <class E>
+hipError_t backward_e(const AttnArgs& a, hipStream_t s) {
+  if (a.D <= 64) return a.vec ? backward<E, 64, true>(a, s) : backward<E, 64, false>(a, s);
+  return a.vec ? backward<E, 128, true>(a, s) : backward<E, 128, false>(a, s);
+}
+
+}  // namespace
+}  // namespace attn
+
+hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s) {
+  return a.dtype == kBF16 ? attn::backward_e<BF16>(a, s) : attn::backward_e<F32>(a, s);
+}
+
+}  // namespace dpf

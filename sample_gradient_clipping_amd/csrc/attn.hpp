@@ -1,0 +1,321 @@
+// Attention: arguments of the kernels, and the tiles they share (attention.hip,
+// attention_bwd.hip).
+#pragma once
+
+#include "lm.hpp"
+
+namespace dpf {
+
+constexpr int kAttnMaxD = 128;
+constexpr int64_t kAttnMaxT = (int64_t)1 << 22;
+constexpr int64_t kAttnMaxTiles = (int64_t)1 << 22;   // batch x heads x tiles of 32 positions
+
+struct AttnArgs {
+  Heads q, k, v, o;         // o: the output (forward), read by the backward
+  Heads dout, dq, dk, dv;   // backward only
+  float* lse;               // [B, Hq, Tq], written (forward) or read (backward)
+  float* delta;             // [B, Hq, Tq] workspace of the backward
+  int dtype;
+  int B, Tq, Tk, Hq, Hkv, D;
+  int causal;
+  float scale;              // > 0
+  // Padding and packing (null without): what `ranges` makes of mask and segments.
+  const uint8_t* mask;      // [B, Tk]
+  const int32_t* segments;  // [B, Tk], not decreasing along T
+  int32_t *lo, *end;        // [B, Tk] workspace
+  uint32_t* bits;           // [B, nwords] workspace: bit t % 32 of word t / 32, active
+  int nwords;               // 2 ceil(Tk / 64)
+  int vec;                  // every row is 16-byte aligned and whole 16-byte pieces
+  float* part;              // attention_part_floats: partial results of keys split over workgroups
+  int splits;
+};
+
+// Workspace of mask and segments, and of split keys, in elements.
+inline int attn_words(int64_t Tk) { return (int)(2 * ((Tk + 63) / 64)); }
+// Fills a.splits; 0 floats without a split.
+size_t attention_part_floats(AttnArgs& a);
+hipError_t launch_attn_ranges(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attention(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);
+
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kOOB = 0x7ffffff0;          // past every buffer's end: such a load gives zeros
+
+// A position's keys are [lo, end) less the inactive ones, up to itself when
+// causal.  Without mask and segments [0, Tk).
+struct Span { int lo, end; };
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b, int p) {
+  if (a.lo == nullptr) return {0, a.Tk};
+  const int64_t e = (int64_t)b * a.Tk + p;
+  return {a.lo[e], a.end[e]};
+}
+
+// LDS tiles: rows of DP elements in 16-byte chunks, chunk c of row r stored at
+// c ^ swz(r), so that 16 rows' equal chunks lie in different banks (row
+// fragments, 16 bytes per lane) and so do 64 bytes of each of 4 rows (the
+// transposing reads).
+template <class E, int DP>
+struct Shape {
+  typedef typename E::storage S;
+  static constexpr int kES = (int)sizeof(S);
+  static constexpr int kRowBytes = DP * kES;
+  static constexpr int kChunks = kRowBytes / 16;    // of a row: 8, 16 or 32
+  static constexpr int kG = kChunks / 2;            // row fragments: two chunks, one per lane half
+  static constexpr int kRowsPerDma = 64 / kChunks;
+  static constexpr int kDB = DP / 32;               // 32-wide blocks of the head
+};
+
+template <int CHUNKS>
+__device__ __forceinline__ int swz(int row) {
+  if constexpr (CHUNKS == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  else return ((row & 3) << 2) | ((row >> 2) & 3);
+}
+
+// 16 bytes per lane from rsrc at voffset straight into LDS at lds + 16 * lane;
+// awaited with wait_loads.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voffset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(voffset), "s"(rsrc), "s"(lds)
+               : "memory");
+}
+// Until every load this wave has queued is there.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Until this wave's LDS reads are back: what they read may then be overwritten.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void tile_barrier() {
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char*)p;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// One head's rows [row0, row0 + ROWS) of `rows` into an LDS tile by NW waves
+// (wave w of them); rows outside [0, rows) and those whose bit of `live` is 0
+// become zeros, and so does what lies past D.  VEC: direct loads to LDS, in
+// flight until wait_loads; else element by element, there after a barrier.
+template <class E, int DP, int ROWS, int NW, bool VEC>
+__device__ __forceinline__ void load_tile(unsigned char* tile, const Heads& h, int64_t head_at,
+                                          int row0, int rows, int D, uint64_t live, int wave,
+                                          int lane) {
+  typedef Shape<E, DP> Sh;
+  typedef typename E::storage S;
+  const S* base = (const S*)h.data + head_at + (int64_t)row0 * h.st;
+  if constexpr (VEC) {
+    constexpr int kPer = ROWS / Sh::kRowsPerDma / NW;
+    static_assert(kPer >= 1, "a wave's share of a tile");
+    const int64_t left = ((int64_t)(rows - 1 - row0) * h.st + D) * Sh::kES;
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)base, (short)0, (int)(left < 0 ? 0 : left < 0x7fff0000 ? left : 0x7fff0000), 0x00020000);
+    const uint32_t at = lds_addr(tile);
+    const int stride = (int)(h.st * Sh::kES);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int first = (wave * kPer + j) * Sh::kRowsPerDma;       // uniform
+      const int row = lane / Sh::kChunks;
+      const int chunk = (lane % Sh::kChunks) ^ swz<Sh::kChunks>(first + row);
+      // row0 may be negative: those rows lie before the tensor
+      const bool in = 16 * chunk < D * Sh::kES && first + row >= -row0 && ((live >> (first + row)) & 1);
+      dma16(rsrc, in ? (first + row) * stride + 16 * chunk : kOOB, uniform(at + first * Sh::kRowBytes));
+    }
+  } else {
+    for (int e = wave * 64 + lane; e < ROWS * DP; e += 64 * NW) {
+      const int row = e / DP, d = e % DP;
+      const bool in = d < D && row0 + row >= 0 && row0 + row < rows && ((live >> row) & 1);
+      S x = 0;
+      if (in) x = base[(int64_t)row * h.st + d];
+      const int chunk = d * Sh::kES / 16;
+      *(S*)(tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) = x;
+    }
+  }
+}
+
+// 16 bytes of a row: 8 bf16 or 4 float32 elements, the operand of one
+// 32x32x16 or four 32x32x2 products (k = lane half, then element).
+template <class E> struct ChunkOf;
+template <> struct ChunkOf<BF16> { typedef u16x8 type; };
+template <> struct ChunkOf<F32> { typedef f32x4 type; };
+template <class E> using Chunk = typename ChunkOf<E>::type;
+
+template <class E>
+__device__ __forceinline__ f32x16 mma(const Chunk<E>& x, const Chunk<E>& y, f32x16 c) {
+  if constexpr (sizeof(typename E::storage) == 2) {
+    return mfma_32x32x16(x, y, c);
+  } else {
+    c = mfma_32x32x2(x.x, y.x, c);
+    c = mfma_32x32x2(x.y, y.y, c);
+    c = mfma_32x32x2(x.z, y.z, c);
+    return mfma_32x32x2(x.w, y.w, c);
+  }
+}
+
+// Row fragment g of rows row0 + 0..31 of an LDS tile.
+template <class E, int DP>
+__device__ __forceinline__ Chunk<E> row_frag(const unsigned char* tile, int row0, int g, int lane) {
+  typedef Shape<E, DP> Sh;
+  const int r = lane & 31, h = lane >> 5;
+  const int c = (2 * g + h) ^ swz<Sh::kChunks>(r);
+  return *(const Chunk<E>*)(tile + (row0 + r) * Sh::kRowBytes + 16 * c);
+}
+
+// The row fragments of one row in memory (this lane's), zeros where !live.
+template <class E, int DP, bool VEC>
+__device__ __forceinline__ void row_frags_from(const typename E::storage* row, bool live, int D, int lane,
+                                               Chunk<E> (&f)[Shape<E, DP>::kG]) {
+  typedef Shape<E, DP> Sh;
+  constexpr int kN = 16 / Sh::kES;
+#pragma unroll
+  for (int g = 0; g < Sh::kG; ++g) {
+    const int d = (2 * g + (lane >> 5)) * kN;
+    Chunk<E> x = {};
+    if constexpr (VEC) {
+      if (live && d < D) x = *(const Chunk<E>*)(row + d);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        if (live && d + k < D) x[k] = row[d + k];
+    }
+    f[g] = x;
+  }
+}
+
+// What a 32x32 accumulator holds per lane (register j: row 8 (j / 4) + 4 half
+// + j % 4), as the right operand of products that sum over its 32 rows: for
+// bf16 two fragments of 8 rows each (rounded to nearest even), for float32 the
+// values themselves.
+template <class E> struct Weights;
+template <> struct Weights<BF16> {
+  u16x8 f[2];
+  __device__ __forceinline__ void set(const f32x16& p) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const f2 x = {p[8 * s + 2 * k], p[8 * s + 2 * k + 1]};
+        w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2));
+      }
+      f[s] = __builtin_bit_cast(u16x8, w);
+    }
+  }
+};
+template <> struct Weights<F32> {
+  f32x16 p;
+  __device__ __forceinline__ void set(const f32x16& x) { p = x; }
+};
+
+// acc += (rows row0 .. row0 + 31 of the tile, columns 32 db ..)^T times w.
+template <class E, int DP>
+__device__ __forceinline__ f32x16 mma_columns(const unsigned char* tile, int row0, int db,
+                                              const Weights<E>& w, f32x16 acc, int lane) {
+  typedef Shape<E, DP> Sh;
+  const int h = lane >> 5;
+  if constexpr (sizeof(typename E::storage) == 2) {
+    const int j = lane & 15, sub = (lane >> 4) & 1;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u16x4 part[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 16 * s + 8 * r + 4 * h + (j >> 2);
+        const int chunk = (4 * db + 2 * sub + ((j & 3) >> 1)) ^ swz<Sh::kChunks>(row);
+        part[r] = lds_read_tr16((const uint16_t*)(tile + (row0 + row) * Sh::kRowBytes + 16 * chunk +
+                                                  8 * (j & 1)));
+      }
+      const u16x8 x = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      acc = mfma_32x32x16(x, w.f[s], acc);
+    }
+  } else {
+    const int d = 32 * db + (lane & 31);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int row = 8 * (j >> 2) + 4 * h + (j & 3);
+      const int chunk = (d >> 2) ^ swz<Sh::kChunks>(row);
+      acc = mfma_32x32x2(*(const float*)(tile + (row0 + row) * Sh::kRowBytes + 16 * chunk + 4 * (d & 3)),
+                         w.p[j], acc);
+    }
+  }
+  return acc;
+}
+
+// Stores this lane's columns of the transposed result (registers of block db:
+// entries 32 db + 8 (j / 4) + 4 half + j % 4 of the row) times f.
+template <class E, int DP, bool VEC>
+__device__ __forceinline__ void store_row(typename E::storage* row, const f32x16 (&acc)[DP / 32], float f,
+                                          int D, int lane) {
+  const int h = lane >> 5;
+#pragma unroll
+  for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = 32 * db + 8 * i + 4 * h;
+      const float x[4] = {acc[db][4 * i] * f, acc[db][4 * i + 1] * f, acc[db][4 * i + 2] * f,
+                          acc[db][4 * i + 3] * f};
+      if constexpr (VEC) {
+        if (d < D) store_f32<E, 4>(row + d, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (d + k < D) {
+            const float y[1] = {x[k]};
+            store_f32<E, 1>(row + d + k, y);
+          }
+      }
+    }
+}
+
+__device__ __forceinline__ int wave_min(int x) {
+#pragma unroll
+  for (int j = 1; j < 64; j <<= 1) x = min(x, lane_xor(x, j));
+  return uniform(x);
+}
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+  for (int j = 1; j < 64; j <<= 1) x = max(x, lane_xor(x, j));
+  return uniform(x);
+}
+
+// The active bits of keys k0 .. k0 + KEYS - 1 (k0 a multiple of KEYS).
+template <int KEYS>
+__device__ __forceinline__ uint64_t live_keys(const AttnArgs& a, int b, int k0,
+                                              uint32_t (&w)[KEYS / 32]) {
+  if (a.bits == nullptr) {
+#pragma unroll
+    for (int n = 0; n < KEYS / 32; ++n) w[n] = ~0u;
+    return ~0ull;
+  }
+  const uint32_t* p = a.bits + (int64_t)b * a.nwords + k0 / 32;
+#pragma unroll
+  for (int n = 0; n < KEYS / 32; ++n) w[n] = uniform(p[n]);
+  return KEYS == 64 ? ((uint64_t)w[KEYS / 32 - 1] << 32) | w[0] : (uint64_t)w[0];
+}
+
+template <int KEYS>
+__device__ __forceinline__ bool all_live(const uint32_t (&w)[KEYS / 32]) {
+  uint32_t x = ~0u;
+#pragma unroll
+  for (int n = 0; n < KEYS / 32; ++n) x &= w[n];
+  return x == ~0u;
+}
+
+// Workgroups that read the same keys and values (the queries of a head, the
+// heads of a group) are given to one XCD one after another, so that they find
+// them in its L2; the longest first.
+__device__ __forceinline__ bool place(int heads, int tiles, int* head, int* tile) {
+  const int L = blockIdx.x, xcd = L & 7, at = L >> 3;
+  *head = xcd * ((heads + 7) / 8) + at / tiles;
+  *tile = at % tiles;
+  return at / tiles < (heads + 7) / 8 && *head < heads;
+}
+
+}  // namespace attn
+}  // namespace dpf

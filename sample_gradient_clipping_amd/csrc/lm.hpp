@@ -134,9 +134,10 @@ __device__ __forceinline__ double lane_xor(double v, int j) {
 }
 
 // philox_block's words, with gfx950's three-way xor: 20 instructions of a block's
-// 100 less.
-__device__ __forceinline__ u32x4 philox_block_xor3(uint64_t seed, uint64_t block) {
-  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = 0u, c3 = 0u;
+// 100 less.  Counter word 2 is 0 in the noise's blocks; dropout's have 1 there, so
+// that the two never draw the same block.
+__device__ __forceinline__ u32x4 philox_block_xor3(uint64_t seed, uint64_t block, uint32_t word2 = 0u) {
+  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = word2, c3 = 0u;
   uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
@@ -274,5 +275,51 @@ struct OrthoArgs {
 bool ortho_coeffs_ok(const OrthoArgs& a);
 size_t ortho_workspace_bytes(const OrthoArgs& a);
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s);
+
+// [B, T, H, D] in device memory, D contiguous, strides in elements.
+struct Heads {
+  void* data;
+  int64_t sb, st, sh;
+};
+
+// Norms of queries and keys and their rotation (rotary.hip).
+constexpr int kRotaryMaxD = 256;
+struct RotaryArgs {
+  Heads q, k;               // [B, T, Hq, D] and [B, T, Hk, D]: the inputs
+  Heads gq, gk;             // backward: the outputs' gradients
+  Heads oq, ok;             // the outputs, or (backward) the inputs' gradients
+  int dtype;
+  int64_t B, T;
+  int Hq, Hk, D;
+  const float *wq, *wk;     // [D] each, or both null: no norm
+  float eps;
+  const double* freqs;      // [pairs] radians per position
+  int pairs;                // rotated entries of a head: 2 * pairs; 0: no rotation
+  float amplitude;
+  int interleaved;
+  Ids positions;            // data null: 0 .. T - 1
+  const uint8_t* mask;      // [B, T] or null
+  float *dwq, *dwk;         // backward: [B, D] each
+  float* part;              // rotary_part_floats
+  int width;                // entries of a 16- or 8-byte piece, or 1 (set by rotary_plan)
+  int tokens;               // of a workgroup (set by rotary_plan)
+};
+// Sets width and tokens; the floats of the weights' partial sums (0: none).
+size_t rotary_plan(RotaryArgs& a, bool backward);
+hipError_t launch_qk_norm_rotary(const RotaryArgs& a, hipStream_t s);
+hipError_t launch_qk_norm_rotary_backward(const RotaryArgs& a, hipStream_t s);
+
+// Dropout (dropout.hip).
+struct DropoutArgs {
+  Act X, R, Y;              // [B, T, D]; R.data null: no residual
+  int dtype;
+  int64_t B, T, D;
+  const uint8_t* mask;
+  uint32_t limit;           // dropped where the 16 random bits are below this
+  float factor;             // of what is kept
+  uint64_t seed, offset;
+  int vec;                  // rows are whole, aligned pieces of 8 entries
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s);
 
 }  // namespace dpf
