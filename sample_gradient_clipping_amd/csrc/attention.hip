@@ -138,68 +138,121 @@ struct State {
   float m, l;           // maximum used (times log2 e) and this lane half's sum
 };
 
+// The tile goes by blocks of 32 keys: while the matrix cores take the scores of
+// the next block, or the outputs of the last one, the vector unit takes the
+// exponentials of this one.  The order is written out, step by step between
+// fences, with every LDS operand read kAhead products early: left to itself the
+// compiler waits for each read, and puts all exponentials before all products.
+constexpr int kAhead = 4;
+
 template <class E, int DP, int KEYS>
 __device__ __forceinline__ void attend(const unsigned char* kt, const unsigned char* vt,
                                        const Chunk<E> (&qf)[Shape<E, DP>::kG], State<E, DP>& st, float c,
                                        int k0, Span keys, bool full, const uint32_t (&live)[KEYS / 32],
-                                       int lane) {
-  constexpr int NB = KEYS / 32;
+                                       const Places& at, int lane) {
+  constexpr int NB = KEYS / 32, G = Shape<E, DP>::kG, DB = DP / 32, CS = ColumnSteps<E>::kN;
   const int h = lane >> 5;
-  f32x16 s[NB];
-#pragma unroll
-  for (int n = 0; n < NB; ++n) {
+  f32x16 s[2];
+  Weights<E> p[2];
+  float m = 0.0f, sum[2] = {};
+
+  const auto exponential = [&](int n, int j) {
+    float x = __builtin_amdgcn_exp2f(fmaf(s[n & 1][j], c, -m));
+    asm volatile("" : "+v"(x));    // here, not where it is used first
+    s[n & 1][j] = x;
+    sum[j & 1] += x;
+  };
+  // scores of block n, with the exponentials of block n - 1 between the products
+  const auto scores = [&](int n) {
+    Chunk<E> k[kAhead];
     f32x16 x = {};
 #pragma unroll
-    for (int g = 0; g < Shape<E, DP>::kG; ++g)
-      x = mma<E>(row_frag<E, DP>(kt, 32 * n, g, lane), qf[g], x);
-    s[n] = x;
-  }
-  if (!full) {
+    for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 32 * n, g, at);
+    fence();
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
+    for (int g = 0; g < G; ++g) {
+      x = mma<E>(k[g % kAhead], qf[g], x);
+      if (g + kAhead < G) k[g % kAhead] = row_frag<E, DP>(kt, 32 * n, g + kAhead, at);
+      if (n > 0) {
+#pragma unroll
+        for (int j = 16 * g / G; j < 16 * (g + 1) / G; ++j) exponential(n - 1, j);
+      }
+      fence();
+    }
+    s[n & 1] = x;
+  };
+  // outputs from block n, with the exponentials of block n + 1 between the products
+  const auto outputs = [&](int n, bool more) {
+    constexpr int N = DB * CS;
+    Column<E> v[kAhead];
+    const auto read = [&](int t) { return column_frag<E, DP>(vt, 32 * n, t % DB, t / DB, at, lane); };
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) v[t] = read(t);
+    fence();
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      st.o[t % DB] = mma_column<E>(v[t % kAhead], p[n & 1], t / DB, st.o[t % DB]);
+      if (t + kAhead < N) v[t % kAhead] = read(t + kAhead);
+      if (more) {
+#pragma unroll
+        for (int j = 16 * t / N; j < 16 * (t + 1) / N; ++j) exponential(n + 1, j);
+      }
+      fence();
+    }
+  };
+  // masks block n and moves the running maximum to it
+  const auto settle = [&](int n) {
+    if (!full) {
+      apart();
       const uint32_t w = live[n] >> (4 * h);
       const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int r = 8 * (j >> 2) + (j & 3);
         const bool in = r >= first && r < past && ((w >> r) & 1);
-        s[n][j] = in ? s[n][j] : -INFINITY;
+        s[n & 1][j] = in ? s[n & 1][j] : -INFINITY;
       }
     }
-  }
-  float top = s[0][0];
+    float top = s[n & 1][0];
 #pragma unroll
-  for (int n = 0; n < NB; ++n)
+    for (int j = 1; j < 16; ++j) top = fmaxf(top, s[n & 1][j]);
+    top = fmaxf(top, lane_xor(top, 32)) * c;
+    if (__any(top > st.m + kSlack)) {
+      apart();
+      const float to = fmaxf(st.m, top);
+      const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - to);
+      st.m = to;
+      st.l = (st.l + (sum[0] + sum[1])) * f;
+      sum[0] = sum[1] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, s[n][j]);
-  top = fmaxf(top, lane_xor(top, 32)) * c;
-  if (__any(top > st.m + kSlack)) {
-    const float m = fmaxf(st.m, top);
-    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
-    st.m = m;
-    st.l *= f;
+      for (int db = 0; db < DB; ++db)
 #pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
+        for (int j = 0; j < 16; ++j) st.o[db][j] *= f;
+      // the block before, whose weights are still to be used
+      if (n > 0) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) st.o[db][j] *= f;
-  }
-  const float m = st.m == -INFINITY ? 0.0f : st.m;
-  Weights<E> p[NB];
-  float sum[4] = {};
-#pragma unroll
-  for (int n = 0; n < NB; ++n) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      s[n][j] = __builtin_amdgcn_exp2f(fmaf(s[n][j], c, -m));
-      sum[j & 3] += s[n][j];
+        for (int j = 0; j < 16; ++j) s[(n - 1) & 1][j] *= f;
+      }
     }
-    p[n].set(s[n]);
+    m = st.m == -INFINITY ? 0.0f : st.m;
+  };
+
+  scores(0);
+  settle(0);
+#pragma unroll
+  for (int n = 1; n < NB; ++n) {
+    scores(n);
+    settle(n);
+    p[(n - 1) & 1].set(s[(n - 1) & 1]);
+    outputs(n - 1, true);
   }
-  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  if (NB == 1) {
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-    for (int n = 0; n < NB; ++n) st.o[db] = mma_columns<E, DP>(vt, 32 * n, db, p[n], st.o[db], lane);
+    for (int j = 0; j < 16; ++j) exponential(0, j);
+  }
+  p[(NB - 1) & 1].set(s[(NB - 1) & 1]);
+  outputs(NB - 1, false);
+  st.l += sum[0] + sum[1];
 }
 
 template <class E, int DP, bool VEC>
@@ -254,6 +307,7 @@ attention_kernel(AttnArgs a) {
     row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
     const float c = a.scale * kLog2e;
+    const Places at = places<E, DP>(lane);
     int buf = 0;
     for (; k0 < end; k0 += KEYS, buf ^= 1) {
       unsigned char* here = smem + buf * 2 * kTile;
@@ -267,7 +321,7 @@ attention_kernel(AttnArgs a) {
       }
       if (k0 < wend && k0 + KEYS > wlo) {
         const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
-        attend<E, DP, KEYS>(here, here + kTile, qf, st, c, k0, keys, full, live, lane);
+        attend<E, DP, KEYS>(here, here + kTile, qf, st, c, k0, keys, full, live, at, lane);
       }
 #pragma unroll
       for (int n = 0; n < KEYS / 32; ++n) live[n] = next[n];
@@ -276,7 +330,7 @@ attention_kernel(AttnArgs a) {
   if (!valid) return;
   const float l = st.l + lane_xor(st.l, 32);
   S* out = (S*)a.o.data + b * a.o.sb + hq * a.o.sh + (int64_t)i * a.o.st;
-  store_row<E, DP, VEC>(out, st.o, some ? 1.0f / l : 0.0f, a.D, lane);
+  store_row<E, DP, VEC>(out, st.o, some, 1.0f / l, a.D, lane);
   if (lane < 32)
     a.lse[((int64_t)b * a.Hq + hq) * a.Tq + i] = some ? kLn2 * (st.m + __log2f(l)) : 0.0f;
 }
@@ -335,6 +389,7 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
     row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
     const float c = a.scale * kLog2e;
+    const Places at = places<E, DP>(lane);
     int buf = 0;
     for (; k0 < end; k0 += step, buf ^= 1) {
       unsigned char* here = mine + buf * 2 * kTile;
@@ -343,7 +398,7 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
       __builtin_amdgcn_wave_barrier();
       if (k0 + step < end) fetch(k0 + step, mine + (buf ^ 1) * 2 * kTile);
       const bool full = k0 >= full_lo && k0 + KEYS <= full_end && live[0] == ~0u;
-      attend<E, DP, KEYS>(here, here + kTile, qf, st, c, k0, keys, full, live, lane);
+      attend<E, DP, KEYS>(here, here + kTile, qf, st, c, k0, keys, full, live, at, lane);
       live[0] = next[0];
     }
   }

@@ -97,6 +97,7 @@ attention_dq_kernel(AttnArgs a) {
     const float lse = some ? a.lse[at] * kLog2e : 0.0f;
     if (valid && h == 0) a.delta[at] = delta;
     const float c = a.scale * kLog2e;
+    const Places pl = places<E, DP>(lane);
     int buf = 0;
     for (; k0 < end; k0 += KEYS, buf ^= 1) {
       const unsigned char* kt = smem + buf * 2 * kTile;
@@ -115,13 +116,14 @@ attention_dq_kernel(AttnArgs a) {
         for (int n = 0; n < KEYS / 32; ++n) {
           f32x16 s = {}, ds = {};
 #pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(kt, 32 * n, g, lane), qf[g], s);
+          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(kt, 32 * n, g, pl), qf[g], s);
 #pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(vt, 32 * n, g, lane), gf[g], ds);
+          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(vt, 32 * n, g, pl), gf[g], ds);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             ds[j] = __builtin_amdgcn_exp2f(fmaf(s[j], c, -lse)) * (ds[j] - delta);
           if (!full) {
+            apart();
             const uint32_t w = live[n] >> (4 * h);
             const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
 #pragma unroll
@@ -135,7 +137,7 @@ attention_dq_kernel(AttnArgs a) {
           wt.set(ds);
 #pragma unroll
           for (int db = 0; db < Sh::kDB; ++db)
-            dq[db] = mma_columns<E, DP>(kt, 32 * n, db, wt, dq[db], lane);
+            dq[db] = mma_columns<E, DP>(kt, 32 * n, db, wt, dq[db], pl, lane);
         }
       }
 #pragma unroll
@@ -146,7 +148,7 @@ attention_dq_kernel(AttnArgs a) {
   }
   if (!valid) return;
   store_row<E, DP, VEC>((S*)a.dq.data + b * a.dq.sb + hq * a.dq.sh + (int64_t)i * a.dq.st, dq,
-                        some ? a.scale : 0.0f, a.D, lane);
+                        some, a.scale, a.D, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -198,6 +200,7 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
   if (lo < end) {
     const int p_first = lo / N * N, steps = (end - p_first + N - 1) / N;
     const float c = a.scale * kLog2e;
+    const Places pl = places<E, DP>(lane);
     Chunk<E> kf[Sh::kG], vf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.k.data + b * a.k.sb + hk * a.k.sh + (int64_t)j0 * a.k.st, some,
                                a.D, lane, kf);
@@ -245,9 +248,9 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
         for (int n = 0; n < N / 32; ++n) {
           f32x16 s = {}, ds = {};
 #pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(qt, 32 * n, g, lane), kf[g], s);
+          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(qt, 32 * n, g, pl), kf[g], s);
 #pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(gt, 32 * n, g, lane), vf[g], ds);
+          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(gt, 32 * n, g, pl), vf[g], ds);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f32x4 l4 = *(const f32x4*)&row_lse[buf][32 * n + 8 * q + 4 * h];
@@ -260,6 +263,7 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
             }
           }
           if (!full) {
+            apart();
             const uint32_t w = live[n] >> (4 * h);
             const int base = p0 + 32 * n + 4 * h;
             const int first = from - base, stop = past - base, self = lone ? j0 - base : -1;
@@ -276,8 +280,8 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
           dw.set(ds);
 #pragma unroll
           for (int db = 0; db < Sh::kDB; ++db) {
-            dv[db] = mma_columns<E, DP>(gt, 32 * n, db, pw, dv[db], lane);
-            dk[db] = mma_columns<E, DP>(qt, 32 * n, db, dw, dk[db], lane);
+            dv[db] = mma_columns<E, DP>(gt, 32 * n, db, pw, dv[db], pl, lane);
+            dk[db] = mma_columns<E, DP>(qt, 32 * n, db, dw, dk[db], pl, lane);
           }
         }
       }
@@ -288,9 +292,9 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
   }
   if (!valid) return;
   store_row<E, DP, VEC>((S*)a.dk.data + b * a.dk.sb + hk * a.dk.sh + (int64_t)j0 * a.dk.st, dk,
-                        some ? a.scale : 0.0f, a.D, lane);
+                        some, a.scale, a.D, lane);
   store_row<E, DP, VEC>((S*)a.dv.data + b * a.dv.sb + hk * a.dv.sh + (int64_t)j0 * a.dv.st, dv,
-                        some ? 1.0f : 0.0f, a.D, lane);
+                        some, 1.0f, a.D, lane);
 }
 
 template <class E, int DP, bool VEC>

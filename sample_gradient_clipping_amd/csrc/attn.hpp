@@ -81,10 +81,20 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voffset, 
                : "v"(voffset), "s"(rsrc), "s"(lds)
                : "memory");
 }
-// Until every load this wave has queued is there.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Until every load this wave has queued is there.  The builtin, not assembly: the
+// compiler has to know that its own loads are back too, or it waits for the next
+// tile's along with them at their first use in the loop.
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0) expcnt(7) lgkmcnt(15)
+  asm volatile("" ::: "memory");
+}
 // Until this wave's LDS reads are back: what they read may then be overwritten.
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // vmcnt(63) expcnt(7) lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
 __device__ __forceinline__ void tile_barrier() {
   wait_lds();
   __builtin_amdgcn_s_barrier();
@@ -156,13 +166,28 @@ __device__ __forceinline__ f32x16 mma(const Chunk<E>& x, const Chunk<E>& y, f32x
   }
 }
 
+// Where a lane's fragments lie in a tile: fragment g of row lane % 32 at row ^
+// (g << 5), the transposing reads of the 32-wide block db and row quarter r at
+// col ^ (db << 6 | r << 5), both plus whole rows (a row's bytes are a multiple of
+// what the exclusive ors touch).
+struct Places {
+  int row, col;
+};
+template <class E, int DP>
+__device__ __forceinline__ Places places(int lane) {
+  typedef Shape<E, DP> Sh;
+  const int h = lane >> 5, r = lane & 31, j = lane & 15, q = j >> 2;
+  Places p;
+  p.row = r * Sh::kRowBytes + 16 * (h ^ swz<Sh::kChunks>(r));
+  p.col = (4 * h + q) * Sh::kRowBytes + 8 * (j & 1) +
+          16 * ((2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) ^ swz<Sh::kChunks>(4 * h + q));
+  return p;
+}
+
 // Row fragment g of rows row0 + 0..31 of an LDS tile.
 template <class E, int DP>
-__device__ __forceinline__ Chunk<E> row_frag(const unsigned char* tile, int row0, int g, int lane) {
-  typedef Shape<E, DP> Sh;
-  const int r = lane & 31, h = lane >> 5;
-  const int c = (2 * g + h) ^ swz<Sh::kChunks>(r);
-  return *(const Chunk<E>*)(tile + (row0 + r) * Sh::kRowBytes + 16 * c);
+__device__ __forceinline__ Chunk<E> row_frag(const unsigned char* tile, int row0, int g, const Places& at) {
+  return *(const Chunk<E>*)(tile + (at.row ^ (g << 5)) + row0 * Shape<E, DP>::kRowBytes);
 }
 
 // The row fragments of one row in memory (this lane's), zeros where !live.
@@ -213,53 +238,85 @@ template <> struct Weights<F32> {
   __device__ __forceinline__ void set(const f32x16& x) { p = x; }
 };
 
-// acc += (rows row0 .. row0 + 31 of the tile, columns 32 db ..)^T times w.
+// acc += (rows row0 .. row0 + 31 of the tile, columns 32 db ..)^T times w, in
+// kColumnSteps products (bf16: two of 16 rows; float32: 16 of two).
+template <class E> struct ColumnSteps;
+template <> struct ColumnSteps<BF16> { static constexpr int kN = 2; };
+template <> struct ColumnSteps<F32> { static constexpr int kN = 16; };
+
+// The left operand of step s.
+template <class E> struct ColumnOf;
+template <> struct ColumnOf<BF16> { typedef u16x8 type; };
+template <> struct ColumnOf<F32> { typedef float type; };
+template <class E> using Column = typename ColumnOf<E>::type;
+
+template <class E, int DP>
+__device__ __forceinline__ Column<E> column_frag(const unsigned char* tile, int row0, int db, int s,
+                                                 const Places& at, int lane) {
+  typedef Shape<E, DP> Sh;
+  if constexpr (sizeof(typename E::storage) == 2) {
+    u16x4 part[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      part[r] = lds_read_tr16((const uint16_t*)(tile + (at.col ^ (db << 6 | r << 5)) +
+                                                (row0 + 16 * s + 8 * r) * Sh::kRowBytes));
+    return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  } else {
+    const int h = lane >> 5, d = 32 * db + (lane & 31), row = 8 * (s >> 2) + 4 * h + (s & 3);
+    const int chunk = (d >> 2) ^ swz<Sh::kChunks>(row);
+    return *(const float*)(tile + (row0 + row) * Sh::kRowBytes + 16 * chunk + 4 * (d & 3));
+  }
+}
+template <class E>
+__device__ __forceinline__ f32x16 mma_column(const Column<E>& x, const Weights<E>& w, int s, const f32x16& acc) {
+  if constexpr (sizeof(typename E::storage) == 2) return mfma_32x32x16(x, w.f[s], acc);
+  else return mfma_32x32x2(x, w.p[s], acc);
+}
 template <class E, int DP>
 __device__ __forceinline__ f32x16 mma_columns(const unsigned char* tile, int row0, int db,
-                                              const Weights<E>& w, f32x16 acc, int lane) {
-  typedef Shape<E, DP> Sh;
-  const int h = lane >> 5;
-  if constexpr (sizeof(typename E::storage) == 2) {
-    const int j = lane & 15, sub = (lane >> 4) & 1;
+                                              const Weights<E>& w, f32x16 acc, const Places& at, int lane) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u16x4 part[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 16 * s + 8 * r + 4 * h + (j >> 2);
-        const int chunk = (4 * db + 2 * sub + ((j & 3) >> 1)) ^ swz<Sh::kChunks>(row);
-        part[r] = lds_read_tr16((const uint16_t*)(tile + (row0 + row) * Sh::kRowBytes + 16 * chunk +
-                                                  8 * (j & 1)));
-      }
-      const u16x8 x = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
-      acc = mfma_32x32x16(x, w.f[s], acc);
-    }
-  } else {
-    const int d = 32 * db + (lane & 31);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int row = 8 * (j >> 2) + 4 * h + (j & 3);
-      const int chunk = (d >> 2) ^ swz<Sh::kChunks>(row);
-      acc = mfma_32x32x2(*(const float*)(tile + (row0 + row) * Sh::kRowBytes + 16 * chunk + 4 * (d & 3)),
-                         w.p[j], acc);
-    }
-  }
+  for (int s = 0; s < ColumnSteps<E>::kN; ++s)
+    acc = mma_column<E>(column_frag<E, DP>(tile, row0, db, s, at, lane), w, s, acc);
   return acc;
 }
 
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// The order the scheduler is asked for: instructions by kind.
+constexpr int kVector = 0x2, kMatrix = 0x8, kReads = 0x100;
+// N products, each with READS LDS reads of its operand, which are issued AHEAD
+// products early: a read takes longer than a product, and left alone the
+// compiler waits for each.
+template <int N, int READS, int AHEAD>
+__device__ __forceinline__ void feed() {
+  __builtin_amdgcn_sched_group_barrier(kReads, READS * AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
+    if (i < N - AHEAD) __builtin_amdgcn_sched_group_barrier(kReads, READS, 0);
+  }
+}
+
+// Keeps what follows in a branch of its own: where the compiler runs it always
+// and selects, a full tile pays for its mask (128 instructions of 370 per tile).
+__device__ __forceinline__ void apart() { asm volatile("; masked" ::); }
+
 // Stores this lane's columns of the transposed result (registers of block db:
-// entries 32 db + 8 (j / 4) + 4 half + j % 4 of the row) times f.
+// entries 32 db + 8 (j / 4) + 4 half + j % 4 of the row) times f, zeros where
+// !live, whatever the registers hold.
 template <class E, int DP, bool VEC>
-__device__ __forceinline__ void store_row(typename E::storage* row, const f32x16 (&acc)[DP / 32], float f,
-                                          int D, int lane) {
+__device__ __forceinline__ void store_row(typename E::storage* row, const f32x16 (&acc)[DP / 32], bool live,
+                                          float f, int D, int lane) {
   const int h = lane >> 5;
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int d = 32 * db + 8 * i + 4 * h;
-      const float x[4] = {acc[db][4 * i] * f, acc[db][4 * i + 1] * f, acc[db][4 * i + 2] * f,
-                          acc[db][4 * i + 3] * f};
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = live ? acc[db][4 * i + k] * f : 0.0f;
       if constexpr (VEC) {
         if (d < D) store_f32<E, 4>(row + d, x);
       } else {
