@@ -143,13 +143,11 @@ struct State {
 // exponentials of this one.  The order is written out, step by step between
 // fences, with every LDS operand read kAhead products early: left to itself the
 // compiler waits for each read, and puts all exponentials before all products.
-constexpr int kAhead = 4;
-
 template <class E, int DP, int KEYS>
-__device__ __forceinline__ void attend(const unsigned char* kt, const unsigned char* vt,
+__device__ __forceinline__ void attend(const Places& kt, const Places& vt,
                                        const Chunk<E> (&qf)[Shape<E, DP>::kG], State<E, DP>& st, float c,
                                        int k0, Span keys, bool full, const uint32_t (&live)[KEYS / 32],
-                                       const Places& at, int lane) {
+                                       int lane) {
   constexpr int NB = KEYS / 32, G = Shape<E, DP>::kG, DB = DP / 32, CS = ColumnSteps<E>::kN;
   const int h = lane >> 5;
   f32x16 s[2];
@@ -167,12 +165,12 @@ __device__ __forceinline__ void attend(const unsigned char* kt, const unsigned c
     Chunk<E> k[kAhead];
     f32x16 x = {};
 #pragma unroll
-    for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 32 * n, g, at);
+    for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 32 * n, g);
     fence();
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       x = mma<E>(k[g % kAhead], qf[g], x);
-      if (g + kAhead < G) k[g % kAhead] = row_frag<E, DP>(kt, 32 * n, g + kAhead, at);
+      if (g + kAhead < G) k[g % kAhead] = row_frag<E, DP>(kt, 32 * n, g + kAhead);
       if (n > 0) {
 #pragma unroll
         for (int j = 16 * g / G; j < 16 * (g + 1) / G; ++j) exponential(n - 1, j);
@@ -185,7 +183,7 @@ __device__ __forceinline__ void attend(const unsigned char* kt, const unsigned c
   const auto outputs = [&](int n, bool more) {
     constexpr int N = DB * CS;
     Column<E> v[kAhead];
-    const auto read = [&](int t) { return column_frag<E, DP>(vt, 32 * n, t % DB, t / DB, at, lane); };
+    const auto read = [&](int t) { return column_frag<E, DP>(vt, 32 * n, t % DB, t / DB, lane); };
 #pragma unroll
     for (int t = 0; t < kAhead; ++t) v[t] = read(t);
     fence();
@@ -262,7 +260,7 @@ attention_kernel(AttnArgs a) {
   typedef typename E::storage S;
   constexpr int KEYS = KeysOf<E>::kKeys;
   constexpr int kTile = KEYS * Sh::kRowBytes;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][K, V] tiles
+  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [2][K, V] tiles
   __shared__ int bound[2][kWaves];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int tiles = (a.Tq + kQ - 1) / kQ;
@@ -321,7 +319,9 @@ attention_kernel(AttnArgs a) {
       }
       if (k0 < wend && k0 + KEYS > wlo) {
         const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
-        attend<E, DP, KEYS>(here, here + kTile, qf, st, c, k0, keys, full, live, at, lane);
+        const uint32_t base = lds_addr(here);
+        attend<E, DP, KEYS>(in_tile(at, base), in_tile(at, base + kTile), qf, st, c, k0, keys, full, live,
+                            lane);
       }
 #pragma unroll
       for (int n = 0; n < KEYS / 32; ++n) live[n] = next[n];
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
   typedef typename E::storage S;
   constexpr int NW = FewOf<E>::kWaves, KEYS = kFewKeys;
   constexpr int kTile = KEYS * Sh::kRowBytes;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [wave][2][K, V], then joins
+  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [wave][2][K, V], then joins
   __shared__ float ms[NW][32], ls[NW][32];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int split = blockIdx.x % a.splits, head = blockIdx.x / a.splits;
@@ -398,7 +398,9 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
       __builtin_amdgcn_wave_barrier();
       if (k0 + step < end) fetch(k0 + step, mine + (buf ^ 1) * 2 * kTile);
       const bool full = k0 >= full_lo && k0 + KEYS <= full_end && live[0] == ~0u;
-      attend<E, DP, KEYS>(here, here + kTile, qf, st, c, k0, keys, full, live, at, lane);
+      const uint32_t base = lds_addr(here);
+      attend<E, DP, KEYS>(in_tile(at, base), in_tile(at, base + kTile), qf, st, c, k0, keys, full, live,
+                          lane);
       live[0] = next[0];
     }
   }

@@ -26,7 +26,7 @@ constexpr int kWaves = 4;
 constexpr int kNT = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;      // queries (keys) of a workgroup
 
-template <class E> struct StepOf;       // keys (queries) of a tile
+template <class E> struct StepOf;       // keys of a tile
 template <> struct StepOf<BF16> { static constexpr int kN = 64; };
 template <> struct StepOf<F32> { static constexpr int kN = 32; };
 
@@ -41,7 +41,7 @@ attention_dq_kernel(AttnArgs a) {
   typedef typename E::storage S;
   constexpr int KEYS = StepOf<E>::kN;
   constexpr int kTile = KEYS * Sh::kRowBytes;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][K, V] tiles
+  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [2][K, V] tiles
   __shared__ int bound[2][kWaves];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   const int tiles = (a.Tq + kRows - 1) / kRows;
@@ -94,14 +94,12 @@ attention_dq_kernel(AttnArgs a) {
     delta += lane_xor(delta, 32);
     row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
-    const float lse = some ? a.lse[at] * kLog2e : 0.0f;
+    const float base = some ? -a.lse[at] / a.scale : 0.0f;
     if (valid && h == 0) a.delta[at] = delta;
     const float c = a.scale * kLog2e;
     const Places pl = places<E, DP>(lane);
     int buf = 0;
     for (; k0 < end; k0 += KEYS, buf ^= 1) {
-      const unsigned char* kt = smem + buf * 2 * kTile;
-      const unsigned char* vt = kt + kTile;
       unsigned char* there = smem + (buf ^ 1) * 2 * kTile;
       if constexpr (VEC) wait_loads();
       tile_barrier();        // this tile is there; the other one has been read
@@ -112,32 +110,91 @@ attention_dq_kernel(AttnArgs a) {
       }
       if (k0 < wend && k0 + KEYS > wlo) {
         const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
+        const uint32_t here = lds_addr(smem) + buf * 2 * kTile;
+        // S starts from -lse / scale and dO V^T from -delta: P = 2^(c S), dS = P dP
+        const auto start = [&](f32x16& s, f32x16& dp) {
 #pragma unroll
-        for (int n = 0; n < KEYS / 32; ++n) {
-          f32x16 s = {}, ds = {};
+          for (int j = 0; j < 16; ++j) {
+            s[j] = base;
+            dp[j] = -delta;
+          }
+        };
+        const auto mask = [&](int n, f32x16& s) {
+          if (full) return;
+          apart();
+          const uint32_t w = lone ? 0u : (n == 0 ? live[0] : live[KEYS / 32 - 1]) >> (4 * h);
+          const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
 #pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(kt, 32 * n, g, pl), qf[g], s);
+          for (int j = 0; j < 16; ++j) {
+            const int r = 8 * (j >> 2) + (j & 3);
+            const bool in = r >= first && r < past && ((w >> r) & 1);
+            s[j] = in ? s[j] : -INFINITY;
+          }
+        };
+        if constexpr (sizeof(S) == 2) {
+          // per block of 32 keys G products for S, G for dP with the exponentials
+          // between them, 2 DB for dq; operands read kAhead products early
+          constexpr int G = Sh::kG, DB = Sh::kDB, T = 2 * G + 2 * DB;
+#pragma unroll 1
+          for (int n = 0; n < KEYS / 32; ++n) {
+            const Places kt = in_tile(pl, here + n * 32 * Sh::kRowBytes);
+            const Places vt = in_tile(pl, here + kTile + n * 32 * Sh::kRowBytes);
+            const auto operand = [&](int t) -> u16x8 {
+              if (t < G) return row_frag<E, DP>(kt, 0, t);
+              if (t < 2 * G) return row_frag<E, DP>(vt, 0, t - G);
+              return column_frag<E, DP>(kt, 0, (t - 2 * G) % DB, (t - 2 * G) / DB, lane);
+            };
+            u16x8 x[kAhead];
+            f32x16 s, dp;
+            Weights<E> w;
+            start(s, dp);
 #pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(vt, 32 * n, g, pl), gf[g], ds);
+            for (int t = 0; t < kAhead; ++t) x[t] = operand(t);
+            fence();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            ds[j] = __builtin_amdgcn_exp2f(fmaf(s[j], c, -lse)) * (ds[j] - delta);
-          if (!full) {
-            apart();
-            const uint32_t w = live[n] >> (4 * h);
-            const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
+            for (int t = 0; t < T; ++t) {
+              const u16x8 y = x[t % kAhead];
+              if (t < G) s = mma<E>(y, qf[t], s);
+              else if (t < 2 * G) dp = mma<E>(y, gf[t - G], dp);
+              else dq[(t - 2 * G) % DB] = mma_column<E>(y, w, (t - 2 * G) / DB, dq[(t - 2 * G) % DB]);
+              if (t + kAhead < T) x[t % kAhead] = operand(t + kAhead);
+              if (t >= G && t < 2 * G) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int r = 8 * (j >> 2) + (j & 3);
-              const bool in = r >= first && r < past && ((w >> r) & 1) && !lone;
-              ds[j] = in ? ds[j] : 0.0f;
+                for (int j = 16 * (t - G) / G; j < 16 * (t - G + 1) / G; ++j) {
+                  float e = __builtin_amdgcn_exp2f(s[j] * c);
+                  asm volatile("" : "+v"(e));
+                  s[j] = e;
+                }
+              }
+              fence();
+              if (t == G - 1) mask(n, s);
+              if (t == 2 * G - 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) dp[j] *= s[j];
+                w.set(dp);
+              }
             }
           }
-          Weights<E> wt;
-          wt.set(ds);
+        } else {
 #pragma unroll
-          for (int db = 0; db < Sh::kDB; ++db)
-            dq[db] = mma_columns<E, DP>(kt, 32 * n, db, wt, dq[db], pl, lane);
+          for (int n = 0; n < KEYS / 32; ++n) {
+            const Places kt = in_tile(pl, here + n * 32 * Sh::kRowBytes);
+            const Places vt = in_tile(pl, here + kTile + n * 32 * Sh::kRowBytes);
+            f32x16 s, dp;
+            start(s, dp);
+#pragma unroll
+            for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(kt, 0, g), qf[g], s);
+#pragma unroll
+            for (int g = 0; g < Sh::kG; ++g) dp = mma<E>(row_frag<E, DP>(vt, 0, g), gf[g], dp);
+            mask(n, s);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dp[j] *= __builtin_amdgcn_exp2f(s[j] * c);
+            Weights<E> w;
+            w.set(dp);
+#pragma unroll
+            for (int db = 0; db < Sh::kDB; ++db)
+              dq[db] = mma_columns<E, DP>(kt, 0, db, w, dq[db], lane);
+          }
         }
       }
 #pragma unroll
@@ -152,17 +209,30 @@ attention_dq_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// dk and dv: each wave 32 keys (its lanes), whose rows of K and V it holds in
-// registers; tiles of queries and of their output gradients go through LDS, for
-// each head of the group in turn.
+// dk and dv: each wave 32 keys (its lanes), whose rows of K it holds in registers,
+// and of V in registers (heads of 64) or LDS (heads of 128, whose sums take 128
+// registers: a wave with both in registers would have its SIMD alone, and nothing
+// to overlap its exponentials with); tiles of queries and of their output
+// gradients go through LDS, for each head of the group in turn.
 // ---------------------------------------------------------------------------
+template <class E, int DP>
+struct Dkv {
+  static constexpr int kN = sizeof(typename E::storage) == 2 && DP == 64 ? 64 : 32;   // queries of a tile
+  static constexpr bool kValuesInLds = DP == 128;
+  static constexpr int kValues = kValuesInLds ? kRows * Shape<E, DP>::kRowBytes : 0;
+  static constexpr int kLds = kValues + 4 * kN * Shape<E, DP>::kRowBytes;
+};
+
 template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 ? 2 : 1) void
+attention_dkv_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
-  constexpr int N = StepOf<E>::kN;
+  typedef Dkv<E, DP> Z;
+  constexpr int N = Z::kN;
   constexpr int kTile = N * Sh::kRowBytes;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [2][Q, dO] tiles
+  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char shared_tiles[];   // V, [2][Q, dO]
+  unsigned char* const smem = shared_tiles + Z::kValues;
   __shared__ int bound[2][kWaves];
   __shared__ __attribute__((aligned(16))) float row_lse[2][N], row_delta[2][N];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
@@ -201,11 +271,26 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
     const int p_first = lo / N * N, steps = (end - p_first + N - 1) / N;
     const float c = a.scale * kLog2e;
     const Places pl = places<E, DP>(lane);
-    Chunk<E> kf[Sh::kG], vf[Sh::kG];
+    Chunk<E> kf[Sh::kG], vf[Z::kValuesInLds ? 1 : Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.k.data + b * a.k.sb + hk * a.k.sh + (int64_t)j0 * a.k.st, some,
                                a.D, lane, kf);
-    row_frags_from<E, DP, VEC>((const S*)a.v.data + b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st, some,
-                               a.D, lane, vf);
+    if constexpr (Z::kValuesInLds) {
+      // what an inactive key's row holds reaches nothing but its own sums, which
+      // are not used
+#pragma unroll
+      for (int r = 0; r < kRows; r += 64)
+        load_tile<E, DP, 64, kWaves, VEC>(shared_tiles + r * Sh::kRowBytes, a.v, b * a.v.sb + hk * a.v.sh,
+                                          tile * kRows + r, a.Tk, a.D, ~0ull, wave, lane);
+    } else {
+      row_frags_from<E, DP, VEC>((const S*)a.v.data + b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st,
+                                 some, a.D, lane, vf);
+    }
+    const float inv_scale = -1.0f / a.scale;
+    const Places values = in_tile(pl, lds_addr(shared_tiles) + 32 * wave * Sh::kRowBytes);
+    const auto value_frag = [&](int g) {
+      if constexpr (Z::kValuesInLds) return row_frag<E, DP>(values, 0, g);
+      else return vf[g];
+    };
     uint32_t live[N / 32], next[N / 32];
     float value = 0.0f;                   // of the next tile's lse (threads 0 ..) or delta (64 ..)
     const int row = threadIdx.x & 63;
@@ -217,9 +302,9 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
                                        b * a.dout.sb + hq * a.dout.sh, p0 - off, a.Tq, a.D, m, wave, lane);
       const int i = p0 - off + row;
       value = 0.0f;
-      if (wave < 2 && row < N && i >= 0 && i < a.Tq) {
+      if (wave < 2 && row < N && i >= 0 && i < a.Tq && ((m >> row) & 1)) {
         const int64_t e = ((int64_t)b * a.Hq + hq) * a.Tq + i;
-        value = wave == 0 ? a.lse[e] * kLog2e : a.delta[e];
+        value = wave == 0 ? a.lse[e] * inv_scale : -a.delta[e];
       }
     };
     const auto keep = [&](int buf) {
@@ -241,47 +326,119 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
       const bool more = it + 1 < steps * group;
       if (more) fetch(p1, hq1, buf ^ 1);
       if (p0 < wend && p0 + N > wlo) {
-        const unsigned char* qt = smem + buf * 2 * kTile;
-        const unsigned char* gt = qt + kTile;
+        const uint32_t here = lds_addr(smem) + buf * 2 * kTile;
+        const Places qt = in_tile(pl, here), gt = in_tile(pl, here + kTile);
         const bool full = p0 >= full_lo && p0 + N <= full_end && all_live<N>(live);
-#pragma unroll
-        for (int n = 0; n < N / 32; ++n) {
-          f32x16 s = {}, ds = {};
-#pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(qt, 32 * n, g, pl), kf[g], s);
-#pragma unroll
-          for (int g = 0; g < Sh::kG; ++g) ds = mma<E>(row_frag<E, DP>(gt, 32 * n, g, pl), vf[g], ds);
+// S starts from -lse / scale and dO V^T from -delta: P = 2^(c S), dS = P dP
+        const auto start = [&](const float* from_rows, int n, f32x16& x) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const f32x4 l4 = *(const f32x4*)&row_lse[buf][32 * n + 8 * q + 4 * h];
-            const f32x4 d4 = *(const f32x4*)&row_delta[buf][32 * n + 8 * q + 4 * h];
+            const f32x4 y = *(const f32x4*)&from_rows[32 * n + 8 * q + 4 * h];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int j = 4 * q + k;
-              s[j] = __builtin_amdgcn_exp2f(fmaf(s[j], c, -l4[k]));
-              ds[j] = s[j] * (ds[j] - d4[k]);
+            for (int k = 0; k < 4; ++k) x[4 * q + k] = y[k];
+          }
+        };
+        const auto mask = [&](int n, f32x16& s) {
+          if (full) return;
+          apart();
+          const uint32_t w = live[n] >> (4 * h);
+          const int base = p0 + 32 * n + 4 * h, first = from - base, stop = past - base;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int r = 8 * (j >> 2) + (j & 3);
+            const bool in = r >= first && r < stop && ((w >> r) & 1);
+            s[j] = in ? s[j] : -INFINITY;
+          }
+        };
+        // position j0's only key is j0: dS = 0
+        const auto alone = [&](int n, f32x16& dp) {
+          if (full) return;
+          apart();
+          const int self = lone ? j0 - (p0 + 32 * n + 4 * h) : -1;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) dp[j] = 8 * (j >> 2) + (j & 3) == self ? 0.0f : dp[j];
+        };
+        if constexpr (sizeof(S) == 2) {
+          // per block of 32 queries G products for S, G for dP with the
+          // exponentials between them, 2 DB for dv with dS between them, 2 DB for
+          // dk; operands read kAhead products early
+          constexpr int G = Sh::kG, DB = Sh::kDB, T = 2 * G + 4 * DB;
+#pragma unroll
+          for (int n = 0; n < N / 32; ++n) {
+            const auto operand = [&](int t) -> u16x8 {
+              if (t < G) return row_frag<E, DP>(qt, 32 * n, t);
+              if (t < 2 * G) return row_frag<E, DP>(gt, 32 * n, t - G);
+              const int u = (t - 2 * G) % (2 * DB);
+              return column_frag<E, DP>(t < 2 * G + 2 * DB ? gt : qt, 32 * n, u % DB, u / DB, lane);
+            };
+            u16x8 x[kAhead], v[2];
+            f32x16 s, dp;
+            Weights<E> pw, dw;
+            start(row_lse[buf], n, s);
+#pragma unroll
+            for (int t = 0; t < kAhead; ++t) x[t] = operand(t);
+            fence();
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+              const u16x8 y = x[t % kAhead];
+              const int u = (t - 2 * G) % (2 * DB), db = u % DB, half = u / DB;
+              if (t < G) s = mma<E>(y, kf[t], s);
+              else if (t < 2 * G) dp = mma<E>(y, v[t % 2], dp);
+              else if (t < 2 * G + 2 * DB) dv[db] = mma_column<E>(y, pw, half, dv[db]);
+              else dk[db] = mma_column<E>(y, dw, half, dk[db]);
+              if (t + kAhead < T) x[t % kAhead] = operand(t + kAhead);
+              if (t + 2 >= G && t + 2 < 2 * G) v[t % 2] = value_frag(t + 2 - G);
+              if (t == G - 2) start(row_delta[buf], n, dp);
+              if (t >= G && t < 2 * G) {
+#pragma unroll
+                for (int j = 16 * (t - G) / G; j < 16 * (t - G + 1) / G; ++j) {
+                  float e = __builtin_amdgcn_exp2f(s[j] * c);
+                  asm volatile("" : "+v"(e));
+                  s[j] = e;
+                }
+              }
+              if (t >= 2 * G && t < 2 * G + 2 * DB) {
+#pragma unroll
+                for (int j = 16 * u / (2 * DB); j < 16 * (u + 1) / (2 * DB); ++j) {
+                  float e = dp[j] * s[j];
+                  asm volatile("" : "+v"(e));
+                  dp[j] = e;
+                }
+              }
+              fence();
+              if (t == G - 1) mask(n, s);
+              if (t == 2 * G - 1) {
+                alone(n, dp);
+                pw.set(s);
+              }
+              if (t == 2 * G + 2 * DB - 1) dw.set(dp);
             }
           }
-          if (!full) {
-            apart();
-            const uint32_t w = live[n] >> (4 * h);
-            const int base = p0 + 32 * n + 4 * h;
-            const int first = from - base, stop = past - base, self = lone ? j0 - base : -1;
+        } else {
+#pragma unroll
+          for (int n = 0; n < N / 32; ++n) {
+            f32x16 s, dp;
+            start(row_lse[buf], n, s);
+            start(row_delta[buf], n, dp);
+#pragma unroll
+            for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(qt, 32 * n, g), kf[g], s);
+#pragma unroll
+            for (int g = 0; g < Sh::kG; ++g) dp = mma<E>(row_frag<E, DP>(gt, 32 * n, g), value_frag(g), dp);
+            mask(n, s);
+            alone(n, dp);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int r = 8 * (j >> 2) + (j & 3);
-              const bool in = r >= first && r < stop && ((w >> r) & 1);
-              s[j] = in ? s[j] : 0.0f;
-              ds[j] = in && r != self ? ds[j] : 0.0f;
+              s[j] = __builtin_amdgcn_exp2f(s[j] * c);
+              dp[j] *= s[j];
             }
-          }
-          Weights<E> pw, dw;
-          pw.set(s);
-          dw.set(ds);
+            Weights<E> pw, dw;
+            pw.set(s);
+            dw.set(dp);
 #pragma unroll
-          for (int db = 0; db < Sh::kDB; ++db) {
-            dv[db] = mma_columns<E, DP>(gt, 32 * n, db, pw, dv[db], pl, lane);
-            dk[db] = mma_columns<E, DP>(qt, 32 * n, db, dw, dk[db], pl, lane);
+            for (int db = 0; db < Sh::kDB; ++db) {
+              dv[db] = mma_columns<E, DP>(gt, 32 * n, db, pw, dv[db], lane);
+              dk[db] = mma_columns<E, DP>(qt, 32 * n, db, dw, dk[db], lane);
+            }
           }
         }
       }
@@ -300,12 +457,12 @@ __global__ __launch_bounds__(kNT, 1) void attention_dkv_kernel(AttnArgs a) {
 template <class E, int DP, bool VEC>
 hipError_t backward(const AttnArgs& a, hipStream_t s) {
   typedef Shape<E, DP> Sh;
-  constexpr int lds = 4 * StepOf<E>::kN * Sh::kRowBytes;
+  constexpr int lds = 4 * StepOf<E>::kN * Sh::kRowBytes, dkv_lds = Dkv<E, DP>::kLds;
   static hipError_t once[2] = {
       hipFuncSetAttribute((const void*)attention_dq_kernel<E, DP, VEC>,
                           hipFuncAttributeMaxDynamicSharedMemorySize, lds),
       hipFuncSetAttribute((const void*)attention_dkv_kernel<E, DP, VEC>,
-                          hipFuncAttributeMaxDynamicSharedMemorySize, lds)};
+                          hipFuncAttributeMaxDynamicSharedMemorySize, dkv_lds)};
   if (once[0] != hipSuccess) return once[0];
   if (once[1] != hipSuccess) return once[1];
   const int64_t qt = (a.Tq + kRows - 1) / kRows, kt = (a.Tk + kRows - 1) / kRows;
@@ -314,7 +471,7 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((attention_dq_kernel<E, DP, VEC>), dim3((unsigned)(qh * qt)), dim3(kNT), lds, s, a);
   timing_end("attention_dq", s);
   timing_begin("attention_dkv", s);
-  hipLaunchKernelGGL((attention_dkv_kernel<E, DP, VEC>), dim3((unsigned)(kh * kt)), dim3(kNT), lds, s, a);
+  hipLaunchKernelGGL((attention_dkv_kernel<E, DP, VEC>), dim3((unsigned)(kh * kt)), dim3(kNT), dkv_lds, s, a);
   timing_end("attention_dkv", s);
   return hipGetLastError();
 }

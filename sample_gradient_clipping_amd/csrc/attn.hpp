@@ -166,12 +166,13 @@ __device__ __forceinline__ f32x16 mma(const Chunk<E>& x, const Chunk<E>& y, f32x
   }
 }
 
-// Where a lane's fragments lie in a tile: fragment g of row lane % 32 at row ^
-// (g << 5), the transposing reads of the 32-wide block db and row quarter r at
-// col ^ (db << 6 | r << 5), both plus whole rows (a row's bytes are a multiple of
-// what the exclusive ors touch).
+// Where a lane's fragments lie in a tile at LDS address `tile` (a multiple of
+// kTileAlign): fragment g of row lane % 32 at row ^ (g << 5), the transposing reads
+// of the 32-wide block db and row quarter r at col ^ (db << 6 | r << 5), both plus
+// whole rows (of at least as many bytes as the exclusive ors touch).
+constexpr int kTileAlign = 512;
 struct Places {
-  int row, col;
+  uint32_t row, col;
 };
 template <class E, int DP>
 __device__ __forceinline__ Places places(int lane) {
@@ -183,11 +184,24 @@ __device__ __forceinline__ Places places(int lane) {
           16 * ((2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) ^ swz<Sh::kChunks>(4 * h + q));
   return p;
 }
+// The places of a tile, not derived from those of others: the addresses are then
+// formed where they are used (one exclusive or each) instead of being kept in
+// registers for every tile.
+__device__ __forceinline__ Places in_tile(const Places& p, uint32_t tile) {
+  Places x{p.row + tile, p.col + tile};
+  asm volatile("" : "+v"(x.row), "+v"(x.col));
+  return x;
+}
+
+template <class T>
+__device__ __forceinline__ T lds_at(uint32_t at) {
+  return *(const __attribute__((address_space(3))) T*)(uintptr_t)at;
+}
 
 // Row fragment g of rows row0 + 0..31 of an LDS tile.
 template <class E, int DP>
-__device__ __forceinline__ Chunk<E> row_frag(const unsigned char* tile, int row0, int g, const Places& at) {
-  return *(const Chunk<E>*)(tile + (at.row ^ (g << 5)) + row0 * Shape<E, DP>::kRowBytes);
+__device__ __forceinline__ Chunk<E> row_frag(const Places& at, int row0, int g) {
+  return lds_at<Chunk<E>>((at.row ^ (g << 5)) + row0 * Shape<E, DP>::kRowBytes);
 }
 
 // The row fragments of one row in memory (this lane's), zeros where !live.
@@ -251,20 +265,21 @@ template <> struct ColumnOf<F32> { typedef float type; };
 template <class E> using Column = typename ColumnOf<E>::type;
 
 template <class E, int DP>
-__device__ __forceinline__ Column<E> column_frag(const unsigned char* tile, int row0, int db, int s,
-                                                 const Places& at, int lane) {
+__device__ __forceinline__ Column<E> column_frag(const Places& at, int row0, int db, int s, int lane) {
   typedef Shape<E, DP> Sh;
   if constexpr (sizeof(typename E::storage) == 2) {
     u16x4 part[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
-      part[r] = lds_read_tr16((const uint16_t*)(tile + (at.col ^ (db << 6 | r << 5)) +
-                                                (row0 + 16 * s + 8 * r) * Sh::kRowBytes));
+      part[r] = __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(uintptr_t)(
+          (at.col ^ (db << 6 | r << 5)) + (row0 + 16 * s + 8 * r) * Sh::kRowBytes)));
     return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
+    // col is made for the transposing reads: its row and its chunk differ here
     const int h = lane >> 5, d = 32 * db + (lane & 31), row = 8 * (s >> 2) + 4 * h + (s & 3);
     const int chunk = (d >> 2) ^ swz<Sh::kChunks>(row);
-    return *(const float*)(tile + (row0 + row) * Sh::kRowBytes + 16 * chunk + 4 * (d & 3));
+    const uint32_t tile = at.row - places<E, DP>(lane).row;
+    return lds_at<float>(tile + (row0 + row) * Sh::kRowBytes + 16 * chunk + 4 * (d & 3));
   }
 }
 template <class E>
@@ -273,30 +288,19 @@ __device__ __forceinline__ f32x16 mma_column(const Column<E>& x, const Weights<E
   else return mfma_32x32x2(x, w.p[s], acc);
 }
 template <class E, int DP>
-__device__ __forceinline__ f32x16 mma_columns(const unsigned char* tile, int row0, int db,
-                                              const Weights<E>& w, f32x16 acc, const Places& at, int lane) {
+__device__ __forceinline__ f32x16 mma_columns(const Places& at, int row0, int db, const Weights<E>& w,
+                                              f32x16 acc, int lane) {
 #pragma unroll
   for (int s = 0; s < ColumnSteps<E>::kN; ++s)
-    acc = mma_column<E>(column_frag<E, DP>(tile, row0, db, s, at, lane), w, s, acc);
+    acc = mma_column<E>(column_frag<E, DP>(at, row0, db, s, lane), w, s, acc);
   return acc;
 }
 
-__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+// Products that an operand is read ahead of its own: an LDS read takes longer than
+// a product.
+constexpr int kAhead = 4;
 
-// The order the scheduler is asked for: instructions by kind.
-constexpr int kVector = 0x2, kMatrix = 0x8, kReads = 0x100;
-// N products, each with READS LDS reads of its operand, which are issued AHEAD
-// products early: a read takes longer than a product, and left alone the
-// compiler waits for each.
-template <int N, int READS, int AHEAD>
-__device__ __forceinline__ void feed() {
-  __builtin_amdgcn_sched_group_barrier(kReads, READS * AHEAD, 0);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
-    if (i < N - AHEAD) __builtin_amdgcn_sched_group_barrier(kReads, READS, 0);
-  }
-}
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // Keeps what follows in a branch of its own: where the compiler runs it always
 // and selects, a full tile pays for its mask (128 instructions of 370 per tile).
