@@ -14,7 +14,8 @@
 // accumulator's registers, the right operand of O^T = V^T P^T (with the rows of
 // V read in the accumulator's order by the transposing LDS reads).  The
 // exponentials are rounded to bf16 for that product (what its operand type
-// holds); the sum of them, the maximum and the output stay in float32.
+// holds); their sum is that of the unrounded ones (lse is float32), and it, the
+// maximum and the output stay in float32.
 #include "attn.hpp"
 
 #include <algorithm>
@@ -299,8 +300,9 @@ attention_kernel(AttnArgs a) {
     uint32_t live[KEYS / 32], next[KEYS / 32];
     int k0 = lo / KEYS * KEYS;
     uint64_t m = live_keys<KEYS>(a, b, k0, live);
-    load_tile<E, DP, KEYS, kWaves, VEC>(smem, a.k, kat, k0, a.Tk, a.D, m, wave, lane);
-    load_tile<E, DP, KEYS, kWaves, VEC>(smem + kTile, a.v, vat, k0, a.Tk, a.D, m, wave, lane);
+    const Loader<E, DP, KEYS, kWaves, VEC> load_k(a.k, a.D, wave, lane), load_v(a.v, a.D, wave, lane);
+    load_k(smem, a.k, kat, k0, a.Tk, m);
+    load_v(smem + kTile, a.v, vat, k0, a.Tk, m);
     Chunk<E> qf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
@@ -314,8 +316,8 @@ attention_kernel(AttnArgs a) {
       tile_barrier();        // this tile is there; the other one has been read
       if (k0 + KEYS < end) {
         m = live_keys<KEYS>(a, b, k0 + KEYS, next);
-        load_tile<E, DP, KEYS, kWaves, VEC>(there, a.k, kat, k0 + KEYS, a.Tk, a.D, m, wave, lane);
-        load_tile<E, DP, KEYS, kWaves, VEC>(there + kTile, a.v, vat, k0 + KEYS, a.Tk, a.D, m, wave, lane);
+        load_k(there, a.k, kat, k0 + KEYS, a.Tk, m);
+        load_v(there + kTile, a.v, vat, k0 + KEYS, a.Tk, m);
       }
       if (k0 < wend && k0 + KEYS > wlo) {
         const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
@@ -378,10 +380,11 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
     const int step = a.splits * NW * KEYS;
     int k0 = lo / KEYS * KEYS + (split * NW + wave) * KEYS;
     uint32_t live[1] = {}, next[1] = {};
+    const Loader<E, DP, KEYS, 1, VEC> load_k(a.k, a.D, 0, lane), load_v(a.v, a.D, 0, lane);
     const auto fetch = [&](int at, unsigned char* to) {
       const uint64_t m = live_keys<KEYS>(a, b, at, next);
-      load_tile<E, DP, KEYS, 1, VEC>(to, a.k, kat, at, a.Tk, a.D, m, 0, lane);
-      load_tile<E, DP, KEYS, 1, VEC>(to + kTile, a.v, vat, at, a.Tk, a.D, m, 0, lane);
+      load_k(to, a.k, kat, at, a.Tk, m);
+      load_v(to + kTile, a.v, vat, at, a.Tk, m);
     };
     if (k0 < end) fetch(k0, mine);
     live[0] = next[0];

@@ -78,8 +78,9 @@ attention_dq_kernel(AttnArgs a) {
     uint32_t live[KEYS / 32], next[KEYS / 32];
     int k0 = lo / KEYS * KEYS;
     uint64_t m = live_keys<KEYS>(a, b, k0, live);
-    load_tile<E, DP, KEYS, kWaves, VEC>(smem, a.k, kat, k0, a.Tk, a.D, m, wave, lane);
-    load_tile<E, DP, KEYS, kWaves, VEC>(smem + kTile, a.v, vat, k0, a.Tk, a.D, m, wave, lane);
+    const Loader<E, DP, KEYS, kWaves, VEC> load_k(a.k, a.D, wave, lane), load_v(a.v, a.D, wave, lane);
+    load_k(smem, a.k, kat, k0, a.Tk, m);
+    load_v(smem + kTile, a.v, vat, k0, a.Tk, m);
     Chunk<E> qf[Sh::kG], gf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.o.data + b * a.o.sb + hq * a.o.sh + (int64_t)i * a.o.st, some,
                                a.D, lane, qf);
@@ -105,8 +106,8 @@ attention_dq_kernel(AttnArgs a) {
       tile_barrier();        // this tile is there; the other one has been read
       if (k0 + KEYS < end) {
         m = live_keys<KEYS>(a, b, k0 + KEYS, next);
-        load_tile<E, DP, KEYS, kWaves, VEC>(there, a.k, kat, k0 + KEYS, a.Tk, a.D, m, wave, lane);
-        load_tile<E, DP, KEYS, kWaves, VEC>(there + kTile, a.v, vat, k0 + KEYS, a.Tk, a.D, m, wave, lane);
+        load_k(there, a.k, kat, k0 + KEYS, a.Tk, m);
+        load_v(there + kTile, a.v, vat, k0 + KEYS, a.Tk, m);
       }
       if (k0 < wend && k0 + KEYS > wlo) {
         const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
@@ -277,10 +278,10 @@ attention_dkv_kernel(AttnArgs a) {
     if constexpr (Z::kValuesInLds) {
       // what an inactive key's row holds reaches nothing but its own sums, which
       // are not used
+      const Loader<E, DP, 64, kWaves, VEC> load_v(a.v, a.D, wave, lane);
 #pragma unroll
       for (int r = 0; r < kRows; r += 64)
-        load_tile<E, DP, 64, kWaves, VEC>(shared_tiles + r * Sh::kRowBytes, a.v, b * a.v.sb + hk * a.v.sh,
-                                          tile * kRows + r, a.Tk, a.D, ~0ull, wave, lane);
+        load_v(shared_tiles + r * Sh::kRowBytes, a.v, b * a.v.sb + hk * a.v.sh, tile * kRows + r, a.Tk, ~0ull);
     } else {
       row_frags_from<E, DP, VEC>((const S*)a.v.data + b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st,
                                  some, a.D, lane, vf);
@@ -294,12 +295,12 @@ attention_dkv_kernel(AttnArgs a) {
     uint32_t live[N / 32], next[N / 32];
     float value = 0.0f;                   // of the next tile's lse (threads 0 ..) or delta (64 ..)
     const int row = threadIdx.x & 63;
+    const Loader<E, DP, N, kWaves, VEC> load_q(a.q, a.D, wave, lane), load_g(a.dout, a.D, wave, lane);
     const auto fetch = [&](int p0, int hq, int buf) {
-      const uint64_t m = live_keys<N>(a, b, p0, next);
-      load_tile<E, DP, N, kWaves, VEC>(smem + buf * 2 * kTile, a.q, b * a.q.sb + hq * a.q.sh, p0 - off,
-                                       a.Tq, a.D, m, wave, lane);
-      load_tile<E, DP, N, kWaves, VEC>(smem + buf * 2 * kTile + kTile, a.dout,
-                                       b * a.dout.sb + hq * a.dout.sh, p0 - off, a.Tq, a.D, m, wave, lane);
+      uint64_t m = live_keys<N>(a, b, p0, next);
+      if (p0 < off) m &= ~0ull << (off - p0);        // no queries at these positions
+      load_q(smem + buf * 2 * kTile, a.q, b * a.q.sb + hq * a.q.sh, p0 - off, a.Tq, m);
+      load_g(smem + buf * 2 * kTile + kTile, a.dout, b * a.dout.sb + hq * a.dout.sh, p0 - off, a.Tq, m);
       const int i = p0 - off + row;
       value = 0.0f;
       if (wave < 2 && row < N && i >= 0 && i < a.Tq && ((m >> row) & 1)) {

@@ -2,6 +2,8 @@
 // attention_bwd.hip).
 #pragma once
 
+#include <type_traits>
+
 #include "lm.hpp"
 
 namespace dpf {
@@ -73,13 +75,14 @@ __device__ __forceinline__ int swz(int row) {
   else return ((row & 3) << 2) | ((row >> 2) & 3);
 }
 
-// 16 bytes per lane from rsrc at voffset straight into LDS at lds + 16 * lane;
+// 16 bytes per lane from rsrc at voffset straight into LDS at lds + at + 16 * lane;
 // awaited with wait_loads.
+template <int AT>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voffset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                :
-               : "v"(voffset), "s"(rsrc), "s"(lds)
-               : "memory");
+               : "v"(voffset), "s"(rsrc), "s"(lds), "n"(AT)
+               : "memory", "scc");
 }
 // Until every load this wave has queued is there.  The builtin, not assembly: the
 // compiler has to know that its own loads are back too, or it waits for the next
@@ -107,45 +110,71 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// One head's rows [row0, row0 + ROWS) of `rows` into an LDS tile by NW waves
-// (wave w of them); rows outside [0, rows) and those whose bit of `live` is 0
-// become zeros, and so does what lies past D.  VEC: direct loads to LDS, in
-// flight until wait_loads; else element by element, there after a barrier.
-template <class E, int DP, int ROWS, int NW, bool VEC>
-__device__ __forceinline__ void load_tile(unsigned char* tile, const Heads& h, int64_t head_at,
-                                          int row0, int rows, int D, uint64_t live, int wave,
-                                          int lane) {
-  typedef Shape<E, DP> Sh;
-  typedef typename E::storage S;
-  const S* base = (const S*)h.data + head_at + (int64_t)row0 * h.st;
-  if constexpr (VEC) {
-    constexpr int kPer = ROWS / Sh::kRowsPerDma / NW;
-    static_assert(kPer >= 1, "a wave's share of a tile");
-    const int64_t left = ((int64_t)(rows - 1 - row0) * h.st + D) * Sh::kES;
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)base, (short)0, (int)(left < 0 ? 0 : left < 0x7fff0000 ? left : 0x7fff0000), 0x00020000);
-    const uint32_t at = lds_addr(tile);
-    const int stride = (int)(h.st * Sh::kES);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int first = (wave * kPer + j) * Sh::kRowsPerDma;       // uniform
-      const int row = lane / Sh::kChunks;
-      const int chunk = (lane % Sh::kChunks) ^ swz<Sh::kChunks>(first + row);
-      // row0 may be negative: those rows lie before the tensor
-      const bool in = 16 * chunk < D * Sh::kES && first + row >= -row0 && ((live >> (first + row)) & 1);
-      dma16(rsrc, in ? (first + row) * stride + 16 * chunk : kOOB, uniform(at + first * Sh::kRowBytes));
-    }
-  } else {
-    for (int e = wave * 64 + lane; e < ROWS * DP; e += 64 * NW) {
-      const int row = e / DP, d = e % DP;
-      const bool in = d < D && row0 + row >= 0 && row0 + row < rows && ((live >> row) & 1);
-      S x = 0;
-      if (in) x = base[(int64_t)row * h.st + d];
-      const int chunk = d * Sh::kES / 16;
-      *(S*)(tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) = x;
-    }
+// Brings one head's rows [row0, row0 + ROWS) of `rows` into an LDS tile, by NW
+// waves (wave w of them).  Rows outside [0, rows) and those whose bit of `live` is
+// 0 become zeros (of a negative row0 the caller's live has zeros there), and so
+// does what lies past D.  VEC: direct loads to LDS, in flight until wait_loads;
+// a lane's offsets within a tile are formed once, so that a tile costs two
+// instructions per load and a buffer descriptor.  Else element by element, there
+// after a barrier.
+template <int J, int PER, class F>
+__device__ __forceinline__ void each(const F& f) {
+  if constexpr (J < PER) {
+    f(std::integral_constant<int, J>());
+    each<J + 1, PER>(f);
   }
 }
+template <class E, int DP, int ROWS, int NW, bool VEC>
+struct Loader {
+  typedef Shape<E, DP> Sh;
+  typedef typename E::storage S;
+  static constexpr int kPer = VEC ? ROWS / Sh::kRowsPerDma / NW : 1;
+  static_assert(kPer >= 1, "a wave's share of a tile");
+  int off[kPer];
+  int stride, D, wave, lane;
+  __device__ __forceinline__ Loader(const Heads& h, int d, int w, int l) : D(d), wave(w), lane(l) {
+    stride = (int)(h.st * Sh::kES);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int row = (w * kPer + j) * Sh::kRowsPerDma + l / Sh::kChunks;
+        const int chunk = (l % Sh::kChunks) ^ swz<Sh::kChunks>(row);
+        off[j] = 16 * chunk < d * Sh::kES ? row * stride + 16 * chunk : kOOB;
+      }
+    }
+  }
+  __device__ __forceinline__ void operator()(unsigned char* tile, const Heads& h, int64_t head_at, int row0,
+                                             int rows, uint64_t live) const {
+    if constexpr (VEC) {
+      const char* base = (const char*)h.data + head_at * Sh::kES + (int64_t)row0 * stride;
+      const int n = rows - row0;
+      const uint64_t left = (uint64_t)(uint32_t)(n - 1) * (uint32_t)stride + (uint32_t)(D * Sh::kES);
+      const int records = n <= 0 ? 0 : left < 0x7fff0000ull ? (int)left : 0x7fff0000;
+      const __amdgpu_buffer_rsrc_t rsrc =
+          __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, records, 0x00020000);
+      const uint32_t at = uniform((int)lds_addr(tile) + wave * kPer * 1024);
+      constexpr uint64_t kAll = ROWS >= 64 ? ~0ull : (1ull << (ROWS & 63)) - 1;
+      if ((live & kAll) == kAll) {
+        each<0, kPer>([&](auto j) { dma16<1024 * j>(rsrc, off[j], at); });
+      } else {
+        each<0, kPer>([&](auto j) {
+          const int row = (wave * kPer + j) * Sh::kRowsPerDma + lane / Sh::kChunks;
+          dma16<1024 * j>(rsrc, (live >> row) & 1 ? off[j] : kOOB, at);
+        });
+      }
+    } else {
+      const S* base = (const S*)h.data + head_at + (int64_t)row0 * h.st;
+      for (int e = wave * 64 + lane; e < ROWS * DP; e += 64 * NW) {
+        const int row = e / DP, d = e % DP;
+        const bool in = d < D && row0 + row >= 0 && row0 + row < rows && ((live >> row) & 1);
+        S x = 0;
+        if (in) x = base[(int64_t)row * h.st + d];
+        const int chunk = d * Sh::kES / 16;
+        *(S*)(tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) = x;
+      }
+    }
+  }
+};
 
 // 16 bytes of a row: 8 bf16 or 4 float32 elements, the operand of one
 // 32x32x16 or four 32x32x2 products (k = lane half, then element).
@@ -225,6 +254,13 @@ __device__ __forceinline__ void row_frags_from(const typename E::storage* row, b
   }
 }
 
+// Two values as bf16, to nearest even, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), b2));
+}
+
 // What a 32x32 accumulator holds per lane (register j: row 8 (j / 4) + 4 half
 // + j % 4), as the right operand of products that sum over its 32 rows: for
 // bf16 two fragments of 8 rows each (rounded to nearest even), for float32 the
@@ -233,16 +269,11 @@ template <class E> struct Weights;
 template <> struct Weights<BF16> {
   u16x8 f[2];
   __device__ __forceinline__ void set(const f32x16& p) {
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    typedef float f2 __attribute__((ext_vector_type(2)));
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       u32x4 w;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const f2 x = {p[8 * s + 2 * k], p[8 * s + 2 * k + 1]};
-        w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2));
-      }
+      for (int k = 0; k < 4; ++k) w[k] = pack_bf16(p[8 * s + 2 * k], p[8 * s + 2 * k + 1]);
       f[s] = __builtin_bit_cast(u16x8, w);
     }
   }
@@ -322,7 +353,14 @@ __device__ __forceinline__ void store_row(typename E::storage* row, const f32x16
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = live ? acc[db][4 * i + k] * f : 0.0f;
       if constexpr (VEC) {
-        if (d < D) store_f32<E, 4>(row + d, x);
+        if (d < D) {
+          if constexpr (sizeof(typename E::storage) == 2) {
+            typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+            *(u2*)(row + d) = u2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+          } else {
+            store_f32<E, 4>(row + d, x);
+          }
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
