@@ -32,10 +32,6 @@ constexpr int kQ = 32 * kWaves;         // queries of a workgroup
 // raises no maximum rescales nothing.
 constexpr float kSlack = 8.0f;
 
-template <class E> struct KeysOf;
-template <> struct KeysOf<BF16> { static constexpr int kKeys = 64; };
-template <> struct KeysOf<F32> { static constexpr int kKeys = 32; };
-
 // ---------------------------------------------------------------------------
 // Mask and segments
 // ---------------------------------------------------------------------------
@@ -131,142 +127,139 @@ __global__ __launch_bounds__(256) void attn_ranges_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// A wave's 32 queries and one tile of keys
+// A wave's 32 queries against tiles of 32 keys
 // ---------------------------------------------------------------------------
+constexpr int kKeys = 32;
+
 template <class E, int DP>
 struct State {
   f32x16 o[DP / 32];    // O^T: this lane's query, relative to m
   float m, l;           // maximum used (times log2 e) and this lane half's sum
 };
 
-// The tile goes by blocks of 32 keys: while the matrix cores take the scores of
-// the next block, or the outputs of the last one, the vector unit takes the
-// exponentials of this one.  The order is written out, step by step between
-// fences, with every LDS operand read kAhead products early: left to itself the
-// compiler waits for each read, and puts all exponentials before all products.
-template <class E, int DP, int KEYS>
-__device__ __forceinline__ void attend(const Places& kt, const Places& vt,
-                                       const Chunk<E> (&qf)[Shape<E, DP>::kG], State<E, DP>& st, float c,
-                                       int k0, Span keys, bool full, const uint32_t (&live)[KEYS / 32],
-                                       int lane) {
-  constexpr int NB = KEYS / 32, G = Shape<E, DP>::kG, DB = DP / 32, CS = ColumnSteps<E>::kN;
-  const int h = lane >> 5;
-  f32x16 s[2];
-  Weights<E> p[2];
-  float m = 0.0f, sum[2] = {};
+// What of a tile a lane's query sees: keys [lo, end) with their bit of `live`.
+struct Sight {
+  int lo, end;
+  uint32_t live;
+  bool full;            // every query of the wave sees every key of the tile
+};
 
-  const auto exponential = [&](int n, int j) {
-    float x = __builtin_amdgcn_exp2f(fmaf(s[n & 1][j], c, -m));
+// One step: the weighted values of one tile (CURRENT: its scores are in s) and
+// the scores of the next (NEXT: into s).  While the matrix cores take the next
+// scores the vector unit takes this tile's exponentials, and while they take its
+// weighted values, the next scores' maximum.  The order is written out, product by
+// product between fences, with every LDS operand read kAhead products early: left
+// to itself the compiler waits for each read, and puts all exponentials before all
+// products.  `loads` queues the loads of later tiles, behind the first reads.
+// Returns the maximum of the next scores, unscaled.
+template <class E, int DP, bool CURRENT, bool NEXT, class Loads>
+__device__ __forceinline__ float step(const Places& kt, const Places& vt,
+                                      const Chunk<E> (&qf)[Shape<E, DP>::kG], State<E, DP>& st, f32x16& s,
+                                      float c, int k0, const Sight& see, int lane, const Loads& loads) {
+  constexpr int G = Shape<E, DP>::kG, DB = DP / 32, N = DB * ColumnSteps<E>::kN;
+  const float m = st.m == -INFINITY ? 0.0f : st.m;
+  float sum[2] = {};
+  const auto exponential = [&](int j) {
+    float x = __builtin_amdgcn_exp2f(fmaf(s[j], c, -m));
     asm volatile("" : "+v"(x));    // here, not where it is used first
-    s[n & 1][j] = x;
+    s[j] = x;
     sum[j & 1] += x;
   };
-  // scores of block n, with the exponentials of block n - 1 between the products
-  const auto scores = [&](int n) {
+  f32x16 x = {};
+  Column<E> v[kAhead];
+  const auto read = [&](int t) { return column_frag<E, DP>(vt, 0, t % DB, t / DB, lane); };
+  if constexpr (NEXT) {
     Chunk<E> k[kAhead];
-    f32x16 x = {};
 #pragma unroll
-    for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 32 * n, g);
+    for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 0, g);
+    fence();
+    loads();
     fence();
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       x = mma<E>(k[g % kAhead], qf[g], x);
-      if (g + kAhead < G) k[g % kAhead] = row_frag<E, DP>(kt, 32 * n, g + kAhead);
-      if (n > 0) {
+      if (g + kAhead < G) k[g % kAhead] = row_frag<E, DP>(kt, 0, g + kAhead);
+      else if (CURRENT) v[g + kAhead - G] = read(g + kAhead - G);
+      if constexpr (CURRENT) {
 #pragma unroll
-        for (int j = 16 * g / G; j < 16 * (g + 1) / G; ++j) exponential(n - 1, j);
+        for (int j = 16 * g / G; j < 16 * (g + 1) / G; ++j) exponential(j);
       }
       fence();
     }
-    s[n & 1] = x;
-  };
-  // outputs from block n, with the exponentials of block n + 1 between the products
-  const auto outputs = [&](int n, bool more) {
-    constexpr int N = DB * CS;
-    Column<E> v[kAhead];
-    const auto read = [&](int t) { return column_frag<E, DP>(vt, 32 * n, t % DB, t / DB, lane); };
+  } else {
 #pragma unroll
     for (int t = 0; t < kAhead; ++t) v[t] = read(t);
     fence();
+    loads();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) exponential(j);
+  }
+  if (NEXT && !see.full) {
+    apart();
+    const int h = lane >> 5;
+    const uint32_t w = see.live >> (4 * h);
+    const int first = see.lo - k0 - 4 * h, past = see.end - k0 - 4 * h;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int r = 8 * (j >> 2) + (j & 3);
+      const bool in = r >= first && r < past && ((w >> r) & 1);
+      x[j] = in ? x[j] : -INFINITY;
+    }
+  }
+  float top = -INFINITY;
+  if constexpr (CURRENT) {
+    Weights<E> p;
+    p.set(s);
+    st.l += sum[0] + sum[1];
+    fence();
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      st.o[t % DB] = mma_column<E>(v[t % kAhead], p[n & 1], t / DB, st.o[t % DB]);
+      st.o[t % DB] = mma_column<E>(v[t % kAhead], p, t / DB, st.o[t % DB]);
       if (t + kAhead < N) v[t % kAhead] = read(t + kAhead);
-      if (more) {
+      if constexpr (NEXT) {
 #pragma unroll
-        for (int j = 16 * t / N; j < 16 * (t + 1) / N; ++j) exponential(n + 1, j);
+        for (int j = 16 * t / N; j < 16 * (t + 1) / N; ++j) top = fmaxf(top, x[j]);
+        asm volatile("" : "+v"(top));
       }
       fence();
     }
-  };
-  // masks block n and moves the running maximum to it
-  const auto settle = [&](int n) {
-    if (!full) {
-      apart();
-      const uint32_t w = live[n] >> (4 * h);
-      const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
+  } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int r = 8 * (j >> 2) + (j & 3);
-        const bool in = r >= first && r < past && ((w >> r) & 1);
-        s[n & 1][j] = in ? s[n & 1][j] : -INFINITY;
-      }
-    }
-    float top = s[n & 1][0];
-#pragma unroll
-    for (int j = 1; j < 16; ++j) top = fmaxf(top, s[n & 1][j]);
-    top = fmaxf(top, lane_xor(top, 32)) * c;
-    if (__any(top > st.m + kSlack)) {
-      apart();
-      const float to = fmaxf(st.m, top);
-      const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - to);
-      st.m = to;
-      st.l = (st.l + (sum[0] + sum[1])) * f;
-      sum[0] = sum[1] = 0.0f;
-#pragma unroll
-      for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) st.o[db][j] *= f;
-      // the block before, whose weights are still to be used
-      if (n > 0) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[(n - 1) & 1][j] *= f;
-      }
-    }
-    m = st.m == -INFINITY ? 0.0f : st.m;
-  };
+    for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
+  }
+  if constexpr (NEXT) s = x;
+  return top;
+}
 
-  scores(0);
-  settle(0);
+// Moves the running maximum to scores of maximum `top` that are next.
+template <class E, int DP>
+__device__ __forceinline__ void settle(State<E, DP>& st, float top, float c) {
+  top = fmaxf(top, lane_xor(top, 32)) * c;
+  if (__any(top > st.m + kSlack)) {
+    apart();
+    const float to = fmaxf(st.m, top);
+    const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - to);
+    st.m = to;
+    st.l *= f;
 #pragma unroll
-  for (int n = 1; n < NB; ++n) {
-    scores(n);
-    settle(n);
-    p[(n - 1) & 1].set(s[(n - 1) & 1]);
-    outputs(n - 1, true);
-  }
-  if (NB == 1) {
+    for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) exponential(0, j);
+      for (int j = 0; j < 16; ++j) st.o[db][j] *= f;
   }
-  p[(NB - 1) & 1].set(s[(NB - 1) & 1]);
-  outputs(NB - 1, false);
-  st.l += sum[0] + sum[1];
 }
 
 template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 ? 2 : 1) void
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 4 ? 1 : DP == 64 ? 3 : 2) void
 attention_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
-  constexpr int KEYS = KeysOf<E>::kKeys;
-  constexpr int kTile = KEYS * Sh::kRowBytes;
-  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [2][K, V] tiles
+  constexpr int kTile = kKeys * Sh::kRowBytes;
+  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // K [2], V [2] tiles
   __shared__ int bound[2][kWaves];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int tiles = (a.Tq + kQ - 1) / kQ;
   int head, tile;
-  if (!place(a.B * a.Hq, tiles, &head, &tile)) return;
+  place(a.B * a.Hq, tiles, &head, &tile);
   tile = tiles - 1 - tile;
   const int b = head / a.Hq, hq = head % a.Hq, hk = hq / (a.Hq / a.Hkv);
   const int i = tile * kQ + wave * 32 + (lane & 31), p = a.Tk - a.Tq + i;
@@ -297,37 +290,76 @@ attention_kernel(AttnArgs a) {
   st.l = 0.0f;
   if (lo < end) {
     const int64_t kat = b * a.k.sb + hk * a.k.sh, vat = b * a.v.sb + hk * a.v.sh;
-    uint32_t live[KEYS / 32], next[KEYS / 32];
-    int k0 = lo / KEYS * KEYS;
-    uint64_t m = live_keys<KEYS>(a, b, k0, live);
-    const Loader<E, DP, KEYS, kWaves, VEC> load_k(a.k, a.D, wave, lane), load_v(a.v, a.D, wave, lane);
-    load_k(smem, a.k, kat, k0, a.Tk, m);
-    load_v(smem + kTile, a.v, vat, k0, a.Tk, m);
+    Loader<E, DP, kKeys, kWaves, VEC> load_k(a.k, a.Tk, a.D, wave, lane), load_v(a.v, a.Tk, a.D, wave, lane);
+    const float c = a.scale * kLog2e;
+    const Places pl = places<E, DP>(lane);
+    const uint32_t kt = lds_addr(smem), vt = kt + 2 * kTile;
+    const int first = lo / kKeys, tiles = (end + kKeys - 1) / kKeys - first;
+    const auto place_of = [&](int t) { return (first + t) * kKeys; };
+    Sight see{keys.lo, keys.end, 0, false};
+    const auto look = [&](int t) {
+      uint32_t live[1];
+      const uint64_t m = live_keys<kKeys>(a, b, place_of(t), live);
+      see.live = live[0];
+      see.full = place_of(t) >= full_lo && place_of(t) + kKeys <= full_end && live[0] == ~0u;
+      return m;
+    };
+    load_k.start(a.k, kat, place_of(0));
+    load_v.start(a.v, vat, place_of(0));
+    // keys' rows of masked positions need no zeros: their scores are selected away
+    const auto fetch_k = [&](int t) {
+      if (t < tiles) load_k(kt + (t & 1) * kTile, place_of(t), ~0ull);
+    };
+    const auto fetch_v = [&](int t, uint64_t m) { load_v(vt + (t & 1) * kTile, place_of(t), m); };
+    // tile t's values and tile t + 1's keys are there, and what the step before read
+    // is free
+    const auto arrive = [&]() {
+      wait_loads();
+      tile_barrier();
+    };
+    // the loads for the step after step t
+    uint64_t m = 0;
+    const auto loads = [&](int t) {
+      if (t + 1 < tiles) fetch_v(t + 1, m);
+      fetch_k(t + 2);
+    };
+    const auto pass = [&](int t) {
+      arrive();
+      if (t + 1 < tiles) m = look(t + 1);
+      loads(t);
+    };
+    const auto none = [] {};
+    const auto keys_at = [&](int t) { return in_tile(pl, kt + (t & 1) * kTile); };
+    const auto values_at = [&](int t) { return in_tile(pl, vt + (t & 1) * kTile); };
+    fetch_v(0, look(0));
+    fetch_k(0);
+    fetch_k(1);
     Chunk<E> qf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
-    const float c = a.scale * kLog2e;
-    const Places at = places<E, DP>(lane);
-    int buf = 0;
-    for (; k0 < end; k0 += KEYS, buf ^= 1) {
-      unsigned char* here = smem + buf * 2 * kTile;
-      unsigned char* there = smem + (buf ^ 1) * 2 * kTile;
-      if constexpr (VEC) wait_loads();
-      tile_barrier();        // this tile is there; the other one has been read
-      if (k0 + KEYS < end) {
-        m = live_keys<KEYS>(a, b, k0 + KEYS, next);
-        load_k(there, a.k, kat, k0 + KEYS, a.Tk, m);
-        load_v(there + kTile, a.v, vat, k0 + KEYS, a.Tk, m);
+    wait_loads();
+    tile_barrier();
+    int t = 0;
+    if (wlo < wend) {
+      // this wave's tiles; it keeps the workgroup's barriers before and after
+      const int from = wlo / kKeys - first, last = (wend - 1) / kKeys - first;
+      f32x16 s;
+      for (; t + 1 < from; ++t) pass(t);
+      if (from > 0) pass(t++);
+      settle<E, DP>(st, step<E, DP, false, true>(keys_at(t), values_at(t), qf, st, s, c, place_of(t), see,
+                                                 lane, none), c);
+      for (; t < last; ++t) {
+        arrive();
+        m = look(t + 1);
+        settle<E, DP>(st, step<E, DP, true, true>(keys_at(t + 1), values_at(t), qf, st, s, c,
+                                                  place_of(t + 1), see, lane, [&] { loads(t); }), c);
       }
-      if (k0 < wend && k0 + KEYS > wlo) {
-        const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
-        const uint32_t base = lds_addr(here);
-        attend<E, DP, KEYS>(in_tile(at, base), in_tile(at, base + kTile), qf, st, c, k0, keys, full, live,
-                            lane);
-      }
-#pragma unroll
-      for (int n = 0; n < KEYS / 32; ++n) live[n] = next[n];
+      arrive();
+      if (t + 1 < tiles) m = look(t + 1);
+      step<E, DP, true, false>(keys_at(t), values_at(t), qf, st, s, c, 0, see, lane, [&] { loads(t); });
+      ++t;
     }
+    for (; t < tiles; ++t) pass(t);
   }
   if (!valid) return;
   const float l = st.l + lane_xor(st.l, 32);
@@ -347,13 +379,12 @@ attention_kernel(AttnArgs a) {
 template <class E> struct FewOf;
 template <> struct FewOf<BF16> { static constexpr int kWaves = 4; };
 template <> struct FewOf<F32> { static constexpr int kWaves = 2; };
-constexpr int kFewKeys = 32;
 
 template <class E, int DP, bool VEC>
 __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
-  constexpr int NW = FewOf<E>::kWaves, KEYS = kFewKeys;
+  constexpr int NW = FewOf<E>::kWaves, KEYS = kKeys;
   constexpr int kTile = KEYS * Sh::kRowBytes;
   extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [wave][2][K, V], then joins
   __shared__ float ms[NW][32], ls[NW][32];
@@ -377,16 +408,19 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
   unsigned char* mine = smem + wave * 4 * kTile;
   if (lo < end) {
     const int64_t kat = b * a.k.sb + hk * a.k.sh, vat = b * a.v.sb + hk * a.v.sh;
-    const int step = a.splits * NW * KEYS;
+    const int stride = a.splits * NW * KEYS;
     int k0 = lo / KEYS * KEYS + (split * NW + wave) * KEYS;
     uint32_t live[1] = {}, next[1] = {};
-    const Loader<E, DP, KEYS, 1, VEC> load_k(a.k, a.D, 0, lane), load_v(a.v, a.D, 0, lane);
-    const auto fetch = [&](int at, unsigned char* to) {
+    Loader<E, DP, KEYS, 1, VEC> load_k(a.k, a.Tk, a.D, 0, lane), load_v(a.v, a.Tk, a.D, 0, lane);
+    load_k.start(a.k, kat, k0);
+    load_v.start(a.v, vat, k0);
+    const auto fetch = [&](int at, uint32_t to) {
       const uint64_t m = live_keys<KEYS>(a, b, at, next);
-      load_k(to, a.k, kat, at, a.Tk, m);
-      load_v(to + kTile, a.v, vat, at, a.Tk, m);
+      load_k(to, at, m);
+      load_v(to + kTile, at, m);
     };
-    if (k0 < end) fetch(k0, mine);
+    const uint32_t own_tiles = lds_addr(mine);
+    if (k0 < end) fetch(k0, own_tiles);
     live[0] = next[0];
     Chunk<E> qf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
@@ -394,16 +428,19 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
     const float c = a.scale * kLog2e;
     const Places at = places<E, DP>(lane);
     int buf = 0;
-    for (; k0 < end; k0 += step, buf ^= 1) {
-      unsigned char* here = mine + buf * 2 * kTile;
+    for (; k0 < end; k0 += stride, buf ^= 1) {
       wait_loads();
       wait_lds();
       __builtin_amdgcn_wave_barrier();
-      if (k0 + step < end) fetch(k0 + step, mine + (buf ^ 1) * 2 * kTile);
-      const bool full = k0 >= full_lo && k0 + KEYS <= full_end && live[0] == ~0u;
-      const uint32_t base = lds_addr(here);
-      attend<E, DP, KEYS>(in_tile(at, base), in_tile(at, base + kTile), qf, st, c, k0, keys, full, live,
-                          lane);
+      if (k0 + stride < end) fetch(k0 + stride, own_tiles + (buf ^ 1) * 2 * kTile);
+      const Sight see{keys.lo, keys.end, live[0],
+                      k0 >= full_lo && k0 + KEYS <= full_end && live[0] == ~0u};
+      const uint32_t base = own_tiles + buf * 2 * kTile;
+      const Places kt = in_tile(at, base), vt = in_tile(at, base + kTile);
+      f32x16 s;
+      const auto none = [] {};
+      settle<E, DP>(st, step<E, DP, false, true>(kt, vt, qf, st, s, c, k0, see, lane, none), c);
+      step<E, DP, true, false>(kt, vt, qf, st, s, c, k0, see, lane, none);
       live[0] = next[0];
     }
   }
@@ -490,7 +527,7 @@ hipError_t forward(const AttnArgs& a, hipStream_t s) {
   typedef Shape<E, DP> Sh;
   if (a.splits > 0) {
     constexpr int NW = FewOf<E>::kWaves;
-    constexpr int lds = std::max(NW * 4 * kFewKeys * Sh::kRowBytes, NW * 32 * DP * 4);
+    constexpr int lds = std::max(NW * 4 * kKeys * Sh::kRowBytes, NW * 32 * DP * 4);
     static hipError_t once = hipFuncSetAttribute((const void*)attention_few_kernel<E, DP, VEC>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (once != hipSuccess) return once;
@@ -500,12 +537,12 @@ hipError_t forward(const AttnArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((attention_join_kernel<E, DP>), dim3(heads * rows), dim3(64), 0, s, a);
     return hipGetLastError();
   }
-  constexpr int lds = 4 * KeysOf<E>::kKeys * Sh::kRowBytes;
+  constexpr int lds = 4 * kKeys * Sh::kRowBytes;
   static hipError_t once = hipFuncSetAttribute((const void*)attention_kernel<E, DP, VEC>,
                                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (once != hipSuccess) return once;
   const int64_t tiles = (a.Tq + kQ - 1) / kQ, heads = (int64_t)a.B * a.Hq;
-  hipLaunchKernelGGL((attention_kernel<E, DP, VEC>), dim3((unsigned)((heads + 7) / 8 * 8 * tiles)),
+  hipLaunchKernelGGL((attention_kernel<E, DP, VEC>), dim3((unsigned)(heads * tiles)),
                      dim3(kNT), lds, s, a);
   return hipGetLastError();
 }
@@ -525,7 +562,7 @@ size_t attention_part_floats(AttnArgs& a) {
   if (rows > 32) return 0;
   const int64_t heads = (int64_t)a.B * a.Hkv;
   const int waves = a.dtype == kBF16 ? attn::FewOf<BF16>::kWaves : attn::FewOf<F32>::kWaves;
-  const int64_t most = (a.Tk + waves * attn::kFewKeys * 2 - 1) / (waves * attn::kFewKeys * 2);
+  const int64_t most = (a.Tk + waves * attn::kKeys * 2 - 1) / (waves * attn::kKeys * 2);
   a.splits = (int)std::max<int64_t>(1, std::min<int64_t>({most, (512 + heads - 1) / heads, 64}));
   return a.splits == 1 ? 0 : (size_t)(heads * a.splits * rows) * ((a.D <= 64 ? 64 : 128) + 2);
 }

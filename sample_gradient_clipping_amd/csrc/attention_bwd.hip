@@ -46,7 +46,7 @@ attention_dq_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   const int tiles = (a.Tq + kRows - 1) / kRows;
   int head, tile;
-  if (!place(a.B * a.Hq, tiles, &head, &tile)) return;
+  place(a.B * a.Hq, tiles, &head, &tile);
   tile = tiles - 1 - tile;
   const int b = head / a.Hq, hq = head % a.Hq, hk = hq / (a.Hq / a.Hkv);
   const int i = tile * kRows + wave * 32 + (lane & 31), p = a.Tk - a.Tq + i;
@@ -78,9 +78,12 @@ attention_dq_kernel(AttnArgs a) {
     uint32_t live[KEYS / 32], next[KEYS / 32];
     int k0 = lo / KEYS * KEYS;
     uint64_t m = live_keys<KEYS>(a, b, k0, live);
-    const Loader<E, DP, KEYS, kWaves, VEC> load_k(a.k, a.D, wave, lane), load_v(a.v, a.D, wave, lane);
-    load_k(smem, a.k, kat, k0, a.Tk, m);
-    load_v(smem + kTile, a.v, vat, k0, a.Tk, m);
+    Loader<E, DP, KEYS, kWaves, VEC> load_k(a.k, a.Tk, a.D, wave, lane), load_v(a.v, a.Tk, a.D, wave, lane);
+    load_k.start(a.k, kat, k0);
+    load_v.start(a.v, vat, k0);
+    const uint32_t tiles_at = lds_addr(smem);
+    load_k(tiles_at, k0, m);
+    load_v(tiles_at + kTile, k0, m);
     Chunk<E> qf[Sh::kG], gf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.o.data + b * a.o.sb + hq * a.o.sh + (int64_t)i * a.o.st, some,
                                a.D, lane, qf);
@@ -101,13 +104,13 @@ attention_dq_kernel(AttnArgs a) {
     const Places pl = places<E, DP>(lane);
     int buf = 0;
     for (; k0 < end; k0 += KEYS, buf ^= 1) {
-      unsigned char* there = smem + (buf ^ 1) * 2 * kTile;
+      const uint32_t there = tiles_at + (buf ^ 1) * 2 * kTile;
       if constexpr (VEC) wait_loads();
       tile_barrier();        // this tile is there; the other one has been read
       if (k0 + KEYS < end) {
         m = live_keys<KEYS>(a, b, k0 + KEYS, next);
-        load_k(there, a.k, kat, k0 + KEYS, a.Tk, m);
-        load_v(there + kTile, a.v, vat, k0 + KEYS, a.Tk, m);
+        load_k(there, k0 + KEYS, m);
+        load_v(there + kTile, k0 + KEYS, m);
       }
       if (k0 < wend && k0 + KEYS > wlo) {
         const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
@@ -239,7 +242,7 @@ attention_dkv_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   const int tiles = (a.Tk + kRows - 1) / kRows, group = a.Hq / a.Hkv, off = a.Tk - a.Tq;
   int head, tile;
-  if (!place(a.B * a.Hkv, tiles, &head, &tile)) return;
+  place(a.B * a.Hkv, tiles, &head, &tile);
   const int b = head / a.Hkv, hk = head % a.Hkv;
   const int j0 = tile * kRows + wave * 32 + (lane & 31);
   const bool valid = j0 < a.Tk;
@@ -278,10 +281,11 @@ attention_dkv_kernel(AttnArgs a) {
     if constexpr (Z::kValuesInLds) {
       // what an inactive key's row holds reaches nothing but its own sums, which
       // are not used
-      const Loader<E, DP, 64, kWaves, VEC> load_v(a.v, a.D, wave, lane);
+      Loader<E, DP, 64, kWaves, VEC> load_v(a.v, a.Tk, a.D, wave, lane);
+      load_v.start(a.v, b * a.v.sb + hk * a.v.sh, tile * kRows);
 #pragma unroll
       for (int r = 0; r < kRows; r += 64)
-        load_v(shared_tiles + r * Sh::kRowBytes, a.v, b * a.v.sb + hk * a.v.sh, tile * kRows + r, a.Tk, ~0ull);
+        load_v(lds_addr(shared_tiles) + r * Sh::kRowBytes, tile * kRows + r, ~0ull);
     } else {
       row_frags_from<E, DP, VEC>((const S*)a.v.data + b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st,
                                  some, a.D, lane, vf);
@@ -295,12 +299,17 @@ attention_dkv_kernel(AttnArgs a) {
     uint32_t live[N / 32], next[N / 32];
     float value = 0.0f;                   // of the next tile's lse (threads 0 ..) or delta (64 ..)
     const int row = threadIdx.x & 63;
-    const Loader<E, DP, N, kWaves, VEC> load_q(a.q, a.D, wave, lane), load_g(a.dout, a.D, wave, lane);
+    Loader<E, DP, N, kWaves, VEC> load_q(a.q, a.Tq, a.D, wave, lane), load_g(a.dout, a.Tq, a.D, wave, lane);
     const auto fetch = [&](int p0, int hq, int buf) {
       uint64_t m = live_keys<N>(a, b, p0, next);
       if (p0 < off) m &= ~0ull << (off - p0);        // no queries at these positions
-      load_q(smem + buf * 2 * kTile, a.q, b * a.q.sb + hq * a.q.sh, p0 - off, a.Tq, m);
-      load_g(smem + buf * 2 * kTile + kTile, a.dout, b * a.dout.sb + hq * a.dout.sh, p0 - off, a.Tq, m);
+      if (p0 == p_first) {                           // the next head
+        load_q.start(a.q, b * a.q.sb + hq * a.q.sh, p0 - off);
+        load_g.start(a.dout, b * a.dout.sb + hq * a.dout.sh, p0 - off);
+      }
+      const uint32_t to = lds_addr(smem) + buf * 2 * kTile;
+      load_q(to, p0 - off, m);
+      load_g(to + kTile, p0 - off, m);
       const int i = p0 - off + row;
       value = 0.0f;
       if (wave < 2 && row < N && i >= 0 && i < a.Tq && ((m >> row) & 1)) {
@@ -467,7 +476,7 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
   if (once[0] != hipSuccess) return once[0];
   if (once[1] != hipSuccess) return once[1];
   const int64_t qt = (a.Tq + kRows - 1) / kRows, kt = (a.Tk + kRows - 1) / kRows;
-  const int64_t qh = ((int64_t)a.B * a.Hq + 7) / 8 * 8, kh = ((int64_t)a.B * a.Hkv + 7) / 8 * 8;
+  const int64_t qh = (int64_t)a.B * a.Hq, kh = (int64_t)a.B * a.Hkv;
   timing_begin("attention_dq", s);
   hipLaunchKernelGGL((attention_dq_kernel<E, DP, VEC>), dim3((unsigned)(qh * qt)), dim3(kNT), lds, s, a);
   timing_end("attention_dq", s);

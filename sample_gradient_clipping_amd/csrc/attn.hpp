@@ -110,13 +110,6 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Brings one head's rows [row0, row0 + ROWS) of `rows` into an LDS tile, by NW
-// waves (wave w of them).  Rows outside [0, rows) and those whose bit of `live` is
-// 0 become zeros (of a negative row0 the caller's live has zeros there), and so
-// does what lies past D.  VEC: direct loads to LDS, in flight until wait_loads;
-// a lane's offsets within a tile are formed once, so that a tile costs two
-// instructions per load and a buffer descriptor.  Else element by element, there
-// after a barrier.
 template <int J, int PER, class F>
 __device__ __forceinline__ void each(const F& f) {
   if constexpr (J < PER) {
@@ -124,15 +117,28 @@ __device__ __forceinline__ void each(const F& f) {
     each<J + 1, PER>(f);
   }
 }
+
+// Brings rows [row0, row0 + ROWS) of one head's `rows` rows into an LDS tile, by
+// NW waves (wave w of them).  Rows outside [0, rows) and those whose bit of `live`
+// is 0 become zeros (of a negative row0 the caller's live has zeros there), and so
+// does what lies past D.  VEC: direct loads to LDS, in flight until wait_loads.
+// Scalar instructions are not free (a wave issues one in about five cycles): a
+// lane's offsets within a tile are formed once and a buffer descriptor serves the
+// 2^30 bytes after its first row, so that a tile costs a dozen of them.  Not VEC:
+// element by element, there after a barrier.
 template <class E, int DP, int ROWS, int NW, bool VEC>
 struct Loader {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
   static constexpr int kPer = VEC ? ROWS / Sh::kRowsPerDma / NW : 1;
   static_assert(kPer >= 1, "a wave's share of a tile");
+  const char* head;
+  __amdgpu_buffer_rsrc_t rsrc;
+  int first;              // row of the descriptor's base
   int off[kPer];
-  int stride, D, wave, lane;
-  __device__ __forceinline__ Loader(const Heads& h, int d, int w, int l) : D(d), wave(w), lane(l) {
+  int stride, rows, D, wave, lane;
+  __device__ __forceinline__ Loader(const Heads& h, int n, int d, int w, int l)
+      : head(nullptr), first(0), rows(n), D(d), wave(w), lane(l) {
     stride = (int)(h.st * Sh::kES);
     if constexpr (VEC) {
 #pragma unroll
@@ -143,34 +149,46 @@ struct Loader {
       }
     }
   }
-  __device__ __forceinline__ void operator()(unsigned char* tile, const Heads& h, int64_t head_at, int row0,
-                                             int rows, uint64_t live) const {
+  // The head at element `at` of h, tiles from row0 on.
+  __device__ __forceinline__ void start(const Heads& h, int64_t at, int row0) {
+    head = (const char*)h.data + at * Sh::kES;
+    if constexpr (VEC) base_at(row0);
+    else stride = 0, strides = h.st;
+  }
+  int64_t strides;        // not VEC: of a row, in elements
+  __device__ __forceinline__ void base_at(int row0) {
+    first = row0;
+    const int n = rows - row0;
+    const uint64_t left = (uint64_t)(uint32_t)(n - 1) * (uint32_t)stride + (uint32_t)(D * Sh::kES);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(head + (int64_t)row0 * stride), (short)0,
+                                             n <= 0 ? 0 : left < 0x7fff0000ull ? (int)left : 0x7fff0000,
+                                             0x00020000);
+  }
+  __device__ __forceinline__ void operator()(uint32_t tile, int row0, uint64_t live) {
     if constexpr (VEC) {
-      const char* base = (const char*)h.data + head_at * Sh::kES + (int64_t)row0 * stride;
-      const int n = rows - row0;
-      const uint64_t left = (uint64_t)(uint32_t)(n - 1) * (uint32_t)stride + (uint32_t)(D * Sh::kES);
-      const int records = n <= 0 ? 0 : left < 0x7fff0000ull ? (int)left : 0x7fff0000;
-      const __amdgpu_buffer_rsrc_t rsrc =
-          __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, records, 0x00020000);
-      const uint32_t at = uniform((int)lds_addr(tile) + wave * kPer * 1024);
+      if ((int64_t)(row0 - first) * stride > (1 << 30)) base_at(row0);
+      // an out-of-range offset stays one: it is above every descriptor's 2^31 bytes
+      const int at = (row0 - first) * stride;
+      const uint32_t to = uniform((int)tile + wave * kPer * 1024);
       constexpr uint64_t kAll = ROWS >= 64 ? ~0ull : (1ull << (ROWS & 63)) - 1;
       if ((live & kAll) == kAll) {
-        each<0, kPer>([&](auto j) { dma16<1024 * j>(rsrc, off[j], at); });
+        each<0, kPer>([&](auto j) { dma16<1024 * j>(rsrc, off[j] + at, to); });
       } else {
         each<0, kPer>([&](auto j) {
           const int row = (wave * kPer + j) * Sh::kRowsPerDma + lane / Sh::kChunks;
-          dma16<1024 * j>(rsrc, (live >> row) & 1 ? off[j] : kOOB, at);
+          dma16<1024 * j>(rsrc, (live >> row) & 1 ? off[j] + at : kOOB, to);
         });
       }
     } else {
-      const S* base = (const S*)h.data + head_at + (int64_t)row0 * h.st;
+      const S* base = (const S*)head + (int64_t)row0 * strides;
       for (int e = wave * 64 + lane; e < ROWS * DP; e += 64 * NW) {
         const int row = e / DP, d = e % DP;
         const bool in = d < D && row0 + row >= 0 && row0 + row < rows && ((live >> row) & 1);
         S x = 0;
-        if (in) x = base[(int64_t)row * h.st + d];
+        if (in) x = base[(int64_t)row * strides + d];
         const int chunk = d * Sh::kES / 16;
-        *(S*)(tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) = x;
+        *(__attribute__((address_space(3))) S*)(uintptr_t)(
+            tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) = x;
       }
     }
   }
@@ -406,14 +424,20 @@ __device__ __forceinline__ bool all_live(const uint32_t (&w)[KEYS / 32]) {
   return x == ~0u;
 }
 
-// Workgroups that read the same keys and values (the queries of a head, the
-// heads of a group) are given to one XCD one after another, so that they find
-// them in its L2; the longest first.
-__device__ __forceinline__ bool place(int heads, int tiles, int* head, int* tile) {
-  const int L = blockIdx.x, xcd = L & 7, at = L >> 3;
-  *head = xcd * ((heads + 7) / 8) + at / tiles;
-  *tile = at % tiles;
-  return at / tiles < (heads + 7) / 8 && *head < heads;
+// Head and tile of a workgroup (heads * tiles of them).  Workgroups that read the
+// same keys and values (the tiles of a head, the heads of a group) are given to one
+// XCD one after another, so that they find them in its L2; the heads left over by
+// eight go to all XCDs, tile by tile.
+__device__ __forceinline__ void place(int heads, int tiles, int* head, int* tile) {
+  const int L = blockIdx.x, each = heads / 8, rest = heads % 8, whole = 8 * each * tiles;
+  if (L < whole) {
+    const int at = L >> 3;
+    *head = (L & 7) * each + at / tiles;
+    *tile = at % tiles;
+  } else {
+    *head = 8 * each + (L - whole) % rest;
+    *tile = (L - whole) / rest;
+  }
 }
 
 }  // namespace attn
