@@ -24,9 +24,6 @@ namespace dpf {
 namespace attn {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kNT = 64 * kWaves;
-constexpr int kQ = 32 * kWaves;         // queries of a workgroup
 // The running maximum follows the scores only where they rise above it by more
 // than this (in powers of two): the weights then stay below 2^8, and a tile that
 // raises no maximum rescales nothing.
@@ -150,7 +147,7 @@ struct Sight {
 // weighted values, the next scores' maximum.  The order is written out, product by
 // product between fences, with every LDS operand read kAhead products early: left
 // to itself the compiler waits for each read, and puts all exponentials before all
-// products.  `loads` queues the loads of later tiles, behind the first reads.
+// products.  `loads` queues the loads of later tiles, number i, or all (-1).
 // Returns the maximum of the next scores, unscaled.
 template <class E, int DP, bool CURRENT, bool NEXT, class Loads>
 __device__ __forceinline__ float step(const Places& kt, const Places& vt,
@@ -165,6 +162,13 @@ __device__ __forceinline__ float step(const Places& kt, const Places& vt,
     s[j] = x;
     sum[j & 1] += x;
   };
+  // product u of the G + N: its share of the loads
+  const auto between = [&](int u) {
+    constexpr int L = Loads::kN, S = G + N;
+    each<0, L>([&](auto i) {
+      if (u == S * i / L + 1) loads(i);
+    });
+  };
   f32x16 x = {};
   Column<E> v[kAhead];
   const auto read = [&](int t) { return column_frag<E, DP>(vt, 0, t % DB, t / DB, lane); };
@@ -173,8 +177,7 @@ __device__ __forceinline__ float step(const Places& kt, const Places& vt,
 #pragma unroll
     for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 0, g);
     fence();
-    loads();
-    fence();
+    if constexpr (!CURRENT) loads(std::integral_constant<int, -1>());
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       x = mma<E>(k[g % kAhead], qf[g], x);
@@ -183,6 +186,7 @@ __device__ __forceinline__ float step(const Places& kt, const Places& vt,
       if constexpr (CURRENT) {
 #pragma unroll
         for (int j = 16 * g / G; j < 16 * (g + 1) / G; ++j) exponential(j);
+        between(g);
       }
       fence();
     }
@@ -190,7 +194,7 @@ __device__ __forceinline__ float step(const Places& kt, const Places& vt,
 #pragma unroll
     for (int t = 0; t < kAhead; ++t) v[t] = read(t);
     fence();
-    loads();
+    loads(std::integral_constant<int, -1>());
 #pragma unroll
     for (int j = 0; j < 16; ++j) exponential(j);
   }
@@ -220,6 +224,7 @@ __device__ __forceinline__ float step(const Places& kt, const Places& vt,
 #pragma unroll
         for (int j = 16 * t / N; j < 16 * (t + 1) / N; ++j) top = fmaxf(top, x[j]);
         asm volatile("" : "+v"(top));
+        between(G + t);
       }
       fence();
     }
@@ -230,6 +235,33 @@ __device__ __forceinline__ float step(const Places& kt, const Places& vt,
   if constexpr (NEXT) s = x;
   return top;
 }
+
+// The loads behind step t: tile t + 1's values and tile t + 2's keys.
+template <class E, int DP, int NW, bool VEC>
+struct Queue {
+  typedef Loader<E, DP, kKeys, NW, VEC> Load;
+  static constexpr int kPer = Load::kPer, kN = VEC ? 2 * kPer : 1;
+  static constexpr int kTile = kKeys * Shape<E, DP>::kRowBytes;
+  Load &k, &v;
+  uint32_t kt, vt;
+  int t, tiles, at;
+  uint64_t live;          // of tile t + 1
+  template <int I>
+  __device__ __forceinline__ void operator()(std::integral_constant<int, I>) const {
+    if constexpr (!VEC || I < 0) {
+      if (t + 1 < tiles) v(vt + ((t + 1) & 1) * kTile, at + kKeys, live);
+      if (t + 2 < tiles) k(kt + (t & 1) * kTile, at + 2 * kKeys, ~0ull);
+    } else if constexpr (I < kPer) {
+      v.template issue<I>();
+    } else {
+      k.template issue<I - kPer>();
+    }
+  }
+};
+struct NoLoads {
+  static constexpr int kN = 0;
+  __device__ __forceinline__ void operator()(std::integral_constant<int, -1>) const {}
+};
 
 // Moves the running maximum to scores of maximum `top` that are next.
 template <class E, int DP>
@@ -248,14 +280,16 @@ __device__ __forceinline__ void settle(State<E, DP>& st, float top, float c) {
   }
 }
 
-template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 4 ? 1 : DP == 64 ? 3 : 2) void
+// NW waves, 32 queries each, share the tiles.
+template <class E, int DP, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, sizeof(typename E::storage) == 4 ? 1 : DP == 64 ? 4 : 3) void
 attention_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
+  constexpr int kQ = 32 * NW;             // queries of a workgroup
   constexpr int kTile = kKeys * Sh::kRowBytes;
   extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // K [2], V [2] tiles
-  __shared__ int bound[2][kWaves];
+  __shared__ int bound[2][NW];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int tiles = (a.Tq + kQ - 1) / kQ;
   int head, tile;
@@ -277,7 +311,7 @@ attention_kernel(AttnArgs a) {
   __syncthreads();
   int lo = bound[0][0], end = bound[1][0];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) {
+  for (int w = 1; w < NW; ++w) {
     lo = min(lo, bound[0][w]);
     end = max(end, bound[1][w]);
   }
@@ -290,7 +324,7 @@ attention_kernel(AttnArgs a) {
   st.l = 0.0f;
   if (lo < end) {
     const int64_t kat = b * a.k.sb + hk * a.k.sh, vat = b * a.v.sb + hk * a.v.sh;
-    Loader<E, DP, kKeys, kWaves, VEC> load_k(a.k, a.Tk, a.D, wave, lane), load_v(a.v, a.Tk, a.D, wave, lane);
+    Loader<E, DP, kKeys, NW, VEC> load_k(a.k, a.Tk, a.D, wave, lane), load_v(a.v, a.Tk, a.D, wave, lane);
     const float c = a.scale * kLog2e;
     const Places pl = places<E, DP>(lane);
     const uint32_t kt = lds_addr(smem), vt = kt + 2 * kTile;
@@ -306,60 +340,30 @@ attention_kernel(AttnArgs a) {
     };
     load_k.start(a.k, kat, place_of(0));
     load_v.start(a.v, vat, place_of(0));
-    // keys' rows of masked positions need no zeros: their scores are selected away
-    const auto fetch_k = [&](int t) {
-      if (t < tiles) load_k(kt + (t & 1) * kTile, place_of(t), ~0ull);
+    const auto fetch = [&](int t) {
+      if (t >= tiles) return;
+      const uint64_t m = look(t);
+      // keys' rows of masked positions need no zeros: their scores are selected away
+      load_k(kt + (t & 1) * kTile, place_of(t), ~0ull);
+      load_v(vt + (t & 1) * kTile, place_of(t), m);
     };
-    const auto fetch_v = [&](int t, uint64_t m) { load_v(vt + (t & 1) * kTile, place_of(t), m); };
-    // tile t's values and tile t + 1's keys are there, and what the step before read
-    // is free
-    const auto arrive = [&]() {
-      wait_loads();
-      tile_barrier();
-    };
-    // the loads for the step after step t
-    uint64_t m = 0;
-    const auto loads = [&](int t) {
-      if (t + 1 < tiles) fetch_v(t + 1, m);
-      fetch_k(t + 2);
-    };
-    const auto pass = [&](int t) {
-      arrive();
-      if (t + 1 < tiles) m = look(t + 1);
-      loads(t);
-    };
-    const auto none = [] {};
-    const auto keys_at = [&](int t) { return in_tile(pl, kt + (t & 1) * kTile); };
-    const auto values_at = [&](int t) { return in_tile(pl, vt + (t & 1) * kTile); };
-    fetch_v(0, look(0));
-    fetch_k(0);
-    fetch_k(1);
+    fetch(0);
     Chunk<E> qf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
-    wait_loads();
-    tile_barrier();
-    int t = 0;
-    if (wlo < wend) {
-      // this wave's tiles; it keeps the workgroup's barriers before and after
-      const int from = wlo / kKeys - first, last = (wend - 1) / kKeys - first;
-      f32x16 s;
-      for (; t + 1 < from; ++t) pass(t);
-      if (from > 0) pass(t++);
-      settle<E, DP>(st, step<E, DP, false, true>(keys_at(t), values_at(t), qf, st, s, c, place_of(t), see,
-                                                 lane, none), c);
-      for (; t < last; ++t) {
-        arrive();
-        m = look(t + 1);
-        settle<E, DP>(st, step<E, DP, true, true>(keys_at(t + 1), values_at(t), qf, st, s, c,
-                                                  place_of(t + 1), see, lane, [&] { loads(t); }), c);
+    f32x16 s;
+    const NoLoads none;
+    for (int t = 0; t < tiles; ++t) {
+      const Sight now = see;
+      wait_loads();
+      tile_barrier();        // this tile is there; the other one has been read
+      fetch(t + 1);
+      if (place_of(t) < wend && place_of(t) + kKeys > wlo) {
+        const Places kn = in_tile(pl, kt + (t & 1) * kTile), vn = in_tile(pl, vt + (t & 1) * kTile);
+        settle<E, DP>(st, step<E, DP, false, true>(kn, vn, qf, st, s, c, place_of(t), now, lane, none), c);
+        step<E, DP, true, false>(kn, vn, qf, st, s, c, 0, now, lane, none);
       }
-      arrive();
-      if (t + 1 < tiles) m = look(t + 1);
-      step<E, DP, true, false>(keys_at(t), values_at(t), qf, st, s, c, 0, see, lane, [&] { loads(t); });
-      ++t;
     }
-    for (; t < tiles; ++t) pass(t);
   }
   if (!valid) return;
   const float l = st.l + lane_xor(st.l, 32);
@@ -438,7 +442,7 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
       const uint32_t base = own_tiles + buf * 2 * kTile;
       const Places kt = in_tile(at, base), vt = in_tile(at, base + kTile);
       f32x16 s;
-      const auto none = [] {};
+      const NoLoads none;
       settle<E, DP>(st, step<E, DP, false, true>(kt, vt, qf, st, s, c, k0, see, lane, none), c);
       step<E, DP, true, false>(kt, vt, qf, st, s, c, k0, see, lane, none);
       live[0] = next[0];
@@ -522,6 +526,18 @@ __global__ __launch_bounds__(64) void attention_join_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+template <class E, int DP, int NW, bool VEC>
+hipError_t tiled(const AttnArgs& a, hipStream_t s) {
+  constexpr int lds = 4 * kKeys * Shape<E, DP>::kRowBytes;
+  static hipError_t once = hipFuncSetAttribute((const void*)attention_kernel<E, DP, NW, VEC>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (once != hipSuccess) return once;
+  const int64_t tiles = (a.Tq + 32 * NW - 1) / (32 * NW);
+  hipLaunchKernelGGL((attention_kernel<E, DP, NW, VEC>), dim3((unsigned)(a.B * a.Hq * tiles)), dim3(64 * NW),
+                     lds, s, a);
+  return hipGetLastError();
+}
+
 template <class E, int DP, bool VEC>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
   typedef Shape<E, DP> Sh;
@@ -537,14 +553,7 @@ hipError_t forward(const AttnArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((attention_join_kernel<E, DP>), dim3(heads * rows), dim3(64), 0, s, a);
     return hipGetLastError();
   }
-  constexpr int lds = 4 * kKeys * Sh::kRowBytes;
-  static hipError_t once = hipFuncSetAttribute((const void*)attention_kernel<E, DP, VEC>,
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (once != hipSuccess) return once;
-  const int64_t tiles = (a.Tq + kQ - 1) / kQ, heads = (int64_t)a.B * a.Hq;
-  hipLaunchKernelGGL((attention_kernel<E, DP, VEC>), dim3((unsigned)(heads * tiles)),
-                     dim3(kNT), lds, s, a);
-  return hipGetLastError();
+  return tiled<E, DP, 4, VEC>(a, s);
 }
 
 template <class E>
