@@ -282,7 +282,7 @@ __device__ __forceinline__ void settle(State<E, DP>& st, float top, float c) {
 
 // NW waves, 32 queries each, share the tiles.
 template <class E, int DP, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, sizeof(typename E::storage) == 4 ? 1 : DP == 64 ? 4 : 3) void
+__global__ __launch_bounds__(64 * NW, sizeof(typename E::storage) == 4 ? 1 : !VEC ? 2 : DP == 64 ? 4 : 3) void
 attention_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
@@ -349,7 +349,7 @@ attention_kernel(AttnArgs a) {
     };
     fetch(0);
     Chunk<E> qf[Sh::kG];
-    row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
+    row_frags_from<E, DP, VEC>((const S*)a.q.data, b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
     f32x16 s;
     const NoLoads none;
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel
     if (k0 < end) fetch(k0, own_tiles);
     live[0] = next[0];
     Chunk<E> qf[Sh::kG];
-    row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
+    row_frags_from<E, DP, VEC>((const S*)a.q.data, b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
     const float c = a.scale * kLog2e;
     const Places at = places<E, DP>(lane);

@@ -35,7 +35,7 @@ template <> struct StepOf<F32> { static constexpr int kN = 32; };
 // keys and values through LDS.
 // ---------------------------------------------------------------------------
 template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 ? 2 : 1) void
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && VEC ? 2 : 1) void
 attention_dq_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
@@ -85,9 +85,9 @@ attention_dq_kernel(AttnArgs a) {
     load_k(tiles_at, k0, m);
     load_v(tiles_at + kTile, k0, m);
     Chunk<E> qf[Sh::kG], gf[Sh::kG];
-    row_frags_from<E, DP, VEC>((const S*)a.o.data + b * a.o.sb + hq * a.o.sh + (int64_t)i * a.o.st, some,
+    row_frags_from<E, DP, VEC>((const S*)a.o.data, b * a.o.sb + hq * a.o.sh + (int64_t)i * a.o.st, some,
                                a.D, lane, qf);
-    row_frags_from<E, DP, VEC>((const S*)a.dout.data + b * a.dout.sb + hq * a.dout.sh +
+    row_frags_from<E, DP, VEC>((const S*)a.dout.data, b * a.dout.sb + hq * a.dout.sh +
                                (int64_t)i * a.dout.st, some, a.D, lane, gf);
     float delta = 0.0f;
 #pragma unroll
@@ -96,7 +96,7 @@ attention_dq_kernel(AttnArgs a) {
       for (int k = 0; k < 16 / Sh::kES; ++k)
         delta = fmaf(E::to_float(qf[g][k]), E::to_float(gf[g][k]), delta);
     delta += lane_xor(delta, 32);
-    row_frags_from<E, DP, VEC>((const S*)a.q.data + b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
+    row_frags_from<E, DP, VEC>((const S*)a.q.data, b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
     const float base = some ? -a.lse[at] / a.scale : 0.0f;
     if (valid && h == 0) a.delta[at] = delta;
@@ -228,7 +228,7 @@ struct Dkv {
 };
 
 template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 ? 2 : 1) void
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && VEC ? 2 : 1) void
 attention_dkv_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
@@ -276,7 +276,7 @@ attention_dkv_kernel(AttnArgs a) {
     const float c = a.scale * kLog2e;
     const Places pl = places<E, DP>(lane);
     Chunk<E> kf[Sh::kG], vf[Z::kValuesInLds ? 1 : Sh::kG];
-    row_frags_from<E, DP, VEC>((const S*)a.k.data + b * a.k.sb + hk * a.k.sh + (int64_t)j0 * a.k.st, some,
+    row_frags_from<E, DP, VEC>((const S*)a.k.data, b * a.k.sb + hk * a.k.sh + (int64_t)j0 * a.k.st, some,
                                a.D, lane, kf);
     if constexpr (Z::kValuesInLds) {
       // what an inactive key's row holds reaches nothing but its own sums, which
@@ -287,7 +287,7 @@ attention_dkv_kernel(AttnArgs a) {
       for (int r = 0; r < kRows; r += 64)
         load_v(lds_addr(shared_tiles) + r * Sh::kRowBytes, tile * kRows + r, ~0ull);
     } else {
-      row_frags_from<E, DP, VEC>((const S*)a.v.data + b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st,
+      row_frags_from<E, DP, VEC>((const S*)a.v.data, b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st,
                                  some, a.D, lane, vf);
     }
     const float inv_scale = -1.0f / a.scale;

@@ -198,15 +198,28 @@ struct Loader {
       ready(tile, row0, live);
       each<0, kPer>([&](auto j) { issue<j>(); });
     } else {
-      const S* base = (const S*)head + (int64_t)row0 * strides;
-      for (int e = wave * 64 + lane; e < ROWS * DP; e += 64 * NW) {
-        const int row = e / DP, d = e % DP;
-        const bool in = d < D && row0 + row >= 0 && row0 + row < rows && ((live >> row) & 1);
-        S x = 0;
-        if (in) x = base[(int64_t)row * strides + d];
-        const int chunk = d * Sh::kES / 16;
-        *(__attribute__((address_space(3))) S*)(uintptr_t)(
-            tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) = x;
+      // kBatch loads in flight at a time; an element outside is loaded from the
+      // head's first one and not used
+      constexpr int kEach = ROWS * DP / (64 * NW), kBatch = kEach < 8 ? kEach : 8;
+#pragma unroll 1
+      for (int j0 = 0; j0 < kEach; j0 += kBatch) {
+        S x[kBatch];
+        uint32_t in = 0;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int e = (j0 + j) * 64 * NW + wave * 64 + lane, row = e / DP, d = e % DP, i = row0 + row;
+          const bool inside = d < D && i >= 0 && i < rows && ((live >> row) & 1);
+          x[j] = ((const S*)head)[inside ? (int64_t)i * strides + d : 0];
+          in |= (uint32_t)inside << j;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int e = (j0 + j) * 64 * NW + wave * 64 + lane, row = e / DP, d = e % DP;
+          const int chunk = d * Sh::kES / 16;
+          *(__attribute__((address_space(3))) S*)(uintptr_t)(
+              tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) =
+              (in >> j) & 1 ? x[j] : (S)0;
+        }
       }
     }
   }
@@ -269,24 +282,28 @@ __device__ __forceinline__ Chunk<E> row_frag(const Places& at, int row0, int g) 
   return lds_at<Chunk<E>>((at.row ^ (g << 5)) + row0 * Shape<E, DP>::kRowBytes);
 }
 
-// The row fragments of one row in memory (this lane's), zeros where !live.
+// The row fragments of one row in memory (this lane's: at element `at` of the array
+// `safe`), zeros where !live.
 template <class E, int DP, bool VEC>
-__device__ __forceinline__ void row_frags_from(const typename E::storage* row, bool live, int D, int lane,
+__device__ __forceinline__ void row_frags_from(const typename E::storage* safe, int64_t at, bool live, int D, int lane,
                                                Chunk<E> (&f)[Shape<E, DP>::kG]) {
   typedef Shape<E, DP> Sh;
   constexpr int kN = 16 / Sh::kES;
+  const typename E::storage* const row = safe + at;
 #pragma unroll
   for (int g = 0; g < Sh::kG; ++g) {
     const int d = (2 * g + (lane >> 5)) * kN;
-    Chunk<E> x = {};
     if constexpr (VEC) {
-      if (live && d < D) x = *(const Chunk<E>*)(row + d);
+      f[g] = Chunk<E>{};
+      if (live && d < D) f[g] = *(const Chunk<E>*)(row + d);
     } else {
 #pragma unroll
-      for (int k = 0; k < kN; ++k)
-        if (live && d + k < D) x[k] = row[d + k];
+      for (int k = 0; k < kN; ++k) {      // what is outside is loaded from the array's start, not used
+        const bool in = live && d + k < D;
+        const typename E::storage x = *(in ? row + (d + k) : safe);
+        f[g][k] = in ? x : (typename E::storage)0;
+      }
     }
-    f[g] = x;
   }
 }
 
