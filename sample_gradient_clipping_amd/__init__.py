@@ -13,7 +13,6 @@ and the pre-clip per-sample norms.  See include/dpfused.h for the contract.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import NamedTuple, Optional, Tuple
@@ -70,8 +69,8 @@ def _act(t) -> DpfAct:
 
 def _stream(t, stream) -> int:
     torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream(t.device)
+    if stream is None:      # torch.cuda.current_stream, without its Stream object (2 us)
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -676,23 +675,38 @@ def token_logprobs_backward(logits, targets, lse, dlogp, entropy=None, dentropy=
     return out
 
 
-def _on(device):
-    """Makes ``device`` the current one for a call whose stream is that device's."""
+def _call(fn, device, *args) -> None:
+    """Runs a library call whose stream is ``device``'s with that device the current one."""
     torch = _torch()
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    _lib.check(st)
 
 
-def _heads(t, name: str) -> DpfHeads:
-    if t.dim() != 4:
+def _heads(t, name: str) -> bytes:
+    """The bytes of t's dpf_heads, packed at once: filling a ctypes structure takes 4 us of the 20
+    that a call for single tokens has."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 4:
         raise ValueError(f"{name} must be [B, T, heads, D]")
     if not t.is_cuda:
         raise ValueError("tensors must be on the GPU")
-    B, T, H, D = t.shape
-    if D > 1 and t.stride(3) != 1:
+    if strides[3] != 1 and shape[3] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return DpfHeads(t.data_ptr(), _dtype_code(t), 0, B, T, H, D, t.stride(0), t.stride(1), t.stride(2))
+    return DpfHeads.pack(t.data_ptr(), _dtype_code(t), 0, *shape, *strides[:3])
+
+
+def _heads_out(t, like, name: str):
+    """(output, its dpf_heads): the caller's ``t``, of ``like``'s shape, dtype and device with any
+    strides, or a new one."""
+    if t is None:
+        t = like.new_empty(like.shape)
+    else:
+        _check_heads_out(t, like, name)
+    return t, _heads(t, name)
 
 
 def _check_heads_out(t, like, name: str) -> None:
@@ -737,20 +751,13 @@ def attention(q, k, v, mask=None, segments=None, causal: bool = True,
     dev = q.device
     _same_device(k, dev, "k")
     _same_device(v, dev, "v")
-    B, T = k.shape[0], k.shape[1]
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _check_heads_out(out, q, "out")
-    lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=dev)
-    oa = _heads(out, "out")
-    with _on(dev):
-        st = _lib.lib().dpfused_attention(
-            ctypes.byref(qa), ctypes.byref(ka), ctypes.byref(va), _mask_ptr(mask, B, T, dev),
-            _segments_ptr(segments, B, T, dev), int(bool(causal)),
-            math.nan if scale is None else float(scale), ctypes.byref(oa), lse.data_ptr(),
-            _stream(q, stream))
-    _lib.check(st)
+    B, T, _, _ = k.shape
+    out, oa = _heads_out(out, q, "out")
+    b, n, h, _ = q.shape
+    lse = torch.empty((b, h, n), dtype=torch.float32, device=dev)
+    _call(_lib.lib().dpfused_attention, dev, qa, ka, va, _mask_ptr(mask, B, T, dev),
+          _segments_ptr(segments, B, T, dev), int(bool(causal)),
+          math.nan if scale is None else float(scale), oa, lse.data_ptr(), _stream(q, stream))
     return AttentionOutput(out, lse)
 
 
@@ -760,29 +767,19 @@ def attention_backward(dout, q, k, v, out, lse, mask=None, segments=None, causal
 
     dq, dk and dv may be given, with any strides: as parts of one [B, T, (Hq + 2 Hkv) D] array
     they are the G of the fused projection's linear_clip_accumulate."""
-    torch = _torch()
     dev = q.device
     args = [_heads(t, name) for t, name in ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"))]
     for t, name in ((dout, "dout"), (k, "k"), (v, "v"), (out, "out")):
         _same_device(t, dev, name)
     _check_out(lse, (q.shape[0], q.shape[2], q.shape[1]), "lse", dev)
     B, T = k.shape[0], k.shape[1]
-    grads = []
-    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        if t is None:
-            t = torch.empty(like.shape, dtype=like.dtype, device=dev)
-        else:
-            _check_heads_out(t, like, name)
-        grads.append(t)
-    outs = [_heads(t, name) for t, name in zip(grads, ("dq", "dk", "dv"))]
-    with _on(dev):
-        st = _lib.lib().dpfused_attention_backward(
-            *[ctypes.byref(a) for a in args], lse.data_ptr(), _mask_ptr(mask, B, T, dev),
-            _segments_ptr(segments, B, T, dev), int(bool(causal)),
-            math.nan if scale is None else float(scale), *[ctypes.byref(a) for a in outs],
-            _stream(q, stream))
-    _lib.check(st)
-    return tuple(grads)
+    dq, a = _heads_out(dq, q, "dq")
+    dk, b = _heads_out(dk, k, "dk")
+    dv, c = _heads_out(dv, v, "dv")
+    _call(_lib.lib().dpfused_attention_backward, dev, *args, lse.data_ptr(),
+          _mask_ptr(mask, B, T, dev), _segments_ptr(segments, B, T, dev), int(bool(causal)),
+          math.nan if scale is None else float(scale), a, b, c, _stream(q, stream))
+    return dq, dk, dv
 
 
 def rotary_frequencies(dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -855,23 +852,13 @@ def qk_norm_rotary(q, k, q_weight=None, k_weight=None, freqs=None, positions=Non
 
     freqs: float64 [pairs], see rotary_frequencies (None: no rotation); positions [B, T] int32 or
     int64 (default 0 .. T - 1); rows whose mask byte is 0 give 0."""
-    torch = _torch()
     qa, ka = _heads(q, "q"), _heads(k, "k")
     qw, kw, fr, pairs, pos, mp = _rotary_args(q, k, q_weight, k_weight, freqs, positions, mask)
-    outs = []
-    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if t is None:
-            t = torch.empty(like.shape, dtype=like.dtype, device=q.device)
-        else:
-            _check_heads_out(t, like, name)
-        outs.append(t)
-    oq, ok = _heads(outs[0], "q_out"), _heads(outs[1], "k_out")
-    with _on(q.device):
-        st = _lib.lib().dpfused_qk_norm_rotary(
-            ctypes.byref(qa), ctypes.byref(ka), qw, kw, float(eps), fr, pairs, float(amplitude),
-            int(bool(interleaved)), pos, mp, ctypes.byref(oq), ctypes.byref(ok), _stream(q, stream))
-    _lib.check(st)
-    return outs[0], outs[1]
+    q_out, oq = _heads_out(q_out, q, "q_out")
+    k_out, ok = _heads_out(k_out, k, "k_out")
+    _call(_lib.lib().dpfused_qk_norm_rotary, q.device, qa, ka, qw, kw, float(eps), fr, pairs,
+          float(amplitude), int(bool(interleaved)), pos, mp, oq, ok, _stream(q, stream))
+    return q_out, k_out
 
 
 class QkGradients(NamedTuple):
@@ -899,24 +886,15 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, 
     _same_device(dq_out, dev, "dq_out")
     _same_device(dk_out, dev, "dk_out")
     qw, kw, fr, pairs, pos, mp = _rotary_args(q, k, q_weight, k_weight, freqs, positions, mask)
-    grads = []
-    for t, like, name in ((dq, q, "dq"), (dk, k, "dk")):
-        if t is None:
-            t = torch.empty(like.shape, dtype=like.dtype, device=dev)
-        else:
-            _check_heads_out(t, like, name)
-        grads.append(t)
+    dq, oq = _heads_out(dq, q, "dq")
+    dk, ok = _heads_out(dk, k, "dk")
     dqw = dkw = None
     if q_weight is not None and k_weight is not None:
         dqw, dkw = torch.empty((2, q.shape[0], 1, q.shape[3]), dtype=torch.float32, device=dev).unbind(0)
-    oq, ok = _heads(grads[0], "dq"), _heads(grads[1], "dk")
-    with _on(dev):
-        st = _lib.lib().dpfused_qk_norm_rotary_backward(
-            ctypes.byref(ga), ctypes.byref(gb), ctypes.byref(qa), ctypes.byref(ka), qw, kw, float(eps),
-            fr, pairs, float(amplitude), int(bool(interleaved)), pos, mp, ctypes.byref(oq),
-            ctypes.byref(ok), _ptr(dqw), _ptr(dkw), _stream(q, stream))
-    _lib.check(st)
-    return QkGradients(grads[0], grads[1], dqw, dkw)
+    _call(_lib.lib().dpfused_qk_norm_rotary_backward, dev, ga, gb, qa, ka, qw, kw, float(eps), fr,
+          pairs, float(amplitude), int(bool(interleaved)), pos, mp, oq, ok, _ptr(dqw), _ptr(dkw),
+          _stream(q, stream))
+    return QkGradients(dq, dk, dqw, dkw)
 
 
 def dropout(x, p: float, seed: int = 0, offset: int = 0, residual=None, mask=None, out=None,
@@ -928,11 +906,10 @@ def dropout(x, p: float, seed: int = 0, offset: int = 0, residual=None, mask=Non
     The gradient to x is dropout(dy, p, seed, offset), to the residual dy.  A call consumes
     dropout_blocks(x.numel()) blocks of the seed: advance offset by as much.  They are apart from
     the noise's blocks."""
-    torch = _torch()
     xa = _act(x)
     B, T, D = x.shape
     if out is None:
-        out = torch.empty((B, T, D), dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     for t, name in ((out, "out"), (residual, "residual")):
         if t is None:
             continue
@@ -941,12 +918,9 @@ def dropout(x, p: float, seed: int = 0, offset: int = 0, residual=None, mask=Non
         _same_device(t, x.device, name)
     ra = None if residual is None else _act(residual)
     oa = _act(out)
-    with _on(x.device):
-        st = _lib.lib().dpfused_dropout(
-            ctypes.byref(xa), None if ra is None else ctypes.byref(ra),
-            _mask_ptr(mask, B, T, x.device), float(p), int(seed), int(offset), ctypes.byref(oa),
-            _stream(x, stream))
-    _lib.check(st)
+    _call(_lib.lib().dpfused_dropout, x.device, ctypes.byref(xa),
+          None if ra is None else ctypes.byref(ra), _mask_ptr(mask, B, T, x.device), float(p),
+          int(seed), int(offset), ctypes.byref(oa), _stream(x, stream))
     return out
 
 

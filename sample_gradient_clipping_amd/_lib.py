@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdpfused.so")
 
@@ -63,6 +64,7 @@ class DpfHeads(ctypes.Structure):
         ("stride_t", ctypes.c_int64),
         ("stride_h", ctypes.c_int64),
     ]
+    pack = staticmethod(struct.Struct("Pii7q").pack)      # the same bytes, from the fields in order
 
 
 class DpfError(RuntimeError):
@@ -72,6 +74,8 @@ class DpfError(RuntimeError):
 
 
 _lib = None
+
+_HEADS = ctypes.c_void_p     # dpf_heads: a DpfHeads by reference, or its bytes
 
 # name -> (restype, argtypes)
 _SIGNATURES = {
@@ -146,24 +150,24 @@ _SIGNATURES = {
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(DpfAct),
         ctypes.c_void_p]),
     "dpfused_attention": (ctypes.c_int, [
-        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
-        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.POINTER(DpfHeads),
+        _HEADS, _HEADS, _HEADS,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, _HEADS,
         ctypes.c_void_p, ctypes.c_void_p]),
     "dpfused_attention_backward": (ctypes.c_int, [
-        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
-        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p,
-        ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.POINTER(DpfHeads),
-        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p]),
+        _HEADS, _HEADS, _HEADS,
+        _HEADS, _HEADS, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, _HEADS,
+        _HEADS, _HEADS, ctypes.c_void_p]),
     "dpfused_qk_norm_rotary": (ctypes.c_int, [
-        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p,
+        _HEADS, _HEADS, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int32,
-        ctypes.POINTER(DpfIds), ctypes.c_void_p, ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
+        ctypes.POINTER(DpfIds), ctypes.c_void_p, _HEADS, _HEADS,
         ctypes.c_void_p]),
     "dpfused_qk_norm_rotary_backward": (ctypes.c_int, [
-        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads),
-        ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
+        _HEADS, _HEADS, _HEADS,
+        _HEADS, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
         ctypes.c_int64, ctypes.c_float, ctypes.c_int32, ctypes.POINTER(DpfIds), ctypes.c_void_p,
-        ctypes.POINTER(DpfHeads), ctypes.POINTER(DpfHeads), ctypes.c_void_p, ctypes.c_void_p,
+        _HEADS, _HEADS, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_void_p]),
     "dpfused_dropout": (ctypes.c_int, [
         ctypes.POINTER(DpfAct), ctypes.POINTER(DpfAct), ctypes.c_void_p, ctypes.c_float,

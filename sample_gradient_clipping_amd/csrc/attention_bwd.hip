@@ -218,33 +218,47 @@ attention_dq_kernel(AttnArgs a) {
 // registers: a wave with both in registers would have its SIMD alone, and nothing
 // to overlap its exponentials with); tiles of queries and of their output
 // gradients go through LDS, for each head of the group in turn.
+//
+// SHARE, where the workgroups would be few: the four waves of a workgroup have the
+// same 32 keys, each with tiles of its own every fourth (head, queries) step, and
+// the first adds their sums in order.
 // ---------------------------------------------------------------------------
-template <class E, int DP>
+template <class E, int DP, bool SHARE>
 struct Dkv {
-  static constexpr int kN = sizeof(typename E::storage) == 2 && DP == 64 ? 64 : 32;   // queries of a tile
+  static constexpr int kKeys = SHARE ? 32 : kRows;                  // keys of a workgroup
+  // queries of a tile
+  static constexpr int kN = sizeof(typename E::storage) == 2 && DP == 64 && !SHARE ? 64 : 32;
+  static constexpr int kTile = kN * Shape<E, DP>::kRowBytes;
   static constexpr bool kValuesInLds = DP == 128;
-  static constexpr int kValues = kValuesInLds ? kRows * Shape<E, DP>::kRowBytes : 0;
-  static constexpr int kLds = kValues + 4 * kN * Shape<E, DP>::kRowBytes;
+  static constexpr int kValues = kValuesInLds ? kKeys * Shape<E, DP>::kRowBytes : 0;
+  // pairs of tiles of a set, sets of a workgroup
+  static constexpr int kPairs = SHARE && kTile * 16 + kValues > 150 * 1024 ? 1 : 2;
+  static constexpr int kSets = SHARE ? kWaves : 1;
+  static constexpr int kLds = kValues + kSets * kPairs * 2 * kTile;
+  // sums of all waves but one, where the tiles were
+  static_assert(!SHARE || kLds - kValues >= (kWaves - 1) * DP * 64 * 4, "room for the waves' sums");
+  static_assert(kLds <= 156 * 1024, "LDS");
 };
 
-template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && VEC ? 2 : 1) void
+template <class E, int DP, bool VEC, bool SHARE>
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && VEC && !SHARE ? 2 : 1) void
 attention_dkv_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
-  typedef Dkv<E, DP> Z;
-  constexpr int N = Z::kN;
-  constexpr int kTile = N * Sh::kRowBytes;
-  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char shared_tiles[];   // V, [2][Q, dO]
-  unsigned char* const smem = shared_tiles + Z::kValues;
+  typedef Dkv<E, DP, SHARE> Z;
+  constexpr int N = Z::kN, kTile = Z::kTile;
+  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char shared_tiles[];   // V, [sets][pairs][Q, dO]
   __shared__ int bound[2][kWaves];
-  __shared__ __attribute__((aligned(16))) float row_lse[2][N], row_delta[2][N];
+  __shared__ __attribute__((aligned(16))) float row_lse[Z::kSets][2][N],
+      row_delta[Z::kSets][2][N];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
-  const int tiles = (a.Tk + kRows - 1) / kRows, group = a.Hq / a.Hkv, off = a.Tk - a.Tq;
+  const int set = SHARE ? wave : 0;
+  const uint32_t smem = lds_addr(shared_tiles) + Z::kValues + set * Z::kPairs * 2 * kTile;
+  const int tiles = (a.Tk + Z::kKeys - 1) / Z::kKeys, group = a.Hq / a.Hkv, off = a.Tk - a.Tq;
   int head, tile;
   place(a.B * a.Hkv, tiles, &head, &tile);
   const int b = head / a.Hkv, hk = head % a.Hkv;
-  const int j0 = tile * kRows + wave * 32 + (lane & 31);
+  const int j0 = tile * Z::kKeys + (SHARE ? 0 : wave * 32) + (lane & 31);
   const bool valid = j0 < a.Tk;
   const Span sp = valid ? span_of(a, b, j0) : Span{0, 0};
   // positions whose queries see this key: [from, past), active
@@ -281,62 +295,85 @@ attention_dkv_kernel(AttnArgs a) {
     if constexpr (Z::kValuesInLds) {
       // what an inactive key's row holds reaches nothing but its own sums, which
       // are not used
-      Loader<E, DP, 64, kWaves, VEC> load_v(a.v, a.Tk, a.D, wave, lane);
-      load_v.start(a.v, b * a.v.sb + hk * a.v.sh, tile * kRows);
+      constexpr int kR = SHARE ? 32 : 64;
+      Loader<E, DP, kR, kWaves, VEC> load_v(a.v, a.Tk, a.D, wave, lane);
+      load_v.start(a.v, b * a.v.sb + hk * a.v.sh, tile * Z::kKeys);
 #pragma unroll
-      for (int r = 0; r < kRows; r += 64)
-        load_v(lds_addr(shared_tiles) + r * Sh::kRowBytes, tile * kRows + r, ~0ull);
+      for (int r = 0; r < Z::kKeys; r += kR)
+        load_v(lds_addr(shared_tiles) + r * Sh::kRowBytes, tile * Z::kKeys + r, ~0ull);
     } else {
       row_frags_from<E, DP, VEC>((const S*)a.v.data, b * a.v.sb + hk * a.v.sh + (int64_t)j0 * a.v.st,
                                  some, a.D, lane, vf);
     }
     const float inv_scale = -1.0f / a.scale;
-    const Places values = in_tile(pl, lds_addr(shared_tiles) + 32 * wave * Sh::kRowBytes);
+    const Places values = in_tile(pl, lds_addr(shared_tiles) + (SHARE ? 0 : 32 * wave) * Sh::kRowBytes);
     const auto value_frag = [&](int g) {
       if constexpr (Z::kValuesInLds) return row_frag<E, DP>(values, 0, g);
       else return vf[g];
     };
     uint32_t live[N / 32], next[N / 32];
-    float value = 0.0f;                   // of the next tile's lse (threads 0 ..) or delta (64 ..)
-    const int row = threadIdx.x & 63;
-    Loader<E, DP, N, kWaves, VEC> load_q(a.q, a.Tq, a.D, wave, lane), load_g(a.dout, a.Tq, a.D, wave, lane);
+    // this thread's row of the next tile: its lse (kind 0) or delta (kind 1)
+    float value = 0.0f;
+    const int row = SHARE ? lane & 31 : threadIdx.x & 63, kind = SHARE ? h : wave;
+    constexpr int kLoaders = SHARE ? 1 : kWaves;
+    Loader<E, DP, N, kLoaders, VEC> load_q(a.q, a.Tq, a.D, SHARE ? 0 : wave, lane),
+        load_g(a.dout, a.Tq, a.D, SHARE ? 0 : wave, lane);
     const auto fetch = [&](int p0, int hq, int buf) {
       uint64_t m = live_keys<N>(a, b, p0, next);
       if (p0 < off) m &= ~0ull << (off - p0);        // no queries at these positions
-      if (p0 == p_first) {                           // the next head
+      if (SHARE || p0 == p_first) {                  // the next head
         load_q.start(a.q, b * a.q.sb + hq * a.q.sh, p0 - off);
         load_g.start(a.dout, b * a.dout.sb + hq * a.dout.sh, p0 - off);
       }
-      const uint32_t to = lds_addr(smem) + buf * 2 * kTile;
+      const uint32_t to = smem + buf * 2 * kTile;
       load_q(to, p0 - off, m);
       load_g(to + kTile, p0 - off, m);
       const int i = p0 - off + row;
       value = 0.0f;
-      if (wave < 2 && row < N && i >= 0 && i < a.Tq && ((m >> row) & 1)) {
+      if (kind < 2 && row < N && i >= 0 && i < a.Tq && ((m >> row) & 1)) {
         const int64_t e = ((int64_t)b * a.Hq + hq) * a.Tq + i;
-        value = wave == 0 ? a.lse[e] * inv_scale : -a.delta[e];
+        value = kind == 0 ? a.lse[e] * inv_scale : -a.delta[e];
       }
     };
     const auto keep = [&](int buf) {
-      if (wave < 2 && row < N) (wave == 0 ? row_lse : row_delta)[buf][row] = value;
+      if (kind < 2 && row < N) (kind == 0 ? row_lse : row_delta)[set][buf][row] = value;
     };
-    fetch(p_first, hk * group, 0);
-    keep(0);
-    int buf = 0, p0 = p_first, hq = hk * group;
-    for (int it = 0; it < steps * group; ++it, buf ^= 1) {
+    constexpr int kStride = Z::kSets;      // a wave of SHARE takes every fourth step
+    const int all = steps * group;
+    const auto position = [&](int it) { return p_first + it % steps * N; };
+    const auto query_head = [&](int it) { return hk * group + it / steps; };
+    int buf = 0, p0 = position(set), hq = query_head(set);
+    if (set < all) {
+      fetch(p0, hq, 0);
+      keep(0);
+    }
+    if (SHARE && Z::kValuesInLds) {
+      if constexpr (VEC) wait_loads();
+      tile_barrier();        // the values are there
+    }
+    for (int it = set; it < all; it += kStride, buf ^= Z::kPairs - 1) {
 #pragma unroll
       for (int n = 0; n < N / 32; ++n) live[n] = next[n];
       int p1 = p0 + N, hq1 = hq;
-      if (p1 >= end) {
+      if (SHARE) {
+        p1 = position(it + kStride);
+        hq1 = query_head(it + kStride);
+      } else if (p1 >= end) {
         p1 = p_first;
         ++hq1;
       }
       if constexpr (VEC) wait_loads();
-      tile_barrier();        // this tile is there; the other one has been read
-      const bool more = it + 1 < steps * group;
-      if (more) fetch(p1, hq1, buf ^ 1);
+      // this tile is there; the other one has been read
+      if constexpr (SHARE) {
+        wait_lds();
+        asm volatile("" ::: "memory");
+      } else {
+        tile_barrier();
+      }
+      const bool more = it + kStride < all;
+      if (more && Z::kPairs == 2) fetch(p1, hq1, buf ^ 1);
       if (p0 < wend && p0 + N > wlo) {
-        const uint32_t here = lds_addr(smem) + buf * 2 * kTile;
+        const uint32_t here = smem + buf * 2 * kTile;
         const Places qt = in_tile(pl, here), gt = in_tile(pl, here + kTile);
         const bool full = p0 >= full_lo && p0 + N <= full_end && all_live<N>(live);
 // S starts from -lse / scale and dO V^T from -delta: P = 2^(c S), dS = P dP
@@ -384,7 +421,7 @@ attention_dkv_kernel(AttnArgs a) {
             u16x8 x[kAhead], v[2];
             f32x16 s, dp;
             Weights<E> pw, dw;
-            start(row_lse[buf], n, s);
+            start(row_lse[set][buf], n, s);
 #pragma unroll
             for (int t = 0; t < kAhead; ++t) x[t] = operand(t);
             fence();
@@ -398,7 +435,7 @@ attention_dkv_kernel(AttnArgs a) {
               else dk[db] = mma_column<E>(y, dw, half, dk[db]);
               if (t + kAhead < T) x[t % kAhead] = operand(t + kAhead);
               if (t + 2 >= G && t + 2 < 2 * G) v[t % 2] = value_frag(t + 2 - G);
-              if (t == G - 2) start(row_delta[buf], n, dp);
+              if (t == G - 2) start(row_delta[set][buf], n, dp);
               if (t >= G && t < 2 * G) {
 #pragma unroll
                 for (int j = 16 * (t - G) / G; j < 16 * (t - G + 1) / G; ++j) {
@@ -428,8 +465,8 @@ attention_dkv_kernel(AttnArgs a) {
 #pragma unroll
           for (int n = 0; n < N / 32; ++n) {
             f32x16 s, dp;
-            start(row_lse[buf], n, s);
-            start(row_delta[buf], n, dp);
+            start(row_lse[set][buf], n, s);
+            start(row_delta[set][buf], n, dp);
 #pragma unroll
             for (int g = 0; g < Sh::kG; ++g) s = mma<E>(row_frag<E, DP>(qt, 32 * n, g), kf[g], s);
 #pragma unroll
@@ -452,38 +489,89 @@ attention_dkv_kernel(AttnArgs a) {
           }
         }
       }
-      if (more) keep(buf ^ 1);
+      if (more && Z::kPairs == 1) {      // one pair of tiles: the next after this has been read
+        wait_lds();
+        asm volatile("" ::: "memory");
+        fetch(p1, hq1, 0);
+      }
+      if (more) keep(Z::kPairs == 2 ? buf ^ 1 : 0);
       p0 = p1;
       hq = hq1;
     }
+    if constexpr (SHARE) {     // the waves' sums, added in their order by the first
+      float* const sums = (float*)(shared_tiles + Z::kValues);
+      __syncthreads();
+      if (wave > 0) {
+#pragma unroll
+        for (int db = 0; db < Sh::kDB; ++db)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int at = (((wave - 1) * Sh::kDB + db) * 16 + j) * 128 + lane;
+            sums[at] = dk[db][j];
+            sums[at + 64] = dv[db][j];
+          }
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int w = 0; w < kWaves - 1; ++w)
+#pragma unroll
+          for (int db = 0; db < Sh::kDB; ++db)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int at = ((w * Sh::kDB + db) * 16 + j) * 128 + lane;
+              dk[db][j] += sums[at];
+              dv[db][j] += sums[at + 64];
+            }
+      }
+    }
   }
-  if (!valid) return;
+  if (!valid || (SHARE && wave > 0)) return;
   store_row<E, DP, VEC>((S*)a.dk.data + b * a.dk.sb + hk * a.dk.sh + (int64_t)j0 * a.dk.st, dk,
                         some, a.scale, a.D, lane);
   store_row<E, DP, VEC>((S*)a.dv.data + b * a.dv.sb + hk * a.dv.sh + (int64_t)j0 * a.dv.st, dv,
                         some, 1.0f, a.D, lane);
 }
 
+template <class E, int DP, bool VEC, bool SHARE>
+hipError_t backward_keys(const AttnArgs& a, hipStream_t s) {
+  typedef Dkv<E, DP, SHARE> Z;
+  static hipError_t once = hipFuncSetAttribute((const void*)attention_dkv_kernel<E, DP, VEC, SHARE>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
+  if (once != hipSuccess) return once;
+  const int64_t groups = (int64_t)a.B * a.Hkv * ((a.Tk + Z::kKeys - 1) / Z::kKeys);
+  timing_begin("attention_dkv", s);
+  hipLaunchKernelGGL((attention_dkv_kernel<E, DP, VEC, SHARE>), dim3((unsigned)groups), dim3(kNT), Z::kLds, s,
+                     a);
+  timing_end("attention_dkv", s);
+  return hipGetLastError();
+}
+
 template <class E, int DP, bool VEC>
 hipError_t backward(const AttnArgs& a, hipStream_t s) {
   typedef Shape<E, DP> Sh;
-  constexpr int lds = 4 * StepOf<E>::kN * Sh::kRowBytes, dkv_lds = Dkv<E, DP>::kLds;
-  static hipError_t once[2] = {
-      hipFuncSetAttribute((const void*)attention_dq_kernel<E, DP, VEC>,
-                          hipFuncAttributeMaxDynamicSharedMemorySize, lds),
-      hipFuncSetAttribute((const void*)attention_dkv_kernel<E, DP, VEC>,
-                          hipFuncAttributeMaxDynamicSharedMemorySize, dkv_lds)};
-  if (once[0] != hipSuccess) return once[0];
-  if (once[1] != hipSuccess) return once[1];
-  const int64_t qt = (a.Tq + kRows - 1) / kRows, kt = (a.Tk + kRows - 1) / kRows;
-  const int64_t qh = (int64_t)a.B * a.Hq, kh = (int64_t)a.B * a.Hkv;
+  constexpr int lds = 4 * StepOf<E>::kN * Sh::kRowBytes;
+  static hipError_t once = hipFuncSetAttribute((const void*)attention_dq_kernel<E, DP, VEC>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (once != hipSuccess) return once;
+  const int64_t qt = (a.Tq + kRows - 1) / kRows;
   timing_begin("attention_dq", s);
-  hipLaunchKernelGGL((attention_dq_kernel<E, DP, VEC>), dim3((unsigned)(qh * qt)), dim3(kNT), lds, s, a);
+  hipLaunchKernelGGL((attention_dq_kernel<E, DP, VEC>), dim3((unsigned)((int64_t)a.B * a.Hq * qt)), dim3(kNT),
+                     lds, s, a);
   timing_end("attention_dq", s);
-  timing_begin("attention_dkv", s);
-  hipLaunchKernelGGL((attention_dkv_kernel<E, DP, VEC>), dim3((unsigned)(kh * kt)), dim3(kNT), dkv_lds, s, a);
-  timing_end("attention_dkv", s);
-  return hipGetLastError();
+  // Few workgroups leave compute units idle and give a wave a long chain of steps.
+  // dk and dv with and without SHARE, us (bf16, f32):
+  //   48 workgroups, 16 steps, heads of 64    15.6 / 21.4    36.6 /  111
+  //   96 workgroups, 16 steps, heads of 64    22.4 / 21.3    49.6 /  111
+  //  128 workgroups, 32 steps, heads of 128   48.8 / 53.4     157 /  375
+  //  128 workgroups, 320 steps, heads of 128   217 /  436    1155 / 3633
+  //  192 workgroups, 8 steps, heads of 64     28.2 / 15.8    62.4 / 62.6
+  //  256 workgroups, 64 steps, heads of 128    129 /   97     519 /  739
+  constexpr bool kWide = sizeof(typename E::storage) == 4;
+  const int64_t groups = (int64_t)a.B * a.Hkv * ((a.Tk + kRows - 1) / kRows);
+  const int64_t steps = (int64_t)(a.Hq / a.Hkv) * ((a.Tq + 31) / 32);
+  const bool share = groups <= 64 || (groups <= (kWide ? 256 : 128) && steps >= (kWide ? 16 : 32));
+  return share ? backward_keys<E, DP, VEC, true>(a, s) : backward_keys<E, DP, VEC, false>(a, s);
 }
 
 template <class E>

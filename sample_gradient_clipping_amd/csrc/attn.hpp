@@ -200,7 +200,7 @@ struct Loader {
     } else {
       // kBatch loads in flight at a time; an element outside is loaded from the
       // head's first one and not used
-      constexpr int kEach = ROWS * DP / (64 * NW), kBatch = kEach < 8 ? kEach : 8;
+      constexpr int kEach = ROWS * DP / (64 * NW), kMost = NW == 1 ? 32 : 8, kBatch = kEach < kMost ? kEach : kMost;
 #pragma unroll 1
       for (int j0 = 0; j0 < kEach; j0 += kBatch) {
         S x[kBatch];

@@ -424,3 +424,15 @@ def test_longer_sequences(dtype):
     _check(*_draw(rng, 1, 1500, 1500, 2, 1, 128, dtype), dtype)
     _check(*_draw(rng, 2, 1111, 1111, 1, 1, 64, dtype), dtype, mask=_mask(rng, "prefix", 2, 1111),
            segments=_segments(rng, 2, 1111, 3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 45, 128, 99])
+def test_many_workgroups(D, dtype):
+    """More heads than compute units take at a time, of a length that ends inside a tile: the
+    backward pass then gives each wave keys of its own."""
+    rng = np.random.default_rng(14)
+    _check(*_draw(rng, 5, 70, 70, 54, 27, D, dtype), dtype, mask=_mask(rng, "prefix", 5, 70))
+    _check(*_draw(rng, 33, 33, 41, 4, 4, D, dtype), dtype)
+    _check(*_draw(rng, 29, 130, 130, 3, 3, D, dtype), dtype, causal=False,
+           segments=_segments(rng, 29, 130, 3))
