@@ -122,6 +122,35 @@ __device__ __forceinline__ void each(const F& f) {
   }
 }
 
+// 16 bytes of a row: 8 bf16 or 4 float32 elements, the operand of one
+// 32x32x16 or four 32x32x2 products (k = lane half, then element).
+template <class E> struct ChunkOf;
+template <> struct ChunkOf<BF16> { typedef u16x8 type; };
+template <> struct ChunkOf<F32> { typedef f32x4 type; };
+template <class E> using Chunk = typename ChunkOf<E>::type;
+
+// Entries d .. of a row of D (zeros past D, and all zeros where !in, though the row
+// is read: it lies inside the tensor), of any alignment: the last piece is read from
+// further back, so that nothing past the row is touched, and moved down.
+template <class E>
+__device__ __forceinline__ Chunk<E> load_piece(const typename E::storage* row, int d, int D, bool in) {
+  typedef typename E::storage S;
+  constexpr int kN = 16 / sizeof(S);
+  Chunk<E> x = {};
+  if (D >= kN) {
+    const int back = max(min(d, D) + kN - D, 0);
+    unsigned __int128 y;
+    __builtin_memcpy(&y, row + (min(d, D) - back), 16);
+    y = in && d < D ? y >> (8 * (int)sizeof(S) * (back & (kN - 1))) : 0;
+    x = __builtin_bit_cast(Chunk<E>, y);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kN; ++k)
+      if (in && d + k < D) x[k] = row[d + k];
+  }
+  return x;
+}
+
 // Brings rows [row0, row0 + ROWS) of one head's `rows` rows into an LDS tile, by
 // NW waves (wave w of them).  Rows outside [0, rows) and those whose bit of `live`
 // is 0 become zeros (of a negative row0 the caller's live has zeros there), and so
@@ -129,7 +158,7 @@ __device__ __forceinline__ void each(const F& f) {
 // Scalar instructions are not free (a wave issues one in about five cycles): a
 // lane's offsets within a tile are formed once and a buffer descriptor serves the
 // 2^30 bytes after its first row, so that a tile costs a dozen of them.  Not VEC:
-// element by element, there after a barrier.
+// through registers, in pieces of any alignment, there after a barrier.
 template <class E, int DP, int ROWS, int NW, bool VEC>
 struct Loader {
   typedef Shape<E, DP> Sh;
@@ -198,39 +227,24 @@ struct Loader {
       ready(tile, row0, live);
       each<0, kPer>([&](auto j) { issue<j>(); });
     } else {
-      // kBatch loads in flight at a time; an element outside is loaded from the
-      // head's first one and not used
-      constexpr int kEach = ROWS * DP / (64 * NW), kMost = NW == 1 ? 32 : 8, kBatch = kEach < kMost ? kEach : kMost;
-#pragma unroll 1
-      for (int j0 = 0; j0 < kEach; j0 += kBatch) {
-        S x[kBatch];
-        uint32_t in = 0;
+      // all loads in flight, a piece outside from the head's first row and not used
+      constexpr int kEach = ROWS * Sh::kChunks / (64 * NW);
+      Chunk<E> x[kEach];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int e = (j0 + j) * 64 * NW + wave * 64 + lane, row = e / DP, d = e % DP, i = row0 + row;
-          const bool inside = d < D && i >= 0 && i < rows && ((live >> row) & 1);
-          x[j] = ((const S*)head)[inside ? (int64_t)i * strides + d : 0];
-          in |= (uint32_t)inside << j;
-        }
+      for (int j = 0; j < kEach; ++j) {
+        const int e = (j * NW + wave) * 64 + lane, row = e / Sh::kChunks, i = row0 + row;
+        const bool in = i >= 0 && i < rows && ((live >> row) & 1);
+        x[j] = load_piece<E>((const S*)head + (in ? i : 0) * strides, e % Sh::kChunks * (16 / Sh::kES), D, in);
+      }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int e = (j0 + j) * 64 * NW + wave * 64 + lane, row = e / DP, d = e % DP;
-          const int chunk = d * Sh::kES / 16;
-          *(__attribute__((address_space(3))) S*)(uintptr_t)(
-              tile + row * Sh::kRowBytes + 16 * (chunk ^ swz<Sh::kChunks>(row)) + d * Sh::kES % 16) =
-              (in >> j) & 1 ? x[j] : (S)0;
-        }
+      for (int j = 0; j < kEach; ++j) {
+        const int e = (j * NW + wave) * 64 + lane, row = e / Sh::kChunks;
+        *(__attribute__((address_space(3))) Chunk<E>*)(uintptr_t)(
+            tile + row * Sh::kRowBytes + 16 * ((e % Sh::kChunks) ^ swz<Sh::kChunks>(row))) = x[j];
       }
     }
   }
 };
-
-// 16 bytes of a row: 8 bf16 or 4 float32 elements, the operand of one
-// 32x32x16 or four 32x32x2 products (k = lane half, then element).
-template <class E> struct ChunkOf;
-template <> struct ChunkOf<BF16> { typedef u16x8 type; };
-template <> struct ChunkOf<F32> { typedef f32x4 type; };
-template <class E> using Chunk = typename ChunkOf<E>::type;
 
 template <class E>
 __device__ __forceinline__ f32x16 mma(const Chunk<E>& x, const Chunk<E>& y, f32x16 c) {
@@ -297,12 +311,7 @@ __device__ __forceinline__ void row_frags_from(const typename E::storage* safe, 
       f[g] = Chunk<E>{};
       if (live && d < D) f[g] = *(const Chunk<E>*)(row + d);
     } else {
-#pragma unroll
-      for (int k = 0; k < kN; ++k) {      // what is outside is loaded from the array's start, not used
-        const bool in = live && d + k < D;
-        const typename E::storage x = *(in ? row + (d + k) : safe);
-        f[g][k] = in ? x : (typename E::storage)0;
-      }
+      f[g] = load_piece<E>(live ? row : safe, d, D, live);
     }
   }
 }
@@ -401,22 +410,25 @@ __device__ __forceinline__ void store_row(typename E::storage* row, const f32x16
       float x[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = live ? acc[db][4 * i + k] * f : 0.0f;
-      if constexpr (VEC) {
-        if (d < D) {
-          if constexpr (sizeof(typename E::storage) == 2) {
-            typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-            *(u2*)(row + d) = u2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-          } else {
-            store_f32<E, 4>(row + d, x);
-          }
-        }
+      typedef typename E::storage S;
+      typedef S four __attribute__((ext_vector_type(4)));
+      four y;
+      if constexpr (sizeof(S) == 2) {
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        y = __builtin_bit_cast(four, u2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])});
       } else {
+        y = four{x[0], x[1], x[2], x[3]};
+      }
+      if constexpr (VEC) {
+        if (d < D) *(four*)(row + d) = y;
+      } else {
+        if (d + 4 <= D) {
+          __builtin_memcpy(row + d, &y, sizeof(y));
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (d + k < D) {
-            const float y[1] = {x[k]};
-            store_f32<E, 1>(row + d + k, y);
-          }
+          for (int k = 0; k < 3; ++k)
+            if (d + k < D) row[d + k] = y[k];
+        }
       }
     }
 }
