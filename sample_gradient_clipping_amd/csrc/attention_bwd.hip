@@ -241,7 +241,7 @@ struct Dkv {
 };
 
 template <class E, int DP, bool VEC, bool SHARE>
-__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && VEC && !SHARE ? 2 : 1) void
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && !SHARE ? 2 : 1) void
 attention_dkv_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;

@@ -280,18 +280,26 @@ __global__ __launch_bounds__(kNT) void qk_norm_rotary_backward_kernel(RotaryArgs
   }
 }
 
-// dw[b][d] = the chunks' sums in order: 8 threads per entry, each every eighth
-// chunk, then their sums.
+// dw[b][d] = the chunks' sums: kSlices threads per entry, each every kSlices-th
+// chunk, then their sums in order.
+constexpr int kSlices = 16, kEntries = kNT / kSlices;
 __global__ __launch_bounds__(kNT) void qk_norm_weights_kernel(RotaryArgs a, int chunks) {
-  const int64_t e = (int64_t)blockIdx.x * (kNT / 8) + threadIdx.x / 8;
-  const int k = threadIdx.x & 7;
-  const int64_t b = e / (2 * a.D);
-  const int which = (int)(e % (2 * a.D)) / a.D, d = (int)(e % a.D);
+  __shared__ float sums[kSlices][kEntries];
+  const int x = threadIdx.x % kEntries, k = threadIdx.x / kEntries;
+  const int64_t e = (int64_t)blockIdx.x * kEntries + x, b = e / (2 * a.D);
+  const int i = (int)(e % (2 * a.D));
   float s = 0.0f;
-  if (b < a.B)
-    for (int c = k; c < chunks; c += 8) s += a.part[((b * chunks + c) * 2 + which) * a.D + d];
-  s = group_sum<8>(s);
-  if (b < a.B && k == 0) (which == 0 ? a.dwq : a.dwk)[b * a.D + d] = s;
+  if (b < a.B) {
+    const float* from = a.part + b * chunks * 2 * a.D + i;
+#pragma unroll 8
+    for (int c = k; c < chunks; c += kSlices) s += from[(int64_t)c * 2 * a.D];
+  }
+  sums[k][x] = s;
+  __syncthreads();
+  if (b >= a.B || k != 0) return;
+#pragma unroll
+  for (int j = 1; j < kSlices; ++j) s += sums[j][x];
+  (i < a.D ? a.dwq : a.dwk)[b * a.D + i % a.D] = s;
 }
 
 int64_t chunks_of(const RotaryArgs& a) { return (a.T + a.tokens - 1) / a.tokens; }
@@ -368,7 +376,7 @@ hipError_t launch_qk_norm_rotary_backward(const RotaryArgs& a, hipStream_t s) {
   timing_end("qk_norm_rotary_backward", s);
   if (e != hipSuccess || a.wq == nullptr) return e;
   timing_begin("qk_norm_weights", s);
-  hipLaunchKernelGGL(qk_norm_weights_kernel, dim3((unsigned)((a.B * 2 * a.D + kNT / 8 - 1) / (kNT / 8))),
+  hipLaunchKernelGGL(qk_norm_weights_kernel, dim3((unsigned)((a.B * 2 * a.D + kEntries - 1) / kEntries)),
                      dim3(kNT), 0, s, a, (int)chunks_of(a));
   timing_end("qk_norm_weights", s);
   return hipGetLastError();
