@@ -600,7 +600,9 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  *
  * Scores, softmax and sums are float32; for bf16 inputs the weights
  * e^{s_ij - m} are rounded to bf16 for their product with the values.  bf16
- * products run on bf16 matrix cores, float32 ones on float32 ones.
+ * products run on bf16 matrix cores, float32 ones on float32 ones.  A score
+ * whose D products have magnitudes that sum to a is off by up to D 2^-24 scale a,
+ * and its weight by that relative to it: scores of 10^4 and more are not for this.
  *
  * A NaN or infinity in an active position reaches the outputs of its own
  * sample (of any of its positions that share a tile of keys, also those that
@@ -613,7 +615,7 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  *              position, not decreasing along T (else some pairs of equal
  *              numbers do not see each other; nothing worse)
  *   causal     0 or 1
- *   scale      finite and > 0, or NaN for 1 / sqrt(D)
+ *   scale      2^-64 .. 2^64, or NaN for 1 / sqrt(D)
  *   out        like q; must not overlap an input
  *   lse        [B, Hq, Tq] float32, contiguous (the backward call's input)
  *

@@ -1937,8 +1937,9 @@ dpf_status check_attention(const dpf_heads* q, const dpf_heads* k, const dpf_hea
   if (q->H % k->H != 0)
     return fail(DPF_ERR_INVALID_ARGUMENT, "the queries' heads are not a multiple of the keys'");
   if (causal != 0 && causal != 1) return fail(DPF_ERR_INVALID_ARGUMENT, "causal must be 0 or 1");
-  if (!std::isnan(scale) && !(scale > 0.0f && std::isfinite(scale)))
-    return fail(DPF_ERR_INVALID_ARGUMENT, "scale must be finite and > 0 (or NaN for the default)");
+  // the backward pass starts its scores from -lse / scale, which has to be finite
+  if (!std::isnan(scale) && !(scale >= 0x1p-64f && scale <= 0x1p64f))
+    return fail(DPF_ERR_INVALID_ARGUMENT, "scale must lie in 2^-64 .. 2^64 (or be NaN for the default)");
   if (q->D > dpf::kAttnMaxD) return fail(DPF_ERR_UNSUPPORTED, "heads are wider than 128");
   if (k->T > dpf::kAttnMaxT || q->B > dpf::kAttnMaxTiles || q->H > dpf::kAttnMaxTiles ||
       q->B * q->H > dpf::kAttnMaxTiles / ((k->T + 31) / 32))

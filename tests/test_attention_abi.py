@@ -298,3 +298,11 @@ def test_oracle_dropout_law():
     from oracle.philox import philox_words_scalar
     noise = np.array(philox_words_scalar(7, 3, 2), np.uint32).view(np.uint16)
     assert not np.array_equal(noise.reshape(-1), bits[:16])               # apart from the noise's
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -65, 1e-38, 2.0 ** 65, 3e38])
+def test_scale_out_of_range(scale):
+    """lse / scale has to stay finite."""
+    L = _lib.lib()
+    assert _forward(L, scale=scale) == BAD
+    assert _backward(L, scale=scale) == BAD

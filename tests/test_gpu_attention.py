@@ -436,3 +436,54 @@ def test_many_workgroups(D, dtype):
     _check(*_draw(rng, 33, 33, 41, 4, 4, D, dtype), dtype)
     _check(*_draw(rng, 29, 130, 130, 3, 3, D, dtype), dtype, causal=False,
            segments=_segments(rng, 29, 130, 3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 2.0 ** -30])
+def test_smallest_scales(scale, dtype):
+    """All weights of a row alike: lse = log n, lse / scale up to 10^20.  (The scores' sums then
+    round at lse / scale, D = 16 terms of half a step of lse <= 5.1 each: 82 u of a weight, within
+    the bar's Tk + 16 = 166.)"""
+    rng = np.random.default_rng(15)
+    _check(*_draw(rng, 2, 150, 150, 2, 1, 16, dtype), dtype, mask=_mask(rng, "holes", 2, 150), scale=scale)
+
+
+@pytest.mark.parametrize("D", [64, 45, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_queries_beside_nan(D, dtype):
+    """Rows whose own mask byte is 0 give exact zeros and take part in no gradient, though the rows
+    beside them, in the same tile, hold NaN; other samples are not touched."""
+    torch = need_gpu()
+    import sample_gradient_clipping_amd as dp
+    rng = np.random.default_rng(16)
+    B, T, H = 2, 70, 2
+    q, k, v, g = (to_dev(x, dtype, torch) for x in _draw(rng, B, T, T, H, H, D, dtype))
+    mask = np.ones((B, T), np.uint8)
+    mask[:, 1::2] = 0
+    m = _dev(torch, mask)
+    clean = dp.attention(q, k, v, mask=m)
+    clean_grads = dp.attention_backward(g, q, k, v, clean.out, clean.lse, mask=m)
+    for t in (q, k, v, g):
+        t[0, 0] = float("nan")          # an active position of the first sample
+        t[:, 1::2] = float("nan")       # masked ones of both
+    r = dp.attention(q, k, v, mask=m)
+    grads = dp.attention_backward(g, q, k, v, r.out, r.lse, mask=m)
+    torch.cuda.synchronize()
+    for x in (r.out, *grads):
+        assert (x[:, 1::2] == 0).all()
+    assert (r.lse[:, :, 1::2] == 0).all()
+    for x, y in zip((r.out, r.lse, *grads), (clean.out, clean.lse, *clean_grads)):
+        assert torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_far_from_zero(sign, dtype):
+    """Every score near -300 or 300, where e^s is 0 or infinite in float32, with masked keys and
+    queries in each tile: only differences of scores may be raised."""
+    rng = np.random.default_rng(17)
+    q, k, v, dout = _draw(rng, 2, 100, 100, 2, 1, 64, "f32", spread=0.1)
+    q[..., 0], k[..., 0] = 48.0, sign * 50.0
+    if dtype == "bf16":
+        q, k, v, dout = (to_storage(x, dtype) for x in (q, k, v, dout))
+    _check(q, k, v, dout, dtype, mask=_mask(rng, "holes", 2, 100))
