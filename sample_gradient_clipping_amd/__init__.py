@@ -890,7 +890,9 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, 
     dk, ok = _heads_out(dk, k, "dk")
     dqw = dkw = None
     if q_weight is not None and k_weight is not None:
-        dqw, dkw = torch.empty((2, q.shape[0], 1, q.shape[3]), dtype=torch.float32, device=dev).unbind(0)
+        # two allocations: the calls that take them as G want 16-byte alignment
+        dqw, dkw = (torch.empty((q.shape[0], 1, q.shape[3]), dtype=torch.float32, device=dev)
+                    for _ in range(2))
     _call(_lib.lib().dpfused_qk_norm_rotary_backward, dev, ga, gb, qa, ka, qw, kw, float(eps), fr,
           pairs, float(amplitude), int(bool(interleaved)), pos, mp, oq, ok, _ptr(dqw), _ptr(dkw),
           _stream(q, stream))

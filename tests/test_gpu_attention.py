@@ -485,5 +485,5 @@ def test_scores_far_from_zero(sign, dtype):
     q, k, v, dout = _draw(rng, 2, 100, 100, 2, 1, 64, "f32", spread=0.1)
     q[..., 0], k[..., 0] = 48.0, sign * 50.0
     if dtype == "bf16":
-        q, k, v, dout = (to_storage(x, dtype) for x in (q, k, v, dout))
+        q, k, v, dout = (f32_to_bf16_bits(x) for x in (q, k, v, dout))
     _check(q, k, v, dout, dtype, mask=_mask(rng, "holes", 2, 100))
