@@ -100,6 +100,10 @@ attention_dq_kernel(AttnArgs a) {
                                a.D, lane, qf);
     const float base = some ? -a.lse[at] / a.scale : 0.0f;
     if (valid && h == 0) a.delta[at] = delta;
+    // a wave whose keys all lie in one tile takes delta as sum_j P_ij dO_i . v_j:
+    // from the rounded output it is off by 2^-9 of |dO| |O|, which shows where the
+    // keys are few
+    const bool once = sizeof(S) == 2 && wlo / KEYS == (wend - 1) / KEYS;
     const float c = a.scale * kLog2e;
     const Places pl = places<E, DP>(lane);
     int buf = 0;
@@ -136,6 +140,27 @@ attention_dq_kernel(AttnArgs a) {
           }
         };
         if constexpr (sizeof(S) == 2) {
+          if (once) {
+            float sum = 0.0f;
+#pragma unroll 1
+            for (int n = 0; n < KEYS / 32; ++n) {
+              const Places kt = in_tile(pl, here + n * 32 * Sh::kRowBytes);
+              const Places vt = in_tile(pl, here + kTile + n * 32 * Sh::kRowBytes);
+              f32x16 s, dp;
+              start(s, dp);
+#pragma unroll
+              for (int g = 0; g < Sh::kG; ++g) {
+                s = mma<E>(row_frag<E, DP>(kt, 0, g), qf[g], s);
+                dp = mma<E>(row_frag<E, DP>(vt, 0, g), gf[g], dp);
+                fence();
+              }
+              mask(n, s);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum = fmaf(__builtin_amdgcn_exp2f(s[j] * c), dp[j], sum);
+            }
+            delta += sum + lane_xor(sum, 32);     // dp started from -delta
+            if (some && h == 0) a.delta[((int64_t)b * a.Hq + hq) * a.Tq + i] = delta;
+          }
           // per block of 32 keys G products for S, G for dP with the exponentials
           // between them, 2 DB for dq; operands read kAhead products early
           constexpr int G = Sh::kG, DB = Sh::kDB, T = 2 * G + 2 * DB;
