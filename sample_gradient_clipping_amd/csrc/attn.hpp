@@ -470,13 +470,19 @@ __device__ __forceinline__ bool all_live(const uint32_t (&w)[KEYS / 32]) {
 // Head and tile of a workgroup (heads * tiles of them).  Workgroups that read the
 // same keys and values (the tiles of a head, the heads of a group) are given to one
 // XCD one after another, so that they find them in its L2; the heads left over by
-// eight go to all XCDs, tile by tile.
+// eight go to all XCDs, tile by tile.  An XCD takes its heads in sets of up to
+// kHeadsAtOnce, a set's first tiles (callers count from the longest ones of a
+// causal call) before its next: head after head, the last head's long tiles came
+// last and left compute units idle.
+constexpr int kHeadsAtOnce = 8;
 __device__ __forceinline__ void place(int heads, int tiles, int* head, int* tile) {
   const int L = blockIdx.x, each = heads / 8, rest = heads % 8, whole = 8 * each * tiles;
   if (L < whole) {
-    const int at = L >> 3;
-    *head = (L & 7) * each + at / tiles;
-    *tile = at % tiles;
+    const int sets = (each + kHeadsAtOnce - 1) / kHeadsAtOnce, most = (each + sets - 1) / sets;
+    const int at = L >> 3, set = at / (most * tiles), in_set = at % (most * tiles);
+    const int n = min(most, each - set * most);
+    *head = (L & 7) * each + set * most + in_set % n;
+    *tile = in_set / n;
   } else {
     *head = 8 * each + (L - whole) % rest;
     *tile = (L - whole) / rest;
