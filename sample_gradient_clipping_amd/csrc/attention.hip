@@ -293,7 +293,7 @@ attention_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int tiles = (a.Tq + kQ - 1) / kQ;
   int head, tile;
-  place(a.B * a.Hq, tiles, &head, &tile);
+  place(a.B * a.Hq, tiles, max(heads_at_once<E>(a), a.Hq / a.Hkv), &head, &tile);
   tile = tiles - 1 - tile;
   const int b = head / a.Hq, hq = head % a.Hq, hk = hq / (a.Hq / a.Hkv);
   const int i = tile * kQ + wave * 32 + (lane & 31), p = a.Tk - a.Tq + i;

@@ -46,7 +46,7 @@ attention_dq_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
   const int tiles = (a.Tq + kRows - 1) / kRows;
   int head, tile;
-  place(a.B * a.Hq, tiles, &head, &tile);
+  place(a.B * a.Hq, tiles, max(heads_at_once<E>(a), a.Hq / a.Hkv), &head, &tile);
   tile = tiles - 1 - tile;
   const int b = head / a.Hq, hq = head % a.Hq, hk = hq / (a.Hq / a.Hkv);
   const int i = tile * kRows + wave * 32 + (lane & 31), p = a.Tk - a.Tq + i;
@@ -281,7 +281,7 @@ attention_dkv_kernel(AttnArgs a) {
   const uint32_t smem = lds_addr(shared_tiles) + Z::kValues + set * Z::kPairs * 2 * kTile;
   const int tiles = (a.Tk + Z::kKeys - 1) / Z::kKeys, group = a.Hq / a.Hkv, off = a.Tk - a.Tq;
   int head, tile;
-  place(a.B * a.Hkv, tiles, &head, &tile);
+  place(a.B * a.Hkv, tiles, heads_at_once<E>(a), &head, &tile);
   const int b = head / a.Hkv, hk = head % a.Hkv;
   const int j0 = tile * Z::kKeys + (SHARE ? 0 : wave * 32) + (lane & 31);
   const bool valid = j0 < a.Tk;

@@ -467,18 +467,27 @@ __device__ __forceinline__ bool all_live(const uint32_t (&w)[KEYS / 32]) {
   return x == ~0u;
 }
 
+// Heads of a set (see place) that read keys and values of their own: a large set
+// balances better, but its keys and values leave the L2 of 4 MB (gradients of
+// 8x2048, 40x128 in sets of 4, 5, 8: 1402, 1411, 1460 us; of 32x512, 12x64: 119, 122,
+// 116).  Heads of a group count once.
+template <class E>
+__device__ __forceinline__ int heads_at_once(const AttnArgs& a) {
+  return (int64_t)a.Tk * a.D * (int)sizeof(typename E::storage) > 256 * 1024 ? 4 : 8;
+}
+
 // Head and tile of a workgroup (heads * tiles of them).  Workgroups that read the
 // same keys and values (the tiles of a head, the heads of a group) are given to one
 // XCD one after another, so that they find them in its L2; the heads left over by
 // eight go to all XCDs, tile by tile.  An XCD takes its heads in sets of up to
-// kHeadsAtOnce, a set's first tiles (callers count from the longest ones of a
-// causal call) before its next: head after head, the last head's long tiles came
-// last and left compute units idle.
-constexpr int kHeadsAtOnce = 8;
-__device__ __forceinline__ void place(int heads, int tiles, int* head, int* tile) {
+// `at_once`, a set's first tiles (callers count from the longest ones of a causal
+// call) before its next: head after head, the last head's long tiles came last and
+// left compute units idle (8x2048, 40x128: 442 us, in sets of 4 408; packed 1x8192,
+// 40/8x128: 264, in sets of 5 219).
+__device__ __forceinline__ void place(int heads, int tiles, int at_once, int* head, int* tile) {
   const int L = blockIdx.x, each = heads / 8, rest = heads % 8, whole = 8 * each * tiles;
   if (L < whole) {
-    const int sets = (each + kHeadsAtOnce - 1) / kHeadsAtOnce, most = (each + sets - 1) / sets;
+    const int sets = (each + at_once - 1) / at_once, most = (each + sets - 1) / sets;
     const int at = L >> 3, set = at / (most * tiles), in_set = at % (most * tiles);
     const int n = min(most, each - set * most);
     *head = (L & 7) * each + set * most + in_set % n;
