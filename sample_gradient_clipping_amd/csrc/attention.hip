@@ -376,19 +376,27 @@ attention_kernel(AttnArgs a) {
 // ---------------------------------------------------------------------------
 // Few queries over many keys
 // ---------------------------------------------------------------------------
-// Up to 32 (query, head of the group) pairs are one wave's rows, so the group's keys and values are read once; the tiles of
-// keys are dealt to the waves of a.splits workgroups, each with tiles of LDS of
-// its own (no barriers until the end).  A workgroup joins its waves through
-// LDS; several workgroups' results are joined by a second kernel.
-template <class E> struct FewOf;
-template <> struct FewOf<BF16> { static constexpr int kWaves = 4; };
-template <> struct FewOf<F32> { static constexpr int kWaves = 2; };
+// Up to 32 (query, head of the group) pairs are one wave's rows, so the group's
+// keys and values are read once; the tiles of keys are dealt to the waves of
+// a.splits workgroups, each with tiles of LDS of its own (no barriers until the
+// end).  A workgroup joins its waves through LDS; several workgroups' results are
+// joined by a second kernel.  HBM bounds it: what counts is that all compute units
+// start at once and end together, so there are as many workgroups as compute
+// units, not more (16x1 over 4096, 40/8x128: 58 us in one round of 256, 65 in two;
+// 1x1 over 65536, 32/8x128: 64 and 86); half of them still draw most of what HBM
+// gives.  Where the heads alone are more, workgroups of two waves, two to a compute
+// unit (100x8 heads over 1000: 80 us, 90 with four waves).  Float32 tiles leave room
+// for two waves.
+constexpr int kUnits = 256;
+int few_waves(const AttnArgs& a) {
+  return a.dtype == kBF16 && (int64_t)a.B * a.Hkv <= kUnits ? 4 : 2;
+}
 
-template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(64 * FewOf<E>::kWaves, 1) void attention_few_kernel(AttnArgs a) {
+template <class E, int DP, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, 1) void attention_few_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
-  constexpr int NW = FewOf<E>::kWaves, KEYS = kKeys;
+  constexpr int KEYS = kKeys;
   constexpr int kTile = KEYS * Sh::kRowBytes;
   extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [wave][2][K, V], then joins
   __shared__ float ms[NW][32], ls[NW][32];
@@ -504,15 +512,21 @@ __global__ __launch_bounds__(64) void attention_join_kernel(AttnArgs a) {
   const int qi = rr / group, qh = hk * group + rr % group;
   const float* po = a.part + ((int64_t)head * a.splits * rows + rr) * (DP + 2);
   const int64_t step = (int64_t)rows * (DP + 2);
-  float M = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, po[s * step + DP]);
-  float o[DP / 64] = {}, L = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float m = po[s * step + DP];
-    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
-    L += f * po[s * step + DP + 1];
+  // lane s has split s's maximum and sum (at most 64 of them)
+  const bool in = lane < a.splits;
+  const float m = in ? po[lane * step + DP] : -INFINITY, l = in ? po[lane * step + DP + 1] : 0.0f;
+  float M = m;
 #pragma unroll
-    for (int k = 0; k < DP / 64; ++k) o[k] += f * po[s * step + 64 * k + lane];
+  for (int j = 1; j < 64; j <<= 1) M = fmaxf(M, lane_xor(M, j));
+  const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+  float o[DP / 64] = {}, L = f * l;
+#pragma unroll
+  for (int j = 1; j < 64; j <<= 1) L += lane_xor(L, j);
+#pragma unroll 8
+  for (int s = 0; s < a.splits; ++s) {
+    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), s));
+#pragma unroll
+    for (int k = 0; k < DP / 64; ++k) o[k] += w * po[s * step + 64 * k + lane];
   }
   const Span sp = span_of(a, b, a.Tk - a.Tq + qi);
   const bool any = sp.lo < sp.end;
@@ -538,22 +552,25 @@ hipError_t tiled(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class E, int DP, int NW, bool VEC>
+hipError_t few(const AttnArgs& a, hipStream_t s) {
+  constexpr int lds = std::max(NW * 4 * kKeys * Shape<E, DP>::kRowBytes, NW * 32 * DP * 4);
+  static hipError_t once = hipFuncSetAttribute((const void*)attention_few_kernel<E, DP, NW, VEC>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (once != hipSuccess) return once;
+  const unsigned heads = (unsigned)(a.B * a.Hkv), rows = (unsigned)(a.Tq * (a.Hq / a.Hkv));
+  hipLaunchKernelGGL((attention_few_kernel<E, DP, NW, VEC>), dim3(heads * a.splits), dim3(64 * NW), lds, s, a);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((attention_join_kernel<E, DP>), dim3(heads * rows), dim3(64), 0, s, a);
+  return hipGetLastError();
+}
+
 template <class E, int DP, bool VEC>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
-  typedef Shape<E, DP> Sh;
-  if (a.splits > 0) {
-    constexpr int NW = FewOf<E>::kWaves;
-    constexpr int lds = std::max(NW * 4 * kKeys * Sh::kRowBytes, NW * 32 * DP * 4);
-    static hipError_t once = hipFuncSetAttribute((const void*)attention_few_kernel<E, DP, VEC>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (once != hipSuccess) return once;
-    const unsigned heads = (unsigned)(a.B * a.Hkv), rows = (unsigned)(a.Tq * (a.Hq / a.Hkv));
-    hipLaunchKernelGGL((attention_few_kernel<E, DP, VEC>), dim3(heads * a.splits), dim3(64 * NW), lds, s, a);
-    if (a.splits > 1)
-      hipLaunchKernelGGL((attention_join_kernel<E, DP>), dim3(heads * rows), dim3(64), 0, s, a);
-    return hipGetLastError();
-  }
-  return tiled<E, DP, 4, VEC>(a, s);
+  if (a.splits == 0) return tiled<E, DP, 4, VEC>(a, s);
+  if constexpr (sizeof(typename E::storage) == 2)
+    if (few_waves(a) == 4) return few<E, DP, 4, VEC>(a, s);
+  return few<E, DP, 2, VEC>(a, s);
 }
 
 template <class E>
@@ -570,9 +587,8 @@ size_t attention_part_floats(AttnArgs& a) {
   a.splits = 0;
   if (rows > 32) return 0;
   const int64_t heads = (int64_t)a.B * a.Hkv;
-  const int waves = a.dtype == kBF16 ? attn::FewOf<BF16>::kWaves : attn::FewOf<F32>::kWaves;
-  const int64_t most = (a.Tk + waves * attn::kKeys * 2 - 1) / (waves * attn::kKeys * 2);
-  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>({most, (512 + heads - 1) / heads, 64}));
+  const int keys = attn::few_waves(a) * attn::kKeys * 2;
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(a.Tk + keys - 1) / keys, attn::kUnits / heads, 64}));
   return a.splits == 1 ? 0 : (size_t)(heads * a.splits * rows) * ((a.D <= 64 ? 64 : 128) + 2);
 }
 

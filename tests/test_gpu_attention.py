@@ -487,3 +487,20 @@ def test_scores_far_from_zero(sign, dtype):
     if dtype == "bf16":
         q, k, v, dout = (f32_to_bf16_bits(x) for x in (q, k, v, dout))
     _check(q, k, v, dout, dtype, mask=_mask(rng, "holes", 2, 100))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 45, 128])
+def test_single_tokens_of_many_sequences(D, dtype):
+    """More heads than compute units, so that no head's keys are split."""
+    rng = np.random.default_rng(18)
+    _check(*_draw(rng, 300, 1, 70, 2, 1, D, dtype), dtype, mask=_mask(rng, "left", 300, 70), back=False)
+    _check(*_draw(rng, 260, 2, 33, 1, 1, D, dtype), dtype, back=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_single_tokens_over_a_long_cache(dtype):
+    """Keys split as often as they are at most."""
+    rng = np.random.default_rng(19)
+    _check(*_draw(rng, 1, 1, 17003, 4, 1, 64, dtype), dtype, back=False)
+    _check(*_draw(rng, 1, 3, 17003, 2, 1, 16, dtype), dtype, mask=_mask(rng, "holes", 1, 17003), back=False)
