@@ -26,30 +26,41 @@ constexpr int kWaves = 4;
 constexpr int kNT = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;      // queries (keys) of a workgroup
 
-template <class E> struct StepOf;       // keys of a tile
-template <> struct StepOf<BF16> { static constexpr int kN = 64; };
-template <> struct StepOf<F32> { static constexpr int kN = 32; };
-
 // ---------------------------------------------------------------------------
 // dq and delta: as the forward pass, each wave 32 queries (its lanes), tiles of
-// keys and values through LDS.
+// keys and values through LDS.  SHARE, where the workgroups would be few: the four
+// waves of a workgroup have the same 32 queries, each with tiles of its own every
+// fourth step of 32 keys, and the first adds their sums in order.
 // ---------------------------------------------------------------------------
-template <class E, int DP, bool VEC>
-__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && VEC ? 2 : 1) void
+template <class E, int DP, bool SHARE>
+struct Dq {
+  static constexpr int kQueries = SHARE ? 32 : kRows;
+  static constexpr int kN = sizeof(typename E::storage) == 2 && !SHARE ? 64 : 32;     // keys of a tile
+  static constexpr int kTile = kN * Shape<E, DP>::kRowBytes;
+  // pairs of tiles of a set, sets of a workgroup
+  static constexpr int kPairs = SHARE && kTile * 16 > 150 * 1024 ? 1 : 2;
+  static constexpr int kSets = SHARE ? kWaves : 1;
+  static constexpr int kLds = kSets * kPairs * 2 * kTile;
+  static_assert(!SHARE || kLds >= (kWaves - 1) * DP * 32 * 4, "room for the waves' sums");
+  static_assert(kLds <= 156 * 1024, "LDS");
+};
+
+template <class E, int DP, bool VEC, bool SHARE>
+__global__ __launch_bounds__(kNT, sizeof(typename E::storage) == 2 && VEC && !SHARE ? 2 : 1) void
 attention_dq_kernel(AttnArgs a) {
   typedef Shape<E, DP> Sh;
   typedef typename E::storage S;
-  constexpr int KEYS = StepOf<E>::kN;
-  constexpr int kTile = KEYS * Sh::kRowBytes;
-  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [2][K, V] tiles
+  typedef Dq<E, DP, SHARE> Z;
+  constexpr int KEYS = Z::kN, kTile = Z::kTile;
+  extern __shared__ __attribute__((aligned(kTileAlign))) unsigned char smem[];   // [sets][pairs][K, V] tiles
   __shared__ int bound[2][kWaves];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
-  const int tiles = (a.Tq + kRows - 1) / kRows;
+  const int tiles = (a.Tq + Z::kQueries - 1) / Z::kQueries;
   int head, tile;
   place(a.B * a.Hq, tiles, max(heads_at_once<E>(a), a.Hq / a.Hkv), &head, &tile);
   tile = tiles - 1 - tile;
   const int b = head / a.Hq, hq = head % a.Hq, hk = hq / (a.Hq / a.Hkv);
-  const int i = tile * kRows + wave * 32 + (lane & 31), p = a.Tk - a.Tq + i;
+  const int i = tile * Z::kQueries + (SHARE ? 0 : wave * 32) + (lane & 31), p = a.Tk - a.Tq + i;
   const bool valid = i < a.Tq;
   Span keys = valid ? span_of(a, b, p) : Span{0, 0};
   if (a.causal && valid) keys.end = min(keys.end, p + 1);
@@ -76,14 +87,20 @@ attention_dq_kernel(AttnArgs a) {
   if (lo < end) {
     const int64_t kat = b * a.k.sb + hk * a.k.sh, vat = b * a.v.sb + hk * a.v.sh;
     uint32_t live[KEYS / 32], next[KEYS / 32];
-    int k0 = lo / KEYS * KEYS;
-    uint64_t m = live_keys<KEYS>(a, b, k0, live);
-    Loader<E, DP, KEYS, kWaves, VEC> load_k(a.k, a.Tk, a.D, wave, lane), load_v(a.v, a.Tk, a.D, wave, lane);
+    constexpr int kStride = KEYS * Z::kSets, kLoaders = SHARE ? 1 : kWaves;
+    int k0 = lo / KEYS * KEYS + (SHARE ? wave * KEYS : 0);
+    uint64_t m = 0;
+    Loader<E, DP, KEYS, kLoaders, VEC> load_k(a.k, a.Tk, a.D, SHARE ? 0 : wave, lane),
+        load_v(a.v, a.Tk, a.D, SHARE ? 0 : wave, lane);
     load_k.start(a.k, kat, k0);
     load_v.start(a.v, vat, k0);
-    const uint32_t tiles_at = lds_addr(smem);
-    load_k(tiles_at, k0, m);
-    load_v(tiles_at + kTile, k0, m);
+    const uint32_t tiles_at = lds_addr(smem) + (SHARE ? wave * Z::kPairs * 2 * kTile : 0);
+    const auto fetch = [&](int at, uint32_t to, uint32_t (&bits)[KEYS / 32]) {
+      m = live_keys<KEYS>(a, b, at, bits);
+      load_k(to, at, m);
+      load_v(to + kTile, at, m);
+    };
+    if (!SHARE || k0 < end) fetch(k0, tiles_at, live);
     Chunk<E> qf[Sh::kG], gf[Sh::kG];
     row_frags_from<E, DP, VEC>((const S*)a.o.data, b * a.o.sb + hq * a.o.sh + (int64_t)i * a.o.st, some,
                                a.D, lane, qf);
@@ -99,66 +116,92 @@ attention_dq_kernel(AttnArgs a) {
     row_frags_from<E, DP, VEC>((const S*)a.q.data, b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
     const float base = some ? -a.lse[at] / a.scale : 0.0f;
-    if (valid && h == 0) a.delta[at] = delta;
-    // a wave whose keys all lie in one tile takes delta as sum_j P_ij dO_i . v_j:
-    // from the rounded output it is off by 2^-9 of |dO| |O|, which shows where the
-    // keys are few
-    const bool once = sizeof(S) == 2 && wlo / KEYS == (wend - 1) / KEYS;
+    if (valid && h == 0 && (!SHARE || wave == 0)) a.delta[at] = delta;
     const float c = a.scale * kLog2e;
     const Places pl = places<E, DP>(lane);
     int buf = 0;
-    for (; k0 < end; k0 += KEYS, buf ^= 1) {
-      const uint32_t there = tiles_at + (buf ^ 1) * 2 * kTile;
-      if constexpr (VEC) wait_loads();
-      tile_barrier();        // this tile is there; the other one has been read
-      if (k0 + KEYS < end) {
-        m = live_keys<KEYS>(a, b, k0 + KEYS, next);
-        load_k(there, k0 + KEYS, m);
-        load_v(there + kTile, k0 + KEYS, m);
+    bool full = false;
+    // S starts from -lse / scale and dO V^T from -delta: P = 2^(c S), dS = P dP
+    const auto start = [&](f32x16& s, f32x16& dp) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        s[j] = base;
+        dp[j] = -delta;
       }
-      if (k0 < wend && k0 + KEYS > wlo) {
-        const bool full = k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live);
-        const uint32_t here = lds_addr(smem) + buf * 2 * kTile;
-        // S starts from -lse / scale and dO V^T from -delta: P = 2^(c S), dS = P dP
-        const auto start = [&](f32x16& s, f32x16& dp) {
+    };
+    const auto mask = [&](int n, f32x16& s) {
+      if (full) return;
+      apart();
+      const uint32_t w0 = live[0], w1 = live[KEYS / 32 - 1], w = lone ? 0u : (n == 0 ? w0 : w1) >> (4 * h);
+      const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            s[j] = base;
-            dp[j] = -delta;
-          }
-        };
-        const auto mask = [&](int n, f32x16& s) {
-          if (full) return;
-          apart();
-          const uint32_t w = lone ? 0u : (n == 0 ? live[0] : live[KEYS / 32 - 1]) >> (4 * h);
-          const int first = keys.lo - k0 - 32 * n - 4 * h, past = keys.end - k0 - 32 * n - 4 * h;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int r = 8 * (j >> 2) + (j & 3);
-            const bool in = r >= first && r < past && ((w >> r) & 1);
-            s[j] = in ? s[j] : -INFINITY;
-          }
-        };
-        if constexpr (sizeof(S) == 2) {
-          if (once) {
-            float sum = 0.0f;
+      for (int j = 0; j < 16; ++j) {
+        const int r = 8 * (j >> 2) + (j & 3);
+        const bool in = r >= first && r < past && ((w >> r) & 1);
+        s[j] = in ? s[j] : -INFINITY;
+      }
+    };
+    // a row's sum_j P_ij (dO_i . v_j - delta_i) over the keys of a tile
+    const auto rest = [&](uint32_t here) {
+      float sum = 0.0f;
 #pragma unroll 1
-            for (int n = 0; n < KEYS / 32; ++n) {
-              const Places kt = in_tile(pl, here + n * 32 * Sh::kRowBytes);
-              const Places vt = in_tile(pl, here + kTile + n * 32 * Sh::kRowBytes);
-              f32x16 s, dp;
-              start(s, dp);
+      for (int n = 0; n < KEYS / 32; ++n) {
+        const Places kt = in_tile(pl, here + n * 32 * Sh::kRowBytes);
+        const Places vt = in_tile(pl, here + kTile + n * 32 * Sh::kRowBytes);
+        f32x16 s, dp;
+        start(s, dp);
 #pragma unroll
-              for (int g = 0; g < Sh::kG; ++g) {
-                s = mma<E>(row_frag<E, DP>(kt, 0, g), qf[g], s);
-                dp = mma<E>(row_frag<E, DP>(vt, 0, g), gf[g], dp);
-                fence();
-              }
-              mask(n, s);
+        for (int g = 0; g < Sh::kG; ++g) {
+          s = mma<E>(row_frag<E, DP>(kt, 0, g), qf[g], s);
+          dp = mma<E>(row_frag<E, DP>(vt, 0, g), gf[g], dp);
+          fence();
+        }
+        mask(n, s);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) sum = fmaf(__builtin_amdgcn_exp2f(s[j] * c), dp[j], sum);
-            }
-            delta += sum + lane_xor(sum, 32);     // dp started from -delta
+        for (int j = 0; j < 16; ++j) sum = fmaf(__builtin_amdgcn_exp2f(s[j] * c), dp[j], sum);
+      }
+      return sum + lane_xor(sum, 32);
+    };
+    const auto all_seen = [&] { return k0 >= full_lo && k0 + KEYS <= full_end && all_live<KEYS>(live); };
+    // Where the keys are few, delta is sum_j P_ij dO_i . v_j: from the rounded output
+    // it is off by 2^-9 of |dO| |O|, which shows there.
+    // A wave's keys in one tile, or (SHARE) a tile or none for each wave:
+    const bool once = sizeof(S) == 2 && (SHARE ? (end - 1) / KEYS - lo / KEYS < kWaves
+                                               : wlo / KEYS == (wend - 1) / KEYS);
+    if constexpr (SHARE && sizeof(S) == 2) {
+      if (once) {
+        __shared__ float sums[kWaves][32];
+        float sum = 0.0f;
+        if (k0 < end) {
+          if constexpr (VEC) wait_loads();
+          wait_lds();
+          asm volatile("" ::: "memory");
+          full = all_seen();
+          sum = rest(tiles_at);
+        }
+        if (h == 0) sums[wave][lane] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) delta += sums[w][lane & 31];
+        if (some && h == 0 && wave == 0) a.delta[at] = delta;
+      }
+    }
+    for (; k0 < end; k0 += kStride, buf ^= Z::kPairs - 1) {
+      const uint32_t here = tiles_at + buf * 2 * kTile, there = tiles_at + (buf ^ 1) * 2 * kTile;
+      if constexpr (VEC) wait_loads();
+      // this tile is there; the other one has been read
+      if constexpr (SHARE) {
+        wait_lds();
+        asm volatile("" ::: "memory");
+      } else {
+        tile_barrier();
+      }
+      if (Z::kPairs == 2 && k0 + kStride < end) fetch(k0 + kStride, there, next);
+      if (k0 < wend && k0 + KEYS > wlo) {
+        full = all_seen();
+        if constexpr (sizeof(S) == 2) {
+          if (!SHARE && once) {
+            delta += rest(here);                  // dP started from -delta
             if (some && h == 0) a.delta[((int64_t)b * a.Hq + hq) * a.Tq + i] = delta;
           }
           // per block of 32 keys G products for S, G for dP with the exponentials
@@ -226,13 +269,37 @@ attention_dq_kernel(AttnArgs a) {
           }
         }
       }
+      if (Z::kPairs == 1 && k0 + kStride < end) {      // one pair of tiles: the next after this has been read
+        wait_lds();
+        asm volatile("" ::: "memory");
+        fetch(k0 + kStride, tiles_at, next);
+      }
 #pragma unroll
       for (int n = 0; n < KEYS / 32; ++n) live[n] = next[n];
     }
-  } else if (valid && h == 0) {
+    if constexpr (SHARE) {     // the waves' sums, added in their order by the first
+      float* const sums = (float*)smem;
+      __syncthreads();
+      if (wave > 0) {
+#pragma unroll
+        for (int db = 0; db < Sh::kDB; ++db)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sums[(((wave - 1) * Sh::kDB + db) * 16 + j) * 64 + lane] = dq[db][j];
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int w = 0; w < kWaves - 1; ++w)
+#pragma unroll
+          for (int db = 0; db < Sh::kDB; ++db)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dq[db][j] += sums[((w * Sh::kDB + db) * 16 + j) * 64 + lane];
+      }
+    }
+  } else if (valid && h == 0 && (!SHARE || wave == 0)) {
     a.delta[at] = 0.0f;
   }
-  if (!valid) return;
+  if (!valid || (SHARE && wave > 0)) return;
   store_row<E, DP, VEC>((S*)a.dq.data + b * a.dq.sb + hq * a.dq.sh + (int64_t)i * a.dq.st, dq,
                         some, a.scale, a.D, lane);
 }
@@ -558,8 +625,36 @@ attention_dkv_kernel(AttnArgs a) {
                         some, 1.0f, a.D, lane);
 }
 
+// Few workgroups leave compute units idle and give a wave a long chain of steps.
+// With and without SHARE, us (bf16, f32; workgroups as without, steps of 32):
+//                                            dq                       dk and dv
+//   48, 16 steps, heads of 64     12.5 / 18.4  26.2 / 69.6   15.6 / 21.4  36.6 /  111
+//   96, 16 steps, heads of 64            19.3  33.5 / 70.2   22.4 / 21.3  49.6 /  111
+//  128, 32 steps, heads of 128    33.6 / 36.4   106 /  250   48.8 / 53.4   157 /  375
+//  128, 320 steps, heads of 128                               217 /  436  1155 / 3633
+//  192, 8 steps, heads of 64                                 28.2 / 15.8  62.4 / 62.6
+//  256, 64 steps, heads of 128           60.6   345 /  489    129 /   97   519 /  739
+template <class E>
+bool shared(int64_t groups, int64_t steps) {
+  constexpr bool kWide = sizeof(typename E::storage) == 4;
+  return groups <= 64 || (groups <= (kWide ? 256 : 128) && steps >= (kWide ? 16 : 32));
+}
+
 template <class E, int DP, bool VEC, bool SHARE>
-hipError_t backward_keys(const AttnArgs& a, hipStream_t s) {
+hipError_t queries(const AttnArgs& a, hipStream_t s) {
+  typedef Dq<E, DP, SHARE> Z;
+  static hipError_t once = hipFuncSetAttribute((const void*)attention_dq_kernel<E, DP, VEC, SHARE>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
+  if (once != hipSuccess) return once;
+  const int64_t groups = (int64_t)a.B * a.Hq * ((a.Tq + Z::kQueries - 1) / Z::kQueries);
+  timing_begin("attention_dq", s);
+  hipLaunchKernelGGL((attention_dq_kernel<E, DP, VEC, SHARE>), dim3((unsigned)groups), dim3(kNT), Z::kLds, s, a);
+  timing_end("attention_dq", s);
+  return hipGetLastError();
+}
+
+template <class E, int DP, bool VEC, bool SHARE>
+hipError_t keys(const AttnArgs& a, hipStream_t s) {
   typedef Dkv<E, DP, SHARE> Z;
   static hipError_t once = hipFuncSetAttribute((const void*)attention_dkv_kernel<E, DP, VEC, SHARE>,
                                                hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
@@ -574,29 +669,13 @@ hipError_t backward_keys(const AttnArgs& a, hipStream_t s) {
 
 template <class E, int DP, bool VEC>
 hipError_t backward(const AttnArgs& a, hipStream_t s) {
-  typedef Shape<E, DP> Sh;
-  constexpr int lds = 4 * StepOf<E>::kN * Sh::kRowBytes;
-  static hipError_t once = hipFuncSetAttribute((const void*)attention_dq_kernel<E, DP, VEC>,
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (once != hipSuccess) return once;
-  const int64_t qt = (a.Tq + kRows - 1) / kRows;
-  timing_begin("attention_dq", s);
-  hipLaunchKernelGGL((attention_dq_kernel<E, DP, VEC>), dim3((unsigned)((int64_t)a.B * a.Hq * qt)), dim3(kNT),
-                     lds, s, a);
-  timing_end("attention_dq", s);
-  // Few workgroups leave compute units idle and give a wave a long chain of steps.
-  // dk and dv with and without SHARE, us (bf16, f32):
-  //   48 workgroups, 16 steps, heads of 64    15.6 / 21.4    36.6 /  111
-  //   96 workgroups, 16 steps, heads of 64    22.4 / 21.3    49.6 /  111
-  //  128 workgroups, 32 steps, heads of 128   48.8 / 53.4     157 /  375
-  //  128 workgroups, 320 steps, heads of 128   217 /  436    1155 / 3633
-  //  192 workgroups, 8 steps, heads of 64     28.2 / 15.8    62.4 / 62.6
-  //  256 workgroups, 64 steps, heads of 128    129 /   97     519 /  739
-  constexpr bool kWide = sizeof(typename E::storage) == 4;
-  const int64_t groups = (int64_t)a.B * a.Hkv * ((a.Tk + kRows - 1) / kRows);
-  const int64_t steps = (int64_t)(a.Hq / a.Hkv) * ((a.Tq + 31) / 32);
-  const bool share = groups <= 64 || (groups <= (kWide ? 256 : 128) && steps >= (kWide ? 16 : 32));
-  return share ? backward_keys<E, DP, VEC, true>(a, s) : backward_keys<E, DP, VEC, false>(a, s);
+  const int64_t q = (int64_t)a.B * a.Hq * ((a.Tq + kRows - 1) / kRows);
+  const int64_t k = (int64_t)a.B * a.Hkv * ((a.Tk + kRows - 1) / kRows);
+  const hipError_t e = shared<E>(q, (a.Tk + 31) / 32) ? queries<E, DP, VEC, true>(a, s)
+                                                      : queries<E, DP, VEC, false>(a, s);
+  if (e != hipSuccess) return e;
+  return shared<E>(k, (int64_t)(a.Hq / a.Hkv) * ((a.Tq + 31) / 32)) ? keys<E, DP, VEC, true>(a, s)
+                                                                    : keys<E, DP, VEC, false>(a, s);
 }
 
 template <class E>
