@@ -141,64 +141,25 @@ struct Sight {
   bool full;            // every query of the wave sees every key of the tile
 };
 
-// One step: the weighted values of one tile (CURRENT: its scores are in s) and
-// the scores of the next (NEXT: into s).  While the matrix cores take the next
-// scores the vector unit takes this tile's exponentials, and while they take its
-// weighted values, the next scores' maximum.  The order is written out, product by
-// product between fences, with every LDS operand read kAhead products early: left
-// to itself the compiler waits for each read, and puts all exponentials before all
-// products.  `loads` queues the loads of later tiles, number i, or all (-1).
-// Returns the maximum of the next scores, unscaled.
-template <class E, int DP, bool CURRENT, bool NEXT, class Loads>
-__device__ __forceinline__ float step(const Places& kt, const Places& vt,
-                                      const Chunk<E> (&qf)[Shape<E, DP>::kG], State<E, DP>& st, f32x16& s,
-                                      float c, int k0, const Sight& see, int lane, const Loads& loads) {
-  constexpr int G = Shape<E, DP>::kG, DB = DP / 32, N = DB * ColumnSteps<E>::kN;
-  const float m = st.m == -INFINITY ? 0.0f : st.m;
-  float sum[2] = {};
-  const auto exponential = [&](int j) {
-    float x = __builtin_amdgcn_exp2f(fmaf(s[j], c, -m));
-    asm volatile("" : "+v"(x));    // here, not where it is used first
-    s[j] = x;
-    sum[j & 1] += x;
-  };
-  // product u of the G + N: its share of the loads
-  const auto between = [&](int u) {
-    constexpr int L = Loads::kN, S = G + N;
-    each<0, L>([&](auto i) {
-      if (u == S * i / L + 1) loads(i);
-    });
-  };
-  f32x16 x = {};
-  Column<E> v[kAhead];
-  const auto read = [&](int t) { return column_frag<E, DP>(vt, 0, t % DB, t / DB, lane); };
-  if constexpr (NEXT) {
-    Chunk<E> k[kAhead];
+// The scores of a tile, masked; returns their maximum, unscaled.  Every LDS operand
+// is read kAhead products early, and fences keep that order: left to itself the
+// compiler waits for each read.
+template <class E, int DP>
+__device__ __forceinline__ float scores(const Places& kt, const Chunk<E> (&qf)[Shape<E, DP>::kG], f32x16& s,
+                                        int k0, const Sight& see, int lane) {
+  constexpr int G = Shape<E, DP>::kG;
+  Chunk<E> k[kAhead];
 #pragma unroll
-    for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 0, g);
+  for (int g = 0; g < kAhead; ++g) k[g] = row_frag<E, DP>(kt, 0, g);
+  fence();
+  s = f32x16{};
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    s = mma<E>(k[g % kAhead], qf[g], s);
+    if (g + kAhead < G) k[g % kAhead] = row_frag<E, DP>(kt, 0, g + kAhead);
     fence();
-    if constexpr (!CURRENT) loads(std::integral_constant<int, -1>());
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      x = mma<E>(k[g % kAhead], qf[g], x);
-      if (g + kAhead < G) k[g % kAhead] = row_frag<E, DP>(kt, 0, g + kAhead);
-      else if (CURRENT) v[g + kAhead - G] = read(g + kAhead - G);
-      if constexpr (CURRENT) {
-#pragma unroll
-        for (int j = 16 * g / G; j < 16 * (g + 1) / G; ++j) exponential(j);
-        between(g);
-      }
-      fence();
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < kAhead; ++t) v[t] = read(t);
-    fence();
-    loads(std::integral_constant<int, -1>());
-#pragma unroll
-    for (int j = 0; j < 16; ++j) exponential(j);
   }
-  if (NEXT && !see.full) {
+  if (!see.full) {
     apart();
     const int h = lane >> 5;
     const uint32_t w = see.live >> (4 * h);
@@ -207,63 +168,46 @@ __device__ __forceinline__ float step(const Places& kt, const Places& vt,
     for (int j = 0; j < 16; ++j) {
       const int r = 8 * (j >> 2) + (j & 3);
       const bool in = r >= first && r < past && ((w >> r) & 1);
-      x[j] = in ? x[j] : -INFINITY;
+      s[j] = in ? s[j] : -INFINITY;
     }
   }
   float top = -INFINITY;
-  if constexpr (CURRENT) {
-    Weights<E> p;
-    p.set(s);
-    st.l += sum[0] + sum[1];
-    fence();
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-      st.o[t % DB] = mma_column<E>(v[t % kAhead], p, t / DB, st.o[t % DB]);
-      if (t + kAhead < N) v[t % kAhead] = read(t + kAhead);
-      if constexpr (NEXT) {
-#pragma unroll
-        for (int j = 16 * t / N; j < 16 * (t + 1) / N; ++j) top = fmaxf(top, x[j]);
-        asm volatile("" : "+v"(top));
-        between(G + t);
-      }
-      fence();
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
-  }
-  if constexpr (NEXT) s = x;
+  for (int j = 0; j < 16; ++j) top = fmaxf(top, s[j]);
   return top;
 }
 
-// The loads behind step t: tile t + 1's values and tile t + 2's keys.
-template <class E, int DP, int NW, bool VEC>
-struct Queue {
-  typedef Loader<E, DP, kKeys, NW, VEC> Load;
-  static constexpr int kPer = Load::kPer, kN = VEC ? 2 * kPer : 1;
-  static constexpr int kTile = kKeys * Shape<E, DP>::kRowBytes;
-  Load &k, &v;
-  uint32_t kt, vt;
-  int t, tiles, at;
-  uint64_t live;          // of tile t + 1
-  template <int I>
-  __device__ __forceinline__ void operator()(std::integral_constant<int, I>) const {
-    if constexpr (!VEC || I < 0) {
-      if (t + 1 < tiles) v(vt + ((t + 1) & 1) * kTile, at + kKeys, live);
-      if (t + 2 < tiles) k(kt + (t & 1) * kTile, at + 2 * kKeys, ~0ull);
-    } else if constexpr (I < kPer) {
-      v.template issue<I>();
-    } else {
-      k.template issue<I - kPer>();
-    }
+// Adds a tile's weighted values, its scores in s.
+template <class E, int DP>
+__device__ __forceinline__ void values(const Places& vt, State<E, DP>& st, f32x16& s, float c, int lane) {
+  constexpr int DB = DP / 32, N = DB * ColumnSteps<E>::kN;
+  const float m = st.m == -INFINITY ? 0.0f : st.m;
+  const auto read = [&](int t) { return column_frag<E, DP>(vt, 0, t % DB, t / DB, lane); };
+  Column<E> v[kAhead];
+#pragma unroll
+  for (int t = 0; t < kAhead; ++t) v[t] = read(t);
+  fence();
+  float sum[2] = {};
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float x = __builtin_amdgcn_exp2f(fmaf(s[j], c, -m));
+    asm volatile("" : "+v"(x));    // here, not where it is used first
+    s[j] = x;
+    sum[j & 1] += x;
   }
-};
-struct NoLoads {
-  static constexpr int kN = 0;
-  __device__ __forceinline__ void operator()(std::integral_constant<int, -1>) const {}
-};
+  Weights<E> p;
+  p.set(s);
+  st.l += sum[0] + sum[1];
+  fence();
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    st.o[t % DB] = mma_column<E>(v[t % kAhead], p, t / DB, st.o[t % DB]);
+    if (t + kAhead < N) v[t % kAhead] = read(t + kAhead);
+    fence();
+  }
+}
 
-// Moves the running maximum to scores of maximum `top` that are next.
+// Moves the running maximum to the scores of maximum `top`.
 template <class E, int DP>
 __device__ __forceinline__ void settle(State<E, DP>& st, float top, float c) {
   top = fmaxf(top, lane_xor(top, 32)) * c;
@@ -352,7 +296,6 @@ attention_kernel(AttnArgs a) {
     row_frags_from<E, DP, VEC>((const S*)a.q.data, b * a.q.sb + hq * a.q.sh + (int64_t)i * a.q.st, some,
                                a.D, lane, qf);
     f32x16 s;
-    const NoLoads none;
     for (int t = 0; t < tiles; ++t) {
       const Sight now = see;
       wait_loads();
@@ -360,8 +303,8 @@ attention_kernel(AttnArgs a) {
       fetch(t + 1);
       if (place_of(t) < wend && place_of(t) + kKeys > wlo) {
         const Places kn = in_tile(pl, kt + (t & 1) * kTile), vn = in_tile(pl, vt + (t & 1) * kTile);
-        settle<E, DP>(st, step<E, DP, false, true>(kn, vn, qf, st, s, c, place_of(t), now, lane, none), c);
-        step<E, DP, true, false>(kn, vn, qf, st, s, c, 0, now, lane, none);
+        settle<E, DP>(st, scores<E, DP>(kn, qf, s, place_of(t), now, lane), c);
+        values<E, DP>(vn, st, s, c, lane);
       }
     }
   }
@@ -450,9 +393,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attention_few_kernel(AttnArgs a) {
       const uint32_t base = own_tiles + buf * 2 * kTile;
       const Places kt = in_tile(at, base), vt = in_tile(at, base + kTile);
       f32x16 s;
-      const NoLoads none;
-      settle<E, DP>(st, step<E, DP, false, true>(kt, vt, qf, st, s, c, k0, see, lane, none), c);
-      step<E, DP, true, false>(kt, vt, qf, st, s, c, k0, see, lane, none);
+      settle<E, DP>(st, scores<E, DP>(kt, qf, s, k0, see, lane), c);
+      values<E, DP>(vt, st, s, c, lane);
       live[0] = next[0];
     }
   }

@@ -197,35 +197,25 @@ struct Loader {
                                              n <= 0 ? 0 : left < 0x7fff0000ull ? (int)left : 0x7fff0000,
                                              0x00020000);
   }
-  // Readies the loads of a tile; then issue<J>, J = 0 .. kPer - 1, queues them, each
-  // where the caller wants it: one takes the address unit 16 cycles, and the waves
-  // of a workgroup that queue them all at once after a barrier wait for each other
-  // (183 of 896 ns per step of the forward pass went there).
-  uint32_t to;
-  int now[kPer];
-  __device__ __forceinline__ void ready(uint32_t tile, int row0, uint64_t live) {
-    if ((int64_t)(row0 - first) * stride > (1 << 30)) base_at(row0);
-    // an out-of-range offset stays one: it is above every descriptor's 2^31 bytes
-    const int at = (row0 - first) * stride;
-    to = uniform((int)tile + wave * kPer * 1024);
-    constexpr uint64_t kAll = ROWS >= 64 ? ~0ull : (1ull << (ROWS & 63)) - 1;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) now[j] = off[j] + at;
-    if ((live & kAll) != kAll) {
-      apart();
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int row = (wave * kPer + j) * Sh::kRowsPerDma + lane / Sh::kChunks;
-        now[j] = (live >> row) & 1 ? now[j] : kOOB;
-      }
-    }
-  }
-  template <int J>
-  __device__ __forceinline__ void issue() const { dma16<1024 * J>(rsrc, now[J], to); }
   __device__ __forceinline__ void operator()(uint32_t tile, int row0, uint64_t live) {
     if constexpr (VEC) {
-      ready(tile, row0, live);
-      each<0, kPer>([&](auto j) { issue<j>(); });
+      if ((int64_t)(row0 - first) * stride > (1 << 30)) base_at(row0);
+      // an out-of-range offset stays one: it is above every descriptor's 2^31 bytes
+      const int at = (row0 - first) * stride;
+      const uint32_t to = uniform((int)tile + wave * kPer * 1024);
+      constexpr uint64_t kAll = ROWS >= 64 ? ~0ull : (1ull << (ROWS & 63)) - 1;
+      int now[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) now[j] = off[j] + at;
+      if ((live & kAll) != kAll) {
+        apart();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int row = (wave * kPer + j) * Sh::kRowsPerDma + lane / Sh::kChunks;
+          now[j] = (live >> row) & 1 ? now[j] : kOOB;
+        }
+      }
+      each<0, kPer>([&](auto j) { dma16<1024 * j>(rsrc, now[j], to); });
     } else {
       // all loads in flight, a piece outside from the head's first row and not used
       constexpr int kEach = ROWS * Sh::kChunks / (64 * NW);
