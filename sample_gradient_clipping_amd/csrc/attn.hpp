@@ -51,7 +51,7 @@ struct Span { int lo, end; };
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int b, int p) {
   if (a.lo == nullptr) return {0, a.Tk};
   const int64_t e = (int64_t)b * a.Tk + p;
-  return {a.lo[e], a.end[e]};
+  return {max(a.lo[e], 0), min(a.end[e], a.Tk)};     // no address from memory unchecked
 }
 
 // LDS tiles: rows of DP elements in 16-byte chunks, chunk c of row r stored at
