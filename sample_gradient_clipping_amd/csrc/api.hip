@@ -1921,8 +1921,8 @@ bool heads_vec(const dpf_heads* a) {
          (h.st * es) % 16 == 0 && (h.sh * es) % 16 == 0 && h.st * es <= ((int64_t)1 << 24);
 }
 
-dpf_status check_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v, int32_t causal,
-                           float scale) {
+dpf_status check_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v,
+                           const int32_t* segments, int32_t causal, float scale, const float* lse) {
   dpf_status st = check_heads(q, "q", false);
   if (st == DPF_OK) st = check_heads(k, "k", false);
   if (st == DPF_OK) st = check_heads(v, "v", false);
@@ -1937,6 +1937,9 @@ dpf_status check_attention(const dpf_heads* q, const dpf_heads* k, const dpf_hea
   if (q->H % k->H != 0)
     return fail(DPF_ERR_INVALID_ARGUMENT, "the queries' heads are not a multiple of the keys'");
   if (causal != 0 && causal != 1) return fail(DPF_ERR_INVALID_ARGUMENT, "causal must be 0 or 1");
+  if (lse == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "lse is NULL");
+  if (((uintptr_t)lse & 3u) != 0 || ((uintptr_t)segments & 3u) != 0)
+    return fail(DPF_ERR_UNSUPPORTED, "lse or segments is not aligned to its elements");
   // the backward pass starts its scores from -lse / scale, which has to be finite
   if (!std::isnan(scale) && !(scale >= 0x1p-64f && scale <= 0x1p64f))
     return fail(DPF_ERR_INVALID_ARGUMENT, "scale must lie in 2^-64 .. 2^64 (or be NaN for the default)");
@@ -2090,10 +2093,9 @@ dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_h
                              const uint8_t* mask, const int32_t* segments, int32_t causal,
                              float scale, const dpf_heads* out, float* lse, void* stream) {
   CallScope call_("dpfused_attention");
-  dpf_status st = check_attention(q, k, v, causal, scale);
+  dpf_status st = check_attention(q, k, v, segments, causal, scale, lse);
   if (st == DPF_OK) st = check_heads(out, "out", true);
   if (st != DPF_OK) return st;
-  if (lse == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "lse is NULL");
   if (out->dtype != q->dtype) return fail(DPF_ERR_UNSUPPORTED, "q and out have different dtypes");
   if (!heads_alike(q, out)) return fail(DPF_ERR_INVALID_ARGUMENT, "q and out have different shapes");
   if ((st = check_apart(out, "out", q, "q")) != DPF_OK) return st;
@@ -2120,14 +2122,13 @@ dpf_status dpfused_attention_backward(const dpf_heads* dout, const dpf_heads* q,
                                       int32_t causal, float scale, const dpf_heads* dq,
                                       const dpf_heads* dk, const dpf_heads* dv, void* stream) {
   CallScope call_("dpfused_attention_backward");
-  dpf_status st = check_attention(q, k, v, causal, scale);
+  dpf_status st = check_attention(q, k, v, segments, causal, scale, lse);
   if (st == DPF_OK) st = check_heads(dout, "dout", false);
   if (st == DPF_OK) st = check_heads(out, "out", false);
   if (st == DPF_OK) st = check_heads(dq, "dq", true);
   if (st == DPF_OK) st = check_heads(dk, "dk", true);
   if (st == DPF_OK) st = check_heads(dv, "dv", true);
   if (st != DPF_OK) return st;
-  if (lse == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, "lse is NULL");
   for (const dpf_heads* h : {dout, out, dq, dk, dv})
     if (h->dtype != q->dtype) return fail(DPF_ERR_UNSUPPORTED, "the tensors have different dtypes");
   if (!heads_alike(q, dout) || !heads_alike(q, out) || !heads_alike(q, dq))

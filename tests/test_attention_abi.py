@@ -306,3 +306,10 @@ def test_scale_out_of_range(scale):
     L = _lib.lib()
     assert _forward(L, scale=scale) == BAD
     assert _backward(L, scale=scale) == BAD
+
+
+def test_misaligned_statistics():
+    L = _lib.lib()
+    for wrong in (1, 2, 3):
+        assert _forward(L, lse=at(9) + wrong) == UNS
+        assert _backward(L, lse=at(20) + wrong) == UNS
