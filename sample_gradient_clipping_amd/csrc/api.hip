@@ -2104,12 +2104,14 @@ dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_h
   hipStream_t s = static_cast<hipStream_t>(stream);
   dpf::AttnArgs a = attention_args(q, k, v, out, mask, segments, causal, scale, lse);
   Workspace ws(s);
-  const AttnWs o = reserve_ranges(a, ws);
   const size_t floats = dpf::attention_part_floats(a);
+  // a short mask is read by the kernel of many queries itself
+  const bool ranges = !(a.splits == 0 && segments == nullptr && a.Tk <= dpf::kRowMask);
+  const AttnWs o = ranges ? reserve_ranges(a, ws) : AttnWs{};
   const size_t part = floats != 0 ? ws.reserve(floats * sizeof(float)) : 0;
   if (!ws.allocate()) return fail(DPF_ERR_OUT_OF_MEMORY, "workspace allocation failed");
   if (floats != 0) a.part = ws.at<float>(part);
-  hipError_t e = queue_ranges(a, ws, o, s);
+  hipError_t e = ranges ? queue_ranges(a, ws, o, s) : hipSuccess;
   if (e == hipSuccess) e = dpf::launch_attention(a, s);
   if (e != hipSuccess) return hip_fail(e, "attention launch");
   return ok();

@@ -224,6 +224,31 @@ __device__ __forceinline__ void settle(State<E, DP>& st, float top, float c) {
   }
 }
 
+// The mask of a sample of up to kRowMask positions, in scalar registers: its call
+// needs no launch for ranges (32x128, 16x64: 18.5 us with one, 13.3 without).
+struct RowMask {
+  static_assert(kRowMask == 256, "four words");
+  uint64_t m0, m1, m2, m3;
+  __device__ __forceinline__ void read(const AttnArgs& a, int b, int lane) {
+    const uint8_t* row = a.mask + (int64_t)b * a.Tk;
+    const auto part = [&](int k) { return __ballot(row[min(k, a.Tk - 1)] != 0 && k < a.Tk); };
+    m0 = part(lane);
+    m1 = part(64 + lane);
+    m2 = part(128 + lane);
+    m3 = part(192 + lane);
+  }
+  __device__ __forceinline__ Span span() const {      // from the first active position to the last
+    const auto first = [](uint64_t m) { return __ffsll((unsigned long long)m) - 1; };
+    const auto past = [](uint64_t m) { return 64 - __clzll((long long)m); };
+    return {m0 ? first(m0) : m1 ? 64 + first(m1) : m2 ? 128 + first(m2) : 192 + first(m3),
+            m3 ? 192 + past(m3) : m2 ? 128 + past(m2) : m1 ? 64 + past(m1) : past(m0)};
+  }
+  __device__ __forceinline__ uint32_t word(int k0) const {      // of positions k0 .. k0 + 31
+    const uint64_t low = k0 < 64 ? m0 : m1, high = k0 < 192 ? m2 : m3;
+    return (uint32_t)((k0 < 128 ? low : high) >> (k0 & 32));
+  }
+};
+
 // NW waves, 32 queries each, share the tiles.
 template <class E, int DP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, sizeof(typename E::storage) == 4 ? 1 : !VEC ? 2 : DP == 64 ? 4 : 3) void
@@ -242,7 +267,15 @@ attention_kernel(AttnArgs a) {
   const int b = head / a.Hq, hq = head % a.Hq, hk = hq / (a.Hq / a.Hkv);
   const int i = tile * kQ + wave * 32 + (lane & 31), p = a.Tk - a.Tq + i;
   const bool valid = i < a.Tq;
-  Span keys = valid ? span_of(a, b, p) : Span{0, 0};
+  const bool row_mask = a.mask != nullptr && a.lo == nullptr;
+  RowMask row;
+  Span keys = {0, 0};
+  if (row_mask) {
+    row.read(a, b, lane);
+    if (valid && a.mask[(int64_t)b * a.Tk + p] != 0) keys = row.span();
+  } else if (valid) {
+    keys = span_of(a, b, p);
+  }
   if (a.causal && valid) keys.end = min(keys.end, p + 1);
   const bool some = keys.lo < keys.end;
   // what any query of the wave needs, and what all of them may see
@@ -277,7 +310,9 @@ attention_kernel(AttnArgs a) {
     Sight see{keys.lo, keys.end, 0, false};
     const auto look = [&](int t) {
       uint32_t live[1];
-      const uint64_t m = live_keys<kKeys>(a, b, place_of(t), live);
+      uint64_t m;
+      if (row_mask) m = live[0] = row.word(place_of(t));
+      else m = live_keys<kKeys>(a, b, place_of(t), live);
       see.live = live[0];
       see.full = place_of(t) >= full_lo && place_of(t) + kKeys <= full_end && live[0] == ~0u;
       return m;

@@ -33,6 +33,7 @@ struct AttnArgs {
 };
 
 // Workspace of mask and segments, and of split keys, in elements.
+constexpr int kRowMask = 256;             // positions whose mask a wave keeps by itself (forward)
 inline int attn_words(int64_t Tk) { return (int)(2 * ((Tk + 63) / 64)); }
 // Fills a.splits; 0 floats without a split.
 size_t attention_part_floats(AttnArgs& a);

@@ -403,8 +403,8 @@ def test_captured_and_replayed(D):
 def test_workspace_limit_fails_before_anything_is_written():
     torch = need_gpu()
     import sample_gradient_clipping_amd as dp
-    q = torch.randn((1, 64, 2, 64), device="cuda")
-    mask = torch.ones((1, 64), dtype=torch.uint8, device="cuda")
+    q = torch.randn((1, 300, 2, 64), device="cuda")
+    mask = torch.ones((1, 300), dtype=torch.uint8, device="cuda")
     out = torch.full_like(q, 5.0)
     dp.set_option("workspace_limit_bytes", 16)
     try:
@@ -504,3 +504,13 @@ def test_single_tokens_over_a_long_cache(dtype):
     rng = np.random.default_rng(19)
     _check(*_draw(rng, 1, 1, 17003, 4, 1, 64, dtype), dtype, back=False)
     _check(*_draw(rng, 1, 3, 17003, 2, 1, 16, dtype), dtype, mask=_mask(rng, "holes", 1, 17003), back=False)
+
+
+@pytest.mark.parametrize("kind", ["prefix", "left", "holes"])
+@pytest.mark.parametrize("T", [63, 64, 65, 128, 191, 192, 255, 256, 257])
+def test_masks_of_short_samples(T, kind):
+    """Up to 256 positions the forward pass reads the mask itself."""
+    rng = np.random.default_rng(20)
+    for causal, Tq in ((True, T), (False, T), (True, 33)):
+        _check(*_draw(rng, 3, Tq, T, 2, 2, 64, "bf16"), "bf16", mask=_mask(rng, kind, 3, T), causal=causal)
+    _check(*_draw(rng, 2, T, T, 2, 1, 24, "f32"), "f32", mask=_mask(rng, kind, 2, T))
