@@ -105,6 +105,8 @@ def _check_out(t, shape, name: str, device, dtype=None) -> None:
     dtype = torch.float32 if dtype is None else dtype
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype == dtype and t.shape == tuple(shape) and t.is_contiguous() and t.device == device:
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(int(d) for d in shape):
@@ -488,6 +490,10 @@ def scaled_accumulate(X, G, c, mask=None, noise_std: float = 0.0, seed: int = 0,
 
 
 def _ids(t, name: str) -> DpfIds:
+    return DpfIds(*_ids_fields(t, name))
+
+
+def _ids_fields(t, name: str) -> tuple:
     torch = _torch()
     if t.dim() != 2:
         raise ValueError(f"{name} must be [B, T]")
@@ -499,8 +505,8 @@ def _ids(t, name: str) -> DpfIds:
     if T > 1 and t.stride(1) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     # a single sample's stride is arbitrary: nothing is read past its row
-    return DpfIds(t.data_ptr(), DPF_I64 if t.dtype == torch.int64 else DPF_I32, 0, B, T,
-                  t.stride(0) if B > 1 else T)
+    return (t.data_ptr(), DPF_I64 if t.dtype == torch.int64 else DPF_I32, 0, B, T,
+            t.stride(0) if B > 1 else T)
 
 
 def embedding_lookup(ids, table, mask=None, scale: float = 1.0, out_dtype=None, out=None,
@@ -836,10 +842,10 @@ def _rotary_args(q, k, q_weight, k_weight, freqs, positions, mask):
         _check_out(freqs, freqs.shape, "freqs", dev, torch.float64)
     pa = None
     if positions is not None:
-        pa = _ids(positions, "positions")
+        pa = DpfIds.pack(*_ids_fields(positions, "positions"))
         _same_device(positions, dev, "positions")
-    return (_ptr(q_weight), _ptr(k_weight), _ptr(freqs), 0 if freqs is None else int(freqs.shape[0]),
-            None if pa is None else ctypes.byref(pa), _mask_ptr(mask, q.shape[0], q.shape[1], dev))
+    return (_ptr(q_weight), _ptr(k_weight), _ptr(freqs), 0 if freqs is None else freqs.shape[0], pa,
+            _mask_ptr(mask, q.shape[0], q.shape[1], dev))
 
 
 def qk_norm_rotary(q, k, q_weight=None, k_weight=None, freqs=None, positions=None, mask=None,
@@ -899,6 +905,18 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, 
     return QkGradients(dq, dk, dqw, dkw)
 
 
+def _rows(t) -> bytes:
+    """The bytes of t's dpf_act, packed at once."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError("activations must be [B, T, D]")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if strides[2] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return DpfAct.pack(t.data_ptr(), _dtype_code(t), 0, *shape, *strides[:2])
+
+
 def dropout(x, p: float, seed: int = 0, offset: int = 0, residual=None, mask=None, out=None,
             stream=None):
     """residual + dropout(x) for x [B, T, D] (bf16 or fp32), the mask drawn from (seed, offset)
@@ -908,8 +926,8 @@ def dropout(x, p: float, seed: int = 0, offset: int = 0, residual=None, mask=Non
     The gradient to x is dropout(dy, p, seed, offset), to the residual dy.  A call consumes
     dropout_blocks(x.numel()) blocks of the seed: advance offset by as much.  They are apart from
     the noise's blocks."""
-    xa = _act(x)
-    B, T, D = x.shape
+    xa = _rows(x)
+    B, T, _ = x.shape
     if out is None:
         out = x.new_empty(x.shape)
     for t, name in ((out, "out"), (residual, "residual")):
@@ -918,11 +936,10 @@ def dropout(x, p: float, seed: int = 0, offset: int = 0, residual=None, mask=Non
         if t.dtype != x.dtype or t.shape != x.shape:
             raise ValueError(f"{name} must be {tuple(x.shape)} of {x.dtype}")
         _same_device(t, x.device, name)
-    ra = None if residual is None else _act(residual)
-    oa = _act(out)
-    _call(_lib.lib().dpfused_dropout, x.device, ctypes.byref(xa),
-          None if ra is None else ctypes.byref(ra), _mask_ptr(mask, B, T, x.device), float(p),
-          int(seed), int(offset), ctypes.byref(oa), _stream(x, stream))
+    ra = None if residual is None else _rows(residual)
+    oa = _rows(out)
+    _call(_lib.lib().dpfused_dropout, x.device, xa, ra, _mask_ptr(mask, B, T, x.device), float(p),
+          int(seed), int(offset), oa, _stream(x, stream))
     return out
 
 

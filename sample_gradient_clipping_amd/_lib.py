@@ -36,6 +36,7 @@ class DpfAct(ctypes.Structure):
         ("stride_b", ctypes.c_int64),
         ("stride_t", ctypes.c_int64),
     ]
+    pack = staticmethod(struct.Struct("Pii5q").pack)      # the same bytes, from the fields in order
 
 
 class DpfIds(ctypes.Structure):
@@ -48,6 +49,7 @@ class DpfIds(ctypes.Structure):
         ("T", ctypes.c_int64),
         ("stride_b", ctypes.c_int64),
     ]
+    pack = staticmethod(struct.Struct("Pii3q").pack)      # the same bytes, from the fields in order
 
 
 class DpfHeads(ctypes.Structure):
@@ -75,7 +77,8 @@ class DpfError(RuntimeError):
 
 _lib = None
 
-_HEADS = ctypes.c_void_p     # dpf_heads: a DpfHeads by reference, or its bytes
+# dpf_heads, dpf_act, dpf_ids: the structure by reference, or its bytes
+_HEADS = _ROWS = _IDS = ctypes.c_void_p
 
 # name -> (restype, argtypes)
 _SIGNATURES = {
@@ -161,17 +164,17 @@ _SIGNATURES = {
     "dpfused_qk_norm_rotary": (ctypes.c_int, [
         _HEADS, _HEADS, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int32,
-        ctypes.POINTER(DpfIds), ctypes.c_void_p, _HEADS, _HEADS,
+        _IDS, ctypes.c_void_p, _HEADS, _HEADS,
         ctypes.c_void_p]),
     "dpfused_qk_norm_rotary_backward": (ctypes.c_int, [
         _HEADS, _HEADS, _HEADS,
         _HEADS, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
-        ctypes.c_int64, ctypes.c_float, ctypes.c_int32, ctypes.POINTER(DpfIds), ctypes.c_void_p,
+        ctypes.c_int64, ctypes.c_float, ctypes.c_int32, _IDS, ctypes.c_void_p,
         _HEADS, _HEADS, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_void_p]),
     "dpfused_dropout": (ctypes.c_int, [
-        ctypes.POINTER(DpfAct), ctypes.POINTER(DpfAct), ctypes.c_void_p, ctypes.c_float,
-        ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(DpfAct), ctypes.c_void_p]),
+        _ROWS, _ROWS, ctypes.c_void_p, ctypes.c_float,
+        ctypes.c_uint64, ctypes.c_uint64, _ROWS, ctypes.c_void_p]),
     "dpfused_dropout_blocks": (ctypes.c_uint64, [ctypes.c_int64]),
     "dpfused_orthogonalize": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
