@@ -16,6 +16,11 @@
 // exponentials are rounded to bf16 for that product (what its operand type
 // holds); their sum is that of the unrounded ones (lse is float32), and it, the
 // maximum and the output stay in float32.
+//
+// 8x2048, 40x128 bf16: 410 us, 840 TFLOP/s.  A tile of 32 x 32 x 128 takes 16 matrix
+// instructions (512 cycles) and about 130 others (500 cycles, 256 of them the
+// exponentials); three waves per SIMD overlap two thirds to four fifths of that.
+// Tiles of 32 keys are what leaves registers for three (64 keys, two waves: 444 us).
 #include "attn.hpp"
 
 #include <algorithm>
@@ -37,7 +42,7 @@ constexpr float kSlack = 8.0f;
 // position), so a causal row with one key has lo == p and any other with one
 // key end == lo + 1.  Segment numbers do not decrease, so the start of the
 // first position's segment and the end of the last one's are found by 64-way
-// search, the boundaries between by a vote.
+// search, the boundaries between by a vote.  A chain of latencies: 3 to 5 us.
 __device__ __forceinline__ int first_from(const int32_t* id, int l, int r, int32_t least, int lane) {
   // smallest index in [l, r) whose id is >= least, else r
   while (l < r) {

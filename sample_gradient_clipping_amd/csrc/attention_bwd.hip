@@ -16,6 +16,10 @@
 // A query that sees one key only has P = 1 and dS = 0 exactly; its delta comes
 // from the rounded output and would leave a difference that is all rounding, so
 // such a pair's dS is set to 0.
+//
+// 8x2048, 40x128 bf16: dq 590 us, dk and dv 850 (870 and 810 TFLOP/s of the products
+// run); 32x512, 12x64: 57 and 68.  Matrix instructions and the exponentials' vector
+// work bound both, at two waves per SIMD (the sums take 64 and 128 registers).
 #include "attn.hpp"
 
 namespace dpf {
@@ -468,7 +472,7 @@ attention_dkv_kernel(AttnArgs a) {
         const uint32_t here = smem + buf * 2 * kTile;
         const Places qt = in_tile(pl, here), gt = in_tile(pl, here + kTile);
         const bool full = p0 >= full_lo && p0 + N <= full_end && all_live<N>(live);
-// S starts from -lse / scale and dO V^T from -delta: P = 2^(c S), dS = P dP
+        // S starts from -lse / scale and dO V^T from -delta: P = 2^(c S), dS = P dP
         const auto start = [&](const float* from_rows, int n, f32x16& x) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
