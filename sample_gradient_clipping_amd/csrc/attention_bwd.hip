@@ -638,10 +638,14 @@ attention_dkv_kernel(AttnArgs a) {
 //  128, 320 steps, heads of 128                               217 /  436  1155 / 3633
 //  192, 8 steps, heads of 64                                 28.2 / 15.8  62.4 / 62.6
 //  256, 64 steps, heads of 128           60.6   345 /  489    129 /   97   519 /  739
+// Up to 32 rows leave three waves of four without work: with SHARE, dk and dv of
+// 512x32, 16/2x64 f32 100 us, without 251; of 512x32, 16/8x128 bf16, whose workgroups
+// then have a compute unit alone, 253 and 91.
 template <class E>
-bool shared(int64_t groups, int64_t steps) {
+bool shared(int64_t rows, int64_t groups, int64_t steps) {
   constexpr bool kWide = sizeof(typename E::storage) == 4;
-  return groups <= 64 || (groups <= (kWide ? 256 : 128) && steps >= (kWide ? 16 : 32));
+  return groups <= 64 || (kWide && rows <= 32 && steps > 1) ||
+         (groups <= (kWide ? 256 : 128) && steps >= (kWide ? 16 : 32));
 }
 
 template <class E, int DP, bool VEC, bool SHARE>
@@ -675,10 +679,10 @@ template <class E, int DP, bool VEC>
 hipError_t backward(const AttnArgs& a, hipStream_t s) {
   const int64_t q = (int64_t)a.B * a.Hq * ((a.Tq + kRows - 1) / kRows);
   const int64_t k = (int64_t)a.B * a.Hkv * ((a.Tk + kRows - 1) / kRows);
-  const hipError_t e = shared<E>(q, (a.Tk + 31) / 32) ? queries<E, DP, VEC, true>(a, s)
+  const hipError_t e = shared<E>(a.Tq, q, (a.Tk + 31) / 32) ? queries<E, DP, VEC, true>(a, s)
                                                       : queries<E, DP, VEC, false>(a, s);
   if (e != hipSuccess) return e;
-  return shared<E>(k, (int64_t)(a.Hq / a.Hkv) * ((a.Tq + 31) / 32)) ? keys<E, DP, VEC, true>(a, s)
+  return shared<E>(a.Tk, k, (int64_t)(a.Hq / a.Hkv) * ((a.Tq + 31) / 32)) ? keys<E, DP, VEC, true>(a, s)
                                                                     : keys<E, DP, VEC, false>(a, s);
 }
 

@@ -514,3 +514,11 @@ def test_masks_of_short_samples(T, kind):
     for causal, Tq in ((True, T), (False, T), (True, 33)):
         _check(*_draw(rng, 3, Tq, T, 2, 2, 64, "bf16"), "bf16", mask=_mask(rng, kind, 3, T), causal=causal)
     _check(*_draw(rng, 2, T, T, 2, 1, 24, "f32"), "f32", mask=_mask(rng, kind, 2, T))
+
+
+@pytest.mark.parametrize("D", [64, 45, 128])
+def test_short_samples_of_many_heads(D):
+    """float32, up to 32 keys or queries, more workgroups than compute units: the waves share them."""
+    rng = np.random.default_rng(21)
+    _check(*_draw(rng, 40, 7, 7, 28, 7, D, "f32"), "f32", mask=_mask(rng, "left", 40, 7))
+    _check(*_draw(rng, 70, 5, 90, 4, 4, D, "f32"), "f32", causal=False)
