@@ -1889,20 +1889,28 @@ bool heads_same(const dpf_heads* a, const dpf_heads* b) {
 }
 
 // Whether two tensors of heads share no element, as far as this can be seen:
-// their ranges are apart, or both step through the same rows (equal stride_t, and
-// stride_b a multiple of it) and take different parts of each.
+// their ranges are apart, or, modulo one of the strides, they are.  A dimension whose
+// stride is a multiple of that step moves no entry modulo it, the others span what
+// lies within a step; parts of a fused row (a step of stride_t, of stride_b where
+// T is 1), of a sample (stride_b) or of a head (stride_h) are seen to be apart so.
 bool heads_apart(const dpf_heads* a, const dpf_heads* b) {
-  const int64_t ea = (int64_t)elem_size(a->dtype), eb = (int64_t)elem_size(b->dtype);
-  if (!ranges_overlap(a->data, (size_t)(heads_extent(a) * ea), b->data, (size_t)(heads_extent(b) * eb)))
+  const int64_t es = (int64_t)elem_size(a->dtype), eb = (int64_t)elem_size(b->dtype);
+  if (!ranges_overlap(a->data, (size_t)(heads_extent(a) * es), b->data, (size_t)(heads_extent(b) * eb)))
     return true;
-  const int64_t row = a->stride_t * ea;
-  if (a->dtype != b->dtype || a->T == 1 || b->T == 1 || a->stride_t != b->stride_t) return false;
-  if ((a->B > 1 && a->stride_b % a->stride_t != 0) || (b->B > 1 && b->stride_b % b->stride_t != 0))
-    return false;
-  const int64_t na = ((a->H - 1) * a->stride_h + a->D) * ea, nb = ((b->H - 1) * b->stride_h + b->D) * eb;
-  int64_t at = (int64_t)((intptr_t)a->data - (intptr_t)b->data) % row;
-  if (at < 0) at += row;
-  return at >= nb && at + na <= row;
+  if (es != eb) return false;
+  const auto within = [](const dpf_heads* t, int64_t step) {    // elements spanned modulo the step
+    return (t->B > 1 && t->stride_b % step != 0 ? (t->B - 1) * t->stride_b : 0) +
+           (t->T > 1 && t->stride_t % step != 0 ? (t->T - 1) * t->stride_t : 0) +
+           (t->H > 1 && t->stride_h % step != 0 ? (t->H - 1) * t->stride_h : 0) + t->D;
+  };
+  const int64_t dims[3] = {a->H, a->T, a->B}, steps[3] = {a->stride_h, a->stride_t, a->stride_b};
+  for (int k = 0; k < 3; ++k) {
+    if (dims[k] == 1 || steps[k] == 0) continue;
+    int64_t at = (int64_t)((intptr_t)a->data - (intptr_t)b->data) / es % steps[k];
+    if (at < 0) at += steps[k];
+    if (at >= within(b, steps[k]) && at + within(a, steps[k]) <= steps[k]) return true;
+  }
+  return false;
 }
 
 // Strides as the kernels take them: those of dimensions of one entry are free, and
