@@ -728,7 +728,7 @@ dpf_status dpfused_qk_norm_rotary_backward(
  *                    aligned to their elements only (16 bytes and D a multiple
  *                    of 8 for the wide path); residual may be NULL; y may be x
  *                    or the residual itself (same pointer and strides), else must
- *                    not overlap them
+ *                    not overlap them (other parts of the same rows do not)
  *   p                in [0, 1); p' = 1 is refused
  *
  * Errors: DPF_ERR_INVALID_ARGUMENT for NULL x or y, shapes that disagree, bad

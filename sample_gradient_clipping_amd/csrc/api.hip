@@ -2083,6 +2083,10 @@ dpf_status check_in_place(const dpf_heads* out, const char* name, const dpf_head
   return DPF_OK;
 }
 
+dpf_heads as_heads(const dpf_act* a) {
+  return dpf_heads{const_cast<void*>(a->data), a->dtype, 0, a->B, a->T, 1, a->D, a->stride_b, a->stride_t, 0};
+}
+
 // An activation whose rows need no alignment.
 dpf_status check_rows(const dpf_act* a, const char* name) {
   if (a == nullptr) return fail(DPF_ERR_INVALID_ARGUMENT, std::string(name) + " is NULL");
@@ -2256,7 +2260,8 @@ dpf_status dpfused_dropout(const dpf_act* x, const dpf_act* residual, const uint
   for (const dpf_act* t : {x, residual}) {
     if (t == nullptr) continue;
     const bool same = t->data == y->data && t->stride_b == y->stride_b && t->stride_t == y->stride_t;
-    if (!same && ranges_overlap(t->data, (size_t)act_bytes(t), y->data, (size_t)act_bytes(y)))
+    const dpf_heads in = as_heads(t), out = as_heads(y);
+    if (!same && !heads_apart(&out, &in))
       return fail(DPF_ERR_INVALID_ARGUMENT, "y overlaps an input without being it");
   }
   dpf::DropoutArgs a{};
