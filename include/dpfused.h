@@ -680,7 +680,7 @@ dpf_status dpfused_attention_backward(const dpf_heads* dout, const dpf_heads* q,
  * one weight without the other, neither weights nor pairs, pairs < 0 or
  * 2 * pairs > D, freqs NULL where pairs > 0, eps, amplitude or interleaved out of
  * range, overlapping outputs; DPF_ERR_UNSUPPORTED for dtypes, alignment (freqs:
- * 8 bytes, weights: 4), D > 256, B * T > 2^24 or B * T * (Hq + Hk) > 2^31. */
+ * 8 bytes, weights: 4), D > 256, B * T >= 2^24 or B * T * (Hq + Hk) > 2^31. */
 dpf_status dpfused_qk_norm_rotary(const dpf_heads* q, const dpf_heads* k, const float* q_weight,
                                   const float* k_weight, float eps, const double* freqs,
                                   int64_t pairs, float amplitude, int32_t interleaved,

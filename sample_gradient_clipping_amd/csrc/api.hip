@@ -2038,10 +2038,11 @@ dpf_status check_rotary(const dpf_heads* q, const dpf_heads* k, const float* qw,
     if (positions->B != q->B || positions->T != q->T)
       return fail(DPF_ERR_INVALID_ARGUMENT, "q and positions disagree on B or T");
   }
+  // a workgroup of 256 threads for each position at most, and fewer than 2^32 threads in a launch
   const int64_t most = (int64_t)1 << 31;
-  if (q->H > most || k->H > most || q->B > ((int64_t)1 << 24) / q->T ||
+  if (q->H > most || k->H > most || q->B > (((int64_t)1 << 24) - 1) / q->T ||
       q->B * q->T > most / (q->H + k->H))
-    return fail(DPF_ERR_UNSUPPORTED, "too many rows (B * T <= 2^24, B * T * (Hq + Hk) <= 2^31)");
+    return fail(DPF_ERR_UNSUPPORTED, "too many rows (B * T < 2^24, B * T * (Hq + Hk) <= 2^31)");
   return DPF_OK;
 }
 
