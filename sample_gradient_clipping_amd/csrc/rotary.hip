@@ -282,12 +282,14 @@ __global__ __launch_bounds__(kNT) void qk_norm_rotary_backward_kernel(RotaryArgs
 }
 
 // dw[b][d] = the chunks' sums: kSlices threads per entry, each every kSlices-th
-// chunk, then their sums in order.
+// chunk, then their sums in order.  Workgroups in rows of kRowOfGroups: one dimension
+// of a launch holds fewer than 2^32 threads, and 2^20 samples of 128 entries need as many.
+constexpr int64_t kRowOfGroups = 1 << 23;
 constexpr int kSlices = 16, kEntries = kNT / kSlices;
 __global__ __launch_bounds__(kNT) void qk_norm_weights_kernel(RotaryArgs a, int chunks) {
   __shared__ float sums[kSlices][kEntries];
   const int x = threadIdx.x % kEntries, k = threadIdx.x / kEntries;
-  const int64_t e = (int64_t)blockIdx.x * kEntries + x, b = e / (2 * a.D);
+  const int64_t e = (blockIdx.y * kRowOfGroups + blockIdx.x) * kEntries + x, b = e / (2 * a.D);
   const int i = (int)(e % (2 * a.D));
   float s = 0.0f;
   if (b < a.B) {
@@ -377,7 +379,9 @@ hipError_t launch_qk_norm_rotary_backward(const RotaryArgs& a, hipStream_t s) {
   timing_end("qk_norm_rotary_backward", s);
   if (e != hipSuccess || a.wq == nullptr) return e;
   timing_begin("qk_norm_weights", s);
-  hipLaunchKernelGGL(qk_norm_weights_kernel, dim3((unsigned)((a.B * 2 * a.D + kEntries - 1) / kEntries)),
+  const int64_t groups = (a.B * 2 * a.D + kEntries - 1) / kEntries;
+  hipLaunchKernelGGL(qk_norm_weights_kernel,
+                     dim3((unsigned)std::min(groups, kRowOfGroups), (unsigned)((groups + kRowOfGroups - 1) / kRowOfGroups)),
                      dim3(kNT), 0, s, a, (int)chunks_of(a));
   timing_end("qk_norm_weights", s);
   return hipGetLastError();
