@@ -243,8 +243,9 @@ __global__ __launch_bounds__(kNT) void qk_norm_rotary_backward_kernel(RotaryArgs
         for (int i = 0; i < NU; ++i)
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            d1[i][e] = f * (d1[i][e] - dot * x[i][e]);
-            d2[i][e] = f * (d2[i][e] - dot * y[i][e]);
+            // a masked row's zeros, whatever the weights hold
+            d1[i][e] = live ? f * (d1[i][e] - dot * x[i][e]) : 0.0f;
+            d2[i][e] = live ? f * (d2[i][e] - dot * y[i][e]) : 0.0f;
           }
       }
 #pragma unroll
