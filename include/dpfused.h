@@ -622,10 +622,10 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  * Errors: DPF_ERR_INVALID_ARGUMENT for NULL pointers, a dimension < 1, shapes
  * that disagree, Tq > Tk, Hq not a multiple of Hkv, bad strides, causal or
  * scale, overlapping outputs; DPF_ERR_UNSUPPORTED for an unknown dtype, mixed
- * dtypes, a misaligned pointer, a non-zero reserved field, D > 128, Tk > 2^22 or
- * B * Hq * ceil(Tk / 32) > 2^22; DPF_ERR_OUT_OF_MEMORY where the workspace (12
- * bytes per position with mask or segments; 4 (D + 2) bytes, D rounded up to 64 or
- * 128, per query, head and split of the keys) cannot be had. */
+ * dtypes, a misaligned pointer, a non-zero reserved field, D > 128, Tk > 2^22,
+ * B * Tk > 2^31 or B * Hq * ceil(Tq / 32) > 2^22; DPF_ERR_OUT_OF_MEMORY where the
+ * workspace (12 bytes per position with mask or segments; 4 (D + 2) bytes, D rounded
+ * up to 64 or 128, per query, head and split of the keys) cannot be had. */
 dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v,
                              const uint8_t* mask, const int32_t* segments, int32_t causal,
                              float scale, const dpf_heads* out, float* lse, void* stream);
@@ -645,8 +645,8 @@ dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_h
  *   dout, out      like q;  dq like q, dk like k, dv like v; the gradients may
  *                  be parts of one array (the G of a fused projection's clip
  *                  call) but must not overlap an input or each other
- *   other arguments and errors as above; the workspace holds 4 bytes per query
- *   and head more. */
+ *   other arguments and errors as above, and B * Hkv * ceil(Tk / 32) <= 2^22; the
+ *   workspace holds 4 bytes per query and head more. */
 dpf_status dpfused_attention_backward(const dpf_heads* dout, const dpf_heads* q,
                                       const dpf_heads* k, const dpf_heads* v,
                                       const dpf_heads* out, const float* lse,

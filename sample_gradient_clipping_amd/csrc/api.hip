@@ -1930,7 +1930,8 @@ bool heads_vec(const dpf_heads* a) {
 }
 
 dpf_status check_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v,
-                           const int32_t* segments, int32_t causal, float scale, const float* lse) {
+                           const int32_t* segments, int32_t causal, float scale, const float* lse,
+                           bool backward) {
   dpf_status st = check_heads(q, "q", false);
   if (st == DPF_OK) st = check_heads(k, "k", false);
   if (st == DPF_OK) st = check_heads(v, "v", false);
@@ -1952,9 +1953,15 @@ dpf_status check_attention(const dpf_heads* q, const dpf_heads* k, const dpf_hea
   if (!std::isnan(scale) && !(scale >= 0x1p-64f && scale <= 0x1p64f))
     return fail(DPF_ERR_INVALID_ARGUMENT, "scale must lie in 2^-64 .. 2^64 (or be NaN for the default)");
   if (q->D > dpf::kAttnMaxD) return fail(DPF_ERR_UNSUPPORTED, "heads are wider than 128");
-  if (k->T > dpf::kAttnMaxT || q->B > dpf::kAttnMaxTiles || q->H > dpf::kAttnMaxTiles ||
-      q->B * q->H > dpf::kAttnMaxTiles / ((k->T + 31) / 32))
-    return fail(DPF_ERR_UNSUPPORTED, "too many positions (Tk <= 2^22, B * Hq * ceil(Tk / 32) <= 2^22)");
+  const auto tiles_ok = [](const dpf_heads* t) {
+    return t->B <= dpf::kAttnMaxTiles && t->H <= dpf::kAttnMaxTiles &&
+           t->B * t->H <= dpf::kAttnMaxTiles / ((t->T + 31) / 32);
+  };
+  if (k->T > dpf::kAttnMaxT || k->B > dpf::kAttnMaxPositions / k->T || !tiles_ok(q))
+    return fail(DPF_ERR_UNSUPPORTED,
+                "too many positions (Tk <= 2^22, B * Tk <= 2^31, B * Hq * ceil(Tq / 32) <= 2^22)");
+  if (backward && !tiles_ok(k))
+    return fail(DPF_ERR_UNSUPPORTED, "too many positions (B * Hkv * ceil(Tk / 32) <= 2^22)");
   return DPF_OK;
 }
 
@@ -2106,7 +2113,7 @@ dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_h
                              const uint8_t* mask, const int32_t* segments, int32_t causal,
                              float scale, const dpf_heads* out, float* lse, void* stream) {
   CallScope call_("dpfused_attention");
-  dpf_status st = check_attention(q, k, v, segments, causal, scale, lse);
+  dpf_status st = check_attention(q, k, v, segments, causal, scale, lse, false);
   if (st == DPF_OK) st = check_heads(out, "out", true);
   if (st != DPF_OK) return st;
   if (out->dtype != q->dtype) return fail(DPF_ERR_UNSUPPORTED, "q and out have different dtypes");
@@ -2137,7 +2144,7 @@ dpf_status dpfused_attention_backward(const dpf_heads* dout, const dpf_heads* q,
                                       int32_t causal, float scale, const dpf_heads* dq,
                                       const dpf_heads* dk, const dpf_heads* dv, void* stream) {
   CallScope call_("dpfused_attention_backward");
-  dpf_status st = check_attention(q, k, v, segments, causal, scale, lse);
+  dpf_status st = check_attention(q, k, v, segments, causal, scale, lse, true);
   if (st == DPF_OK) st = check_heads(dout, "dout", false);
   if (st == DPF_OK) st = check_heads(out, "out", false);
   if (st == DPF_OK) st = check_heads(dq, "dq", true);

@@ -10,7 +10,9 @@ namespace dpf {
 
 constexpr int kAttnMaxD = 128;
 constexpr int64_t kAttnMaxT = (int64_t)1 << 22;
-constexpr int64_t kAttnMaxTiles = (int64_t)1 << 22;   // batch x heads x tiles of 32 positions
+// Batch x heads x tiles of 32 rows: of the queries, and of the keys where their gradients are taken.
+constexpr int64_t kAttnMaxTiles = (int64_t)1 << 22;
+constexpr int64_t kAttnMaxPositions = (int64_t)1 << 31;   // batch x Tk: 256 to a workgroup of `ranges`
 
 struct AttnArgs {
   Heads q, k, v, o;         // o: the output (forward), read by the backward
