@@ -33,11 +33,12 @@ NORMS = ("q_norm", "k_norm")
 
 
 def make_model(V, width, Hq, Hkv, D, seed=0, device="cuda"):
-    """float32 master weights and the rotation's frequencies."""
+    """float32 master weights, the rotation's frequencies and its amplitude."""
     g = torch.Generator().manual_seed(seed)
     draw = lambda *s, scale: (torch.randn(s, generator=g) * scale).to(device)  # noqa: E731
-    freqs, _ = dp.rotary_frequencies(D // 2 * 2, device=device)
-    return {"heads": (Hq, Hkv, D), "freqs": freqs, "table": draw(V, width, scale=1.0),
+    freqs, amplitude = dp.rotary_frequencies(D // 2 * 2, device=device)
+    return {"heads": (Hq, Hkv, D), "freqs": freqs, "amplitude": amplitude,
+            "table": draw(V, width, scale=1.0),
             "wqkv": draw((Hq + 2 * Hkv) * D, width, scale=width ** -0.5),
             "wo": draw(width, Hq * D, scale=(Hq * D) ** -0.5), "w": draw(V, width, scale=width ** -0.5),
             "q_norm": torch.ones(D, device=device), "k_norm": torch.ones(D, device=device)}
@@ -79,7 +80,8 @@ def project(model, ids, positions, dtype):
     X = dp.embedding_lookup(ids, model["table"], out_dtype=dtype)
     qkv = rows_times(X, model["wqkv"].to(dtype).t())
     q, k, _ = split(qkv, model["heads"])
-    return X, qkv, dp.qk_norm_rotary(q, k, model["q_norm"], model["k_norm"], model["freqs"], positions)
+    return X, qkv, dp.qk_norm_rotary(q, k, model["q_norm"], model["k_norm"], model["freqs"], positions,
+                                     amplitude=model["amplitude"])
 
 
 def private_gradients(model, batch, C, sigma, seed, p=0.1, dtype=torch.bfloat16):
@@ -105,7 +107,7 @@ def private_gradients(model, batch, C, sigma, seed, p=0.1, dtype=torch.bfloat16)
     dp.attention_backward(dA, q, k, v, att.out, att.lse, segments=documents, dq=dq, dk=dk, dv=dv)
     before = split(qkv, heads)
     norm = dp.qk_norm_rotary_backward(dq, dk, before[0], before[1], model["q_norm"], model["k_norm"],
-                                      model["freqs"], positions, dq=dq, dk=dk)
+                                      model["freqs"], positions, amplitude=model["amplitude"], dq=dq, dk=dk)
     dX = rows_times(dqkv, model["wqkv"].to(dtype)).add_(dR)
 
     V, one = model["table"].shape[0], torch.ones((B, 1, 1), dtype=torch.float32, device=ids.device)

@@ -604,6 +604,9 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  * whose D products have magnitudes that sum to a is off by up to D 2^-24 scale a,
  * and its weight by that relative to it: scores of 10^4 and more are not for this.
  *
+ * The running maximum is up to 2^8 below the largest weight, and a row is divided by
+ * its sum at the end: 2^8 Tk max |v| has to stay finite in float32.
+ *
  * A NaN or infinity in an active position reaches the outputs of its own
  * sample (of any of its positions that share a tile of keys, also those that
  * do not attend to it), never another sample's; masked positions are never
@@ -624,8 +627,10 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  * scale, overlapping outputs; DPF_ERR_UNSUPPORTED for an unknown dtype, mixed
  * dtypes, a misaligned pointer, a non-zero reserved field, D > 128, Tk > 2^22,
  * B * Tk > 2^31 or B * Hq * ceil(Tq / 32) > 2^22; DPF_ERR_OUT_OF_MEMORY where the
- * workspace (12 bytes per position with mask or segments; 4 (D + 2) bytes, D rounded
- * up to 64 or 128, per query, head and split of the keys) cannot be had. */
+ * workspace cannot be had: with mask or segments 8 bytes per position and 8 per 64
+ * positions of each sample (none for a mask alone with Tk <= 256 and more than 32
+ * queries times heads of a group); where the keys are split 4 (D + 2) bytes, D rounded
+ * up to 64 or 128, per query, head and split. */
 dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_heads* v,
                              const uint8_t* mask, const int32_t* segments, int32_t causal,
                              float scale, const dpf_heads* out, float* lse, void* stream);
@@ -646,7 +651,8 @@ dpf_status dpfused_attention(const dpf_heads* q, const dpf_heads* k, const dpf_h
  *                  be parts of one array (the G of a fused projection's clip
  *                  call) but must not overlap an input or each other
  *   other arguments and errors as above, and B * Hkv * ceil(Tk / 32) <= 2^22; the
- *   workspace holds 4 bytes per query and head more. */
+ *   workspace: with mask or segments as above, whatever Tk is, and 4 bytes per query and
+ *   head. */
 dpf_status dpfused_attention_backward(const dpf_heads* dout, const dpf_heads* q,
                                       const dpf_heads* k, const dpf_heads* v,
                                       const dpf_heads* out, const float* lse,

@@ -18,9 +18,10 @@
 // maximum and the output stay in float32.
 //
 // 8x2048, 40x128 bf16: 410 us, 840 TFLOP/s.  A tile of 32 x 32 x 128 takes 16 matrix
-// instructions (512 cycles) and about 130 others (500 cycles, 256 of them the
-// exponentials); three waves per SIMD overlap two thirds to four fifths of that.
-// Tiles of 32 keys are what leaves registers for three (64 keys, two waves: 444 us).
+// instructions (512 cycles) and about 126 vector ones (500 cycles, 256 of them the
+// exponentials), 71 scalar and 24 LDS ones; of a compute unit's busy time the matrix
+// units work 46%, the vector units 58%.  Tiles of 32 keys are what leaves registers for
+// three waves per SIMD (64 keys, two waves: 444 us).
 #include "attn.hpp"
 
 #include <algorithm>
@@ -42,7 +43,12 @@ constexpr float kSlack = 8.0f;
 // position), so a causal row with one key has lo == p and any other with one
 // key end == lo + 1.  Segment numbers do not decrease, so the start of the
 // first position's segment and the end of the last one's are found by 64-way
-// search, the boundaries between by a vote.  A chain of latencies: 3 to 5 us.
+// search, the boundaries between by a vote.  A chain of latencies: 3 to 5 us without a
+// mask or where padding is short.  The first active position before the wave's own is
+// looked for 64 mask bytes at a time from the segment's start (not causal: the last one
+// from its end), one round trip each: left-padded samples of 8192 positions take 20 us
+// with 4096 of them padded, 34 with 7680, 65536 with half of them padded 175, and 2^20
+// so 2.5 ms, more than the attention of a single token that follows (43, 10, 370, 370).
 __device__ __forceinline__ int first_from(const int32_t* id, int l, int r, int32_t least, int lane) {
   // smallest index in [l, r) whose id is >= least, else r
   while (l < r) {

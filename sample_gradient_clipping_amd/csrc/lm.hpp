@@ -300,7 +300,7 @@ struct RotaryArgs {
   Ids positions;            // data null: 0 .. T - 1
   const uint8_t* mask;      // [B, T] or null
   float *dwq, *dwk;         // backward: [B, D] each
-  float* part;              // rotary_part_floats
+  float* part;              // the weights' partial sums: as many floats as rotary_plan says
   int width;                // entries of a 16- or 8-byte piece, or 1 (set by rotary_plan)
   int tokens;               // of a workgroup (set by rotary_plan)
 };
