@@ -69,8 +69,11 @@ def _act(t) -> DpfAct:
 
 def _stream(t, stream) -> int:
     torch = _torch()
-    if stream is None:      # torch.cuda.current_stream, without its Stream object (2 us)
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:     # torch.cuda.current_stream, without its Stream object (2 us)
+            return raw(t.device.index)
+        stream = torch.cuda.current_stream(t.device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
