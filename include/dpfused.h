@@ -604,8 +604,8 @@ dpf_status dpfused_token_logprobs_backward(const dpf_act* logits, const dpf_ids*
  * whose D products have magnitudes that sum to a is off by up to D 2^-24 scale a,
  * and its weight by that relative to it: scores of 10^4 and more are not for this.
  *
- * The running maximum is up to 2^8 below the largest weight, and a row is divided by
- * its sum at the end: 2^8 Tk max |v| has to stay finite in float32.
+ * Weights are held relative to a running maximum, up to 2^8, and a row is divided by
+ * their sum at the end: 2^8 Tk max |v| has to stay finite in float32.
  *
  * A NaN or infinity in an active position reaches the outputs of its own
  * sample (of any of its positions that share a tile of keys, also those that

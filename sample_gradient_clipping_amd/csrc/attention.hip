@@ -48,7 +48,7 @@ constexpr float kSlack = 8.0f;
 // looked for 64 mask bytes at a time from the segment's start (not causal: the last one
 // from its end), one round trip each: left-padded samples of 8192 positions take 20 us
 // with 4096 of them padded, 34 with 7680, 65536 with half of them padded 175, and 2^20
-// so 2.5 ms, more than the attention of a single token that follows (43, 10, 370, 370).
+// so 2.5 ms, beside 43, 10, 370 and 370 us of a single token's attention.
 __device__ __forceinline__ int first_from(const int32_t* id, int l, int r, int32_t least, int lane) {
   // smallest index in [l, r) whose id is >= least, else r
   while (l < r) {
